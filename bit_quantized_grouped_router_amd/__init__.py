@@ -25,6 +25,8 @@ EXPORTS = [
     "moe_unpermute_combine", "moe_layer_workspace_bytes", "moe_layer_forward",
     "moe_dequant_w4", "moe_status_string", "moe_last_hip_error", "moe_router_logits",
     "moe_layer_forward_hidden", "moe_route_permute", "moe_layer_forward_noalloc",
+    "moe_linear_w4", "moe_kv4_append", "moe_kv4_read", "moe_kv4_attention_workspace_bytes",
+    "moe_kv4_attention",
 ]
 
 
@@ -43,6 +45,21 @@ class MoeW4Weights(ctypes.Structure):
                 ("s2", MoeW4Matrix)]
 
 
+class MoeKv4Dims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("page", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
+class MoeKv4Cache(ctypes.Structure):
+    _fields_ = [("k", MoeW4Matrix), ("v", MoeW4Matrix)]
+
+
+class MoeKv4Batch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("cu", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p)]
+
+
 class MoeError(RuntimeError):
     pass
 
@@ -58,6 +75,9 @@ def load(path: str) -> ctypes.CDLL:
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     D = ctypes.POINTER(MoeDims)
     W = ctypes.POINTER(MoeW4Weights)
+    KD, KC, KB = (ctypes.POINTER(MoeKv4Dims), ctypes.POINTER(MoeKv4Cache),
+                  ctypes.POINTER(MoeKv4Batch))
+    I64 = ctypes.c_int64
     sig = {
         "moe_route": ([P, I32, I32, I32, P, P, P], I32),
         "moe_block_m": ([], I32),
@@ -75,6 +95,13 @@ def load(path: str) -> ctypes.CDLL:
         "moe_layer_forward_hidden": ([D, P, P, W, P, P, SZ, P], I32),
         "moe_route_permute": ([D, P, P, P, P, P, P, P, P, P, P, SZ, P], I32),
         "moe_dequant_w4": ([ctypes.POINTER(MoeW4Matrix), I32, I32, P, P], I32),
+        "moe_linear_w4": ([I32, I32, I32, P, I64, ctypes.POINTER(MoeW4Matrix), P, I32, P, I64, P,
+                           I64, I32, P], I32),
+        "moe_kv4_append": ([KD, KC, I32, P, I64, P, I64, I32, KB, P], I32),
+        "moe_kv4_read": ([KD, KC, I32, P, I64, P, I64, I32, KB, P], I32),
+        "moe_kv4_attention_workspace_bytes": ([KD, I32, I32, I32], SZ),
+        "moe_kv4_attention": ([KD, KC, I32, I32, P, I64, P, I64, KB, ctypes.c_float, I32, I32, P,
+                               SZ, P], I32),
         "moe_status_string": ([I32], ctypes.c_char_p),
         "moe_last_hip_error": ([], I32),
     }
@@ -457,4 +484,216 @@ def moe_dequant_w4(m: W4Matrix, index: int = 0, out=None, stream=None):
     cm = m.c(index)
     _check(lib().moe_dequant_w4(ctypes.byref(cm), rows, cols, _ptr(out), _stream(stream)),
            "moe_dequant_w4")
+    return out
+
+
+# ------------------------------------------------------------------ dense int4-g64 projection
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _on(stream):
+    """The torch context to allocate in for work on ``stream``: memory taken there is
+    handed out again in that stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(h) if h else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _here(**tensors) -> None:
+    """Raise unless every tensor given lives on the current GPU."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise MoeError(f"{name} must live in GPU memory")
+        if t.get_device() != cur:
+            raise MoeError(f"{name} lives on {t.device}; the current device is cuda:{cur}")
+
+
+def _rows(t: torch.Tensor, shape, name: str, dtypes) -> int:
+    """Stride between the rows (first dimension) of t, whose rows must be dense and not
+    overlap; raises for another shape or element type."""
+    if tuple(t.shape) != tuple(shape):
+        raise MoeError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise MoeError(f"{name} has dtype {t.dtype}; expected one of "
+                       f"{', '.join(str(d) for d in dtypes)}")
+    row = 1
+    for i in range(t.dim() - 1, 0, -1):
+        if t.shape[i] > 1 and t.stride(i) != row:
+            raise MoeError(f"{name}: the dimensions after the first must be contiguous")
+        row *= t.shape[i]
+    if t.shape[0] <= 1:
+        return (row + 7) // 8 * 8
+    if t.stride(0) < row:
+        raise MoeError(f"{name}: its rows overlap")
+    return t.stride(0)
+
+
+def _dtype(dtype) -> int:
+    if dtype not in DTYPES:
+        raise MoeError(f"dtype {dtype}; expected torch.bfloat16 or torch.float32")
+    return DTYPES[dtype]
+
+
+def moe_linear_w4(x: torch.Tensor, w: W4Matrix, bias=None, act: str = "none", residual=None, y=None,
+                  out_dtype=None, stream=None):
+    """y [T, rows] = act(x [T, cols] W^T + bias) + residual for one int4-g64 matrix W
+    [rows, cols]. act: none, relu, silu or gelu (erf form). y is bf16 unless out_dtype, y
+    or the residual says fp32; y may be the residual itself (in place)."""
+    if x.dim() != 2 or w.codes.dim() not in (2, 3) or (w.codes.dim() == 3 and w.codes.shape[0] != 1):
+        raise MoeError("x must be [T, cols] and w one matrix: codes [1, rows, cols/2] or [rows, cols/2]")
+    T, cols = x.shape
+    rows = w.codes.shape[-2]
+    if w.codes.shape[-1] * 2 != cols:
+        raise MoeError(f"w has {w.codes.shape[-1] * 2} columns; x has {cols}")
+    if act not in ACTS:
+        raise MoeError(f"act {act!r}; expected one of {', '.join(ACTS)}")
+    _here(x=x, codes=w.codes, scales=w.scales, biases=w.biases, bias=bias, residual=residual, y=y)
+    given = [t.dtype for t in (y, residual) if t is not None]
+    dtype = out_dtype if out_dtype is not None else (given[0] if given else torch.bfloat16)
+    code = _dtype(dtype)
+    xs = _rows(x, (T, cols), "x", BF16)
+    rs = 0 if residual is None else _rows(residual, (T, rows), "residual", (dtype,))
+    if y is None:
+        y = _empty((T, rows), dtype, x.device, stream)
+    ys = _rows(y, (T, rows), "y", (dtype,))
+    if bias is not None:
+        _need(bias, rows * 2, "bias", BF16)
+    _need(w.codes, rows * cols // 2, "codes", U8)
+    _need(w.scales, rows * (cols // GROUP) * 2, "scales", BF16)
+    _need(w.biases, rows * (cols // GROUP) * 2, "biases", BF16)
+    cm = w.c()
+    _check(lib().moe_linear_w4(T, rows, cols, x.data_ptr(), xs, ctypes.byref(cm), _ptr(bias),
+                               ACTS[act], None if residual is None else residual.data_ptr(), rs,
+                               y.data_ptr(), ys, code, _stream(stream)), "moe_linear_w4")
+    return y
+
+
+# ------------------------------------------------------------------ the 4-bit key/value cache
+
+class KV4Cache:
+    """A paged key/value cache in int4-g64: k and v hold codes uint8 [num_pages, Hkv, page,
+    D/2] and scales/biases bf16 [num_pages, Hkv, page, D/64]."""
+
+    def __init__(self, k: W4Matrix, v: W4Matrix):
+        self.k, self.v = k, v
+        if k.codes.dim() != 4:
+            raise MoeError("cache codes must be [num_pages, Hkv, page, D/2]")
+        self.num_pages, self.Hkv, self.page, half = k.codes.shape
+        self.D = 2 * half
+        g = (self.num_pages, self.Hkv, self.page, self.D // GROUP)
+        for n, m in (("k", k), ("v", v)):
+            if m.codes.shape != k.codes.shape:
+                raise MoeError(f"{n}.codes has shape {tuple(m.codes.shape)}; k.codes {tuple(k.codes.shape)}")
+            if m.codes.dtype not in U8:
+                raise MoeError(f"{n}.codes has dtype {m.codes.dtype}; expected torch.uint8")
+            for f in ("scales", "biases"):
+                t = getattr(m, f)
+                if tuple(t.shape) != g or t.dtype not in BF16:
+                    raise MoeError(f"{n}.{f} is {t.dtype} {tuple(t.shape)}; expected bf16 {g}")
+
+    @staticmethod
+    def empty(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> "KV4Cache":
+        """An uninitialised cache."""
+        def plane():
+            g = (num_pages, Hkv, page, D // GROUP)
+            return W4Matrix(torch.empty((num_pages, Hkv, page, D // 2), dtype=torch.uint8, device=device),
+                            torch.empty(g, dtype=torch.bfloat16, device=device),
+                            torch.empty(g, dtype=torch.bfloat16, device=device))
+        return KV4Cache(plane(), plane())
+
+    def c(self) -> MoeKv4Cache:
+        return MoeKv4Cache(self.k.c(), self.v.c())
+
+
+def _kv4(cache: KV4Cache, page_table, cu, kv_len, Hq: int = 0):
+    """The C structs of a cache and a batch, after checking the batch's tensors."""
+    if page_table.dim() != 2 or cu.dim() != 1 or kv_len.dim() != 1:
+        raise MoeError("page_table must be [B, max_pages], cu [B + 1] and kv_len [B]")
+    B, width = page_table.shape
+    if cu.shape[0] != B + 1 or kv_len.shape[0] != B:
+        raise MoeError(f"{B} sequences in page_table, {cu.shape[0] - 1} in cu, {kv_len.shape[0]} in kv_len")
+    for name, t in (("page_table", page_table), ("cu", cu), ("kv_len", kv_len)):
+        if t.dtype != torch.int32:
+            raise MoeError(f"{name} has dtype {t.dtype}; expected torch.int32")
+    _here(page_table=page_table, cu=cu, kv_len=kv_len, k=cache.k.codes, v=cache.v.codes)
+    dm = MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, width)
+    return dm, cache.c(), MoeKv4Batch(_ptr(page_table), _ptr(cu), _ptr(kv_len))
+
+
+def moe_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, page_table, cu, kv_len,
+                   stream=None) -> None:
+    """Quantise new keys and values [T, Hkv, D] (bf16 or fp32) into the cache. Rows
+    cu[b] .. cu[b+1]-1 are the last tokens of sequence b, which then has kv_len[b]."""
+    dm, c, b = _kv4(cache, page_table, cu, kv_len)
+    _here(k=k, v=v)
+    T = k.shape[0]
+    dt = _dtype(k.dtype)
+    shape = (T, cache.Hkv, cache.D)
+    ks, vs = _rows(k, shape, "k", (k.dtype,)), _rows(v, shape, "v", (k.dtype,))
+    _check(lib().moe_kv4_append(ctypes.byref(dm), ctypes.byref(c), T, k.data_ptr(), ks, v.data_ptr(), vs,
+                                dt, ctypes.byref(b), _stream(stream)), "moe_kv4_append")
+
+
+def moe_kv4_read(cache: KV4Cache, page_table, cu, kv_len, T: int, dtype=torch.bfloat16, k=None, v=None,
+                 stream=None):
+    """Keys and values [T, Hkv, D] of the last cu[b+1] - cu[b] tokens of each sequence."""
+    dm, c, b = _kv4(cache, page_table, cu, kv_len)
+    dt = _dtype(dtype)
+    shape = (T, cache.Hkv, cache.D)
+    k = _empty(shape, dtype, page_table.device, stream) if k is None else k
+    v = _empty(shape, dtype, page_table.device, stream) if v is None else v
+    _here(k=k, v=v)
+    ks, vs = _rows(k, shape, "k", (dtype,)), _rows(v, shape, "v", (dtype,))
+    _check(lib().moe_kv4_read(ctypes.byref(dm), ctypes.byref(c), T, k.data_ptr(), ks, v.data_ptr(), vs,
+                              dt, ctypes.byref(b), _stream(stream)), "moe_kv4_read")
+    return k, v
+
+
+def moe_kv4_attention_workspace_bytes(cache: KV4Cache, T: int, Hq: int, B: int, max_pages: int,
+                                      max_new: int, window: int = 0) -> int:
+    dm = MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, max_pages)
+    return lib().moe_kv4_attention_workspace_bytes(ctypes.byref(dm), T, max_new, window)
+
+
+def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, max_new: int,
+                      scale: Optional[float] = None, causal: bool = True, window: int = 0, out=None,
+                      ws=None, stream=None):
+    """Attention of queries q [T, Hq, D] (bf16) over the cache; rows cu[b] .. cu[b+1]-1 are
+    the last tokens of sequence b. max_new: an upper bound of the new tokens of a sequence.
+    scale defaults to D ** -0.5."""
+    if q.dim() != 3:
+        raise MoeError("q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    if D != cache.D:
+        raise MoeError(f"q has {D} channels a head; the cache {cache.D}")
+    dm, c, b = _kv4(cache, page_table, cu, kv_len, Hq)
+    _here(q=q, out=out, ws=ws)
+    qs = _rows(q, (T, Hq, D), "q", BF16)
+    if out is None:
+        out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
+    os_ = _rows(out, (T, Hq, D), "out", BF16)
+    if ws is None:
+        need = lib().moe_kv4_attention_workspace_bytes(ctypes.byref(dm), T, max_new, window)
+        if need:
+            ws = _empty((need,), torch.uint8, q.device, stream)
+    _check(lib().moe_kv4_attention(ctypes.byref(dm), ctypes.byref(c), T, max_new, q.data_ptr(), qs,
+                                   out.data_ptr(), os_, ctypes.byref(b),
+                                   D ** -0.5 if scale is None else scale, int(causal), window, _ptr(ws),
+                                   0 if ws is None else ws.numel() * ws.element_size(),
+                                   _stream(stream)), "moe_kv4_attention")
     return out

@@ -7,7 +7,9 @@
 #include <mutex>
 
 #include "../../include/moe_w4.h"
+#include "moe_kv4.h"
 #include "moe_launch.h"
+#include "moe_linear.h"
 
 using namespace moe;
 
@@ -130,6 +132,69 @@ LayerWs carve_layer(const Dims &dm, char *base) {
   w.logits = take<float>(base, off, (size_t)dm.T * dm.E);  // router scores (hidden-state entry)
   w.bytes = off;
   return w;
+}
+
+// A stride between rows of `row` elements that must stay 16-byte aligned.
+moe_status check_stride(int64_t stride, int64_t row) {
+  if (stride < row) return MOE_E_INVALID;
+  return stride % 8 != 0 ? MOE_E_UNSUPPORTED : MOE_OK;
+}
+
+moe_status check_dtype(int32_t dtype) {
+  return dtype == MOE_BF16 || dtype == MOE_F32 ? MOE_OK : MOE_E_INVALID;
+}
+
+// Shapes of the 4-bit cache; Hq only matters to the attention.
+moe_status check_kv4_dims(const moe_kv4_dims *dm, int32_t T, bool queries) {
+  if (dm == nullptr || T < 0) return MOE_E_INVALID;
+  if (dm->B <= 0 || dm->Hkv <= 0 || dm->D <= 0 || dm->page <= 0 || dm->num_pages <= 0 ||
+      dm->max_pages <= 0)
+    return MOE_E_INVALID;
+  if (queries && (dm->Hq <= 0 || dm->Hq % dm->Hkv != 0)) return MOE_E_INVALID;
+  if (dm->D != 64 && dm->D != 128 && dm->D != 256) return MOE_E_UNSUPPORTED;
+  if (dm->page < 16 || dm->page > 65536 || (dm->page & (dm->page - 1)) != 0) return MOE_E_UNSUPPORTED;
+  if ((long long)dm->max_pages * dm->page >= (1ll << 31)) return MOE_E_UNSUPPORTED;
+  if (dm->B > 65535 || dm->Hkv > 65535 || (queries && dm->Hq > 65535)) return MOE_E_UNSUPPORTED;
+  if ((long long)T * 2 * dm->Hkv * dm->D >= (1ll << 40)) return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
+Kv4Dims to_kv4_dims(const moe_kv4_dims *dm) {
+  return Kv4Dims{dm->B, dm->Hq, dm->Hkv, dm->D, dm->page, __builtin_ctz((unsigned)dm->page),
+                 dm->num_pages, dm->max_pages};
+}
+
+moe_status check_kv4_plane(const moe_kv4_plane &p) {
+  MOE_TRY(check_ptr(p.codes));
+  MOE_TRY(check_ptr(p.scales));
+  return check_ptr(p.biases);
+}
+
+moe_status check_kv4_cache(const moe_kv4_cache *c, const moe_kv4_batch *b) {
+  if (c == nullptr || b == nullptr) return MOE_E_INVALID;
+  MOE_TRY(check_kv4_plane(c->k));
+  MOE_TRY(check_kv4_plane(c->v));
+  MOE_TRY(check_ptr(b->page_table));
+  MOE_TRY(check_ptr(b->cu));
+  return check_ptr(b->kv_len);
+}
+
+Kv4Plane to_kv4_plane(const moe_kv4_plane &p) { return Kv4Plane{p.codes, p.scales, p.biases}; }
+
+Kv4Batch to_kv4_batch(const moe_kv4_batch *b, int32_t T) {
+  return Kv4Batch{b->page_table, b->cu, b->kv_len, T};
+}
+
+// max_new as the kernels take it: no sequence has more new tokens than there
+// are rows.
+int kv4_max_new(int32_t T, int32_t max_new) { return max_new < T ? max_new : T; }
+
+moe_status check_kv4_attention(const moe_kv4_dims *dm, int32_t T, int32_t max_new, int32_t window) {
+  MOE_TRY(check_kv4_dims(dm, T, true));
+  if (max_new < 0 || (max_new == 0 && T > 0) || window < 0) return MOE_E_INVALID;
+  if ((long long)T * dm->Hq >= (1ll << 31) - 64) return MOE_E_UNSUPPORTED;
+  if (T > 0 && !kv4_grid_ok(to_kv4_dims(dm), kv4_max_new(T, max_new), window)) return MOE_E_UNSUPPORTED;
+  return MOE_OK;
 }
 
 // Scratch of moe_layer_forward_noalloc: one copy per GPU, loaded with the
@@ -389,6 +454,92 @@ moe_status moe_dequant_w4(const moe_w4_matrix *m, int32_t rows, int32_t cols, ui
   MOE_TRY(check_matrix(*m));
   MOE_TRY(check_ptr(out));
   return hip_status(launch_dequant(to_w4(*m), rows, cols, out, as_stream(stream)));
+}
+
+moe_status moe_linear_w4(int32_t T, int32_t rows, int32_t cols, const uint16_t *x, int64_t x_stride,
+                         const moe_w4_matrix *w, const uint16_t *bias, int32_t act,
+                         const void *residual, int64_t residual_stride, void *y, int64_t y_stride,
+                         int32_t dtype, void *stream) {
+  if (w == nullptr || T < 0 || rows <= 0 || cols <= 0) return MOE_E_INVALID;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_E_INVALID;
+  MOE_TRY(check_dtype(dtype));
+  if (cols % kGroup != 0 || (long long)rows * cols >= (1ll << 34)) return MOE_E_UNSUPPORTED;
+  if ((long long)T * rows >= (1ll << 40) || (long long)T * cols >= (1ll << 40)) return MOE_E_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!linear_grid_ok(T, rows)) return MOE_E_UNSUPPORTED;
+  MOE_TRY(check_stride(x_stride, cols));
+  if (y_stride < rows || (residual != nullptr && residual_stride < rows)) return MOE_E_INVALID;
+  MOE_TRY(check_ptr(x));
+  MOE_TRY(check_matrix(*w));
+  if (bias != nullptr) MOE_TRY(check_ptr(bias));
+  if (residual != nullptr) MOE_TRY(check_ptr(residual));
+  MOE_TRY(check_ptr(y));
+  if (residual == y && residual_stride != y_stride) return MOE_E_INVALID;
+  const LinearArgs a{T, rows, cols, x, x_stride, to_w4(*w), bias, act, residual, residual_stride, y, y_stride};
+  return hip_status(launch_linear(a, dtype, as_stream(stream)));
+}
+
+moe_status moe_kv4_append(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
+                          const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                          int32_t dtype, const moe_kv4_batch *batch, void *stream) {
+  MOE_TRY(check_kv4_dims(dm, T, false));
+  MOE_TRY(check_dtype(dtype));
+  if (T == 0) return MOE_OK;
+  MOE_TRY(check_stride(k_stride, (int64_t)dm->Hkv * dm->D));
+  MOE_TRY(check_stride(v_stride, (int64_t)dm->Hkv * dm->D));
+  MOE_TRY(check_kv4_cache(cache, batch));
+  MOE_TRY(check_ptr(k));
+  MOE_TRY(check_ptr(v));
+  return hip_status(launch_kv4_append(to_kv4_dims(dm), to_kv4_plane(cache->k), to_kv4_plane(cache->v),
+                                      to_kv4_batch(batch, T), k, v, k_stride, v_stride, dtype,
+                                      as_stream(stream)));
+}
+
+moe_status moe_kv4_read(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T, void *k,
+                        int64_t k_stride, void *v, int64_t v_stride, int32_t dtype,
+                        const moe_kv4_batch *batch, void *stream) {
+  MOE_TRY(check_kv4_dims(dm, T, false));
+  MOE_TRY(check_dtype(dtype));
+  if (T == 0) return MOE_OK;
+  MOE_TRY(check_stride(k_stride, (int64_t)dm->Hkv * dm->D));
+  MOE_TRY(check_stride(v_stride, (int64_t)dm->Hkv * dm->D));
+  MOE_TRY(check_kv4_cache(cache, batch));
+  MOE_TRY(check_ptr(k));
+  MOE_TRY(check_ptr(v));
+  return hip_status(launch_kv4_read(to_kv4_dims(dm), to_kv4_plane(cache->k), to_kv4_plane(cache->v),
+                                    to_kv4_batch(batch, T), k, v, k_stride, v_stride, dtype,
+                                    as_stream(stream)));
+}
+
+size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int32_t max_new,
+                                         int32_t window) {
+  if (check_kv4_attention(dm, T, max_new, window) != MOE_OK || T == 0) return 0;
+  return kv4_attention_ws(to_kv4_dims(dm), kv4_max_new(T, max_new), window);
+}
+
+moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
+                             int32_t max_new, const uint16_t *q, int64_t q_stride, uint16_t *out,
+                             int64_t out_stride, const moe_kv4_batch *batch, float scale,
+                             int32_t causal, int32_t window, void *ws, size_t ws_bytes,
+                             void *stream) {
+  MOE_TRY(check_kv4_attention(dm, T, max_new, window));
+  if (!(scale > 0.0f) || !(scale <= 3.402823466e38f)) return MOE_E_INVALID;
+  if (T == 0) return MOE_OK;
+  MOE_TRY(check_stride(q_stride, (int64_t)dm->Hq * dm->D));
+  MOE_TRY(check_stride(out_stride, (int64_t)dm->Hq * dm->D));
+  MOE_TRY(check_kv4_cache(cache, batch));
+  MOE_TRY(check_ptr(q));
+  MOE_TRY(check_ptr(out));
+  const Kv4Dims d = to_kv4_dims(dm);
+  const int n = kv4_max_new(T, max_new);
+  const size_t need = kv4_attention_ws(d, n, window);
+  if (need > 0) {
+    if (ws_bytes < need) return MOE_E_WORKSPACE;
+    MOE_TRY(check_ptr(ws));
+  }
+  const Kv4Attn at{q, out, q_stride, out_stride, n, scale, causal != 0, window};
+  return hip_status(launch_kv4_attention(d, to_kv4_plane(cache->k), to_kv4_plane(cache->v),
+                                         to_kv4_batch(batch, T), at, ws, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,136 @@
+// The paged int4-g64 key/value cache: its shape, where a token lives in it,
+// and the launchers of the kernels that write, read and attend to it.
+//
+// The index arithmetic is plain C++ (no HIP types), so that it can be checked
+// on the host; every index that comes from device memory (sequence offsets,
+// lengths, page numbers) is brought into range here before it is used.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#ifdef __HIPCC__
+#include <hip/hip_runtime.h>
+#define MOE_HD __host__ __device__ __forceinline__
+#else
+#define MOE_HD inline
+#endif
+
+namespace moe {
+
+struct Kv4Dims {
+  int B, Hq, Hkv, D;
+  int page, page_shift;  // tokens per page, its log2
+  int num_pages, max_pages;
+};
+
+struct Kv4Plane {
+  uint8_t *codes;
+  uint16_t *scales, *biases;
+};
+
+// Per-sequence metadata in device memory, and the rows T of the token tensors.
+struct Kv4Batch {
+  const int32_t *table;  // [B][max_pages] page numbers
+  const int32_t *cu;     // [B+1] first row of each sequence's new tokens
+  const int32_t *len;    // [B] tokens of each sequence, the new ones included
+  int T;
+};
+
+// The new tokens of one sequence: rows begin .. begin + n - 1 of the token
+// tensors, at positions first .. first + n - 1 of the sequence (first may be
+// negative when the caller's lengths do not fit: such positions hold nothing).
+struct Kv4Span {
+  int begin, n;
+  long long first, len;
+};
+
+MOE_HD Kv4Span kv4_span(int cu0, int cu1, int len, int T) {
+  Kv4Span s;
+  s.begin = cu0 < 0 ? 0 : (cu0 > T ? T : cu0);
+  const int end = cu1 > T ? T : cu1;
+  s.n = end > s.begin ? end - s.begin : 0;
+  s.len = len < 0 ? 0 : len;
+  s.first = s.len - s.n;
+  return s;
+}
+
+// Positions a sequence's page table row covers.
+MOE_HD long long kv4_capacity(const Kv4Dims &dm) { return (long long)dm.max_pages << dm.page_shift; }
+
+MOE_HD bool kv4_page_ok(const Kv4Dims &dm, int page) { return page >= 0 && page < dm.num_pages; }
+
+// Cache row (of D/2 bytes of codes) of a slot of a page and a head.
+MOE_HD long long kv4_row(const Kv4Dims &dm, int page, int head, int slot) {
+  return (((long long)page * dm.Hkv + head) << dm.page_shift) + slot;
+}
+
+// Keys a block of query rows at positions p0 .. p1 (p0 <= p1) can see: lo ..
+// hi - 1, empty when hi <= lo.
+struct Kv4Range {
+  long long lo, hi;
+};
+
+MOE_HD Kv4Range kv4_range(const Kv4Dims &dm, long long p0, long long p1, long long len, bool causal,
+                          int window) {
+  const long long cap = kv4_capacity(dm);
+  Kv4Range r;
+  r.hi = len < cap ? len : cap;
+  if (causal && p1 + 1 < r.hi) r.hi = p1 + 1;
+  r.lo = window > 0 && p0 - window + 1 > 0 ? p0 - window + 1 : 0;
+  return r;
+}
+
+constexpr int kKvTile = 32;  // keys a wavefront takes at a time (two 16-key halves, one page each)
+
+// Tiles of a key range, and the share of one of `splits` workgroups: the tiles
+// begin .. end - 1, `used` splits having any. A split takes at least
+// kMinSplitTiles tiles, so a short sequence is spread over fewer workgroups.
+constexpr int kMinSplitTiles = 8;
+struct Kv4Share {
+  int begin, end, used;
+};
+
+MOE_HD Kv4Share kv4_share(const Kv4Range &r, int splits, int split) {
+  const long long t0 = r.lo / kKvTile, t1 = r.hi > r.lo ? (r.hi + kKvTile - 1) / kKvTile : t0;
+  const int n = (int)(t1 - t0);
+  int per = (n + splits - 1) / splits;
+  if (per < kMinSplitTiles) per = kMinSplitTiles;
+  Kv4Share s;
+  s.used = n > 0 ? (n + per - 1) / per : 1;
+  const int b = split * per < n ? split * per : n;
+  const int e = b + per < n ? b + per : n;
+  s.begin = (int)t0 + b;
+  s.end = (int)t0 + e;
+  return s;
+}
+
+#ifdef __HIPCC__
+// dtype: 0 bf16, 1 fp32
+hipError_t launch_kv4_append(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
+                             const Kv4Batch &bt, const void *k, const void *v, long long k_stride,
+                             long long v_stride, int dtype, hipStream_t s);
+hipError_t launch_kv4_read(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
+                           const Kv4Batch &bt, void *k, void *v, long long k_stride,
+                           long long v_stride, int dtype, hipStream_t s);
+
+struct Kv4Attn {
+  const uint16_t *q;
+  uint16_t *out;
+  long long q_stride, out_stride;  // elements between tokens
+  int max_new;
+  float scale;
+  bool causal;
+  int window;
+};
+
+// Workgroups a call's keys are split over, and the bytes of their partial
+// results (0 when they are not split).
+int kv4_splits(const Kv4Dims &dm, int max_new, int window);
+size_t kv4_attention_ws(const Kv4Dims &dm, int max_new, int window);
+bool kv4_grid_ok(const Kv4Dims &dm, int max_new, int window);
+hipError_t launch_kv4_attention(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
+                                const Kv4Batch &bt, const Kv4Attn &at, void *ws, hipStream_t s);
+#endif
+
+}  // namespace moe

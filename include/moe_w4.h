@@ -314,6 +314,145 @@ moe_status moe_layer_forward_hidden(const moe_dims *dm, const uint16_t *x,
 moe_status moe_dequant_w4(const moe_w4_matrix *m, int32_t rows, int32_t cols, uint16_t *out,
                           void *stream);
 
+/* Element types of the entry points below that take more than one. */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+
+/* Activations of moe_linear_w4: z; max(z, 0); z / (1 + exp(-z));
+ * z * (1 + erf(z / sqrt 2)) / 2. */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
+
+/*
+ * moe_linear_w4 - a dense projection with int4-g64 weights and its epilogue
+ * (the q, k, v and output projections around the attention below, or any
+ * dense layer of the same checkpoint format):
+ *   y[t][n] = act(sum_c x[t][c] * W[n][c] + bias[n]) + residual[t][n]
+ * The weights are rebuilt to bf16 as in the expert GEMMs, products are exact
+ * and summed in fp32 in a fixed order; the epilogue is fp32 and y is rounded
+ * once.
+ *   x         bf16 [T][cols], rows x_stride elements apart
+ *   w         one matrix (n = 1) of rows x cols
+ *   bias      bf16 [rows] or NULL
+ *   residual  [T][rows] of y's type, rows residual_stride apart, or NULL; may
+ *             be y itself with the same stride (updated in place)
+ *   y         bf16 or fp32 (dtype) [T][rows], rows y_stride elements apart, out
+ * Limits: T >= 0, rows >= 1, cols >= 1 (MOE_E_INVALID otherwise); cols % 64 == 0,
+ * x_stride % 8 == 0, rows * cols < 2^34, T * rows and T * cols < 2^40
+ * (MOE_E_UNSUPPORTED); strides at least a row long (MOE_E_INVALID).
+ */
+moe_status moe_linear_w4(int32_t T, int32_t rows, int32_t cols, const uint16_t *x, int64_t x_stride,
+                         const moe_w4_matrix *w, const uint16_t *bias, int32_t act,
+                         const void *residual, int64_t residual_stride, void *y, int64_t y_stride,
+                         int32_t dtype, void *stream);
+
+/*
+ * A paged key/value cache held in int4-g64: keys and values are each a stack
+ * of num_pages * Hkv matrices in the weight layout above, with `page` rows (one
+ * per token slot) of D columns, i.e.
+ *   codes  uint8 [num_pages][Hkv][page][D/2]
+ *   scales, biases  bf16 [num_pages][Hkv][page][D/64]
+ * so moe_dequant_w4 shows what a page's head holds.
+ */
+typedef struct {
+  int32_t B;         /* sequences of the batch */
+  int32_t Hq;        /* query heads, a multiple of Hkv (attention only) */
+  int32_t Hkv;       /* key/value heads */
+  int32_t D;         /* channels of a head: 64, 128 or 256 */
+  int32_t page;      /* tokens per page: a power of two, 16 .. 65536 */
+  int32_t num_pages; /* pages of the cache */
+  int32_t max_pages; /* columns of the page table */
+} moe_kv4_dims;
+
+typedef struct {
+  uint8_t *codes;
+  uint16_t *scales;
+  uint16_t *biases;
+} moe_kv4_plane;
+
+typedef struct {
+  moe_kv4_plane k, v;
+} moe_kv4_cache;
+
+/*
+ * The batch, in device memory and the same for append, read and attention.
+ * Sequence b has kv_len[b] tokens, the last n_b = cu[b+1] - cu[b] of which are
+ * rows cu[b] .. cu[b+1]-1 of the call's token tensors (T rows in all); position
+ * p of the sequence lies in page page_table[b][p / page], slot p % page.
+ *   page_table  int32 [B][max_pages]; entries past the sequence's pages are not used
+ *   cu          int32 [B+1], ascending from 0
+ *   kv_len      int32 [B]
+ * Nothing a kernel reads here can make it leave its buffers: offsets are
+ * clamped to 0 .. T, and a position that is negative, past the table, or on
+ * a page outside 0 .. num_pages-1 has no place in the cache (not written, read
+ * back as zeros, not attended to). Rows past cu[B] are not touched.
+ */
+typedef struct {
+  const int32_t *page_table;
+  const int32_t *cu;
+  const int32_t *kv_len;
+} moe_kv4_batch;
+
+/*
+ * Shape limits of the three calls: B, Hkv, page, num_pages, max_pages >= 1, D
+ * and page as above, T >= 0 (MOE_E_INVALID for values < 1, MOE_E_UNSUPPORTED
+ * for other D and page), max_pages * page < 2^31, B, Hq, Hkv <= 65535, T * Hq and
+ * T * 2 Hkv D < 2^40. Token strides are in elements, multiples of 8
+ * (MOE_E_UNSUPPORTED) and at least a token long (MOE_E_INVALID).
+ */
+
+/*
+ * moe_kv4_append - quantise the new tokens' keys and values into the cache.
+ * Per group of 64 channels x: b = bf16(min x), a zero as +0; s = bf16(fp32((max x -
+ * b) * fp32(1/15))) or 0 below 2^-126; code = (x - b) / s rounded to nearest, ties
+ * to even, and clamped to 0 .. 15 (0 where s = 0); max x - b and x - b are
+ * rounded to fp32, the quotient is not. A group that holds a NaN or an
+ * infinity, or whose span or bias overflows, is stored as s = b = NaN.
+ *   k, v  bf16 or fp32 (dtype) [T][Hkv][D], tokens k_stride / v_stride apart
+ * Precondition: the new tokens lie in different slots (two tokens in one slot
+ * leave a mixture of the two there).
+ */
+moe_status moe_kv4_append(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
+                          const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                          int32_t dtype, const moe_kv4_batch *batch, void *stream);
+
+/*
+ * moe_kv4_read - rebuild the same tokens' keys and values, scale * code + bias,
+ * rounded to fp32 and for bf16 once more (n_b = kv_len[b] reads a whole
+ * sequence).
+ *   k, v  bf16 or fp32 (dtype) [T][Hkv][D], out, tokens k_stride / v_stride apart
+ */
+moe_status moe_kv4_read(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T, void *k,
+                        int64_t k_stride, void *v, int64_t v_stride, int32_t dtype,
+                        const moe_kv4_batch *batch, void *stream);
+
+/* Bytes of workspace moe_kv4_attention needs (may be 0; 0 for arguments out of range). */
+size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int32_t max_new,
+                                         int32_t window);
+
+/*
+ * moe_kv4_attention - the new tokens' queries over the cache (their own keys and
+ * values included, so append first).
+ *   out[t][h] = sum_p softmax_p(scale * q[t][h] . k_p) v_p, with k_p, v_p =
+ *   s * code + b not rounded, of cache head h / (Hq / Hkv), over the positions
+ *   p < kv_len that the token at position i sees: p <= i if causal, and
+ *   p > i - window if window > 0. A token that sees none gets zeros. Positions
+ *   it does not see never reach its result, whatever the cache holds there.
+ *   q       bf16 [T][Hq][D], tokens q_stride apart
+ *   out     bf16 [T][Hq][D], out, tokens out_stride apart
+ *   max_new an upper bound of every n_b; a sequence's tokens past it are not computed
+ *   scale   > 0 and finite (MOE_E_INVALID otherwise)
+ *   window  >= 0 (0: none; MOE_E_INVALID when negative)
+ *   ws      >= moe_kv4_attention_workspace_bytes of these dims; may be NULL when that
+ *           is 0. Calls that may overlap need workspaces of their own.
+ * Scores, softmax statistics and sums are fp32; a softmax weight times its
+ * key's scale is rounded to bf16 for the matrix cores. Results repeat bit for
+ * bit.
+ */
+moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
+                             int32_t max_new, const uint16_t *q, int64_t q_stride, uint16_t *out,
+                             int64_t out_stride, const moe_kv4_batch *batch, float scale,
+                             int32_t causal, int32_t window, void *ws, size_t ws_bytes,
+                             void *stream);
+
 const char *moe_status_string(int32_t status);
 
 /* hipError_t of the last MOE_E_HIP on this thread (0 if none). */

@@ -1,0 +1,427 @@
+"""The 4-bit key/value cache and its attention on the GPU against the fp64 oracle.
+
+Cache contents (codes, scales, biases) and what is read back are compared bit for bit.
+Attention is held to the oracle's element-wise bound of what its roundings may cost."""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_grouped_router_amd as M
+from oracle import kv4_oracle as K
+from oracle.moe_oracle import bf16_to_f64, round_to_bf16_bits
+from parity_util import dev_bits, host_bits, say
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    M.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def bf16_values(a):
+    return bf16_to_f64(round_to_bf16_bits(a)).astype(np.float32)
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def make_cache(num_pages, Hkv, page, D, fill=None):
+    c = M.KV4Cache.empty(num_pages, Hkv, page, D)
+    for m in (c.k, c.v):
+        m.codes.fill_(0xA5)
+        for t in (m.scales, m.biases):
+            t.fill_(float("nan") if fill is None else fill)
+    return c
+
+
+def host_planes(c):
+    return [(m.codes.cpu().numpy(), host_bits(m.scales), host_bits(m.biases)) for m in (c.k, c.v)]
+
+
+class Batch:
+    """Ragged sequences on shuffled pages."""
+
+    def __init__(self, rng, new, past, page, spare=2):
+        self.new, self.len = list(new), [n + p for n, p in zip(new, past)]
+        self.page, self.B, self.T = page, len(new), sum(new)
+        self.cu = [0] + list(np.cumsum(new))
+        width = max(1, max(-(-t // page) for t in self.len)) + 1
+        self.num_pages = self.B * width + spare
+        self.table = rng.permutation(self.num_pages)[:self.B * width].reshape(self.B, width)
+        self.dev = (i32(self.table), i32(self.cu), i32(self.len))
+
+    def max_new(self):
+        return max(max(self.new), 1)
+
+
+def tokens(rng, T, H, D, dtype):
+    x = rng.standard_normal((T, H, D)).astype(np.float32)
+    x[:, :, :3] *= 6.0
+    return bf16_values(x) if dtype == BF16 else x
+
+
+def filled(rng, b, Hkv, D):
+    """A cache holding every token of every sequence (written through the framework), NaN elsewhere."""
+    c = make_cache(b.num_pages, Hkv, b.page, D)
+    T = sum(b.len)
+    kv = [tokens(rng, T, Hkv, D, BF16) for _ in range(2)]
+    k, v = (torch.from_numpy(a).cuda().to(BF16) for a in kv)
+    M.moe_kv4_append(c, k, v, b.dev[0], i32([0] + list(np.cumsum(b.len))), b.dev[2])
+    return c
+
+
+def queries(rng, T, Hq, D):
+    x = bf16_values(rng.standard_normal((T, Hq, D)))
+    return x.astype(np.float64), torch.from_numpy(x).cuda().to(BF16)
+
+
+def check(got, want, tol, what=""):
+    got = got.float().cpu().numpy().astype(np.float64)
+    assert (np.isnan(got) == np.isnan(want)).all(), what
+    ok = ~np.isnan(want)
+    off = np.abs(got - want)[ok]
+    t = tol[ok]
+    if off.size:
+        say(f"  {what}: worst {float((off / np.maximum(t, 1e-30)).max()):.3f} of the bound, "
+            f"rms {np.sqrt((off ** 2).mean()):.2e} of {np.sqrt((want[ok] ** 2).mean()):.2e}")
+    assert (off <= t).all(), what
+
+
+# ------------------------------------------------------------------ write and read
+
+CACHE_CASES = [  # new tokens, earlier tokens, Hkv, D, page
+    ([1], [0], 1, 64, 16),
+    ([1] * 8, [15, 16, 31, 0, 5, 700, 63, 64], 2, 256, 16),
+    ([3, 0, 17, 1], [14, 2, 0, 100], 1, 128, 32),
+    ([5, 70], [60, 0], 3, 64, 64),
+    ([2] * 70, list(range(70)), 1, 64, 16),          # more sequences than lanes
+    ([1, 0, 2] * 50, [3] * 150, 2, 128, 256),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new,past,Hkv,D,page", CACHE_CASES)
+def test_append_and_read(new, past, Hkv, D, page, dtype):
+    rng = np.random.default_rng(len(new) * 1000 + D)
+    b = Batch(rng, new, past, page)
+    kv = [tokens(rng, b.T, Hkv, D, dtype) for _ in range(2)]
+    c = make_cache(b.num_pages, Hkv, page, D)
+    # keys and values as slices of one projection's output: strided rows
+    both = torch.from_numpy(np.concatenate(kv, axis=1)).cuda().to(dtype)
+    before = host_planes(c)
+    M.moe_kv4_append(c, both[:, :Hkv], both[:, Hkv:], *b.dev)
+    after = host_planes(c)
+    _, pg, sl = K.token_slots(b.cu, b.len, b.table, page, b.T)
+    for name, x, old, got in zip("kv", kv, before, after):
+        q, s, z = K.quantise(x)
+        for field, a, o, g in zip(("codes", "scales", "biases"), (K.pack(q), s, z), old, got):
+            want = o.copy()
+            for t in range(b.T):
+                want[pg[t], :, sl[t]] = a[t]
+            assert (want == g).all(), f"{name}.{field}"
+    for out in (BF16, F32):
+        k, v = M.moe_kv4_read(c, *b.dev, b.T, dtype=out)
+        for x, got in zip(kv, (k, v)):
+            q, s, z = K.quantise(x)
+            want = K.values(K.pack(q), s, z).astype(np.float32)
+            if out == F32:
+                assert (got.cpu().numpy() == want).all()
+            else:
+                assert (host_bits(got) == round_to_bf16_bits(want)).all()
+
+
+def test_quantiser_edges():
+    """Ties, constant and subnormal groups, outliers, biases above the minimum, NaN and
+    infinities, spans past fp32: codes, scales and biases bit for bit."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((200, 1, 64)).astype(np.float32)
+    x[0], x[1], x[2] = 0.0, 1.25, -0.0
+    x[3] = np.linspace(0, 15, 64)
+    x[4] = np.arange(64) / 4.0 - 0.5          # many exact ties
+    x[5] = np.arange(64) % 31 / 2.0            # every half
+    x[6] *= np.float32(1e-38)
+    x[7] *= np.float32(1e-44)
+    x[8, 0, 7], x[9, 0, 8], x[10, 0, 9] = np.nan, np.inf, -np.inf
+    x[11, 0, :2] = 3.4e38, -3.4e38
+    x[12] = 1.0 + 2.0 ** -8 + 2.0 ** -9        # rounds up to a bias above everything
+    x[13] = 1000.0 + x[13]
+    x[14, 0, 0] = 1e30
+    x[15] = -3.39e38
+    x[16, 0, 0] = -3.4028e38                   # its bias rounds to -inf
+    x[17:60] = np.round(x[17:60] * 4) / 4      # coarse lattices: ties everywhere
+    x[60:90] = np.round(x[60:90] * 8) * np.float32(2.0 ** 20)
+    x[90:120] *= np.float32(2.0) ** rng.integers(-120, 120, (30, 1, 1)).astype(np.float32)
+    for dtype in (F32, BF16):
+        y = x.copy()
+        if dtype == BF16:
+            y = bf16_values(y)
+        b = Batch(rng, [200], [0], 16)
+        c = make_cache(b.num_pages, 1, 16, 64)
+        d = torch.from_numpy(y).cuda().to(dtype)
+        M.moe_kv4_append(c, d, -d, *b.dev)
+        _, pg, sl = K.token_slots(b.cu, b.len, b.table, 16, 200)
+        for sign, got in zip((1, -1), host_planes(c)):
+            q, s, z = K.quantise(sign * y)
+            for name, a, g in zip(("scales", "biases", "codes"), (s, z, K.pack(q)), (got[1], got[2], got[0])):
+                bad = (a != g[pg, :, sl]).reshape(200, -1).any(1)
+                assert not bad.any(), (name, dtype, sign, np.nonzero(bad)[0][:10])
+        k, _ = M.moe_kv4_read(c, *b.dev, 200, dtype=F32)
+        k = k.cpu().numpy()
+        assert np.isnan(k[[8, 9, 10, 11]]).all() and np.isfinite(k[[0, 1, 2, 3, 6, 7, 12, 13, 14]]).all()
+
+
+def test_dequant_w4_sees_the_same_page():
+    rng = np.random.default_rng(6)
+    b = Batch(rng, [16], [0], 16)
+    c = make_cache(b.num_pages, 2, 16, 128, fill=0.0)
+    x = torch.from_numpy(tokens(rng, 16, 2, 128, BF16)).cuda().to(BF16)
+    M.moe_kv4_append(c, x, x, *b.dev)
+    k, _ = M.moe_kv4_read(c, *b.dev, 16)
+    m = M.W4Matrix(c.k.codes.view(-1, 16, 64), c.k.scales.view(-1, 16, 2), c.k.biases.view(-1, 16, 2))
+    for h in range(2):
+        page = M.moe_dequant_w4(m, index=int(b.table[0, 0]) * 2 + h)
+        assert torch.equal(page, k[:, h])
+
+
+def test_tokens_without_a_place():
+    """Pages outside the cache, positions past the table and rows past the last sequence:
+    nothing is written anywhere else; read gives zeros for the first two and leaves the rest."""
+    rng = np.random.default_rng(7)
+    b = Batch(rng, [20, 20, 4], [12, 30, 0], 16)
+    table = b.table.copy()
+    table[0, 1] = b.num_pages       # one past the end
+    table[1, 2] = -5
+    lens = [b.len[0], b.len[1], table.shape[1] * 16 + 2]
+    dev = (i32(table), i32(b.cu), i32(lens))
+    T = b.T + 3
+    x = torch.from_numpy(tokens(rng, T, 1, 64, F32)).cuda()
+    c = make_cache(b.num_pages, 1, 16, 64)
+    before = host_planes(c)
+    M.moe_kv4_append(c, x, x, *dev)
+    _, pg, sl = K.token_slots(b.cu, lens, table, 16, T)
+    placed = (pg >= 0) & (pg < b.num_pages)
+    assert 0 < placed.sum() < b.T
+    q, s, z = K.quantise(x.cpu().numpy())
+    for old, got in zip(before, host_planes(c)):
+        for o, g, a in zip(old, got, (K.pack(q), s, z)):
+            o[pg[placed], :, sl[placed]] = a[placed]
+            assert (o == g).all()
+    k = torch.full((T, 1, 64), 7.0, device="cuda")
+    v = torch.full((T, 1, 64), 7.0, device="cuda")
+    M.moe_kv4_read(c, *dev, T, dtype=F32, k=k, v=v)
+    want = np.where(placed[:, None, None], K.values(K.pack(q), s, z).astype(np.float32), 0)
+    want[b.T:] = 7.0
+    assert (k.cpu().numpy() == want).all() and (v.cpu().numpy() == want).all()
+
+
+# ------------------------------------------------------------------ attention
+
+ATTENTION = [  # new, past, Hq, Hkv, D, page, causal, window
+    ([1], [0], 1, 1, 64, 16, True, 0),
+    ([1], [15], 8, 1, 128, 16, True, 0),
+    ([1], [16], 16, 2, 256, 16, True, 0),
+    ([1, 1, 1], [30, 31, 32], 16, 2, 128, 32, True, 0),
+    ([1] * 9, [0, 7, 63, 64, 65, 127, 128, 500, 1200], 16, 2, 256, 64, True, 0),
+    ([1, 0, 2], [333, 100, 0], 6, 2, 64, 16, True, 0),       # 3 heads a group, an idle sequence
+    ([5, 3], [100, 0], 12, 1, 128, 128, True, 0),            # 12 heads a group
+    ([1], [5000], 8, 8, 64, 256, True, 0),                   # split over workgroups
+    ([1, 1], [9000, 40], 16, 2, 128, 16, True, 0),
+    ([2], [3000], 32, 1, 256, 64, True, 0),                  # two row tiles, split
+    ([3] * 4, [700, 10, 0, 95], 8, 8, 64, 32, True, 100),    # sliding window
+    ([1], [4000], 16, 2, 128, 16, True, 1),                  # sees itself only
+    ([40], [50], 4, 2, 128, 16, True, 17),
+    ([33], [0], 8, 2, 128, 16, True, 0),                     # prompts
+    ([200, 1, 77], [0, 300, 129], 16, 2, 128, 64, True, 0),
+    ([130], [65], 8, 1, 64, 16, True, 0),
+    ([100, 31], [3, 200], 16, 2, 256, 32, True, 0),
+    ([64, 9], [0, 80], 4, 4, 128, 16, False, 0),             # every token sees all
+    ([20], [200], 4, 2, 64, 16, False, 50),
+    ([150], [700], 20, 4, 256, 128, True, 333),
+]
+
+
+@pytest.mark.parametrize("new,past,Hq,Hkv,D,page,causal,window", ATTENTION)
+def test_attention(new, past, Hq, Hkv, D, page, causal, window):
+    rng = np.random.default_rng(Hq * 7 + D + len(new) + sum(past))
+    b = Batch(rng, new, past, page)
+    c = filled(rng, b, Hkv, D)
+    q64, q = queries(rng, b.T, Hq, D)
+    out = M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), causal=causal, window=window)
+    want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, D ** -0.5, causal, window)
+    check(out, want, tol, f"{new} {past} {Hq}/{Hkv}x{D}")
+    again = M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), causal=causal, window=window)
+    assert torch.equal(out, again)
+
+
+def test_attention_scales_and_strides():
+    """Large scores, another scale, queries inside a wider row, an output of its own strides,
+    rows past the last sequence left as they were."""
+    rng = np.random.default_rng(21)
+    b = Batch(rng, [2, 1], [90, 300], 16)
+    c = filled(rng, b, 2, 128)
+    T = b.T + 2
+    x = bf16_values(rng.standard_normal((T, 12, 128)) * 4)
+    wide = torch.from_numpy(x).cuda().to(BF16)
+    room = torch.full((T, 10, 128), 3.0, dtype=BF16, device="cuda")
+    q, out = wide[:, 2:10], room[:, 1:9]
+    for scale in (0.5, 1e-3):
+        M.moe_kv4_attention(c, q, *b.dev, max_new=2, scale=scale, out=out)
+        want, tol = K.attention(x[:b.T, 2:10].astype(np.float64), K.Paged(*host_planes(c), b.table), b.cu,
+                                b.len, float(np.float32(scale)))
+        check(out[:b.T], want, tol, f"scale {scale}")
+        assert (room[b.T:] == 3).all() and (room[:, 0] == 3).all() and (room[:, 9] == 3).all()
+
+
+def test_rows_that_see_nothing():
+    """Positions before the start, empty sequences and missing pages: zeros, never NaN, though
+    the cache holds NaN there; bad pages are skipped."""
+    rng = np.random.default_rng(22)
+    b = Batch(rng, [4, 3, 2, 2], [0, 60, 40, 0], 16)
+    c = filled(rng, b, 2, 64)
+    q64, q = queries(rng, b.T, 4, 64)
+    table = b.table.copy()
+    table[1, 1], table[2, :] = b.num_pages + 3, -1
+    lens = [2, b.len[1], b.len[2], 0]
+    out = M.moe_kv4_attention(c, q, i32(table), i32(b.cu), i32(lens), max_new=4)
+    want, tol = K.attention(q64, K.Paged(*host_planes(c), table), b.cu, lens, 64 ** -0.5)
+    check(out, want, tol, "holes")
+    assert not out[:2].any() and not out[7:].any() and out[2:4].any()
+
+
+def test_hostile_batches_stay_in_their_buffers():
+    """Offsets and lengths that make no sense are clamped: no fault, and rows no sequence
+    claims are left alone."""
+    rng = np.random.default_rng(23)
+    b = Batch(rng, [3, 3], [20, 40], 16)
+    c = filled(rng, b, 2, 64)
+    _, q = queries(rng, b.T, 4, 64)
+    big = 2 ** 31 - 1
+    for cu, lens in (([-5, 3, 900], [23, 43]), ([0, 3, 6], [big, -4]), ([6, 3, 0], [23, 43]),
+                     ([big, -big, 2], [5, 5])):
+        out = torch.full((b.T, 4, 64), 5.0, dtype=BF16, device="cuda")
+        M.moe_kv4_attention(c, q, b.dev[0], i32(cu), i32(lens), max_new=6, out=out)
+        M.moe_kv4_read(c, b.dev[0], i32(cu), i32(lens), b.T)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("past", [40, 3000])
+def test_nan_reaches_only_those_who_see_it(past):
+    """A NaN key and a NaN value at one position: queries at or behind it are NaN (the value's
+    only in its own group of channels), earlier ones are not."""
+    rng = np.random.default_rng(24)
+    b = Batch(rng, [5], [past], 16)
+    q64, q = queries(rng, 5, 2, 128)
+    at = past + 2
+    for which in "kv":
+        c = filled(rng, b, 1, 128)
+        m = getattr(c, which)
+        pg, sl = int(b.table[0, at // 16]), at % 16
+        m.scales[pg, 0, sl, 1] = float("nan")
+        m.biases[pg, 0, sl, 1] = float("nan")
+        out = M.moe_kv4_attention(c, q, *b.dev, max_new=5).float().cpu().numpy()
+        want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, 128 ** -0.5)
+        check(torch.from_numpy(out), want, tol, which)
+        assert np.isfinite(out[:2]).all() and np.isnan(out[2:, :, 64:]).all()
+        assert np.isnan(out[2:, :, :64]).all() == (which == "k")
+
+
+def test_outlier_values_keep_their_neighbours():
+    """A huge value that weighs next to nothing does not cost the others their digits."""
+    rng = np.random.default_rng(25)
+    b = Batch(rng, [1], [99], 16)
+    c = make_cache(b.num_pages, 1, 16, 64)
+    k = bf16_values(rng.standard_normal((100, 1, 64)) * 0.1)
+    v = bf16_values(rng.standard_normal((100, 1, 64)))
+    k[50], v[50] = -40.0, bf16_values(np.array(1e6) * rng.standard_normal(64))
+    x = np.ones((1, 1, 64), dtype=np.float32)
+    cu = i32([0, 100])
+    M.moe_kv4_append(c, *(torch.from_numpy(a).cuda().to(BF16) for a in (k, v)), b.dev[0], cu, b.dev[2])
+    out = M.moe_kv4_attention(c, torch.from_numpy(x).cuda().to(BF16), *b.dev, max_new=1)
+    want, tol = K.attention(x.astype(np.float64), K.Paged(*host_planes(c), b.table), b.cu, b.len, 0.125)
+    check(out, want, tol, "outlier")
+
+
+def test_offsets_past_32_bits():
+    """Pages whose codes lie beyond 2^31 bytes of the cache."""
+    rng = np.random.default_rng(26)
+    Hkv, page, D = 2, 256, 256
+    num_pages = (5 << 30) // (Hkv * page * D // 2)   # 5 GiB of codes a plane
+    c = M.KV4Cache.empty(num_pages, Hkv, page, D)
+    table = np.array([[num_pages - 1, num_pages // 2 + 1, 3]])
+    n = 600
+    kv = [tokens(rng, n, Hkv, D, BF16) for _ in range(2)]
+    k, v = (torch.from_numpy(a).cuda().to(BF16) for a in kv)
+    M.moe_kv4_append(c, k, v, i32(table), i32([0, n]), i32([n]))
+    rk, rv = M.moe_kv4_read(c, i32(table), i32([0, n]), i32([n]), n)
+    planes = []
+    for x, got in zip(kv, (rk, rv)):
+        qc, s, z = K.quantise(x)
+        assert (host_bits(got) == round_to_bf16_bits(K.values(K.pack(qc), s, z).astype(np.float32))).all()
+        full = []
+        for a in (K.pack(qc), s, z):  # the same three pages in a small cache
+            p = np.zeros((3, page, Hkv, a.shape[-1]), dtype=a.dtype)
+            p.reshape(3 * page, Hkv, -1)[:n] = a
+            full.append(p.transpose(0, 2, 1, 3))
+        planes.append(tuple(full))
+    q64, q = queries(rng, 2, 4, D)
+    out = M.moe_kv4_attention(c, q, i32(table), i32([0, 2]), i32([n]), max_new=2)
+    want, tol = K.attention(q64, K.Paged(*planes, np.array([[0, 1, 2]])), [0, 2], [n], D ** -0.5)
+    check(out, want, tol, "far pages")
+
+
+def test_max_new_bounds_what_is_computed():
+    rng = np.random.default_rng(27)
+    b = Batch(rng, [6], [10], 16)
+    c = filled(rng, b, 1, 64)
+    q64, q = queries(rng, 6, 2, 64)
+    whole = M.moe_kv4_attention(c, q, *b.dev, max_new=6)
+    assert torch.equal(whole, M.moe_kv4_attention(c, q, *b.dev, max_new=1000))
+    out = torch.full_like(whole, 9.0)
+    M.moe_kv4_attention(c, q, *b.dev, max_new=4, out=out)
+    assert torch.equal(out[:4], whole[:4]) and (out[4:] == 9).all()
+
+
+def test_empty_calls():
+    c = make_cache(2, 1, 16, 64)
+    e = torch.empty((0, 1, 64), dtype=BF16, device="cuda")
+    dev = (i32([[0]]), i32([0, 0]), i32([5]))
+    M.moe_kv4_append(c, e, e, *dev)
+    assert M.moe_kv4_read(c, *dev, 0)[0].shape == (0, 1, 64)
+    assert M.moe_kv4_attention(c, e, *dev, max_new=0).shape == (0, 1, 64)
+
+
+def test_binding_refusals():
+    c = make_cache(4, 2, 16, 64)
+    q = torch.zeros((2, 4, 64), dtype=BF16, device="cuda")
+    kv = torch.zeros((2, 2, 64), dtype=BF16, device="cuda")
+    dev = (i32([[0, 1]]), i32([0, 2]), i32([5]))
+    out = torch.empty_like(q)
+    bad_attention = [dict(q=q.float()), dict(q=q[:, :3]), dict(q=q[..., :32]), dict(q=q.cpu()),
+                     dict(out=out[:1]), dict(out=out.float()), dict(scale=0.0), dict(window=-1),
+                     dict(max_new=0), dict(table=dev[0].long()), dict(cu=i32([0, 1, 2])), dict(ln=i32([5, 5])),
+                     dict(table=dev[0][0])]
+    for bad in bad_attention:
+        a = dict(q=q, table=dev[0], cu=dev[1], ln=dev[2], max_new=2)
+        a.update(bad)
+        with pytest.raises(M.MoeError):
+            M.moe_kv4_attention(c, a.pop("q"), a.pop("table"), a.pop("cu"), a.pop("ln"), **a)
+    for k, v in ((kv[:, :1], kv), (kv, kv.float()), (kv.half(), kv.half()), (kv.transpose(0, 1), kv), (kv, kv.cpu())):
+        with pytest.raises(M.MoeError):
+            M.moe_kv4_append(c, k, v, *dev)
+    with pytest.raises(M.MoeError):
+        M.moe_kv4_read(c, *dev, 2, dtype=torch.float16)
+    with pytest.raises(M.MoeError):
+        M.moe_kv4_read(c, *dev, 2, k=torch.zeros((2, 2, 64), device="cuda"))
+    long = M.KV4Cache(c.k, c.v)
+    table = i32([[0] * 4096])
+    with pytest.raises(M.MoeError):
+        M.moe_kv4_attention(long, q, table, dev[1], dev[2], max_new=2,
+                            ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
