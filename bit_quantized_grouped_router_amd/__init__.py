@@ -52,7 +52,8 @@ class MoeKv4Dims(ctypes.Structure):
 
 
 class MoeKv4Cache(ctypes.Structure):
-    _fields_ = [("k", MoeW4Matrix), ("v", MoeW4Matrix)]
+    """The two planes k and v of moe_kv4_cache, their pointers in order."""
+    _fields_ = [(f"{p}_{f}", ctypes.c_void_p) for p in "kv" for f in ("codes", "scales", "biases")]
 
 
 class MoeKv4Batch(ctypes.Structure):
@@ -150,8 +151,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
+# handle of the current stream without building a torch.cuda.Stream object (2.7 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -511,26 +518,26 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _here(**tensors) -> None:
-    """Raise unless every tensor given lives on the current GPU."""
+def _wrong_device(**tensors) -> None:
+    """Raise for the first tensor that does not live on the current GPU."""
     cur = torch.cuda.current_device()
     for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
+        if t is not None and not t.is_cuda:
             raise MoeError(f"{name} must live in GPU memory")
-        if t.get_device() != cur:
+        if t is not None and t.get_device() != cur:
             raise MoeError(f"{name} lives on {t.device}; the current device is cuda:{cur}")
 
 
 def _rows(t: torch.Tensor, shape, name: str, dtypes) -> int:
     """Stride between the rows (first dimension) of t, whose rows must be dense and not
     overlap; raises for another shape or element type."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise MoeError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
     if t.dtype not in dtypes:
         raise MoeError(f"{name} has dtype {t.dtype}; expected one of "
                        f"{', '.join(str(d) for d in dtypes)}")
+    if shape[0] > 1 and t.is_contiguous():
+        return t.stride(0)
     row = 1
     for i in range(t.dim() - 1, 0, -1):
         if t.shape[i] > 1 and t.stride(i) != row:
@@ -562,22 +569,29 @@ def moe_linear_w4(x: torch.Tensor, w: W4Matrix, bias=None, act: str = "none", re
         raise MoeError(f"w has {w.codes.shape[-1] * 2} columns; x has {cols}")
     if act not in ACTS:
         raise MoeError(f"act {act!r}; expected one of {', '.join(ACTS)}")
-    _here(x=x, codes=w.codes, scales=w.scales, biases=w.biases, bias=bias, residual=residual, y=y)
-    given = [t.dtype for t in (y, residual) if t is not None]
-    dtype = out_dtype if out_dtype is not None else (given[0] if given else torch.bfloat16)
+    cur = torch.cuda.current_device()
+    for t in (x, w.codes, w.scales, w.biases, bias, residual, y):
+        if t is not None and t.get_device() != cur:
+            _wrong_device(x=x, codes=w.codes, scales=w.scales, biases=w.biases, bias=bias,
+                          residual=residual, y=y)
+    if out_dtype is not None:
+        dtype = out_dtype
+    else:
+        dtype = y.dtype if y is not None else residual.dtype if residual is not None else torch.bfloat16
     code = _dtype(dtype)
     xs = _rows(x, (T, cols), "x", BF16)
     rs = 0 if residual is None else _rows(residual, (T, rows), "residual", (dtype,))
     if y is None:
         y = _empty((T, rows), dtype, x.device, stream)
-    ys = _rows(y, (T, rows), "y", (dtype,))
+        ys = rows
+    else:
+        ys = _rows(y, (T, rows), "y", (dtype,))
     if bias is not None:
         _need(bias, rows * 2, "bias", BF16)
     _need(w.codes, rows * cols // 2, "codes", U8)
     _need(w.scales, rows * (cols // GROUP) * 2, "scales", BF16)
     _need(w.biases, rows * (cols // GROUP) * 2, "biases", BF16)
-    cm = w.c()
-    _check(lib().moe_linear_w4(T, rows, cols, x.data_ptr(), xs, ctypes.byref(cm), _ptr(bias),
+    _check(lib().moe_linear_w4(T, rows, cols, x.data_ptr(), xs, w.c(), _ptr(bias),
                                ACTS[act], None if residual is None else residual.data_ptr(), rs,
                                y.data_ptr(), ys, code, _stream(stream)), "moe_linear_w4")
     return y
@@ -591,20 +605,19 @@ class KV4Cache:
 
     def __init__(self, k: W4Matrix, v: W4Matrix):
         self.k, self.v = k, v
-        if k.codes.dim() != 4:
+        shape = k.codes.shape
+        if len(shape) != 4:
             raise MoeError("cache codes must be [num_pages, Hkv, page, D/2]")
-        self.num_pages, self.Hkv, self.page, half = k.codes.shape
+        self.num_pages, self.Hkv, self.page, half = shape
         self.D = 2 * half
         g = (self.num_pages, self.Hkv, self.page, self.D // GROUP)
         for n, m in (("k", k), ("v", v)):
-            if m.codes.shape != k.codes.shape:
-                raise MoeError(f"{n}.codes has shape {tuple(m.codes.shape)}; k.codes {tuple(k.codes.shape)}")
-            if m.codes.dtype not in U8:
-                raise MoeError(f"{n}.codes has dtype {m.codes.dtype}; expected torch.uint8")
-            for f in ("scales", "biases"):
-                t = getattr(m, f)
-                if tuple(t.shape) != g or t.dtype not in BF16:
-                    raise MoeError(f"{n}.{f} is {t.dtype} {tuple(t.shape)}; expected bf16 {g}")
+            if m.codes.shape != shape or m.codes.dtype not in U8:
+                raise MoeError(f"{n}.codes is {m.codes.dtype} {tuple(m.codes.shape)}; expected "
+                               f"torch.uint8 {tuple(shape)}")
+            if m.scales.shape != g or m.scales.dtype not in BF16 or m.biases.shape != g or m.biases.dtype not in BF16:
+                raise MoeError(f"{n}.scales and biases are {m.scales.dtype} {tuple(m.scales.shape)} and "
+                               f"{m.biases.dtype} {tuple(m.biases.shape)}; expected bf16 {g}")
 
     @staticmethod
     def empty(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> "KV4Cache":
@@ -617,57 +630,68 @@ class KV4Cache:
         return KV4Cache(plane(), plane())
 
     def c(self) -> MoeKv4Cache:
-        return MoeKv4Cache(self.k.c(), self.v.c())
+        k, v = self.k, self.v
+        return MoeKv4Cache(_ptr(k.codes), _ptr(k.scales), _ptr(k.biases),
+                           _ptr(v.codes), _ptr(v.scales), _ptr(v.biases))
 
 
-def _kv4(cache: KV4Cache, page_table, cu, kv_len, Hq: int = 0):
-    """The C structs of a cache and a batch, after checking the batch's tensors."""
+def _kv4(cache: KV4Cache, page_table, cu, kv_len, tokens, Hq: int = 0):
+    """The C structs of a cache and a batch, after checking the batch's tensors and that
+    they, the cache and the token tensors are on the current GPU."""
     if page_table.dim() != 2 or cu.dim() != 1 or kv_len.dim() != 1:
         raise MoeError("page_table must be [B, max_pages], cu [B + 1] and kv_len [B]")
     B, width = page_table.shape
     if cu.shape[0] != B + 1 or kv_len.shape[0] != B:
         raise MoeError(f"{B} sequences in page_table, {cu.shape[0] - 1} in cu, {kv_len.shape[0]} in kv_len")
-    for name, t in (("page_table", page_table), ("cu", cu), ("kv_len", kv_len)):
-        if t.dtype != torch.int32:
-            raise MoeError(f"{name} has dtype {t.dtype}; expected torch.int32")
-    _here(page_table=page_table, cu=cu, kv_len=kv_len, k=cache.k.codes, v=cache.v.codes)
-    dm = MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, width)
-    return dm, cache.c(), MoeKv4Batch(_ptr(page_table), _ptr(cu), _ptr(kv_len))
+    if page_table.dtype != torch.int32 or cu.dtype != torch.int32 or kv_len.dtype != torch.int32:
+        raise MoeError(f"page_table, cu and kv_len are {page_table.dtype}, {cu.dtype} and {kv_len.dtype}; "
+                       "expected torch.int32")
+    cur = torch.cuda.current_device()
+    for t in (page_table, cu, kv_len, cache.k.codes, cache.v.codes, *tokens):
+        if t is not None and t.get_device() != cur:
+            _wrong_device(page_table=page_table, cu=cu, kv_len=kv_len, k_cache=cache.k.codes,
+                          v_cache=cache.v.codes, **{f"token tensor {i}": t for i, t in enumerate(tokens)})
+    return (MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, width), cache.c(),
+            MoeKv4Batch(_ptr(page_table), _ptr(cu), _ptr(kv_len)))
 
 
 def moe_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, page_table, cu, kv_len,
                    stream=None) -> None:
     """Quantise new keys and values [T, Hkv, D] (bf16 or fp32) into the cache. Rows
     cu[b] .. cu[b+1]-1 are the last tokens of sequence b, which then has kv_len[b]."""
-    dm, c, b = _kv4(cache, page_table, cu, kv_len)
-    _here(k=k, v=v)
+    dm, c, b = _kv4(cache, page_table, cu, kv_len, (k, v))
     T = k.shape[0]
     dt = _dtype(k.dtype)
     shape = (T, cache.Hkv, cache.D)
     ks, vs = _rows(k, shape, "k", (k.dtype,)), _rows(v, shape, "v", (k.dtype,))
-    _check(lib().moe_kv4_append(ctypes.byref(dm), ctypes.byref(c), T, k.data_ptr(), ks, v.data_ptr(), vs,
-                                dt, ctypes.byref(b), _stream(stream)), "moe_kv4_append")
+    _check(lib().moe_kv4_append(dm, c, T, k.data_ptr(), ks, v.data_ptr(), vs, dt, b, _stream(stream)),
+           "moe_kv4_append")
 
 
 def moe_kv4_read(cache: KV4Cache, page_table, cu, kv_len, T: int, dtype=torch.bfloat16, k=None, v=None,
                  stream=None):
     """Keys and values [T, Hkv, D] of the last cu[b+1] - cu[b] tokens of each sequence."""
-    dm, c, b = _kv4(cache, page_table, cu, kv_len)
+    dm, c, b = _kv4(cache, page_table, cu, kv_len, (k, v))
     dt = _dtype(dtype)
     shape = (T, cache.Hkv, cache.D)
-    k = _empty(shape, dtype, page_table.device, stream) if k is None else k
-    v = _empty(shape, dtype, page_table.device, stream) if v is None else v
-    _here(k=k, v=v)
-    ks, vs = _rows(k, shape, "k", (dtype,)), _rows(v, shape, "v", (dtype,))
-    _check(lib().moe_kv4_read(ctypes.byref(dm), ctypes.byref(c), T, k.data_ptr(), ks, v.data_ptr(), vs,
-                              dt, ctypes.byref(b), _stream(stream)), "moe_kv4_read")
+    ks = vs = cache.Hkv * cache.D
+    if k is None:
+        k = _empty(shape, dtype, page_table.device, stream)
+    else:
+        ks = _rows(k, shape, "k", (dtype,))
+    if v is None:
+        v = _empty(shape, dtype, page_table.device, stream)
+    else:
+        vs = _rows(v, shape, "v", (dtype,))
+    _check(lib().moe_kv4_read(dm, c, T, k.data_ptr(), ks, v.data_ptr(), vs, dt, b, _stream(stream)),
+           "moe_kv4_read")
     return k, v
 
 
 def moe_kv4_attention_workspace_bytes(cache: KV4Cache, T: int, Hq: int, B: int, max_pages: int,
                                       max_new: int, window: int = 0) -> int:
     dm = MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, max_pages)
-    return lib().moe_kv4_attention_workspace_bytes(ctypes.byref(dm), T, max_new, window)
+    return lib().moe_kv4_attention_workspace_bytes(dm, T, max_new, window)
 
 
 def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, max_new: int,
@@ -681,19 +705,21 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
     T, Hq, D = q.shape
     if D != cache.D:
         raise MoeError(f"q has {D} channels a head; the cache {cache.D}")
-    dm, c, b = _kv4(cache, page_table, cu, kv_len, Hq)
-    _here(q=q, out=out, ws=ws)
+    dm, c, b = _kv4(cache, page_table, cu, kv_len, (q, out, ws), Hq)
     qs = _rows(q, (T, Hq, D), "q", BF16)
     if out is None:
         out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
-    os_ = _rows(out, (T, Hq, D), "out", BF16)
+        os_ = Hq * D
+    else:
+        os_ = _rows(out, (T, Hq, D), "out", BF16)
+    L = lib()
     if ws is None:
-        need = lib().moe_kv4_attention_workspace_bytes(ctypes.byref(dm), T, max_new, window)
+        need = L.moe_kv4_attention_workspace_bytes(dm, T, max_new, window)
         if need:
             ws = _empty((need,), torch.uint8, q.device, stream)
-    _check(lib().moe_kv4_attention(ctypes.byref(dm), ctypes.byref(c), T, max_new, q.data_ptr(), qs,
-                                   out.data_ptr(), os_, ctypes.byref(b),
-                                   D ** -0.5 if scale is None else scale, int(causal), window, _ptr(ws),
-                                   0 if ws is None else ws.numel() * ws.element_size(),
-                                   _stream(stream)), "moe_kv4_attention")
+    else:
+        need = ws.numel() * ws.element_size()
+    _check(L.moe_kv4_attention(dm, c, T, max_new, q.data_ptr(), qs, out.data_ptr(), os_, b,
+                               D ** -0.5 if scale is None else scale, int(causal), window, _ptr(ws),
+                               need, _stream(stream)), "moe_kv4_attention")
     return out

@@ -31,7 +31,7 @@ def dims(B=2, Hq=16, Hkv=2, D=128, page=16, num_pages=9, max_pages=4):
 
 
 def cache(p=FAKE):
-    return M.MoeKv4Cache(plane(p), plane(p))
+    return M.MoeKv4Cache(p, p, p, p, p, p)
 
 
 def batch(p=FAKE):
