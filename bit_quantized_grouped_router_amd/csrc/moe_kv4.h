@@ -83,25 +83,28 @@ MOE_HD Kv4Range kv4_range(const Kv4Dims &dm, long long p0, long long p1, long lo
 
 constexpr int kKvTile = 32;  // keys a wavefront takes at a time (two 16-key halves, one page each)
 
-// Tiles of a key range, and the share of one of `splits` workgroups: the tiles
-// begin .. end - 1, `used` splits having any. A split takes at least
-// kMinSplitTiles tiles, so a short sequence is spread over fewer workgroups.
-constexpr int kMinSplitTiles = 8;
+MOE_HD int kv4_tiles(const Kv4Range &r) {
+  return r.hi > r.lo ? (int)((r.hi + kKvTile - 1) / kKvTile - r.lo / kKvTile) : 0;
+}
+
+// The share of one of `splits` workgroups that take a range's tiles `per` at a
+// time: tiles begin .. end - 1 of the sequence; `used` splits have any. per is
+// raised to what leaves no tile over.
 struct Kv4Share {
   int begin, end, used;
 };
 
-MOE_HD Kv4Share kv4_share(const Kv4Range &r, int splits, int split) {
-  const long long t0 = r.lo / kKvTile, t1 = r.hi > r.lo ? (r.hi + kKvTile - 1) / kKvTile : t0;
-  const int n = (int)(t1 - t0);
-  int per = (n + splits - 1) / splits;
-  if (per < kMinSplitTiles) per = kMinSplitTiles;
+MOE_HD Kv4Share kv4_share(const Kv4Range &r, int per, int splits, int split) {
+  const int t0 = (int)(r.lo / kKvTile), n = kv4_tiles(r);
+  const int least = n / splits + (n % splits != 0);
+  if (per < least) per = least;
+  if (per < 1) per = 1;
   Kv4Share s;
-  s.used = n > 0 ? (n + per - 1) / per : 1;
-  const int b = split * per < n ? split * per : n;
-  const int e = b + per < n ? b + per : n;
-  s.begin = (int)t0 + b;
-  s.end = (int)t0 + e;
+  s.used = n > 0 ? n / per + (n % per != 0) : 1;
+  const long long b = (long long)split * per < n ? (long long)split * per : n;
+  const long long e = b + per < n ? b + per : n;
+  s.begin = t0 + (int)b;
+  s.end = t0 + (int)e;
   return s;
 }
 

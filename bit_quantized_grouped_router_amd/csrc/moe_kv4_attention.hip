@@ -21,18 +21,19 @@
 // products (16x16x32 MFMA, lane l: column l % 16, lane group l / 16):
 //   S^T = K Q^T   rows are keys, columns query rows: a lane ends up with keys
 //                 4 (l/16) .. +3 of each 16-key half for its own query row;
-//   O^T = V^T P^T contracts over those keys, 8 to a lane, in that same order;
-//                 the lane's V operand are the 8 keys' codes of channels
-//                 64 g + 4 (l % 16) + j, nibble j of one 16-bit load a key.
-// The order of the channels inside a contraction is free, so the nibbles of a
-// word are taken in the order 0 4 1 5 2 6 3 7 (one shift and one and-or give
-// two of them) and the query is laid out once to match.
+//   O^T = V^T P^T contracts over those keys, 8 to a lane; the lane's V operand
+//                 are the 8 keys' codes of channel 16 j + l % 16, which one
+//                 transposing LDS read (16 keys by 16 channels of 4 bits a
+//                 lane group) delivers for two j at once.
+// The order inside a contraction is free, so the nibbles of a word are taken
+// in the order 0 4 1 5 2 6 3 7 (one shift and one and-or give two of them),
+// and the query and the weights are laid out to match.
 #include "moe_device.h"
 #include "moe_kv4.h"
 
 namespace moe {
 
-constexpr int kAtWaves = 4;  // wavefronts per workgroup: they share 16 query rows and split the keys
+constexpr int kAtWaves = 8;  // wavefronts per workgroup: they share 16 query rows and split the keys
 constexpr int kAtRows = 16;  // query rows (token, head of the group) per workgroup
 
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -42,16 +43,33 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // the rescale runs once or twice a row instead of at every new maximum.
 constexpr float kSlack = 8.0f;
 
-// Two codes of a word, at bits 0..3 and 16..19 of x, as bf16 16 + code.
-// Shift: where they sit before (bit 4 i goes to bit 3).
-__device__ __forceinline__ uint32_t codes2(uint32_t x, int i) {
-  const uint32_t y = i == 0 ? x << 3 : x >> (4 * i - 3);
-  return (y & 0x00780078u) | 0x41804180u;
+// Constants of the conversion, kept in registers and opaque to the compiler so
+// that it is one shift and one v_and_or_b32 (which takes no literals).
+struct CodeRegs {
+  uint32_t mask, magic;  // 0x00780078 (scalar), 0x41804180 (vector)
+};
+
+__device__ __forceinline__ CodeRegs code_regs() {
+  CodeRegs k;
+  asm("s_mov_b32 %0, 0x00780078" : "=s"(k.mask));
+  asm("v_mov_b32 %0, 0x41804180" : "=v"(k.magic));
+  return k;
 }
 
-__device__ __forceinline__ bf16x8_t codes8(uint32_t c) {
-  const uint4 r = make_uint4(codes2(c, 0), codes2(c, 1), codes2(c, 2), codes2(c, 3));
+// Nibble i of both halves of x as two bf16 16 + code.
+__device__ __forceinline__ uint32_t codes2(uint32_t x, int i, const CodeRegs &k) {
+  return and_or(i == 0 ? x << 3 : x >> (4 * i - 3), k.mask, k.magic);
+}
+
+__device__ __forceinline__ bf16x8_t codes8(uint32_t c, const CodeRegs &k) {
+  const uint4 r = make_uint4(codes2(c, 0, k), codes2(c, 1, k), codes2(c, 2, k), codes2(c, 3, k));
   return __builtin_bit_cast(bf16x8_t, r);
+}
+
+// a plus the two bf16 values of w (products with 1 are exact).
+__device__ __forceinline__ float sum_bf16x2(uint32_t w, float a) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w),
+                                         __builtin_bit_cast(bf16x2_t, 0x3F803F80u), a, false);
 }
 
 // Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
@@ -70,144 +88,228 @@ __device__ __forceinline__ float bf16_at(const uint32_t (&w)[N], int i) {
   return (i & 1) ? __uint_as_float(w[i / 2] & 0xFFFF0000u) : __uint_as_float(w[i / 2] << 16);
 }
 
-// This lane's scales and biases of one 16-key half: 4 keys x NG groups.
-template <int NG>
-struct HalfScales {
-  uint32_t s[2 * NG], b[2 * NG];
+// ---- a wavefront's ring of key tiles in LDS
+//
+// Each wavefront fills its own ring with LDS DMA (no registers, no barriers)
+// and waits only for its own vector-memory counter. A stage holds a tile of
+// 32 keys: codes of the keys, codes of the values, then their scales and
+// biases in the cache's own order. A row's 32-byte groups are XOR-swizzled by
+// (key / 4), so that the 16 rows of a key operand and the 4 rows of a value
+// operand lie in different banks; the DMA's source address carries the
+// swizzle, since its LDS side is in lane order.
+constexpr int kStages = 2;
+
+template <int D>
+struct Ring {
+  static constexpr int NG = D / kGroup;
+  static constexpr int kRow = D / 2;                      // bytes of codes a key
+  static constexpr int kCodes = kKvTile * kRow;           // bytes of a tile's key (or value) codes
+  static constexpr int kMeta = kKvTile * NG * 2;          // bytes of a tile's scales (or biases)
+  static constexpr int kStage = 2 * kCodes + 4 * kMeta;
+  static constexpr int kCodeLoads = kCodes / 1024;        // DMA instructions of 64 x 16 bytes
+  static constexpr int kLoads = 2 * kCodeLoads + 1;       // one takes all the scales and biases
 };
 
-template <int NG>
-__device__ __forceinline__ void load_half_scales(const uint16_t *s, const uint16_t *b, long long at,
-                                                 HalfScales<NG> &h) {
-  if constexpr (NG == 1) {
-    const uint2 x = *(const uint2 *)(s + at), y = *(const uint2 *)(b + at);
-    h.s[0] = x.x, h.s[1] = x.y, h.b[0] = y.x, h.b[1] = y.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NG / 2; ++i) {
-      const uint4 x = *(const uint4 *)(s + at + 8 * i), y = *(const uint4 *)(b + at + 8 * i);
-      h.s[4 * i] = x.x, h.s[4 * i + 1] = x.y, h.s[4 * i + 2] = x.z, h.s[4 * i + 3] = x.w;
-      h.b[4 * i] = y.x, h.b[4 * i + 1] = y.y, h.b[4 * i + 2] = y.z, h.b[4 * i + 3] = y.w;
-    }
-  }
-}
+// s_waitcnt with only the vector-memory counter limited.
+#define MOE_KV_WAIT_VMCNT(n) \
+  __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (0x7 << 4) | (0xF << 8) | (((n) >> 4) << 14))
 
-// Where a 32-key tile lies: the cache rows of its two halves' first keys, and
-// whether their pages exist (a half without one is masked and reads page 0).
-struct TilePlace {
-  long long row[2];
-  bool ok[2];
+typedef int i32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2_t kv_lds_i32x2;
+typedef __attribute__((address_space(3))) void kv_lds_void;
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef const __attribute__((address_space(4))) int32_t kv_const_i32;
+
+// Pages of a tile's two halves (scalar loads; -1: no place).
+struct TilePages {
+  int page[2];
 };
 
-__device__ __forceinline__ TilePlace tile_place(const Kv4Dims &dm, const int32_t *__restrict__ table,
-                                                int head, int tile) {
-  TilePlace p;
+__device__ __forceinline__ TilePages tile_pages(const Kv4Dims &dm, const int32_t *table, int tile) {
+  TilePages p;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const long long t = (long long)tile * kKvTile + 16 * u;
     const bool in = t < kv4_capacity(dm);
-    const int page = table[in ? (int)(t >> dm.page_shift) : 0];
-    p.ok[u] = in && kv4_page_ok(dm, page);
-    p.row[u] = kv4_row(dm, p.ok[u] ? page : 0, head, (int)(t & (dm.page - 1)));
+    const int page = ((kv_const_i32 *)table)[in ? (int)(t >> dm.page_shift) : 0];
+    p.page[u] = in && kv4_page_ok(dm, page) ? page : -1;
   }
   return p;
 }
 
-template <int D>
-struct KeyTile {
-  static constexpr int NG = D / kGroup;
-  uint2 c[2][NG];
-  HalfScales<NG> h[2];
-};
-
-template <int D>
-struct ValueTile {
-  static constexpr int NG = D / kGroup;
-  uint32_t c[NG][4];  // 16 bits of two keys: (0,1) (2,3) of the first half, then of the second
-  HalfScales<NG> h[2];
-};
-
-template <int D>
-__device__ __forceinline__ void load_keys(const Kv4Plane &pl, const TilePlace &p, int lane,
-                                          KeyTile<D> &t) {
-  constexpr int NG = D / kGroup;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const uint8_t *c = pl.codes + p.row[u] * (D / 2);
-    const uint32_t at = (lane & 15) * (D / 2) + (lane >> 4) * 8;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) t.c[u][g] = *(const uint2 *)(c + at + g * 32);
-    load_half_scales<NG>(pl.scales + p.row[u] * NG, pl.biases + p.row[u] * NG, (lane >> 4) * 4 * NG,
-                         t.h[u]);
-  }
+// LDS DMA, 16 bytes a lane, to LDS address dst + 16 * lane (dst wave-uniform).
+// Written as assembly because the compiler, which cannot tell the ring's stages
+// apart, would wait for every DMA in flight before each LDS read; here the
+// waits are the explicit ones in the loop. No register is written. The no-ops
+// cover m0 (one wait state) and scalar operands fresh from the VALU (five).
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(kv_lds_void *)p);
 }
 
+// From base + off, base wave-uniform with `bytes` readable bytes.
+__device__ __forceinline__ void load_lds16(const uint8_t *base, uint32_t bytes, uint32_t off, uint32_t dst) {
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  u32x4_t r;
+  r[0] = __builtin_amdgcn_readfirstlane((uint32_t)b);
+  r[1] = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xFFFFu);
+  r[2] = bytes;
+  r[3] = 0x00020000;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               ::"s"(dst), "v"(off), "s"(r) : "memory");
+}
+
+// From each lane's own address.
+__device__ __forceinline__ void load_lds16(const void *p, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off"
+               ::"s"(dst), "v"(p) : "memory");
+}
+
+// What a lane's DMA and LDS addresses are made of: few registers, from which
+// each tile's addresses follow in an operation or two.
 template <int D>
-__device__ __forceinline__ void load_values(const Kv4Plane &pl, const TilePlace &p, int lane,
-                                            ValueTile<D> &t) {
-  constexpr int NG = D / kGroup;
+struct LaneParts {
+  uint32_t code;             // byte of this lane's chunk in a half's codes, with the swizzle
+  const uint16_t *meta;      // this lane's 16 bytes of the first row's scales or biases
+  uint32_t key, value, scale;  // LDS bytes of its key codes, value codes, scales in a stage
+};
+
+template <int D>
+__device__ __forceinline__ LaneParts<D> lane_parts(const Kv4Plane &kc, const Kv4Plane &vc, int lane) {
+  using R = Ring<D>;
+  constexpr int NG = R::NG, kChunks = R::kRow / 16;
+  LaneParts<D> p;
+  const int key = lane / kChunks, at = lane % kChunks;
+  p.code = (key & 15) * R::kRow + ((((at >> 1) ^ ((key >> 2) & (NG - 1))) << 1) | (at & 1)) * 16;
+  const int array = lane / (4 * NG);  // of 2 NG chunks a half; lanes past 16 NG have none
+  p.meta = (array & 1 ? (array & 2 ? vc.biases : kc.biases) : (array & 2 ? vc.scales : kc.scales)) +
+           (lane % (2 * NG)) * 8;
+  p.key = (lane & 15) * R::kRow + (lane >> 4) * 8 + (((lane >> 2) & (NG - 1)) << 5);
+  // lane k % 8 of a lane group supplies the row of the group's k-th key (4 of
+  // the first half, 4 of the second), lanes 8 .. 15 the next 16 channels
+  p.value = R::kCodes + (4 * (lane >> 4) + (lane & 3) + 4 * (lane & 4)) * R::kRow + (lane & 8) +
+            (((lane >> 4) & (NG - 1)) << 5);
+  p.scale = 2 * R::kCodes + (lane >> 4) * 4 * NG * 2;
+  return p;
+}
+
+// Starts the DMA of one tile into a stage. A half without a page reads page 0
+// (its keys are masked).
+template <int D>
+__device__ __forceinline__ void load_tile(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
+                                          const TilePages &p, int head, int tile, uint32_t dst,
+                                          const LaneParts<D> &lp, int lane) {
+  using R = Ring<D>;
+  constexpr int NG = R::NG;
+  long long row[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const uint8_t *c = pl.codes + p.row[u] * (D / 2);
-    const uint32_t at = (lane >> 4) * 4 * (D / 2) + (lane & 15) * 2;
+  for (int u = 0; u < 2; ++u)
+    row[u] = kv4_row(dm, p.page[u] < 0 ? 0 : p.page[u], head, (tile * kKvTile + 16 * u) & (dm.page - 1));
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+  for (int i = 0; i < R::kCodeLoads; ++i) {
+    if constexpr (NG >= 2) {
+      // an instruction stays in one half: a scalar base and a 32-bit lane
+      // offset (D = 256: the half's second 8 keys, whose swizzle differs by 2)
+      const uint32_t off = NG == 4 && (i & 1) ? (lp.code ^ 64u) + 8 * R::kRow : lp.code;
+      const long long r = row[i / (R::kCodeLoads / 2)] * R::kRow;
+      load_lds16(kc.codes + r, 16 * R::kRow, off, dst + i * 1024);
+      load_lds16(vc.codes + r, 16 * R::kRow, off, dst + R::kCodes + i * 1024);
+    } else {
+      const long long r = (lane >= 32 ? row[1] : row[0]) * R::kRow + lp.code;
+      load_lds16(kc.codes + r, dst + i * 1024);
+      load_lds16(vc.codes + r, dst + R::kCodes + i * 1024);
+    }
+  }
+  if (NG == 4 || lane < 16 * NG)
+    load_lds16(lp.meta + (lane & (2 * NG) ? row[1] : row[0]) * NG, dst + 2 * R::kCodes);
+}
+
+// This lane's scales or biases of one 16-key half: keys 4 (l / 16) .. +3, NG
+// groups each, as packed bf16 pairs.
+template <int NG>
+__device__ __forceinline__ void read_meta(const uint8_t *p, uint32_t (&w)[2 * NG]) {
+  if constexpr (NG == 1) {
+    const uint2 x = *(const uint2 *)p;
+    w[0] = x.x, w[1] = x.y;
+  } else {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t a = *(const uint16_t *)(c + at + (2 * r) * (D / 2) + g * 32);
-        const uint32_t b = *(const uint16_t *)(c + at + (2 * r + 1) * (D / 2) + g * 32);
-        t.c[g][2 * u + r] = a | (b << 16);
-      }
-    load_half_scales<NG>(pl.scales + p.row[u] * NG, pl.biases + p.row[u] * NG, (lane >> 4) * 4 * NG,
-                         t.h[u]);
+    for (int i = 0; i < NG / 2; ++i) {
+      const uint4 x = *(const uint4 *)(p + 16 * i);
+      w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+    }
   }
 }
 
 // What one wavefront has summed up for its 16 query rows; a lane holds its row
-// (column l % 16) and, for each group, channels 64 g + 16 (l / 16) + 4 r + j.
+// (column l % 16) and, for each group, channels 64 g + 16 j + 4 (l / 16) + r.
 template <int D>
 struct RowSums {
   static constexpr int NG = D / kGroup;
   f32x4_t o[NG][4];  // [g][j]: register r
-  f32x4_t w[NG];     // sum of the rounded weights p s (every register the same)
+  float w[NG];       // sum of the rounded weights p s, this lane's keys only
   float c[NG];       // sum of p (b + 8 s), this lane's keys only
   float m, l;        // reference maximum (scaled log2 units); sum of p, this lane's keys only
 };
 
-// One 32-key tile. MASKED: some row does not see some key (t0 .. t1 - 1 is what
-// this lane's row sees) or a page does not exist.
-template <int D, bool MASKED>
-__device__ __forceinline__ void attend_tile(const KeyTile<D> &kt, const ValueTile<D> &vt,
+// One 32-key tile. masked (wave-uniform): some row does not see some key (t0 ..
+// t1 - 1 is what this lane's row sees) or a page does not exist.
+template <int D>
+__device__ __forceinline__ void attend_tile(const uint8_t *stage, const LaneParts<D> &lp,
                                             const bf16x8_t (&q)[D / kGroup][2],
                                             const float (&qsum)[D / kGroup], float scale2,
-                                            int lane, long long key0, long long t0, long long t1,
-                                            const bool (&ok)[2], RowSums<D> &a) {
-  constexpr int NG = D / kGroup;
+                                            bool masked, int lane, int key0, int t0, int t1,
+                                            const TilePages &pages, RowSums<D> &a) {
+  using R = Ring<D>;
+  constexpr int NG = R::NG;
+  const uint8_t *meta = stage + lp.scale;
+  const CodeRegs kr = code_regs();
   float s[8];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
+    uint32_t ws[2 * NG], wb[2 * NG];
+    read_meta<NG>(meta + 16 * u * NG * 2, ws);
+    read_meta<NG>(meta + R::kMeta + 16 * u * NG * 2, wb);
     float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
+      const uint2 c = *(const uint2 *)(stage + (lp.key ^ (g << 5)) + 16 * u * R::kRow);
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(kt.c[u][g].x), q[g][0], acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(kt.c[u][g].y), q[g][1], acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.x, kr), q[g][0], acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.y, kr), q[g][1], acc, 0, 0, 0);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float sc = bf16_at(kt.h[u].s, r * NG + g), bi = bf16_at(kt.h[u].b, r * NG + g);
+        const float sc = bf16_at(ws, r * NG + g), bi = bf16_at(wb, r * NG + g);
         x[r] = fmaf(sc, acc[r], fmaf(fmaf(-16.0f, sc, bi), qsum[g], x[r]));
       }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) s[4 * u + r] = x[r];
+    __builtin_amdgcn_sched_barrier(0);  // one half's operands at a time: registers
   }
-  bool seen[8];
-  if (MASKED) {
+  uint32_t ws[2][2 * NG], wb[2][2 * NG];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    read_meta<NG>(meta + 2 * R::kMeta + 16 * u * NG * 2, ws[u]);
+    read_meta<NG>(meta + 3 * R::kMeta + 16 * u * NG * 2, wb[u]);
+  }
+  if (masked) {
+    // An unseen slot may hold anything, NaN included: its score becomes -inf
+    // and its value's scale and bias 0, by selection and never by a product.
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const long long t = key0 + (i >> 2) * 16 + (lane >> 4) * 4 + (i & 3);
-      seen[i] = ok[i >> 2] && t >= t0 && t < t1;
-      s[i] = seen[i] ? s[i] : kNegInf;
+      const int u = i >> 2, r = i & 3, t = key0 + u * 16 + (lane >> 4) * 4 + r;
+      const bool seen = pages.page[u] >= 0 && t >= t0 && t < t1;
+      s[i] = seen ? s[i] : kNegInf;
+      if constexpr (NG == 1) {
+        const uint32_t keep = seen ? 0xFFFFFFFFu : (r & 1 ? 0x0000FFFFu : 0xFFFF0000u);
+        ws[u][r / 2] &= keep;
+        wb[u][r / 2] &= keep;
+      } else {
+#pragma unroll
+        for (int k = 0; k < NG / 2; ++k) {
+          ws[u][r * NG / 2 + k] = seen ? ws[u][r * NG / 2 + k] : 0u;
+          wb[u][r * NG / 2 + k] = seen ? wb[u][r * NG / 2 + k] : 0u;
+        }
+      }
     }
   }
   float mx = s[0];
@@ -223,8 +325,7 @@ __device__ __forceinline__ void attend_tile(const KeyTile<D> &kt, const ValueTil
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) a.o[g][j][r] *= alpha;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) a.w[g][r] *= alpha;
+      a.w[g] *= alpha;
       a.c[g] *= alpha;
     }
     a.l *= alpha;
@@ -237,32 +338,30 @@ __device__ __forceinline__ void attend_tile(const KeyTile<D> &kt, const ValueTil
     p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale2, -ref));
     a.l += p[i];
   }
-  bf16x8_t ones;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ones[i] = (__bf16)1.0f;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
+    i32x2_t vc[2];  // 8 keys' codes of channels 64 g + 16 j + l % 16, j = 0, 1 and 2, 3
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      vc[i] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+          (kv_lds_i32x2 *)(stage + (lp.value ^ (g << 5)) + 16 * i));
     float ps[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const HalfScales<NG> &h = vt.h[i >> 2];
-      const float sc = bf16_at(h.s, (i & 3) * NG + g), bi = bf16_at(h.b, (i & 3) * NG + g);
-      // a masked slot may hold anything, NaN included: select, never multiply by zero
-      ps[i] = !MASKED || seen[i] ? p[i] * sc : 0.f;
-      const float mid = fmaf(8.0f, sc, bi);
-      a.c[g] = !MASKED || seen[i] ? fmaf(p[i], mid, a.c[g]) : a.c[g];
+      const float sc = bf16_at(ws[i >> 2], (i & 3) * NG + g), bi = bf16_at(wb[i >> 2], (i & 3) * NG + g);
+      ps[i] = p[i] * sc;
+      a.c[g] = fmaf(p[i], fmaf(8.0f, sc, bi), a.c[g]);
     }
-    const uint4 pw = make_uint4(pack_bf16x2(ps[0], ps[1]), pack_bf16x2(ps[2], ps[3]),
-                                pack_bf16x2(ps[4], ps[5]), pack_bf16x2(ps[6], ps[7]));
+    // the keys in the order codes8 takes nibbles
+    const uint4 pw = make_uint4(pack_bf16x2(ps[0], ps[4]), pack_bf16x2(ps[1], ps[5]),
+                                pack_bf16x2(ps[2], ps[6]), pack_bf16x2(ps[3], ps[7]));
     const bf16x8_t pb = __builtin_bit_cast(bf16x8_t, pw);
+    a.w[g] = sum_bf16x2(pw.x, sum_bf16x2(pw.y, sum_bf16x2(pw.z, sum_bf16x2(pw.w, a.w[g]))));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 vw = make_uint4(codes2(vt.c[g][0], j), codes2(vt.c[g][1], j),
-                                  codes2(vt.c[g][2], j), codes2(vt.c[g][3], j));
-      a.o[g][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, vw), pb,
+    for (int j = 0; j < 4; ++j)
+      a.o[g][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8((uint32_t)vc[j >> 1][j & 1], kr), pb,
                                                           a.o[g][j], 0, 0, 0);
-    }
-    a.w[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pb, a.w[g], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -318,20 +417,56 @@ __device__ __forceinline__ void store_row(const Kv4Dims &dm, const Kv4Attn &at, 
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
+// LDS of a workgroup: the rings, or the join of 128 channels (64 for D = 64).
+template <int D>
+constexpr int at_lds_bytes() {
+  const int ring = kAtWaves * kStages * Ring<D>::kStage, join = kAtWaves * kAtRows * ((D < 128 ? D : 128) + 4) * 4;
+  return ring > join ? ring : join;
+}
+
+// Tiles a workgroup takes at least (two a wavefront), and the workgroups a
+// call is spread over: one or two rounds of the 256 CUs.
+constexpr int kMinTiles = 2 * kAtWaves;
+constexpr int kTargetBlocks = 512;
+// Batches up to this size spread their keys evenly over the workgroups (the
+// lengths are on the device, so each wavefront adds them up, 64 at a time);
+// larger ones have enough sequences to fill the card with.
+constexpr int kEvenMaxB = 256;
+
+// Tiles a workgroup takes of a sequence, so that all workgroups of the call
+// have about the same (kv4_share raises it where `splits` are too few).
+__device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Attn &at) {
+  if (dm.B > kEvenMaxB) return kMinTiles;
+  const int lane = threadIdx.x & (kWave - 1), G = dm.Hq / dm.Hkv;
+  float total = 0.f;  // tiles of all tasks; a rough figure will do
+  for (int b = lane; b < dm.B; b += kWave) {
+    const Kv4Span sp = kv4_span(bt.cu[b], bt.cu[b + 1], bt.len[b], bt.T);
+    const int n = min(sp.n, at.max_new);
+    if (n == 0) continue;
+    const Kv4Range r = kv4_range(dm, sp.first, sp.first + n - 1, sp.len, at.causal, at.window);
+    total += (float)kv4_tiles(r) * (float)((n * G + kAtRows - 1) / kAtRows);
+  }
+  total = wave_sum_dpp(total) * dm.Hkv;
+  return max(kMinTiles, (int)fminf(ceilf(total * (1.0f / kTargetBlocks)), 67108864.0f));
+}
+
 template <int D>
 __global__ __launch_bounds__(kAtWaves *kWave, 2) void kv4_attention_kernel(
     Kv4Dims dm, Kv4Plane kc, Kv4Plane vc, Kv4Batch bt, Kv4Attn at, int splits,
     float *__restrict__ part) {
   constexpr int NG = D / kGroup;
-  constexpr int kPad = 4;  // floats between rows in LDS
+  constexpr int kPad = 4;  // floats between rows of the join
+  static_assert(kAtWaves * kAtRows * ((D < 128 ? D : 128) + kPad) * 4 <= at_lds_bytes<D>(), "join fits");
   constexpr int kJoin = D < 128 ? D : 128;  // channels joined at a time
-  __shared__ __attribute__((aligned(16))) float so[kAtWaves][kAtRows][kJoin + kPad];
+  // LDS: the wavefronts' rings; later, over them, the parts to join
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  float(*so)[kAtRows][kJoin + kPad] = (float(*)[kAtRows][kJoin + kPad])smem;
   __shared__ float sm[kAtWaves][kAtRows], sl[kAtWaves][kAtRows];
   const int task = blockIdx.x / splits, split = blockIdx.x % splits;
   const RowTile rt = row_tile(dm, bt, at.max_new, task);
   if (rt.row0 >= rt.rows) return;
   const Kv4Range range = tile_range(dm, rt, at.causal, at.window);
-  const Kv4Share share = kv4_share(range, splits, split);
+  const Kv4Share share = kv4_share(range, splits > 1 ? tiles_per_split(dm, bt, at) : 0, splits, split);
   if (split >= share.used) return;
 
   const int lane = threadIdx.x & (kWave - 1);
@@ -365,11 +500,11 @@ __global__ __launch_bounds__(kAtWaves *kWave, 2) void kv4_attention_kernel(
     }
   }
   // keys this lane's row sees
-  long long t0 = 0, t1 = 0;
+  int t0 = 0, t1 = 0;  // positions in the table fit 31 bits
   if (real) {
     const Kv4Range mine = kv4_range(dm, rt.sp.first + tok, rt.sp.first + tok, rt.sp.len, at.causal, at.window);
-    t0 = mine.lo;
-    t1 = mine.hi;
+    t0 = (int)(mine.lo < mine.hi ? mine.lo : 0);
+    t1 = (int)(mine.lo < mine.hi ? mine.hi : 0);
   }
   // keys every real row sees: tiles inside need no mask
   const int last = min(rt.row0 + kAtRows, rt.rows) - 1;
@@ -383,32 +518,46 @@ __global__ __launch_bounds__(kAtWaves *kWave, 2) void kv4_attention_kernel(
   for (int g = 0; g < NG; ++g) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) a.o[g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    a.w[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    a.c[g] = 0.f;
+    a.w[g] = a.c[g] = 0.f;
   }
   a.m = kNegInf;
   a.l = 0.f;
 
   const int32_t *table = bt.table + (long long)rt.seq * dm.max_pages;
+  uint8_t *ring = smem + wave * kStages * Ring<D>::kStage;
+  const uint32_t ring_at = lds_address(ring);
+  LaneParts<D> lp = lane_parts<D>(kc, vc, lane);
   int tile = share.begin + wave;
-  if (tile < share.end) {
-    KeyTile<D> kt;
-    ValueTile<D> vt;
-    TilePlace here = tile_place(dm, table, rt.head, tile);
-    load_keys<D>(kc, here, lane, kt);
-    load_values<D>(vc, here, lane, vt);
-    for (; tile < share.end; tile += kAtWaves) {
-      const long long key0 = (long long)tile * kKvTile;
-      const bool full = key0 >= all0 && key0 + kKvTile <= all1 && here.ok[0] && here.ok[1];
-      if (full)
-        attend_tile<D, false>(kt, vt, q, qsum, scale2, lane, key0, t0, t1, here.ok, a);
-      else
-        attend_tile<D, true>(kt, vt, q, qsum, scale2, lane, key0, t0, t1, here.ok, a);
-      if (tile + kAtWaves < share.end) {
-        here = tile_place(dm, table, rt.head, tile + kAtWaves);
-        load_keys<D>(kc, here, lane, kt);
-        load_values<D>(vc, here, lane, vt);
-      }
+  const int end = share.end;
+  // pages of the tile in use, of the next one and (not loaded yet) of the one after
+  TilePages here{}, next{}, after{};
+  if (tile < end) {
+    here = tile_pages(dm, table, tile);
+    next = tile_pages(dm, table, min(tile + kAtWaves, end - 1));
+    after = tile_pages(dm, table, min(tile + 2 * kAtWaves, end - 1));
+    load_tile<D>(dm, kc, vc, here, rt.head, tile, ring_at, lp, lane);
+    if (tile + kAtWaves < end)
+      load_tile<D>(dm, kc, vc, next, rt.head, tile + kAtWaves, ring_at + Ring<D>::kStage, lp, lane);
+  }
+  for (int stage = 0; tile < end; tile += kAtWaves, stage ^= 1) {
+    // keeps the compiler from holding every address made of the parts in a register
+    asm volatile("" : "+v"(lp.code), "+v"(lp.key), "+v"(lp.value), "+v"(lp.scale));
+    // this tile has landed; the next one's loads may still be in flight
+    if (tile + kAtWaves < end)
+      MOE_KV_WAIT_VMCNT(Ring<D>::kLoads);
+    else
+      MOE_KV_WAIT_VMCNT(0);
+    asm volatile("" ::: "memory");
+    const int key0 = tile * kKvTile;
+    const bool masked = key0 < all0 || key0 + (long long)kKvTile > all1 || here.page[0] < 0 || here.page[1] < 0;
+    attend_tile<D>(ring + stage * Ring<D>::kStage, lp, q, qsum, scale2, masked, lane, key0, t0, t1, here, a);
+    // every LDS read of this stage is done before the DMA refills it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    here = next;
+    next = after;
+    if (tile + 2 * kAtWaves < end) {
+      load_tile<D>(dm, kc, vc, after, rt.head, tile + 2 * kAtWaves, ring_at + stage * Ring<D>::kStage, lp, lane);
+      after = tile_pages(dm, table, min(tile + 3 * kAtWaves, end - 1));
     }
   }
 
@@ -422,16 +571,14 @@ __global__ __launch_bounds__(kAtWaves *kWave, 2) void kv4_attention_kernel(
   constexpr int kThreadsRow = kJoin / 4;
 #pragma unroll
   for (int c0 = 0; c0 < D; c0 += kJoin) {
-    if (c0 > 0) __syncthreads();
+    __syncthreads();  // every wavefront is done with what lies there
 #pragma unroll
     for (int g = c0 / kGroup; g < (c0 + kJoin) / kGroup; ++g) {
-      const float sum = groups_sum(a.c[g]);
+      const float off = groups_sum(fmaf(-24.0f, a.w[g], a.c[g]));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float off = fmaf(-24.0f, a.w[g][r], sum);
-        *(float4 *)&so[wave][lane & 15][g * kGroup - c0 + (lane >> 4) * 16 + 4 * r] = make_float4(
-            a.o[g][0][r] + off, a.o[g][1][r] + off, a.o[g][2][r] + off, a.o[g][3][r] + off);
-      }
+      for (int j = 0; j < 4; ++j)
+        *(float4 *)&so[wave][lane & 15][g * kGroup - c0 + 16 * j + 4 * (lane >> 4)] = make_float4(
+            a.o[g][j][0] + off, a.o[g][j][1] + off, a.o[g][j][2] + off, a.o[g][j][3] + off);
     }
     __syncthreads();
     for (int r = threadIdx.x / kThreadsRow; r < kAtRows && rt.row0 + r < rt.rows;
@@ -460,23 +607,25 @@ __global__ __launch_bounds__(kAtWaves *kWave, 2) void kv4_attention_kernel(
   }
 }
 
-// Joins the splits' partial results: one workgroup per row of a task.
-template <int D>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Attn at, int splits,
-                                                       long long tasks,
+// Joins the splits' partial results: one workgroup per row of a task and C of
+// its channels. C = D where splits are few; C = 32 where they are many, so that
+// 32 parts are read at a time and the card has more workgroups to run.
+template <int D, int C>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Attn at,
+                                                       int splits, long long tasks,
                                                        const float *__restrict__ part) {
-  constexpr int kThreadsRow = D / 4, kParts = 256 / kThreadsRow;
+  constexpr int kThreadsRow = C / 4, kParts = 256 / kThreadsRow, kChunks = D / C;
   __shared__ float4 so[kParts][kThreadsRow];
   __shared__ float sl[kParts];
-  const int task = blockIdx.x / kAtRows, r = blockIdx.x % kAtRows;
+  const int chunk = blockIdx.x % kChunks, r = blockIdx.x / kChunks % kAtRows, task = blockIdx.x / (kChunks * kAtRows);
   const RowTile rt = row_tile(dm, bt, at.max_new, task);
   if (rt.row0 + r >= rt.rows) return;
   const Kv4Range range = tile_range(dm, rt, at.causal, at.window);
-  const int used = kv4_share(range, splits, 0).used;
+  const int used = kv4_share(range, tiles_per_split(dm, bt, at), splits, 0).used;
   if (used <= 1) return;
   const float *ml = part + tasks * splits * kAtRows * D;
   const long long pr0 = (long long)task * splits * kAtRows + r;
-  // the row's reference: every thread looks at all the splits' (few, and cached)
+  // the row's reference: every wavefront looks at all the splits'
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   float m = kNegInf;
   for (int s = lane; s < used; s += kWave) m = fmaxf(m, ml[(pr0 + (long long)s * kAtRows) * 2]);
@@ -488,7 +637,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
 #pragma unroll 4
   for (int s = part_i; s < used; s += kParts) {
     const long long pr = pr0 + (long long)s * kAtRows;
-    join_part(ml[pr * 2], ml[pr * 2 + 1], m, *(const float4 *)(part + pr * D + c * 4), l, o);
+    join_part(ml[pr * 2], ml[pr * 2 + 1], m, *(const float4 *)(part + pr * D + chunk * C + c * 4), l, o);
   }
   so[part_i][c] = o;
   if (c == 0) sl[part_i] = l;
@@ -500,7 +649,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
       o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
       l += sl[i];
     }
-    store_row(dm, at, rt, r, c * 4, l, o);
+    store_row(dm, at, rt, r, chunk * C + c * 4, l, o);
   }
 }
 
@@ -511,22 +660,21 @@ static long long kv4_tasks(const Kv4Dims &dm, int max_new) {
   return (rows + kAtRows - 1) / kAtRows * dm.Hkv * dm.B;
 }
 
-// Workgroups to aim for: two per CU fit (their LDS and registers), so this is
-// one round of the card's 256 CUs.
-constexpr int kTargetBlocks = 512;
-
+// The most workgroups a sequence's keys are split over: as many as have two
+// tiles a wavefront (of the table's width: the host does not know the
+// lengths), and no more than twice the target over all tasks.
 int kv4_splits(const Kv4Dims &dm, int max_new, int window) {
   const long long tasks = kv4_tasks(dm, max_new);
   long long keys = kv4_capacity(dm);
   if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
-  const long long most = (keys + kKvTile * kMinSplitTiles - 1) / (kKvTile * kMinSplitTiles);
-  long long n = (kTargetBlocks + tasks - 1) / tasks;
+  const long long most = keys / (kKvTile * kMinTiles);
+  long long n = (2 * kTargetBlocks) / tasks;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
 }
 
 bool kv4_grid_ok(const Kv4Dims &dm, int max_new, int window) {
-  return kv4_tasks(dm, max_new) * kAtRows * kv4_splits(dm, max_new, window) < (1ll << 31);
+  return kv4_tasks(dm, max_new) * kAtRows * (dm.D / 32) * kv4_splits(dm, max_new, window) < (1ll << 31);
 }
 
 size_t kv4_attention_ws(const Kv4Dims &dm, int max_new, int window) {
@@ -540,10 +688,18 @@ static hipError_t launch(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &
                          const Kv4Attn &at, float *part, hipStream_t s) {
   const long long tasks = kv4_tasks(dm, at.max_new);
   const int splits = kv4_splits(dm, at.max_new, at.window);
-  kv4_attention_kernel<D><<<(int)(tasks * splits), kAtWaves * kWave, 0, s>>>(dm, kc, vc, bt, at, splits, part);
+  if constexpr (at_lds_bytes<D>() > 64 * 1024) {  // needs an opt-in, once per process
+    static const hipError_t st = hipFuncSetAttribute(
+        (const void *)kv4_attention_kernel<D>, hipFuncAttributeMaxDynamicSharedMemorySize, at_lds_bytes<D>());
+    if (st != hipSuccess) return st;
+  }
+  kv4_attention_kernel<D><<<(int)(tasks * splits), kAtWaves * kWave, at_lds_bytes<D>(), s>>>(
+      dm, kc, vc, bt, at, splits, part);
   if (const hipError_t e = hipGetLastError()) return e;
-  if (splits > 1)
-    kv4_join_kernel<D><<<(int)(tasks * kAtRows), 256, 0, s>>>(dm, bt, at, splits, tasks, part);
+  if (splits > 16)
+    kv4_join_kernel<D, 32><<<(int)(tasks * kAtRows * (D / 32)), 256, 0, s>>>(dm, bt, at, splits, tasks, part);
+  else if (splits > 1)
+    kv4_join_kernel<D, D><<<(int)(tasks * kAtRows), 256, 0, s>>>(dm, bt, at, splits, tasks, part);
   return hipGetLastError();
 }
 

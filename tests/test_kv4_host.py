@@ -152,8 +152,8 @@ extern "C" void range(int page_shift, int max_pages, long long p0, long long p1,
   const Kv4Range r = kv4_range(dims(page_shift, 1, max_pages), p0, p1, len, causal, window);
   o[0] = r.lo, o[1] = r.hi;
 }
-extern "C" void share(long long lo, long long hi, int splits, int split, int *o) {
-  const Kv4Share s = kv4_share(Kv4Range{lo, hi}, splits, split);
+extern "C" void share(long long lo, long long hi, int per, int splits, int split, int *o) {
+  const Kv4Share s = kv4_share(Kv4Range{lo, hi}, per, splits, split);
   o[0] = s.begin, o[1] = s.end, o[2] = s.used;
 }
 extern "C" int page_ok(int num_pages, int page) { return kv4_page_ok(dims(4, num_pages, 1), page); }
@@ -175,7 +175,7 @@ def H(tmp_path_factory):
     h = ctypes.CDLL(str(so))
     ll = ctypes.c_longlong
     h.range.argtypes = [ctypes.c_int, ctypes.c_int, ll, ll, ll, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
-    h.share.argtypes = [ll, ll, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
+    h.share.argtypes = [ll, ll, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
     h.row.restype = ll
     return h
 
@@ -219,10 +219,10 @@ def test_ranges_stay_inside_the_table(H):
 def test_shares_cover_every_tile_once(H):
     o = (ctypes.c_int * 3)()
     for lo, hi in ((0, 0), (5, 5), (9, 3), (0, 1), (0, 32), (31, 33), (100, 100000), (0, BIG), (BIG - 40, BIG)):
-        for splits in (1, 2, 7, 512):
+        for splits, per in ((1, 1), (1, 16), (2, 0), (7, 16), (7, BIG), (512, 1), (512, 40)):
             tiles, used = [], None
             for s in range(splits):
-                H.share(lo, hi, splits, s, o)
+                H.share(lo, hi, per, splits, s, o)
                 used = o[2] if used is None else used
                 assert o[2] == used and 1 <= used <= splits
                 if s >= used:
