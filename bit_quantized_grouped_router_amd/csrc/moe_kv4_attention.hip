@@ -33,8 +33,7 @@
 
 namespace moe {
 
-constexpr int kAtWaves = 8;  // wavefronts per workgroup: they share 16 query rows and split the keys
-constexpr int kAtRows = 16;  // query rows (token, head of the group) per workgroup
+constexpr int kAtRows = 16;  // query rows (token, head of the group) per workgroup; its wavefronts split the keys
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -70,6 +69,43 @@ __device__ __forceinline__ bf16x8_t codes8(uint32_t c, const CodeRegs &k) {
 __device__ __forceinline__ float sum_bf16x2(uint32_t w, float a) {
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w),
                                          __builtin_bit_cast(bf16x2_t, 0x3F803F80u), a, false);
+}
+
+// The affine part of the scores, sum_g (b_tg - 16 s_tg) qsum_g, as one more
+// MFMA of a 16-key half: the operand of the keys is their biases and scales as
+// they lie in the cache, the other one qsum cut into three bf16 (hi, lo, lo2:
+// 24 bits, so nothing is lost) and -16 times that. Contraction slots, by lane
+// group (8 each): b x hi, b x lo | b x lo2, s x hi | s x lo, s x lo2 | none for
+// NG = 4; b x hi, lo, lo2, s x hi | s x lo, lo2 | none for NG = 2; all six in
+// the first group for NG = 1.
+template <int NG>
+__device__ __forceinline__ bf16x8_t affine_query(const float (&qsum)[NG], int group) {
+  uint16_t v[6][NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    float rest = qsum[g];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      v[i][g] = to_bf16(rest);
+      const float part = bf16_to_f32(v[i][g]);
+      v[3 + i][g] = to_bf16(-16.0f * part);
+      rest -= part;
+    }
+  }
+  constexpr int kPer = 8 / NG;  // slots of NG values a lane group
+  uint16_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint16_t x = 0;
+#pragma unroll
+    for (int lg = 0; lg < 4; ++lg) {
+      const int slot = lg * kPer + i / NG;
+      if (slot < 6) x = group == lg ? v[slot][i % NG] : x;
+    }
+    e[i] = x;
+  }
+  return __builtin_bit_cast(bf16x8_t, make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                                 e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16));
 }
 
 // Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
@@ -171,6 +207,7 @@ struct LaneParts {
   uint32_t code;             // byte of this lane's chunk in a half's codes, with the swizzle
   const uint16_t *meta;      // this lane's 16 bytes of the first row's scales or biases
   uint32_t key, value, scale;  // LDS bytes of its key codes, value codes, scales in a stage
+  uint32_t affine0, affine1;   // and of what affine_keys reads
 };
 
 template <int D>
@@ -189,6 +226,9 @@ __device__ __forceinline__ LaneParts<D> lane_parts(const Kv4Plane &kc, const Kv4
   p.value = R::kCodes + (4 * (lane >> 4) + (lane & 3) + 4 * (lane & 4)) * R::kRow + (lane & 8) +
             (((lane >> 4) & (NG - 1)) << 5);
   p.scale = 2 * R::kCodes + (lane >> 4) * 4 * NG * 2;
+  const uint32_t s_at = 2 * R::kCodes + (lane & 15) * NG * 2, b_at = s_at + R::kMeta;
+  p.affine0 = lane >> 4 <= (NG == 4 ? 1 : 0) ? b_at : s_at;
+  p.affine1 = NG == 4 && lane >> 4 == 0 ? b_at : s_at;
   return p;
 }
 
@@ -239,6 +279,24 @@ __device__ __forceinline__ void read_meta(const uint8_t *p, uint32_t (&w)[2 * NG
   }
 }
 
+// The operand of affine_query for the keys of half u: key l % 16.
+template <int NG>
+__device__ __forceinline__ bf16x8_t affine_keys(const uint8_t *stage, const LaneParts<NG * kGroup> &lp, int u) {
+  const uint8_t *p0 = stage + lp.affine0 + 16 * u * NG * 2, *p1 = stage + lp.affine1 + 16 * u * NG * 2;
+  uint4 r;
+  if constexpr (NG == 4) {
+    const uint2 x = *(const uint2 *)p0, y = *(const uint2 *)p1;
+    r = make_uint4(x.x, x.y, y.x, y.y);
+  } else if constexpr (NG == 2) {
+    const uint32_t x = *(const uint32_t *)p0, y = *(const uint32_t *)p1;
+    r = make_uint4(x, x, x, y);
+  } else {
+    const uint32_t x = *(const uint16_t *)p0, y = *(const uint16_t *)p1;
+    r = make_uint4(x | x << 16, x | y << 16, y | y << 16, 0u);
+  }
+  return __builtin_bit_cast(bf16x8_t, r);
+}
+
 // What one wavefront has summed up for its 16 query rows; a lane holds its row
 // (column l % 16) and, for each group, channels 64 g + 16 j + 4 (l / 16) + r.
 template <int D>
@@ -255,7 +313,7 @@ struct RowSums {
 template <int D>
 __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LaneParts<D> &lp,
                                             const bf16x8_t (&q)[D / kGroup][2],
-                                            const float (&qsum)[D / kGroup], float scale2,
+                                            const bf16x8_t &qaff, float scale2,
                                             bool masked, int lane, int key0, int t0, int t1,
                                             const TilePages &pages, RowSums<D> &a) {
   using R = Ring<D>;
@@ -265,10 +323,10 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
   float s[8];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    uint32_t ws[2 * NG], wb[2 * NG];
+    uint32_t ws[2 * NG];
     read_meta<NG>(meta + 16 * u * NG * 2, ws);
-    read_meta<NG>(meta + R::kMeta + 16 * u * NG * 2, wb);
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+    x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(affine_keys<NG>(stage, lp, u), qaff, x, 0, 0, 0);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const uint2 c = *(const uint2 *)(stage + (lp.key ^ (g << 5)) + 16 * u * R::kRow);
@@ -276,10 +334,7 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.x, kr), q[g][0], acc, 0, 0, 0);
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.y, kr), q[g][1], acc, 0, 0, 0);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float sc = bf16_at(ws, r * NG + g), bi = bf16_at(wb, r * NG + g);
-        x[r] = fmaf(sc, acc[r], fmaf(fmaf(-16.0f, sc, bi), qsum[g], x[r]));
-      }
+      for (int r = 0; r < 4; ++r) x[r] = fmaf(bf16_at(ws, r * NG + g), acc[r], x[r]);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) s[4 * u + r] = x[r];
@@ -373,17 +428,13 @@ struct RowTile {
 };
 
 __device__ __forceinline__ RowTile row_tile(const Kv4Dims &dm, const Kv4Batch &bt, int max_new,
-                                            int task) {
-  const int G = dm.Hq / dm.Hkv;
-  const int tiles = (int)(((long long)max_new * G + kAtRows - 1) / kAtRows);
+                                            int tile, int head, int seq) {
   RowTile t;
-  const int tile = task % tiles;
-  task /= tiles;
-  t.head = task % dm.Hkv;
-  t.seq = task / dm.Hkv;
+  t.head = head;
+  t.seq = seq;
   t.row0 = tile * kAtRows;
-  t.sp = kv4_span(bt.cu[t.seq], bt.cu[t.seq + 1], bt.len[t.seq], bt.T);
-  t.rows = min(t.sp.n, max_new) * G;
+  t.sp = kv4_span(bt.cu[seq], bt.cu[seq + 1], bt.len[seq], bt.T);
+  t.rows = min(t.sp.n, max_new) * (dm.Hq / dm.Hkv);
   return t;
 }
 
@@ -395,38 +446,34 @@ __device__ __forceinline__ Kv4Range tile_range(const Kv4Dims &dm, const RowTile 
   return kv4_range(dm, t.sp.first + t.row0 / G, t.sp.first + last / G, t.sp.len, causal, window);
 }
 
-// Adds one part (reference m_i, sum l_i, unnormalised outputs x) to a row's
-// total at reference m. A part that saw no key (l_i = 0) is left out; one whose
-// scores were all NaN has no reference and passes its NaN on.
-__device__ __forceinline__ void join_part(float m_i, float l_i, float m, const float4 &x, float &l,
-                                          float4 &o) {
-  if (m_i == kNegInf && l_i == 0.f) return;
-  const float f = m_i == kNegInf ? 1.f : __builtin_amdgcn_exp2f(m_i - m);
-  l = fmaf(f, l_i, l);
-  o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
+// What a part of a row (reference m_i, sum l_i) counts for at reference m: one
+// that saw no key (l_i = 0) nothing; one whose scores were all NaN has no
+// reference and passes its NaN on.
+__device__ __forceinline__ float part_weight(float m_i, float l_i, float m) {
+  if (m_i == kNegInf) return l_i == 0.f ? 0.f : 1.f;
+  return __builtin_amdgcn_exp2f(m_i - m);
 }
 
-// Channels c .. c + 3 of row r of a tile, divided by the row's sum; a row that
+// Channels c .. c + 3 of a token's head, divided by the row's sum; a row that
 // saw no key is zero.
-__device__ __forceinline__ void store_row(const Kv4Dims &dm, const Kv4Attn &at, const RowTile &rt, int r,
-                                          int c, float l, const float4 &o) {
-  const int G = dm.Hq / dm.Hkv;
+__device__ __forceinline__ void store_row(const Kv4Dims &dm, const Kv4Attn &at, int tok, int head, int c,
+                                          float l, const float4 &o) {
   const float inv = l == 0.f ? 0.f : 1.0f / l;
-  const int i = (rt.row0 + r) / G, h = rt.head * G + (rt.row0 + r) % G;
-  *(uint2 *)(at.out + (rt.sp.begin + i) * at.out_stride + (long long)h * dm.D + c) =
+  *(uint2 *)(at.out + tok * at.out_stride + (long long)head * dm.D + c) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-// LDS of a workgroup: the rings, or the join of 128 channels (64 for D = 64).
-template <int D>
+// LDS of a workgroup of W wavefronts: their rings, and over them, at the end,
+// their results ([wave][16 rows][D + 4] floats).
+template <int D, int W>
 constexpr int at_lds_bytes() {
-  const int ring = kAtWaves * kStages * Ring<D>::kStage, join = kAtWaves * kAtRows * ((D < 128 ? D : 128) + 4) * 4;
-  return ring > join ? ring : join;
+  static_assert(kAtRows * (D + 4) * 4 <= kStages * Ring<D>::kStage, "the results fit over the rings");
+  return W * kStages * Ring<D>::kStage;
 }
 
-// Tiles a workgroup takes at least (two a wavefront), and the workgroups a
-// call is spread over: one or two rounds of the 256 CUs.
-constexpr int kMinTiles = 2 * kAtWaves;
+// Tiles a workgroup takes at least where keys are split, and the workgroups a
+// call is spread over: two rounds of the 256 CUs.
+constexpr int kMinTiles = 16;
 constexpr int kTargetBlocks = 512;
 // Batches up to this size spread their keys evenly over the workgroups (the
 // lengths are on the device, so each wavefront adds them up, 64 at a time);
@@ -450,78 +497,57 @@ __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch
   return max(kMinTiles, (int)fminf(ceilf(total * (1.0f / kTargetBlocks)), 67108864.0f));
 }
 
-template <int D>
-__global__ __launch_bounds__(kAtWaves *kWave, 2) void kv4_attention_kernel(
-    Kv4Dims dm, Kv4Plane kc, Kv4Plane vc, Kv4Batch bt, Kv4Attn at, int splits,
-    float *__restrict__ part) {
+// Grid: x = row tile * splits + split, y = cache head, z = sequence.
+template <int D, int W>
+__global__ __launch_bounds__(W *kWave, D == 256 ? 2 : 4) void kv4_attention_kernel(Kv4Dims dm, Kv4Plane kc, Kv4Plane vc,
+                                                                    Kv4Batch bt, Kv4Attn at, int splits,
+                                                                    float *__restrict__ part) {
   constexpr int NG = D / kGroup;
-  constexpr int kPad = 4;  // floats between rows of the join
-  static_assert(kAtWaves * kAtRows * ((D < 128 ? D : 128) + kPad) * 4 <= at_lds_bytes<D>(), "join fits");
-  constexpr int kJoin = D < 128 ? D : 128;  // channels joined at a time
-  // LDS: the wavefronts' rings; later, over them, the parts to join
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  float(*so)[kAtRows][kJoin + kPad] = (float(*)[kAtRows][kJoin + kPad])smem;
-  __shared__ float sm[kAtWaves][kAtRows], sl[kAtWaves][kAtRows];
-  const int task = blockIdx.x / splits, split = blockIdx.x % splits;
-  const RowTile rt = row_tile(dm, bt, at.max_new, task);
+  __shared__ float sm[W][kAtRows], sl[W][kAtRows];
+  int tile_i = blockIdx.x, split = 0;
+  if (splits > 1) {
+    tile_i = (int)gridDim.x == splits ? 0 : (int)blockIdx.x / splits;
+    split = blockIdx.x - tile_i * splits;
+  }
+  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z);
   if (rt.row0 >= rt.rows) return;
-  const Kv4Range range = tile_range(dm, rt, at.causal, at.window);
-  const Kv4Share share = kv4_share(range, splits > 1 ? tiles_per_split(dm, bt, at) : 0, splits, split);
-  if (split >= share.used) return;
-
+  const int G = dm.Hq / dm.Hkv;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int G = dm.Hq / dm.Hkv;
-  const float scale2 = at.scale * 1.4426950408889634f;  // scores in log2 units
 
-  // this lane's query row, its channels in the order codes8 takes a word's nibbles
-  const int row = rt.row0 + (lane & 15);
-  const bool real = row < rt.rows;
-  const int tok = (real ? row : rt.row0) / G, hd = rt.head * G + (real ? row : rt.row0) % G;
+  // the tile's first and last token, and this lane's query row
+  const int tok0 = rt.row0 == 0 ? 0 : rt.row0 / G;
+  const int in0 = rt.row0 - tok0 * G;  // head of the first row in its group
+  const int row = min(rt.row0 + (lane & 15), rt.rows - 1) - rt.row0 + in0;
+  const bool real = rt.row0 + (lane & 15) < rt.rows;
+  const int tok = tok0 + row / G, hd = rt.head * G + row % G;
+  const int tok1 = __builtin_amdgcn_readlane(tok, 15);
+  // its channels, in the order codes8 takes a word's nibbles
   bf16x8_t q[NG][2];
   float qsum[NG];
-  {
-    const uint16_t *qp = at.q + (rt.sp.begin + tok) * at.q_stride + (long long)hd * D;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint4 x = *(const uint4 *)(qp + g * kGroup + (2 * (lane >> 4) + j) * 8);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += bf16_at(w, i);
-        // pairs (0,4) (1,5) (2,6) (3,7)
-        const uint4 y = make_uint4((w[0] & 0xFFFFu) | (w[2] << 16), (w[0] >> 16) | (w[2] & 0xFFFF0000u),
-                                   (w[1] & 0xFFFFu) | (w[3] << 16), (w[1] >> 16) | (w[3] & 0xFFFF0000u));
-        q[g][j] = __builtin_bit_cast(bf16x8_t, y);
-      }
-      qsum[g] = groups_sum(sum);
-    }
-  }
-  // keys this lane's row sees
-  int t0 = 0, t1 = 0;  // positions in the table fit 31 bits
-  if (real) {
-    const Kv4Range mine = kv4_range(dm, rt.sp.first + tok, rt.sp.first + tok, rt.sp.len, at.causal, at.window);
-    t0 = (int)(mine.lo < mine.hi ? mine.lo : 0);
-    t1 = (int)(mine.lo < mine.hi ? mine.hi : 0);
-  }
-  // keys every real row sees: tiles inside need no mask
-  const int last = min(rt.row0 + kAtRows, rt.rows) - 1;
-  const long long all1 = kv4_range(dm, rt.sp.first + rt.row0 / G, rt.sp.first + rt.row0 / G, rt.sp.len,
-                                   at.causal, at.window).hi;
-  const long long all0 = kv4_range(dm, rt.sp.first + last / G, rt.sp.first + last / G, rt.sp.len,
-                                   at.causal, at.window).lo;
-
-  RowSums<D> a;
+  const uint16_t *qp = at.q + (rt.sp.begin + tok) * at.q_stride + (long long)hd * D + (lane >> 4) * 16;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
+    float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a.o[g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    a.w[g] = a.c[g] = 0.f;
+    for (int j = 0; j < 2; ++j) {
+      const uint4 x = *(const uint4 *)(qp + g * kGroup + j * 8);
+      sum = sum_bf16x2(x.x, sum_bf16x2(x.y, sum_bf16x2(x.z, sum_bf16x2(x.w, sum))));
+      // pairs (0,4) (1,5) (2,6) (3,7)
+      const uint4 y = make_uint4((x.x & 0xFFFFu) | (x.z << 16), (x.x >> 16) | (x.z & 0xFFFF0000u),
+                                 (x.y & 0xFFFFu) | (x.w << 16), (x.y >> 16) | (x.w & 0xFFFF0000u));
+      q[g][j] = __builtin_bit_cast(bf16x8_t, y);
+    }
+    qsum[g] = sum;
   }
-  a.m = kNegInf;
-  a.l = 0.f;
+  // keys the first and the last token see: all rows see those from all0 to all1
+  // and none sees any outside lo .. hi
+  const Kv4Range r0 = kv4_range(dm, rt.sp.first + tok0, rt.sp.first + tok0, rt.sp.len, at.causal, at.window);
+  const Kv4Range r1 = kv4_range(dm, rt.sp.first + tok1, rt.sp.first + tok1, rt.sp.len, at.causal, at.window);
+  const long long all0 = r1.lo, all1 = r0.hi;
+  const Kv4Share share = kv4_share(Kv4Range{r0.lo, r1.hi}, splits > 1 ? tiles_per_split(dm, bt, at) : 0, splits, split);
+  if (split >= share.used) return;
 
   const int32_t *table = bt.table + (long long)rt.seq * dm.max_pages;
   uint8_t *ring = smem + wave * kStages * Ring<D>::kStage;
@@ -533,76 +559,102 @@ __global__ __launch_bounds__(kAtWaves *kWave, 2) void kv4_attention_kernel(
   TilePages here{}, next{}, after{};
   if (tile < end) {
     here = tile_pages(dm, table, tile);
-    next = tile_pages(dm, table, min(tile + kAtWaves, end - 1));
-    after = tile_pages(dm, table, min(tile + 2 * kAtWaves, end - 1));
+    next = tile_pages(dm, table, min(tile + W, end - 1));
+    after = tile_pages(dm, table, min(tile + 2 * W, end - 1));
     load_tile<D>(dm, kc, vc, here, rt.head, tile, ring_at, lp, lane);
-    if (tile + kAtWaves < end)
-      load_tile<D>(dm, kc, vc, next, rt.head, tile + kAtWaves, ring_at + Ring<D>::kStage, lp, lane);
+    if (tile + W < end) load_tile<D>(dm, kc, vc, next, rt.head, tile + W, ring_at + Ring<D>::kStage, lp, lane);
   }
-  for (int stage = 0; tile < end; tile += kAtWaves, stage ^= 1) {
+
+  // keys this lane's row sees (positions in the table fit 31 bits)
+  int t0 = 0, t1 = 0;
+  if (real) {
+    const Kv4Range mine = kv4_range(dm, rt.sp.first + tok, rt.sp.first + tok, rt.sp.len, at.causal, at.window);
+    t0 = (int)(mine.lo < mine.hi ? mine.lo : 0);
+    t1 = (int)(mine.lo < mine.hi ? mine.hi : 0);
+  }
+#pragma unroll
+  for (int g = 0; g < NG; ++g) qsum[g] = groups_sum(qsum[g]);
+  const bf16x8_t qaff = affine_query<NG>(qsum, lane >> 4);
+  const float scale2 = at.scale * 1.4426950408889634f;  // scores in log2 units
+  RowSums<D> a;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a.o[g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    a.w[g] = a.c[g] = 0.f;
+  }
+  a.m = kNegInf;
+  a.l = 0.f;
+
+  for (int stage = 0; tile < end; tile += W, stage ^= 1) {
     // keeps the compiler from holding every address made of the parts in a register
     asm volatile("" : "+v"(lp.code), "+v"(lp.key), "+v"(lp.value), "+v"(lp.scale));
     // this tile has landed; the next one's loads may still be in flight
-    if (tile + kAtWaves < end)
+    if (tile + W < end)
       MOE_KV_WAIT_VMCNT(Ring<D>::kLoads);
     else
       MOE_KV_WAIT_VMCNT(0);
     asm volatile("" ::: "memory");
     const int key0 = tile * kKvTile;
     const bool masked = key0 < all0 || key0 + (long long)kKvTile > all1 || here.page[0] < 0 || here.page[1] < 0;
-    attend_tile<D>(ring + stage * Ring<D>::kStage, lp, q, qsum, scale2, masked, lane, key0, t0, t1, here, a);
+    attend_tile<D>(ring + stage * Ring<D>::kStage, lp, q, qaff, scale2, masked, lane, key0, t0, t1, here, a);
     // every LDS read of this stage is done before the DMA refills it
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     here = next;
     next = after;
-    if (tile + 2 * kAtWaves < end) {
-      load_tile<D>(dm, kc, vc, after, rt.head, tile + 2 * kAtWaves, ring_at + stage * Ring<D>::kStage, lp, lane);
-      after = tile_pages(dm, table, min(tile + 3 * kAtWaves, end - 1));
+    if (tile + 2 * W < end) {
+      load_tile<D>(dm, kc, vc, after, rt.head, tile + 2 * W, ring_at + stage * Ring<D>::kStage, lp, lane);
+      after = tile_pages(dm, table, min(tile + 3 * W, end - 1));
     }
   }
 
-  // join the wavefronts through LDS, kJoin channels at a time: o, reference and
-  // sum of each wavefront's rows, then kThreadsRow threads a row, 4 channels each
+  // Join the wavefronts: each scales what it has to the workgroup's reference
+  // and leaves it in its own ring's place; then the parts are added up, D / 4
+  // threads a row.
   a.l = groups_sum(a.l);
   if (lane < kAtRows) {
     sm[wave][lane] = a.m;
     sl[wave][lane] = a.l;
   }
-  constexpr int kThreadsRow = kJoin / 4;
+  __syncthreads();
+  float m = kNegInf;
 #pragma unroll
-  for (int c0 = 0; c0 < D; c0 += kJoin) {
-    __syncthreads();  // every wavefront is done with what lies there
+  for (int w = 0; w < W; ++w) m = fmaxf(m, sm[w][lane & 15]);
+  const float f = part_weight(a.m, a.l, m);
+  float *so = (float *)ring + (lane & 15) * (D + 4) + 4 * (lane >> 4);
 #pragma unroll
-    for (int g = c0 / kGroup; g < (c0 + kJoin) / kGroup; ++g) {
-      const float off = groups_sum(fmaf(-24.0f, a.w[g], a.c[g]));
+  for (int g = 0; g < NG; ++g) {
+    const float off = groups_sum(fmaf(-24.0f, a.w[g], a.c[g]));
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *(float4 *)&so[wave][lane & 15][g * kGroup - c0 + 16 * j + 4 * (lane >> 4)] = make_float4(
-            a.o[g][j][0] + off, a.o[g][j][1] + off, a.o[g][j][2] + off, a.o[g][j][3] + off);
+    for (int j = 0; j < 4; ++j)
+      *(float4 *)(so + g * kGroup + 16 * j) =
+          make_float4(f * (a.o[g][j][0] + off), f * (a.o[g][j][1] + off), f * (a.o[g][j][2] + off),
+                      f * (a.o[g][j][3] + off));
+  }
+  __syncthreads();
+  constexpr int kThreadsRow = D / 4;
+  const long long task = ((long long)blockIdx.z * dm.Hkv + blockIdx.y) * (gridDim.x / splits) + tile_i;
+  for (int r = threadIdx.x / kThreadsRow; r < kAtRows && rt.row0 + r < rt.rows; r += W * kWave / kThreadsRow) {
+    const int c = (threadIdx.x % kThreadsRow) * 4;
+    float mr = kNegInf, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) mr = fmaxf(mr, sm[w][r]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float4 x = *(const float4 *)((float *)(smem + w * kStages * Ring<D>::kStage) + r * (D + 4) + c);
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+      l = fmaf(part_weight(sm[w][r], sl[w][r], mr), sl[w][r], l);
     }
-    __syncthreads();
-    for (int r = threadIdx.x / kThreadsRow; r < kAtRows && rt.row0 + r < rt.rows;
-         r += kAtWaves * kWave / kThreadsRow) {
-      const int c = (threadIdx.x % kThreadsRow) * 4;
-      float m = sm[0][r];
-#pragma unroll
-      for (int w = 1; w < kAtWaves; ++w) m = fmaxf(m, sm[w][r]);
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kAtWaves; ++w) join_part(sm[w][r], sl[w][r], m, *(const float4 *)&so[w][r][c], l, o);
-      if (share.used > 1) {
-        // partial [task][split][16][D], then reference and sum [task][split][16][2]
-        const long long pr = ((long long)task * splits + split) * kAtRows + r;
-        float *ml = part + (long long)gridDim.x * kAtRows * D + pr * 2;
-        *(float4 *)(part + pr * D + c0 + c) = o;
-        if (c0 + c == 0) {
-          ml[0] = m;
-          ml[1] = l;
-        }
-      } else {
-        store_row(dm, at, rt, r, c0 + c, l, o);
-      }
+    if (share.used > 1) {
+      // partial [task][split][16][D], then reference and sum [task][split][16][2]
+      const long long pr = (task * splits + split) * kAtRows + r;
+      *(float4 *)(part + pr * D + c) = o;
+      if (c == 0)
+        *(float2 *)(part + (long long)gridDim.x * gridDim.y * gridDim.z * kAtRows * D + pr * 2) = make_float2(mr, l);
+    } else {
+      const int x = r + in0, i = tok0 + x / G, h = rt.head * G + x % G;
+      store_row(dm, at, rt.sp.begin + i, h, c, l, o);
     }
   }
 }
@@ -612,19 +664,21 @@ __global__ __launch_bounds__(kAtWaves *kWave, 2) void kv4_attention_kernel(
 // 32 parts are read at a time and the card has more workgroups to run.
 template <int D, int C>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Attn at,
-                                                       int splits, long long tasks,
-                                                       const float *__restrict__ part) {
+                                                       int splits, const float *__restrict__ part) {
   constexpr int kThreadsRow = C / 4, kParts = 256 / kThreadsRow, kChunks = D / C;
   __shared__ float4 so[kParts][kThreadsRow];
   __shared__ float sl[kParts];
-  const int chunk = blockIdx.x % kChunks, r = blockIdx.x / kChunks % kAtRows, task = blockIdx.x / (kChunks * kAtRows);
-  const RowTile rt = row_tile(dm, bt, at.max_new, task);
+  const int chunk = blockIdx.x % kChunks, r = blockIdx.x / kChunks % kAtRows, tile_i = blockIdx.x / (kChunks * kAtRows);
+  const int tiles = gridDim.x / (kChunks * kAtRows);
+  const long long task = ((long long)blockIdx.z * dm.Hkv + blockIdx.y) * tiles + tile_i;
+  const long long tasks = (long long)gridDim.z * gridDim.y * tiles;
+  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z);
   if (rt.row0 + r >= rt.rows) return;
   const Kv4Range range = tile_range(dm, rt, at.causal, at.window);
   const int used = kv4_share(range, tiles_per_split(dm, bt, at), splits, 0).used;
   if (used <= 1) return;
   const float *ml = part + tasks * splits * kAtRows * D;
-  const long long pr0 = (long long)task * splits * kAtRows + r;
+  const long long pr0 = task * splits * kAtRows + r;
   // the row's reference: every wavefront looks at all the splits'
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   float m = kNegInf;
@@ -637,7 +691,11 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
 #pragma unroll 4
   for (int s = part_i; s < used; s += kParts) {
     const long long pr = pr0 + (long long)s * kAtRows;
-    join_part(ml[pr * 2], ml[pr * 2 + 1], m, *(const float4 *)(part + pr * D + chunk * C + c * 4), l, o);
+    const float2 mls = *(const float2 *)(ml + pr * 2);
+    const float4 x = *(const float4 *)(part + pr * D + chunk * C + c * 4);
+    const float f = part_weight(mls.x, mls.y, m);
+    l = fmaf(f, mls.y, l);
+    o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
   }
   so[part_i][c] = o;
   if (c == 0) sl[part_i] = l;
@@ -649,15 +707,19 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
       o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
       l += sl[i];
     }
-    store_row(dm, at, rt, r, chunk * C + c * 4, l, o);
+    const int G = dm.Hq / dm.Hkv, x = rt.row0 + r;
+    store_row(dm, at, rt.sp.begin + x / G, rt.head * G + x % G, chunk * C + c * 4, l, o);
   }
 }
 
-// Row tiles of a call (an upper bound: a sequence may have fewer new tokens
-// than max_new) over all sequences and cache heads.
-static long long kv4_tasks(const Kv4Dims &dm, int max_new) {
+// Row tiles of a sequence and head (an upper bound: it may have fewer new
+// tokens than max_new), and over all sequences and heads.
+static long long kv4_row_tiles(const Kv4Dims &dm, int max_new) {
   const long long rows = (long long)max_new * (dm.Hq / dm.Hkv);
-  return (rows + kAtRows - 1) / kAtRows * dm.Hkv * dm.B;
+  return (rows + kAtRows - 1) / kAtRows;
+}
+static long long kv4_tasks(const Kv4Dims &dm, int max_new) {
+  return kv4_row_tiles(dm, max_new) * dm.Hkv * dm.B;
 }
 
 // The most workgroups a sequence's keys are split over: as many as have two
@@ -673,8 +735,9 @@ int kv4_splits(const Kv4Dims &dm, int max_new, int window) {
   return n < 1 ? 1 : (int)n;
 }
 
+// A launch dimension holds fewer than 2^32 threads (512 to a workgroup).
 bool kv4_grid_ok(const Kv4Dims &dm, int max_new, int window) {
-  return kv4_tasks(dm, max_new) * kAtRows * (dm.D / 32) * kv4_splits(dm, max_new, window) < (1ll << 31);
+  return kv4_row_tiles(dm, max_new) * kv4_splits(dm, max_new, window) < (1ll << 23);
 }
 
 size_t kv4_attention_ws(const Kv4Dims &dm, int max_new, int window) {
@@ -683,23 +746,32 @@ size_t kv4_attention_ws(const Kv4Dims &dm, int max_new, int window) {
   return (size_t)kv4_tasks(dm, max_new) * splits * kAtRows * (dm.D + 2) * sizeof(float);
 }
 
+template <int D, int W>
+static hipError_t launch_main(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
+                              const Kv4Attn &at, int splits, float *part, hipStream_t s) {
+  if constexpr (at_lds_bytes<D, W>() > 64 * 1024) {  // needs an opt-in, once per process
+    static const hipError_t st =
+        hipFuncSetAttribute((const void *)kv4_attention_kernel<D, W>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, at_lds_bytes<D, W>());
+    if (st != hipSuccess) return st;
+  }
+  const dim3 grid((unsigned)(kv4_row_tiles(dm, at.max_new) * splits), dm.Hkv, dm.B);
+  kv4_attention_kernel<D, W><<<grid, W * kWave, at_lds_bytes<D, W>(), s>>>(dm, kc, vc, bt, at, splits, part);
+  return hipGetLastError();
+}
+
 template <int D>
 static hipError_t launch(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
                          const Kv4Attn &at, float *part, hipStream_t s) {
-  const long long tasks = kv4_tasks(dm, at.max_new);
   const int splits = kv4_splits(dm, at.max_new, at.window);
-  if constexpr (at_lds_bytes<D>() > 64 * 1024) {  // needs an opt-in, once per process
-    static const hipError_t st = hipFuncSetAttribute(
-        (const void *)kv4_attention_kernel<D>, hipFuncAttributeMaxDynamicSharedMemorySize, at_lds_bytes<D>());
-    if (st != hipSuccess) return st;
-  }
-  kv4_attention_kernel<D><<<(int)(tasks * splits), kAtWaves * kWave, at_lds_bytes<D>(), s>>>(
-      dm, kc, vc, bt, at, splits, part);
-  if (const hipError_t e = hipGetLastError()) return e;
+  const hipError_t e = splits > 1 ? launch_main<D, 4>(dm, kc, vc, bt, at, splits, part, s)
+                                  : launch_main<D, 8>(dm, kc, vc, bt, at, splits, part, s);
+  if (e != hipSuccess || splits == 1) return e;
+  const unsigned rows = (unsigned)(kv4_row_tiles(dm, at.max_new) * kAtRows);
   if (splits > 16)
-    kv4_join_kernel<D, 32><<<(int)(tasks * kAtRows * (D / 32)), 256, 0, s>>>(dm, bt, at, splits, tasks, part);
-  else if (splits > 1)
-    kv4_join_kernel<D, D><<<(int)(tasks * kAtRows), 256, 0, s>>>(dm, bt, at, splits, tasks, part);
+    kv4_join_kernel<D, 32><<<dim3(rows * (D / 32), dm.Hkv, dm.B), 256, 0, s>>>(dm, bt, at, splits, part);
+  else
+    kv4_join_kernel<D, D><<<dim3(rows, dm.Hkv, dm.B), 256, 0, s>>>(dm, bt, at, splits, part);
   return hipGetLastError();
 }
 
