@@ -471,46 +471,100 @@ constexpr int at_lds_bytes() {
   return W * kStages * Ring<D>::kStage;
 }
 
-// Tiles a workgroup takes at least where keys are split, and the workgroups a
-// call is spread over: two rounds of the 256 CUs.
+// Splitting a sequence's keys over workgroups of 4 wavefronts: at least
+// kMinTiles tiles each (4 a wavefront), and no more workgroups than the card's
+// 256 CUs hold at a time. A workgroup too many runs alone after the others: 516
+// instead of 512 took a batch of 64 mixed sequences from 33 to 57 us.
 constexpr int kMinTiles = 16;
-constexpr int kTargetBlocks = 512;
+// Workgroups of 4 wavefronts a CU holds: wavefronts a SIMD by their registers
+// (216, 130 and 90; a 4-wavefront limit at D = 128 spills a pointer of the loop,
+// and its reload waits for the DMA in flight).
+template <int D>
+constexpr int at_blocks() { return D == 256 ? 2 : D == 128 ? 3 : 5; }
+template <int D>
+constexpr int at_slots() { return 256 * at_blocks<D>(); }
 // Batches up to this size spread their keys evenly over the workgroups (the
 // lengths are on the device, so each wavefront adds them up, 64 at a time);
 // larger ones have enough sequences to fill the card with.
 constexpr int kEvenMaxB = 256;
 
 // Tiles a workgroup takes of a sequence, so that all workgroups of the call
-// have about the same (kv4_share raises it where `splits` are too few).
+// have about the same and all fit the card: sum ceil(n_b / per) <= total / per +
+// tasks. (kv4_share raises it where `splits` are too few.)
+template <int D>
 __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Attn &at) {
   if (dm.B > kEvenMaxB) return kMinTiles;
   const int lane = threadIdx.x & (kWave - 1), G = dm.Hq / dm.Hkv;
-  float total = 0.f;  // tiles of all tasks; a rough figure will do
+  const int cap = (int)kv4_capacity(dm);
+  float total = 0.f, tasks = 0.f;  // rough figures will do
   for (int b = lane; b < dm.B; b += kWave) {
-    const Kv4Span sp = kv4_span(bt.cu[b], bt.cu[b + 1], bt.len[b], bt.T);
-    const int n = min(sp.n, at.max_new);
-    if (n == 0) continue;
-    const Kv4Range r = kv4_range(dm, sp.first, sp.first + n - 1, sp.len, at.causal, at.window);
-    total += (float)kv4_tiles(r) * (float)((n * G + kAtRows - 1) / kAtRows);
+    const int n = min(min(max(bt.cu[b + 1], 0), bt.T) - min(max(bt.cu[b], 0), bt.T), at.max_new);
+    float keys = (float)min(max(bt.len[b], 0), cap);
+    if (at.window > 0) keys = fminf(keys, (float)at.window + (float)n);
+    const float tiles = n > 0 ? ceilf((float)n * G * (1.0f / kAtRows)) : 0.f;
+    total += tiles * (keys * (1.0f / kKvTile) + 1.0f);
+    tasks += tiles;
   }
   total = wave_sum_dpp(total) * dm.Hkv;
-  return max(kMinTiles, (int)fminf(ceilf(total * (1.0f / kTargetBlocks)), 67108864.0f));
+  tasks = wave_sum_dpp(tasks) * dm.Hkv;
+  const float room = fmaxf(at_slots<D>() - tasks, at_slots<D>() / 4);
+  return max(kMinTiles, (int)fminf(ceilf(total / room), 67108864.0f));
 }
 
-// Grid: x = row tile * splits + split, y = cache head, z = sequence.
-template <int D, int W>
-__global__ __launch_bounds__(W *kWave, D == 256 ? 2 : 4) void kv4_attention_kernel(Kv4Dims dm, Kv4Plane kc, Kv4Plane vc,
-                                                                    Kv4Batch bt, Kv4Attn at, int splits,
-                                                                    float *__restrict__ part) {
-  constexpr int NG = D / kGroup;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ float sm[W][kAtRows], sl[W][kAtRows];
-  int tile_i = blockIdx.x, split = 0;
-  if (splits > 1) {
-    tile_i = (int)gridDim.x == splits ? 0 : (int)blockIdx.x / splits;
-    split = blockIdx.x - tile_i * splits;
+// Inclusive sum over the wavefront's lanes (six DPP steps).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);  // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
+}
+
+// Work item `item` of a call whose sequences have one row tile each: the
+// sequences in order, each with its heads and their splits. Returns false past
+// the last. Listing only the splits that have keys keeps the workgroups of a
+// ragged batch evenly spread: with a grid of all possible splits, most of them
+// empty, 128 of 442 waited for a free CU while others idled (49 us, not 33).
+struct Item {
+  int seq, head, split;
+};
+
+__device__ __forceinline__ bool work_item(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Attn &at, int per,
+                                          int splits, int item, Item &it) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int b0 = 0; b0 < dm.B; b0 += kWave) {
+    const int b = min(b0 + lane, dm.B - 1);
+    const Kv4Span sp = kv4_span(bt.cu[b], bt.cu[b + 1], bt.len[b], bt.T);
+    const int n = min(sp.n, at.max_new);
+    const Kv4Range r = kv4_range(dm, sp.first, sp.first + max(n, 1) - 1, sp.len, at.causal, at.window);
+    const int used = b0 + lane < dm.B && n > 0 ? kv4_share(r, per, splits, 0).used : 0;
+    const int upto = wave_scan(used * dm.Hkv);
+    const uint64_t after = __builtin_amdgcn_ballot_w64(upto > item);
+    if (after != 0) {
+      const int w = __builtin_ctzll(after);
+      const int u = __builtin_amdgcn_readlane(used, w);
+      const int at_ = item - (__builtin_amdgcn_readlane(upto, w) - u * dm.Hkv);
+      it.seq = b0 + w;
+      it.head = at_ / u;
+      it.split = at_ - it.head * u;
+      return true;
+    }
+    item -= __builtin_amdgcn_readlane(upto, kWave - 1);
   }
-  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z);
+  return false;
+}
+
+// One row tile of a sequence and head (tile_i of `tiles`), and one split of its keys.
+template <int D, int W>
+__device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
+                                            const Kv4Batch &bt, const Kv4Attn &at, int seq, int head,
+                                            int tile_i, int tiles, int split, int splits, int per,
+                                            uint8_t *smem, float (*sm)[kAtRows], float (*sl)[kAtRows],
+                                            float *__restrict__ part) {
+  constexpr int NG = D / kGroup;
+  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, head, seq);
   if (rt.row0 >= rt.rows) return;
   const int G = dm.Hq / dm.Hkv;
   const int lane = threadIdx.x & (kWave - 1);
@@ -546,7 +600,7 @@ __global__ __launch_bounds__(W *kWave, D == 256 ? 2 : 4) void kv4_attention_kern
   const Kv4Range r0 = kv4_range(dm, rt.sp.first + tok0, rt.sp.first + tok0, rt.sp.len, at.causal, at.window);
   const Kv4Range r1 = kv4_range(dm, rt.sp.first + tok1, rt.sp.first + tok1, rt.sp.len, at.causal, at.window);
   const long long all0 = r1.lo, all1 = r0.hi;
-  const Kv4Share share = kv4_share(Kv4Range{r0.lo, r1.hi}, splits > 1 ? tiles_per_split(dm, bt, at) : 0, splits, split);
+  const Kv4Share share = kv4_share(Kv4Range{r0.lo, r1.hi}, per, splits, split);
   if (split >= share.used) return;
 
   const int32_t *table = bt.table + (long long)rt.seq * dm.max_pages;
@@ -633,7 +687,7 @@ __global__ __launch_bounds__(W *kWave, D == 256 ? 2 : 4) void kv4_attention_kern
   }
   __syncthreads();
   constexpr int kThreadsRow = D / 4;
-  const long long task = ((long long)blockIdx.z * dm.Hkv + blockIdx.y) * (gridDim.x / splits) + tile_i;
+  const long long task = ((long long)seq * dm.Hkv + head) * tiles + tile_i;
   for (int r = threadIdx.x / kThreadsRow; r < kAtRows && rt.row0 + r < rt.rows; r += W * kWave / kThreadsRow) {
     const int c = (threadIdx.x % kThreadsRow) * 4;
     float mr = kNegInf, l = 0.f;
@@ -651,12 +705,39 @@ __global__ __launch_bounds__(W *kWave, D == 256 ? 2 : 4) void kv4_attention_kern
       const long long pr = (task * splits + split) * kAtRows + r;
       *(float4 *)(part + pr * D + c) = o;
       if (c == 0)
-        *(float2 *)(part + (long long)gridDim.x * gridDim.y * gridDim.z * kAtRows * D + pr * 2) = make_float2(mr, l);
+        *(float2 *)(part + (long long)dm.B * dm.Hkv * tiles * splits * kAtRows * D + pr * 2) = make_float2(mr, l);
     } else {
       const int x = r + in0, i = tok0 + x / G, h = rt.head * G + x % G;
       store_row(dm, at, rt.sp.begin + i, h, c, l, o);
     }
   }
+}
+
+// Grid: x = row tile * splits + split, y = cache head, z = sequence; or, where
+// keys are split and a sequence has one row tile (flat), x = work items.
+template <int D, int W>
+__global__ __launch_bounds__(W *kWave, at_blocks<D>()) void kv4_attention_kernel(Kv4Dims dm, Kv4Plane kc, Kv4Plane vc,
+                                                                    Kv4Batch bt, Kv4Attn at, int splits,
+                                                                    bool flat, float *__restrict__ part) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ float sm[W][kAtRows], sl[W][kAtRows];
+  const int per = splits > 1 ? tiles_per_split<D>(dm, bt, at) : 0;
+  int seq = blockIdx.z, head = blockIdx.y, tile_i = blockIdx.x, tiles = gridDim.x, split = 0;
+  if (flat) {
+    // there are never more items than workgroups: a task has at most `splits`
+    Item it;
+    if (!work_item(dm, bt, at, per, splits, blockIdx.x, it)) return;
+    seq = it.seq;
+    head = it.head;
+    split = it.split;
+    tile_i = 0;
+    tiles = 1;
+  } else if (splits > 1) {
+    tiles = gridDim.x / splits;
+    tile_i = blockIdx.x / splits;
+    split = blockIdx.x - tile_i * splits;
+  }
+  attend_rows<D, W>(dm, kc, vc, bt, at, seq, head, tile_i, tiles, split, splits, per, smem, sm, sl, part);
 }
 
 // Joins the splits' partial results: one workgroup per row of a task and C of
@@ -675,7 +756,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
   const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z);
   if (rt.row0 + r >= rt.rows) return;
   const Kv4Range range = tile_range(dm, rt, at.causal, at.window);
-  const int used = kv4_share(range, tiles_per_split(dm, bt, at), splits, 0).used;
+  const int used = kv4_share(range, tiles_per_split<D>(dm, bt, at), splits, 0).used;
   if (used <= 1) return;
   const float *ml = part + tasks * splits * kAtRows * D;
   const long long pr0 = task * splits * kAtRows + r;
@@ -722,15 +803,16 @@ static long long kv4_tasks(const Kv4Dims &dm, int max_new) {
   return kv4_row_tiles(dm, max_new) * dm.Hkv * dm.B;
 }
 
-// The most workgroups a sequence's keys are split over: as many as have two
-// tiles a wavefront (of the table's width: the host does not know the
-// lengths), and no more than twice the target over all tasks.
+// The most workgroups a sequence's keys are split over: as many as have
+// kMinTiles each (of the table's width: the host does not know the lengths),
+// and no more than twice the card's slots over all tasks.
 int kv4_splits(const Kv4Dims &dm, int max_new, int window) {
   const long long tasks = kv4_tasks(dm, max_new);
+  const int slots = dm.D == 256 ? at_slots<256>() : dm.D == 128 ? at_slots<128>() : at_slots<64>();
   long long keys = kv4_capacity(dm);
   if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
   const long long most = keys / (kKvTile * kMinTiles);
-  long long n = (2 * kTargetBlocks) / tasks;
+  long long n = 2 * slots / tasks;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
 }
@@ -755,8 +837,10 @@ static hipError_t launch_main(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pl
                             hipFuncAttributeMaxDynamicSharedMemorySize, at_lds_bytes<D, W>());
     if (st != hipSuccess) return st;
   }
-  const dim3 grid((unsigned)(kv4_row_tiles(dm, at.max_new) * splits), dm.Hkv, dm.B);
-  kv4_attention_kernel<D, W><<<grid, W * kWave, at_lds_bytes<D, W>(), s>>>(dm, kc, vc, bt, at, splits, part);
+  const long long tiles = kv4_row_tiles(dm, at.max_new);
+  const bool flat = splits > 1 && tiles == 1 && dm.B <= kEvenMaxB;
+  const dim3 grid = flat ? dim3((unsigned)(kv4_tasks(dm, at.max_new) * splits)) : dim3((unsigned)(tiles * splits), dm.Hkv, dm.B);
+  kv4_attention_kernel<D, W><<<grid, W * kWave, at_lds_bytes<D, W>(), s>>>(dm, kc, vc, bt, at, splits, flat, part);
   return hipGetLastError();
 }
 
@@ -764,8 +848,11 @@ template <int D>
 static hipError_t launch(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
                          const Kv4Attn &at, float *part, hipStream_t s) {
   const int splits = kv4_splits(dm, at.max_new, at.window);
-  const hipError_t e = splits > 1 ? launch_main<D, 4>(dm, kc, vc, bt, at, splits, part, s)
-                                  : launch_main<D, 8>(dm, kc, vc, bt, at, splits, part, s);
+  // Eight wavefronts where every workgroup has a CU to itself (a short sequence
+  // ends sooner), four where there are more of them or keys are split.
+  const bool few = splits == 1 && kv4_tasks(dm, at.max_new) <= 256;
+  const hipError_t e = few ? launch_main<D, 8>(dm, kc, vc, bt, at, splits, part, s)
+                           : launch_main<D, 4>(dm, kc, vc, bt, at, splits, part, s);
   if (e != hipSuccess || splits == 1) return e;
   const unsigned rows = (unsigned)(kv4_row_tiles(dm, at.max_new) * kAtRows);
   if (splits > 16)
