@@ -17,25 +17,41 @@ namespace moe {
 constexpr int kLnWaves = 8;
 constexpr int kLnRows = 16;
 
-__device__ __forceinline__ float activate(float z, int act) {
-  if (act == kActRelu) return z > 0.f ? z : (z == z ? 0.f : z);
-  if (act == kActSilu) return z / (1.0f + expf(-z));
-  if (act == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? z : (z == z ? 0.f : z);
+  if constexpr (ACT == kActSilu) return z / (1.0f + expf(-z));
+  if constexpr (ACT == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
   return z;
 }
 
-// Bias, activation and residual of one output, and its store.
-template <bool F32>
-__device__ __forceinline__ void linear_store(const LinearArgs &a, int t, int n, float z) {
-  if (a.bias) z += bf16_to_f32(a.bias[n]);
-  z = activate(z, a.act);
-  if (F32) {
-    if (a.residual) z += ((const float *)a.residual)[t * a.r_stride + n];
-    ((float *)a.y)[t * a.y_stride + n] = z;
-  } else {
-    if (a.residual) z += bf16_to_f32(((const uint16_t *)a.residual)[t * a.r_stride + n]);
-    ((uint16_t *)a.y)[t * a.y_stride + n] = to_bf16(z);
+// Calls f with the activation as a compile-time constant.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    default: f(std::integral_constant<int, kActNone>{}); break;
   }
+}
+
+template <bool F32>
+__device__ __forceinline__ float load_residual(const LinearArgs &a, int t, int n) {
+  if (!a.residual) return 0.f;
+  if (F32) return ((const float *)a.residual)[t * a.r_stride + n];
+  return bf16_to_f32(((const uint16_t *)a.residual)[t * a.r_stride + n]);
+}
+
+// y = act(z + bias) + residual, rounded once.
+template <int ACT, bool F32>
+__device__ __forceinline__ void store_output(const LinearArgs &a, int t, int n, float z, float bias,
+                                             float residual) {
+  z = activate<ACT>(z + bias) + residual;
+  if (F32)
+    ((float *)a.y)[t * a.y_stride + n] = z;
+  else
+    ((uint16_t *)a.y)[t * a.y_stride + n] = to_bf16(z);
 }
 
 template <int NT, bool F32>
@@ -76,6 +92,7 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
         x[j][i][1] = *(const uint4 *)(xp[i] + g * kGroup + 8);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // all loads first
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (g0 + j * kLnWaves >= ng) break;
@@ -94,14 +111,17 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
 #pragma unroll
     for (int r = 0; r < 4; ++r) part[wave][i * 16 + (lane & 15)][(lane >> 4) * 4 + r] = acc[i][r];
   __syncthreads();
-  for (int e = threadIdx.x; e < 16 * NT * kLnRows; e += kLnWaves * kWave) {
-    const int t = e / kLnRows, n = e % kLnRows;
-    if (t0 + t >= a.T || n0 + n >= a.rows) continue;
-    float z = 0.f;
+  with_act(a.act, [&](auto act) {
+    for (int e = threadIdx.x; e < 16 * NT * kLnRows; e += kLnWaves * kWave) {
+      const int t = e / kLnRows, n = e % kLnRows;
+      if (t0 + t >= a.T || n0 + n >= a.rows) continue;
+      float z = 0.f;
 #pragma unroll
-    for (int w = 0; w < kLnWaves; ++w) z += part[w][t][n];
-    linear_store<F32>(a, t0 + t, n0 + n, z);
-  }
+      for (int w = 0; w < kLnWaves; ++w) z += part[w][t][n];
+      store_output<act.value, F32>(a, t0 + t, n0 + n, z, a.bias ? bf16_to_f32(a.bias[n0 + n]) : 0.f,
+                                   load_residual<F32>(a, t0 + t, n0 + n));
+    }
+  });
 }
 
 // ------------------------------------------------------------------ large batches
@@ -234,19 +254,25 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
       bv = make_uint4(b[0], b[1], b[2], b[3]);
     }
   };
-  bool fast = true;  // every group of the table takes the fast dequantisation
   auto fill = [&]() {
     const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
-    bool ok = true;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t w0 = (s[i] & 0xFFFFu) | (b[i] << 16), w1 = (s[i] >> 16) | (b[i] & 0xFFFF0000u);
-      table[(2 * i) * kBgRows + lane] = w0;
-      table[(2 * i + 1) * kBgRows + lane] = w1;
-      ok &= (int)dq_fast_ok(w0) & (int)dq_fast_ok(w1);
+      table[(2 * i) * kBgRows + lane] = (s[i] & 0xFFFFu) | (b[i] << 16);
+      table[(2 * i + 1) * kBgRows + lane] = (s[i] >> 16) | (b[i] & 0xFFFF0000u);
     }
-    fast = __builtin_amdgcn_ballot_w64(!ok) == 0;
   };
+  // does every group of the wavefront's rows take the fast dequantisation?
+  bool ok = true;
+#pragma unroll 4
+  for (int g0 = 0; g0 < ng; g0 += kBgChunk) {
+    fetch(g0);
+    const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      ok &= (int)dq_fast_ok((s[i] & 0xFFFFu) | (b[i] << 16)) & (int)dq_fast_ok((s[i] >> 16) | (b[i] & 0xFFFF0000u));
+  }
+  const bool fast = __builtin_amdgcn_ballot_w64(!ok) == 0;
 
   fetch(0);
   fill();
@@ -259,59 +285,90 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
   const DqRegs dk = dq_regs();
   const int lrow = (lane & 31) * 128, lx = (lane & 7) ^ ((lane >> 3) & 1), lh = 4 * (lane >> 5);
 
+  // one K step; the weights of a slice of 16 columns are rebuilt, and its
+  // activation fragments read, while the slice before it is multiplied
   int slot = 0;
-  for (int kt = 0; kt < ng; ++kt, slot = slot == kBgStages - 1 ? 0 : slot + 1) {
+  auto step = [&](auto fast_tag, int kt) {
+    constexpr bool FAST = decltype(fast_tag)::value;
     // stage kt has landed (only the DMA of stage kt + 1 may still be in flight);
     // the barrier also tells that every wavefront is done with stage kt - 1
     if (kt + 1 < ng)
       MOE_LN_WAIT_VMCNT(kBgLoads);
     else
       MOE_LN_WAIT_VMCNT(0);
-    asm volatile("" ::: "memory");
-    if (kt % kBgChunk == 0 && kt > 0) fill();
     lds_barrier();
     asm volatile("" ::: "memory");
     if (kt % kBgChunk == kBgChunk - 1 && kt + 1 < ng) fetch(kt + 1);
     if (kt + 2 < ng) dma(kt + 2, slot == 0 ? 2 : slot - 1);
-    const uint8_t *xs = smem + slot * kBgX;
-    uint4 c[2];
-    uint32_t sb[2];
+    const uint8_t *xs = smem + slot * kBgX + lrow;
+    uint32_t word[2][4];
+    DqGroup q[2];
+    float sc[2], bi[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      c[b] = *(const uint4 *)(cring + slot * kBgCodes + b * 1024 + lane * 16);
-      sb[b] = table[(kt % kBgChunk) * kBgRows + b * 32 + (lane & 31)];
-    }
-    // the step's weights; only this differs between the two dequantisations, so
-    // that the accumulators do not pass through a branch
-    bf16x8_t w[4][2];
-    if (fast) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const DqGroup q = dq_consts(sb[b]);
-        const uint32_t word[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) w[ks][b] = __builtin_bit_cast(bf16x8_t, dequant8_fast(word[ks], q, dk));
-      }
-    } else {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const float sc = bf16_to_f32(sb[b] & 0xFFFFu), bi = bf16_to_f32(sb[b] >> 16);
-        const uint32_t word[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) w[ks][b] = __builtin_bit_cast(bf16x8_t, dequant8(word[ks], sc, bi));
+      const uint4 c = *(const uint4 *)(cring + slot * kBgCodes + b * 1024 + lane * 16);
+      word[b][0] = c.x, word[b][1] = c.y, word[b][2] = c.z, word[b][3] = c.w;
+      const uint32_t sb = table[(kt % kBgChunk) * kBgRows + b * 32 + (lane & 31)];
+      if (FAST) {
+        q[b] = dq_consts(sb);
+      } else {
+        sc[b] = bf16_to_f32(sb & 0xFFFFu);
+        bi[b] = bf16_to_f32(sb >> 16);
       }
     }
+    auto weights = [&](int ks, bf16x8_t (&w)[2]) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint4 v = FAST ? dequant8_fast(word[b][ks], q[b], dk) : dequant8(word[b][ks], sc[b], bi[b]);
+        w[b] = __builtin_bit_cast(bf16x8_t, v);
+      }
+    };
+    auto fragments = [&](int ks, bf16x8_t (&x)[4]) {
+      const uint8_t *p = xs + (((lh + ks) ^ lx) << 4);
+#pragma unroll
+      for (int rb = 0; rb < 4; ++rb) x[rb] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(p + rb * 4096));
+    };
+    bf16x8_t w[2][2], x[2][4];
+    fragments(0, x[0]);
+    weights(0, w[0]);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      const uint8_t *p = xs + lrow + (((lh + ks) ^ lx) << 4);
-#pragma unroll
-      for (int rb = 0; rb < 4; ++rb) {
-        const bf16x8_t x = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(p + rb * 4096));
-        acc[rb][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, w[ks][0], acc[rb][0], 0, 0, 0);
-        acc[rb][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, w[ks][1], acc[rb][1], 0, 0, 0);
+      if (ks < 3) {
+        fragments(ks + 1, x[(ks + 1) & 1]);
+        weights(ks + 1, w[(ks + 1) & 1]);
       }
+#pragma unroll
+      for (int rb = 0; rb < 4; ++rb)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          acc[rb][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[ks & 1][rb], w[ks & 1][b], acc[rb][b], 0, 0, 0);
+      if (FAST && ks < 3) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);  // the next fragments' reads
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA (32 cycles)
+          __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);  // five VALU operations (20)
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-  }
+    slot = slot == kBgStages - 1 ? 0 : slot + 1;
+  };
+  // two whole loops, so that the accumulators meet no branch inside
+  auto run = [&](auto fast_tag) {
+    for (int k0 = 0; k0 < ng; k0 += kBgChunk) {
+      if (k0 > 0) {
+        MOE_LN_WAIT_VMCNT(0);
+        fill();
+      }
+      const int k1 = min(k0 + kBgChunk, ng);
+      for (int kt = k0; kt < k1; ++kt) step(fast_tag, kt);
+    }
+  };
+  if (fast)
+    run(std::true_type{});
+  else
+    run(std::false_type{});
 
   // Epilogue. The sums go through the wavefront's quarter of the LDS, 64 tokens
   // by 64 rows at a time, and leave a token's 64 outputs to a wavefront store.
@@ -332,8 +389,12 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
               acc[half * 2 + rb][b][r];
     const int tb = t0 + half * 64, te = min(64, a.T - tb);
     if (n < a.rows) {
+      const float bias = a.bias ? bf16_to_f32(a.bias[n]) : 0.f;
+      with_act(a.act, [&](auto act) {
 #pragma unroll 4
-      for (int t = 0; t < te; ++t) linear_store<F32>(a, tb + t, n, ep[t * 64 + lane]);
+        for (int t = 0; t < te; ++t)
+          store_output<act.value, F32>(a, tb + t, n, ep[t * 64 + lane], bias, load_residual<F32>(a, tb + t, n));
+      });
     }
   }
 }
