@@ -2,12 +2,13 @@
 //   y[t][n] = act(sum_c x[t][c] W[n][c] + bias[n]) + residual[t][n],
 //   W = bf16(fp32(s q + b)), products of bf16 values exact, sums in fp32.
 //
-// Small batches are bound by the weights' bytes. One workgroup takes 16
-// weight rows and 16, 32 or 64 tokens; its 8 wavefronts take the 64-column
-// groups in turn, rebuild them in registers as the A operand of 16x16x32
-// MFMAs (lane l: row l % 16, columns 16 (l / 16) .. +15 of the group) against
-// the tokens' activations read straight from memory, and join their sums
-// through LDS, where the epilogue runs.
+// Small batches are bound by the weights' bytes, middle ones by how often the
+// activations are read. One workgroup takes 16 RB weight rows and 16 NT tokens;
+// its 8 wavefronts take the 64-column groups in turn, rebuild the rows' weights
+// in registers as the A operand of 16x16x32 MFMAs (lane l: row l % 16, columns
+// 16 (l / 16) .. +15 of the group) against the tokens' activations read
+// straight from memory, and join their sums through LDS, where the epilogue
+// runs.
 #include <type_traits>
 
 #include "moe_linear.h"
@@ -15,7 +16,6 @@
 namespace moe {
 
 constexpr int kLnWaves = 8;
-constexpr int kLnRows = 16;
 
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
@@ -54,38 +54,80 @@ __device__ __forceinline__ void store_output(const LinearArgs &a, int t, int n, 
     ((uint16_t *)a.y)[t * a.y_stride + n] = to_bf16(z);
 }
 
-template <int NT, bool F32>
+// The same for outputs n .. n + 7, with wide accesses.
+template <int ACT, bool F32>
+__device__ __forceinline__ void store_outputs8(const LinearArgs &a, int t, int n, const float (&z)[8],
+                                               const float (&bias)[8]) {
+  float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, y[8];
+  if (a.residual) {
+    if (F32) {
+      const float4 *p = (const float4 *)((const float *)a.residual + t * a.r_stride + n);
+      const float4 u = p[0], v = p[1];
+      r[0] = u.x, r[1] = u.y, r[2] = u.z, r[3] = u.w, r[4] = v.x, r[5] = v.y, r[6] = v.z, r[7] = v.w;
+    } else {
+      const uint4 u = *(const uint4 *)((const uint16_t *)a.residual + t * a.r_stride + n);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+        r[2 * i + 1] = bf16_to_f32(w[i] >> 16);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = activate<ACT>(z[i] + bias[i]) + r[i];
+  if (F32) {
+    float4 *p = (float4 *)((float *)a.y + t * a.y_stride + n);
+    p[0] = make_float4(y[0], y[1], y[2], y[3]);
+    p[1] = make_float4(y[4], y[5], y[6], y[7]);
+  } else {
+    *(uint4 *)((uint16_t *)a.y + t * a.y_stride + n) =
+        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+  }
+}
+
+template <int RB, int NT, bool F32>
 __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a) {
-  __shared__ float part[kLnWaves][16 * NT][kLnRows + 1];
-  const int blocks = (a.rows + kLnRows - 1) / kLnRows;
-  const int n0 = (blockIdx.x % blocks) * kLnRows, t0 = (blockIdx.x / blocks) * 16 * NT;
+  constexpr int kRows = 16 * RB, kTokens = 16 * NT;
+  // groups whose loads are in flight together (registers: 8 a token tile each)
+  constexpr int kBatch = NT >= 3 ? 2 : 4;
+  // one 16-row block of the sums at a time
+  __shared__ float part[kLnWaves][kTokens][16 + 1];
+  const int blocks = (a.rows + kRows - 1) / kRows;
+  const int n0 = (blockIdx.x % blocks) * kRows, t0 = (blockIdx.x / blocks) * kTokens;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c16 = (lane >> 4) * 16;
   const int ng = a.cols / kGroup;
-  const long long wrow = min(n0 + (lane & 15), a.rows - 1);
-  const uint8_t *codes = a.w.codes + wrow * (a.cols / 2) + c16 / 2;
-  const uint16_t *sp = a.w.scales + wrow * ng, *bp = a.w.biases + wrow * ng;
-  const uint16_t *xp[NT];
-  f32x4_t acc[NT];
+  const uint8_t *codes[RB];
+  const uint16_t *sp[RB], *bp[RB], *xp[NT];
+  f32x4_t acc[RB][NT];
+#pragma unroll
+  for (int k = 0; k < RB; ++k) {
+    const long long wrow = min(n0 + 16 * k + (lane & 15), a.rows - 1);
+    codes[k] = a.w.codes + wrow * (a.cols / 2) + c16 / 2;
+    sp[k] = a.w.scales + wrow * ng;
+    bp[k] = a.w.biases + wrow * ng;
+  }
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int t = min(t0 + i * 16 + (lane & 15), a.T - 1);
-    xp[i] = a.x + t * a.x_stride + c16;
-    acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    xp[i] = a.x + min(t0 + i * 16 + (lane & 15), a.T - 1) * a.x_stride + c16;
+#pragma unroll
+    for (int k = 0; k < RB; ++k) acc[k][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-  // four groups at a time: their loads are in flight together
-  constexpr int kBatch = 4;
   for (int g0 = wave; g0 < ng; g0 += kLnWaves * kBatch) {
-    uint2 c[kBatch];
-    uint32_t s[kBatch], b[kBatch];
+    uint2 c[kBatch][RB];
+    uint32_t s[kBatch][RB], b[kBatch][RB];
     uint4 x[kBatch][NT][2];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int g = min(g0 + j * kLnWaves, ng - 1);
-      c[j] = *(const uint2 *)(codes + g * 32);
-      s[j] = sp[g];
-      b[j] = bp[g];
+#pragma unroll
+      for (int k = 0; k < RB; ++k) {
+        c[j][k] = *(const uint2 *)(codes[k] + g * 32);
+        s[j][k] = sp[k][g];
+        b[j][k] = bp[k][g];
+      }
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         x[j][i][0] = *(const uint4 *)(xp[i] + g * kGroup);
@@ -96,32 +138,39 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (g0 + j * kLnWaves >= ng) break;
-      const float sc = bf16_to_f32(s[j]), bi = bf16_to_f32(b[j]);
-      const bf16x8_t w0 = __builtin_bit_cast(bf16x8_t, dequant8(c[j].x, sc, bi));
-      const bf16x8_t w1 = __builtin_bit_cast(bf16x8_t, dequant8(c[j].y, sc, bi));
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8_t, x[j][i][0]), acc[i], 0, 0, 0);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8_t, x[j][i][1]), acc[i], 0, 0, 0);
+      for (int k = 0; k < RB; ++k) {
+        const float sc = bf16_to_f32(s[j][k]), bi = bf16_to_f32(b[j][k]);
+        const bf16x8_t w0 = __builtin_bit_cast(bf16x8_t, dequant8(c[j][k].x, sc, bi));
+        const bf16x8_t w1 = __builtin_bit_cast(bf16x8_t, dequant8(c[j][k].y, sc, bi));
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          acc[k][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8_t, x[j][i][0]), acc[k][i], 0, 0, 0);
+          acc[k][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8_t, x[j][i][1]), acc[k][i], 0, 0, 0);
+        }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int k = 0; k < RB; ++k) {
+    if (k > 0) __syncthreads();  // the block before has been added up
 #pragma unroll
-    for (int r = 0; r < 4; ++r) part[wave][i * 16 + (lane & 15)][(lane >> 4) * 4 + r] = acc[i][r];
-  __syncthreads();
-  with_act(a.act, [&](auto act) {
-    for (int e = threadIdx.x; e < 16 * NT * kLnRows; e += kLnWaves * kWave) {
-      const int t = e / kLnRows, n = e % kLnRows;
-      if (t0 + t >= a.T || n0 + n >= a.rows) continue;
-      float z = 0.f;
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int w = 0; w < kLnWaves; ++w) z += part[w][t][n];
-      store_output<act.value, F32>(a, t0 + t, n0 + n, z, a.bias ? bf16_to_f32(a.bias[n0 + n]) : 0.f,
-                                   load_residual<F32>(a, t0 + t, n0 + n));
-    }
-  });
+      for (int r = 0; r < 4; ++r) part[wave][i * 16 + (lane & 15)][(lane >> 4) * 4 + r] = acc[k][i][r];
+    __syncthreads();
+    with_act(a.act, [&](auto act) {
+      for (int e = threadIdx.x; e < kTokens * 16; e += kLnWaves * kWave) {
+        const int t = t0 + e / 16, n = n0 + 16 * k + e % 16;
+        if (t >= a.T || n >= a.rows) continue;
+        const float bias = a.bias ? bf16_to_f32(a.bias[n]) : 0.f, res = load_residual<F32>(a, t, n);
+        float z = 0.f;
+#pragma unroll
+        for (int w = 0; w < kLnWaves; ++w) z += part[w][e / 16][e % 16];
+        store_output<act.value, F32>(a, t, n, z, bias, res);
+      }
+    });
+  }
 }
 
 // ------------------------------------------------------------------ large batches
@@ -226,11 +275,19 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
   uint8_t *cring = smem + kBgStages * kBgX + wave * 2048;  // this wavefront's part of a stage
   const uint32_t c_lds = ln_lds_address(cring);
   uint32_t *table = (uint32_t *)(smem + kBgStages * (kBgX + kBgCodes)) + wave * 64;
+  // third i of a stage's DMA: 4 instructions for activations, 2 for codes
+  auto dma_part = [&](int step, int slot, int i) {
+    if (i < 2) {
+      ln_dma(xr, x_off[2 * i], step * (kBgK * 2), x_lds + slot * kBgX + i * 8192);
+      ln_dma(xr, x_off[2 * i + 1], step * (kBgK * 2), x_lds + slot * kBgX + i * 8192 + 4096);
+    } else {
+      ln_dma(cr, c_off[0], step * (kBgK / 2), c_lds + slot * kBgCodes);
+      ln_dma(cr, c_off[1], step * (kBgK / 2), c_lds + slot * kBgCodes + 1024);
+    }
+  };
   auto dma = [&](int step, int slot) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ln_dma(xr, x_off[i], step * (kBgK * 2), x_lds + slot * kBgX + i * 4096);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) ln_dma(cr, c_off[b], step * (kBgK / 2), c_lds + slot * kBgCodes + b * 1024);
+    for (int i = 0; i < 3; ++i) dma_part(step, slot, i);
   };
 
   // scales and biases of 8 groups of row `lane` of the wavefront
@@ -262,6 +319,8 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
       table[(2 * i + 1) * kBgRows + lane] = (s[i] >> 16) | (b[i] & 0xFFFF0000u);
     }
   };
+  dma(0, 0);
+  if (ng > 1) dma(1, 1);
   // does every group of the wavefront's rows take the fast dequantisation?
   bool ok = true;
 #pragma unroll 4
@@ -276,8 +335,6 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
 
   fetch(0);
   fill();
-  dma(0, 0);
-  if (ng > 1) dma(1, 1);
 
   f32x16_t acc[4][2];
 #pragma unroll
@@ -299,7 +356,6 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
     lds_barrier();
     asm volatile("" ::: "memory");
     if (kt % kBgChunk == kBgChunk - 1 && kt + 1 < ng) fetch(kt + 1);
-    if (kt + 2 < ng) dma(kt + 2, slot == 0 ? 2 : slot - 1);
     const uint8_t *xs = smem + slot * kBgX + lrow;
     uint32_t word[2][4];
     DqGroup q[2];
@@ -351,6 +407,9 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
         }
       }
       __builtin_amdgcn_sched_barrier(0);
+      // a third of the DMA of stage kt + 2 behind each slice's MFMAs, whose time
+      // covers its issue
+      if (ks < 3 && kt + 2 < ng) dma_part(kt + 2, slot == 0 ? 2 : slot - 1, ks);
     }
     slot = slot == kBgStages - 1 ? 0 : slot + 1;
   };
@@ -376,7 +435,13 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
   // 8 (r / 4) + 4 (l / 32) + r % 4.
   lds_barrier();
   float *ep = (float *)(smem + wave * (64 * 64 * 4));
-  const int n = n0 + lane;
+  // lane l: outputs 8 (l % 8) .. +7 of token l / 8 (+ 8 a turn)
+  const int n = n0 + (lane & 7) * 8;
+  // 16-byte (bf16) and 32-byte (fp32) accesses where rows keep their alignment
+  const bool wide = n + 8 <= a.rows && a.y_stride % 8 == 0 && (!a.residual || a.r_stride % 8 == 0);
+  float bias[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias[i] = a.bias && n + i < a.rows ? bf16_to_f32(a.bias[n + i]) : 0.f;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -387,37 +452,50 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
         for (int r = 0; r < 16; ++r)
           ep[(rb * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * 64 + b * 32 + (lane & 31)] =
               acc[half * 2 + rb][b][r];
-    const int tb = t0 + half * 64, te = min(64, a.T - tb);
-    if (n < a.rows) {
-      const float bias = a.bias ? bf16_to_f32(a.bias[n]) : 0.f;
-      with_act(a.act, [&](auto act) {
-#pragma unroll 4
-        for (int t = 0; t < te; ++t)
-          store_output<act.value, F32>(a, tb + t, n, ep[t * 64 + lane], bias, load_residual<F32>(a, tb + t, n));
-      });
-    }
+    with_act(a.act, [&](auto act) {
+#pragma unroll 2
+      for (int i = 0; i < 8; ++i) {
+        const int tl = i * 8 + (lane >> 3), t = t0 + half * 64 + tl;
+        if (t >= a.T) continue;
+        const float4 z0 = *(const float4 *)(ep + tl * 64 + (lane & 7) * 8);
+        const float4 z1 = *(const float4 *)(ep + tl * 64 + (lane & 7) * 8 + 4);
+        const float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+        if (wide) {
+          store_outputs8<act.value, F32>(a, t, n, z, bias);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (n + j < a.rows) store_output<act.value, F32>(a, t, n + j, z[j], bias[j], load_residual<F32>(a, t, n + j));
+        }
+      }
+    });
   }
 }
 
-static long long linear_blocks(int T, int rows) {
-  return (long long)((rows + kLnRows - 1) / kLnRows) * ((T + 15) / 16);
-}
+// Tiles of the large-batch kernel from which it is the faster one.
+constexpr int kBgMinTiles = 128;
 
-// Below this many tokens the 16-row kernel is faster.
-constexpr int kBgMinT = 128;
+static long long bg_tiles(int T, int rows) {
+  return (long long)((T + kBgTokens - 1) / kBgTokens) * ((rows + kBgRows - 1) / kBgRows);
+}
 
 static bool tiles_fit(const LinearArgs &a) {
   // 32-bit byte offsets within a tile
-  return a.T >= kBgMinT && a.x_stride < (1 << 23) && a.cols < (1 << 23);
+  return bg_tiles(a.T, a.rows) >= kBgMinTiles && a.x_stride < (1 << 23) && a.cols < (1 << 23);
 }
 
-bool linear_grid_ok(int T, int rows) { return linear_blocks(T, rows) < (1ll << 23); }
+template <int RB, int NT>
+static long long ln_blocks(int T, int rows) {
+  return (long long)((rows + 16 * RB - 1) / (16 * RB)) * ((T + 16 * NT - 1) / (16 * NT));
+}
 
-template <int NT>
+// A launch dimension holds fewer than 2^32 threads (512 to a workgroup).
+bool linear_grid_ok(int T, int rows) { return ln_blocks<1, 1>(T, rows) < (1ll << 23); }
+
+template <int RB, int NT>
 static void launch(const LinearArgs &a, int dtype, hipStream_t s) {
-  const int grid = (int)((long long)((a.rows + kLnRows - 1) / kLnRows) * ((a.T + 16 * NT - 1) / (16 * NT)));
-  auto *kernel = dtype ? linear_kernel<NT, true> : linear_kernel<NT, false>;
-  kernel<<<grid, kLnWaves * kWave, 0, s>>>(a);
+  auto *kernel = dtype ? linear_kernel<RB, NT, true> : linear_kernel<RB, NT, false>;
+  kernel<<<(int)ln_blocks<RB, NT>(a.T, a.rows), kLnWaves * kWave, 0, s>>>(a);
 }
 
 static hipError_t launch_tiles(const LinearArgs &a, int dtype, hipStream_t s) {
@@ -430,19 +508,24 @@ static hipError_t launch_tiles(const LinearArgs &a, int dtype, hipStream_t s) {
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, kBgLds);
   }();
   if (st != hipSuccess) return st;
-  const int tiles = ((a.T + kBgTokens - 1) / kBgTokens) * ((a.rows + kBgRows - 1) / kBgRows);
-  kernel<<<(tiles + 7) / 8 * 8, kBgThreads, kBgLds, s>>>(a);
+  kernel<<<(int)((bg_tiles(a.T, a.rows) + 7) / 8 * 8), kBgThreads, kBgLds, s>>>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_linear(const LinearArgs &a, int dtype, hipStream_t s) {
   if (tiles_fit(a)) return launch_tiles(a, dtype, s);
   if (a.T <= 16)
-    launch<1>(a, dtype, s);
+    launch<1, 1>(a, dtype, s);
   else if (a.T <= 32)
-    launch<2>(a, dtype, s);
+    launch<1, 2>(a, dtype, s);
+  else if (a.T <= 48)
+    launch<1, 3>(a, dtype, s);
+  else if (ln_blocks<4, 4>(a.T, a.rows) >= 128)
+    launch<4, 4>(a, dtype, s);
+  else if (ln_blocks<2, 4>(a.T, a.rows) >= 128)
+    launch<2, 4>(a, dtype, s);
   else
-    launch<4>(a, dtype, s);
+    launch<1, 4>(a, dtype, s);
   return hipGetLastError();
 }
 
