@@ -464,9 +464,8 @@ moe_status moe_linear_w4(int32_t T, int32_t rows, int32_t cols, const uint16_t *
   if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_E_INVALID;
   MOE_TRY(check_dtype(dtype));
   if (cols % kGroup != 0 || (long long)rows * cols >= (1ll << 34)) return MOE_E_UNSUPPORTED;
-  if ((long long)T * rows >= (1ll << 40) || (long long)T * cols >= (1ll << 40)) return MOE_E_UNSUPPORTED;
+  if ((long long)T * rows >= (1ll << 36) || (long long)T * cols >= (1ll << 40)) return MOE_E_UNSUPPORTED;
   if (T == 0) return MOE_OK;
-  if (!linear_grid_ok(T, rows)) return MOE_E_UNSUPPORTED;
   MOE_TRY(check_stride(x_stride, cols));
   if (y_stride < rows || (residual != nullptr && residual_stride < rows)) return MOE_E_INVALID;
   MOE_TRY(check_ptr(x));
@@ -476,6 +475,7 @@ moe_status moe_linear_w4(int32_t T, int32_t rows, int32_t cols, const uint16_t *
   MOE_TRY(check_ptr(y));
   if (residual == y && residual_stride != y_stride) return MOE_E_INVALID;
   const LinearArgs a{T, rows, cols, x, x_stride, to_w4(*w), bias, act, residual, residual_stride, y, y_stride};
+  if (!linear_grid_ok(a)) return MOE_E_UNSUPPORTED;
   return hip_status(launch_linear(a, dtype, as_stream(stream)));
 }
 

@@ -20,7 +20,7 @@ struct LinearArgs {
   long long y_stride;
 };
 
-bool linear_grid_ok(int T, int rows);
+bool linear_grid_ok(const LinearArgs &a);
 // dtype of y and the residual: 0 bf16, 1 fp32
 hipError_t launch_linear(const LinearArgs &a, int dtype, hipStream_t s);
 

@@ -2,13 +2,12 @@
 //   y[t][n] = act(sum_c x[t][c] W[n][c] + bias[n]) + residual[t][n],
 //   W = bf16(fp32(s q + b)), products of bf16 values exact, sums in fp32.
 //
-// Small batches are bound by the weights' bytes, middle ones by how often the
-// activations are read. One workgroup takes 16 RB weight rows and 16 NT tokens;
-// its 8 wavefronts take the 64-column groups in turn, rebuild the rows' weights
-// in registers as the A operand of 16x16x32 MFMAs (lane l: row l % 16, columns
-// 16 (l / 16) .. +15 of the group) against the tokens' activations read
-// straight from memory, and join their sums through LDS, where the epilogue
-// runs.
+// Small batches are bound by the weights' bytes. One workgroup takes 16 weight
+// rows and 16 NT tokens; its 8 wavefronts take the 64-column groups in turn,
+// rebuild the rows' weights in registers as the A operand of 16x16x32 MFMAs
+// (lane l: row l % 16, columns 16 (l / 16) .. +15 of the group) against the
+// tokens' activations read straight from memory, and join their sums through
+// LDS, where the epilogue runs.
 #include <type_traits>
 
 #include "moe_linear.h"
@@ -86,48 +85,37 @@ __device__ __forceinline__ void store_outputs8(const LinearArgs &a, int t, int n
   }
 }
 
-template <int RB, int NT, bool F32>
+template <int NT, bool F32>
 __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a) {
-  constexpr int kRows = 16 * RB, kTokens = 16 * NT;
-  // groups whose loads are in flight together (registers: 8 a token tile each)
-  constexpr int kBatch = NT >= 3 ? 2 : 4;
-  // one 16-row block of the sums at a time
+  constexpr int kTokens = 16 * NT;
+  constexpr int kBatch = 4;  // groups whose loads are in flight together
   __shared__ float part[kLnWaves][kTokens][16 + 1];
-  const int blocks = (a.rows + kRows - 1) / kRows;
-  const int n0 = (blockIdx.x % blocks) * kRows, t0 = (blockIdx.x / blocks) * kTokens;
+  const int blocks = (a.rows + 15) / 16;
+  const int n0 = (blockIdx.x % blocks) * 16, t0 = (blockIdx.x / blocks) * kTokens;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c16 = (lane >> 4) * 16;
   const int ng = a.cols / kGroup;
-  const uint8_t *codes[RB];
-  const uint16_t *sp[RB], *bp[RB], *xp[NT];
-  f32x4_t acc[RB][NT];
-#pragma unroll
-  for (int k = 0; k < RB; ++k) {
-    const long long wrow = min(n0 + 16 * k + (lane & 15), a.rows - 1);
-    codes[k] = a.w.codes + wrow * (a.cols / 2) + c16 / 2;
-    sp[k] = a.w.scales + wrow * ng;
-    bp[k] = a.w.biases + wrow * ng;
-  }
+  const long long wrow = min(n0 + (lane & 15), a.rows - 1);
+  const uint8_t *codes = a.w.codes + wrow * (a.cols / 2) + c16 / 2;
+  const uint16_t *sp = a.w.scales + wrow * ng, *bp = a.w.biases + wrow * ng;
+  const uint16_t *xp[NT];
+  f32x4_t acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     xp[i] = a.x + min(t0 + i * 16 + (lane & 15), a.T - 1) * a.x_stride + c16;
-#pragma unroll
-    for (int k = 0; k < RB; ++k) acc[k][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
   for (int g0 = wave; g0 < ng; g0 += kLnWaves * kBatch) {
-    uint2 c[kBatch][RB];
-    uint32_t s[kBatch][RB], b[kBatch][RB];
+    uint2 c[kBatch];
+    uint32_t s[kBatch], b[kBatch];
     uint4 x[kBatch][NT][2];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int g = min(g0 + j * kLnWaves, ng - 1);
-#pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        c[j][k] = *(const uint2 *)(codes[k] + g * 32);
-        s[j][k] = sp[k][g];
-        b[j][k] = bp[k][g];
-      }
+      c[j] = *(const uint2 *)(codes + g * 32);
+      s[j] = sp[g];
+      b[j] = bp[g];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         x[j][i][0] = *(const uint4 *)(xp[i] + g * kGroup);
@@ -138,67 +126,73 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (g0 + j * kLnWaves >= ng) break;
+      const float sc = bf16_to_f32(s[j]), bi = bf16_to_f32(b[j]);
+      const bf16x8_t w0 = __builtin_bit_cast(bf16x8_t, dequant8(c[j].x, sc, bi));
+      const bf16x8_t w1 = __builtin_bit_cast(bf16x8_t, dequant8(c[j].y, sc, bi));
 #pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        const float sc = bf16_to_f32(s[j][k]), bi = bf16_to_f32(b[j][k]);
-        const bf16x8_t w0 = __builtin_bit_cast(bf16x8_t, dequant8(c[j][k].x, sc, bi));
-        const bf16x8_t w1 = __builtin_bit_cast(bf16x8_t, dequant8(c[j][k].y, sc, bi));
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          acc[k][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8_t, x[j][i][0]), acc[k][i], 0, 0, 0);
-          acc[k][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8_t, x[j][i][1]), acc[k][i], 0, 0, 0);
-        }
+      for (int i = 0; i < NT; ++i) {
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8_t, x[j][i][0]), acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8_t, x[j][i][1]), acc[i], 0, 0, 0);
       }
     }
   }
 #pragma unroll
-  for (int k = 0; k < RB; ++k) {
-    if (k > 0) __syncthreads();  // the block before has been added up
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int r = 0; r < 4; ++r) part[wave][i * 16 + (lane & 15)][(lane >> 4) * 4 + r] = acc[i][r];
+  __syncthreads();
+  with_act(a.act, [&](auto act) {
+    for (int e = threadIdx.x; e < kTokens * 16; e += kLnWaves * kWave) {
+      const int t = t0 + e / 16, n = n0 + e % 16;
+      if (t >= a.T || n >= a.rows) continue;
+      const float bias = a.bias ? bf16_to_f32(a.bias[n]) : 0.f, res = load_residual<F32>(a, t, n);
+      float z = 0.f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave][i * 16 + (lane & 15)][(lane >> 4) * 4 + r] = acc[k][i][r];
-    __syncthreads();
-    with_act(a.act, [&](auto act) {
-      for (int e = threadIdx.x; e < kTokens * 16; e += kLnWaves * kWave) {
-        const int t = t0 + e / 16, n = n0 + 16 * k + e % 16;
-        if (t >= a.T || n >= a.rows) continue;
-        const float bias = a.bias ? bf16_to_f32(a.bias[n]) : 0.f, res = load_residual<F32>(a, t, n);
-        float z = 0.f;
-#pragma unroll
-        for (int w = 0; w < kLnWaves; ++w) z += part[w][e / 16][e % 16];
-        store_output<act.value, F32>(a, t, n, z, bias, res);
-      }
-    });
-  }
+      for (int w = 0; w < kLnWaves; ++w) z += part[w][e / 16][e % 16];
+      store_output<act.value, F32>(a, t, n, z, bias, res);
+    }
+  });
 }
 
 // ------------------------------------------------------------------ large batches
 //
-// One workgroup = 4 wavefronts = 128 tokens x 256 weight rows; a wavefront
-// takes all 128 tokens and its own 64 rows, so every weight is rebuilt once per
-// 128 tokens, in registers, as the B operand of 32x32x16 MFMAs (C: lane =
-// weight row, registers = tokens). Per K step of 64 (one group):
-//   - activations (16 KB) come by LDS DMA into a ring of three stages shared by
-//     the workgroup, 16-byte chunks XOR-swizzled by row so that fragment reads
-//     of 8 or 16 rows hit distinct banks;
+// Four wavefronts take a tile of 32 MB tokens x 128 NB weight rows, each all the
+// tokens and its own 32 NB rows, so every weight is rebuilt once per tile, in
+// registers, as the B operand of 32x32x16 MFMAs (C: lane = weight row,
+// registers = tokens). Per K step of 64 (one group):
+//   - activations (4 MB KB) come by LDS DMA into a ring of three stages shared by
+//     the four, 16-byte chunks XOR-swizzled by row so that fragment reads of 8
+//     or 16 rows hit distinct banks;
 //   - codes come by LDS DMA too, into the wavefront's own ring, where each lane
 //     reads back the 16 bytes it fetched (32 columns of one row);
 //   - scales and biases sit in an LDS table of 8 groups of the wavefront's rows,
 //     refilled every 8 steps.
 // All loads of the loop are DMA, two steps ahead, and the loop waits for them
 // by count: a load into registers there would make the compiler wait for every
-// DMA behind it. Two workgroups share a CU (80 KB of LDS, 256 registers), so
-// one rebuilds weights while the other multiplies.
-constexpr int kBgTokens = 128, kBgRows = 256, kBgWaves = 4, kBgThreads = kBgWaves * kWave;
-constexpr int kBgK = kGroup, kBgStages = 3, kBgChunk = 8;
-constexpr int kBgX = kBgTokens * kBgK * 2;                   // bytes of activations a stage
-constexpr int kBgCodes = kBgRows * kBgK / 2;                 // bytes of codes a stage
-constexpr int kBgTable = kBgChunk * kBgRows * 4;             // (scale | bias << 16) words
-constexpr int kBgLds = kBgStages * (kBgX + kBgCodes) + kBgTable;
-constexpr int kBgLoads = kBgX / 4096 + kBgCodes / 4096;      // DMA instructions a wavefront and stage
-static_assert(2 * kBgLds <= 160 * 1024, "two workgroups a CU");
-static_assert(kBgWaves * 64 * 64 * 4 <= kBgLds, "the epilogue fits");
+// DMA behind it.
+//   large batches   MB = 4, NB = 2: two workgroups share a CU (80 KB of LDS, 256
+//                   registers), so one rebuilds weights while the other multiplies;
+//   middle ones     MB = 2, NB = 1 and KS = 2 teams of four wavefronts that split
+//                   the K steps and add up in LDS: there are few tiles then, and
+//                   a step takes its latency, not its work.
+constexpr int kBgStages = 3, kBgChunk = 8;
+
+template <int MB, int NB, int KS>
+struct Bg {
+  static constexpr int kTokens = 32 * MB, kRows = 128 * NB, kWaveRows = 32 * NB;
+  static constexpr int kThreads = KS * 4 * kWave;
+  static constexpr int kX = kTokens * kGroup * 2;      // bytes of activations a stage
+  static constexpr int kCodes = kRows * kGroup / 2;    // bytes of codes a stage
+  static constexpr int kTable = kBgChunk * kRows * 4;  // (scale | bias << 16) words
+  static constexpr int kTeam = kBgStages * (kX + kCodes) + kTable;
+  static constexpr int kLds = KS * kTeam;
+  static constexpr int kLoads = MB + NB;               // DMA instructions a wavefront and stage
+  static constexpr int kPasses = MB == 4 ? 2 : 1;      // of the epilogue
+  static constexpr int kPassTokens = kTokens / kPasses;
+  static_assert(2 * kLds <= 160 * 1024, "two workgroups a CU");
+  static_assert(KS * 4 * kPassTokens * kWaveRows * 4 <= kLds, "the epilogue fits");
+  static_assert(kLoads % 3 == 0, "a third of the loads behind each of three slices");
+};
 
 #define MOE_LN_WAIT_VMCNT(n) \
   __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (0x7 << 4) | (0xF << 8) | (((n) >> 4) << 14))
@@ -242,47 +236,53 @@ __device__ __forceinline__ bool bg_tile(int bid, int tt, int nn, int &t, int &n)
   return true;
 }
 
-template <bool F32>
-__global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs a) {
+template <int MB, int NB, int KS, bool F32>
+__global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(LinearArgs a) {
+  using B = Bg<MB, NB, KS>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   int ti, ni;
-  if (!bg_tile(blockIdx.x, (a.T + kBgTokens - 1) / kBgTokens, (a.rows + kBgRows - 1) / kBgRows, ti, ni)) return;
+  if (!bg_tile(blockIdx.x, (a.T + B::kTokens - 1) / B::kTokens, (a.rows + B::kRows - 1) / B::kRows, ti, ni)) return;
   const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int t0 = ti * kBgTokens, n0 = ni * kBgRows + wave * 64;
+  const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave = wave8 & 3, team = wave8 >> 2;
+  const int t0 = ti * B::kTokens, n0 = ni * B::kRows + wave * B::kWaveRows;
   const int ng = a.cols / kGroup;
-  const int tokens = min(kBgTokens, a.T - t0);
+  const int tokens = min(B::kTokens, a.T - t0);
+  // the team's groups: common steps for all teams, and what is left for the first
+  const int common = ng / KS, left = ng - common * KS;
+  const int first = team == 0 ? 0 : team * common + left;
+  const int steps = common + (team == 0 ? left : 0);
+  uint8_t *const lds = smem + team * B::kTeam;
 
   // activations: DMA instruction i of wavefront w fills rows 32 i + 8 w .. +7,
   // lane l row l / 8 of those, LDS chunk l % 8, which holds the row's chunk
   // (l % 8) ^ (row % 8) ^ (row / 8 % 2). Rows past the last re-read it.
   const ln_u32x4 xr = ln_rsrc(a.x + t0 * a.x_stride, (uint32_t)(((tokens - 1) * a.x_stride + a.cols) * 2));
-  uint32_t x_off[4];
+  uint32_t x_off[MB];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < MB; ++i) {
     const int r = min(32 * i + 8 * wave + (lane >> 3), tokens - 1);
-    x_off[i] = (uint32_t)(r * (int)a.x_stride + (((lane & 7) ^ (lane >> 3) ^ (wave & 1)) * 8)) * 2u;
+    x_off[i] = (uint32_t)(r * (int)a.x_stride + first * kGroup + (((lane & 7) ^ (lane >> 3) ^ (wave & 1)) * 8)) * 2u;
   }
   // codes: instruction b fetches row 32 b + l % 32, columns 32 (l / 32) .. +31
-  const uint8_t *codes = a.w.codes + (long long)min(n0, a.rows - 1) * (a.cols / 2);
-  const int wrows = max(min(64, a.rows - n0), 1);
-  const ln_u32x4 cr = ln_rsrc(codes, (uint32_t)(wrows * (a.cols / 2)));
-  uint32_t c_off[2];
+  const int wrow0 = min(n0, a.rows - 1), wrows = max(min(B::kWaveRows, a.rows - n0), 1);
+  const ln_u32x4 cr = ln_rsrc(a.w.codes + (long long)wrow0 * (a.cols / 2), (uint32_t)(wrows * (a.cols / 2)));
+  uint32_t c_off[NB];
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
-    c_off[b] = (uint32_t)(min(32 * b + (lane & 31), wrows - 1) * (a.cols / 2) + (lane >> 5) * 16);
-  const uint32_t x_lds = ln_lds_address(smem) + wave * 1024;
-  uint8_t *cring = smem + kBgStages * kBgX + wave * 2048;  // this wavefront's part of a stage
+  for (int b = 0; b < NB; ++b)
+    c_off[b] = (uint32_t)(min(32 * b + (lane & 31), wrows - 1) * (a.cols / 2) + first * (kGroup / 2) + (lane >> 5) * 16);
+  const uint32_t x_lds = ln_lds_address(lds) + wave * 1024;
+  uint8_t *cring = lds + kBgStages * B::kX + wave * (NB * 1024);  // this wavefront's part of a stage
   const uint32_t c_lds = ln_lds_address(cring);
-  uint32_t *table = (uint32_t *)(smem + kBgStages * (kBgX + kBgCodes)) + wave * 64;
-  // third i of a stage's DMA: 4 instructions for activations, 2 for codes
+  uint32_t *table = (uint32_t *)(lds + kBgStages * (B::kX + B::kCodes)) + wave * B::kWaveRows;
+  // third i of a stage's DMA instructions: activations first, then codes
   auto dma_part = [&](int step, int slot, int i) {
-    if (i < 2) {
-      ln_dma(xr, x_off[2 * i], step * (kBgK * 2), x_lds + slot * kBgX + i * 8192);
-      ln_dma(xr, x_off[2 * i + 1], step * (kBgK * 2), x_lds + slot * kBgX + i * 8192 + 4096);
-    } else {
-      ln_dma(cr, c_off[0], step * (kBgK / 2), c_lds + slot * kBgCodes);
-      ln_dma(cr, c_off[1], step * (kBgK / 2), c_lds + slot * kBgCodes + 1024);
+#pragma unroll
+    for (int j = i * (B::kLoads / 3); j < (i + 1) * (B::kLoads / 3); ++j) {
+      if (j < MB)
+        ln_dma(xr, x_off[j < MB ? j : 0], step * (kGroup * 2), x_lds + slot * B::kX + j * 4096);
+      else
+        ln_dma(cr, c_off[j < MB ? 0 : j - MB], step * (kGroup / 2), c_lds + slot * B::kCodes + (j - MB) * 1024);
     }
   };
   auto dma = [&](int step, int slot) {
@@ -291,9 +291,10 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
   };
 
   // scales and biases of 8 groups of row `lane` of the wavefront
-  const long long srow = (long long)(min(n0, a.rows - 1) + min(lane, wrows - 1)) * ng;
+  const int trow = min(lane & (B::kWaveRows - 1), wrows - 1);
+  const long long srow = (long long)(wrow0 + trow) * ng + first;
   const uint16_t *sp = a.w.scales + srow, *bp = a.w.biases + srow;
-  const bool vec = ng % 8 == 0;  // 16-byte loads stay aligned
+  const bool vec = ng % 8 == 0 && first % 8 == 0 && steps % 8 == 0;  // 16-byte loads stay aligned and inside
   uint4 sv, bv;
   auto fetch = [&](int g0) {
     if (vec) {
@@ -303,7 +304,7 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
       uint32_t s[4], b[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int g = min(g0 + 2 * i, ng - 1), h = min(g0 + 2 * i + 1, ng - 1);
+        const int g = min(g0 + 2 * i, steps - 1), h = min(g0 + 2 * i + 1, steps - 1);
         s[i] = sp[g] | (uint32_t)sp[h] << 16;
         b[i] = bp[g] | (uint32_t)bp[h] << 16;
       }
@@ -313,58 +314,63 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
   };
   auto fill = [&]() {
     const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+    uint32_t *t = table + (lane & (B::kWaveRows - 1));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      table[(2 * i) * kBgRows + lane] = (s[i] & 0xFFFFu) | (b[i] << 16);
-      table[(2 * i + 1) * kBgRows + lane] = (s[i] >> 16) | (b[i] & 0xFFFF0000u);
+      t[(2 * i) * B::kRows] = (s[i] & 0xFFFFu) | (b[i] << 16);
+      t[(2 * i + 1) * B::kRows] = (s[i] >> 16) | (b[i] & 0xFFFF0000u);
     }
   };
-  dma(0, 0);
-  if (ng > 1) dma(1, 1);
-  // does every group of the wavefront's rows take the fast dequantisation?
-  bool ok = true;
+  bool ok = true;  // every group of the wavefront's rows takes the fast dequantisation
+  if (steps > 0) {
+    dma(0, 0);
+    if (steps > 1) dma(1, 1);
 #pragma unroll 4
-  for (int g0 = 0; g0 < ng; g0 += kBgChunk) {
-    fetch(g0);
-    const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+    for (int g0 = 0; g0 < steps; g0 += kBgChunk) {
+      fetch(g0);
+      const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ok &= (int)dq_fast_ok((s[i] & 0xFFFFu) | (b[i] << 16)) & (int)dq_fast_ok((s[i] >> 16) | (b[i] & 0xFFFF0000u));
+      for (int i = 0; i < 4; ++i)
+        ok &= (int)dq_fast_ok((s[i] & 0xFFFFu) | (b[i] << 16)) & (int)dq_fast_ok((s[i] >> 16) | (b[i] & 0xFFFF0000u));
+    }
+    fetch(0);
+    fill();
   }
   const bool fast = __builtin_amdgcn_ballot_w64(!ok) == 0;
 
-  fetch(0);
-  fill();
-
-  f32x16_t acc[4][2];
+  f32x16_t acc[MB][NB];
 #pragma unroll
-  for (int rb = 0; rb < 4; ++rb) acc[rb][0] = acc[rb][1] = f32x16_t{0};
+  for (int rb = 0; rb < MB; ++rb)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[rb][b] = f32x16_t{0};
   const DqRegs dk = dq_regs();
   const int lrow = (lane & 31) * 128, lx = (lane & 7) ^ ((lane >> 3) & 1), lh = 4 * (lane >> 5);
 
+  // Wait for stage kt (only the DMA of stage kt + 1 may still be in flight) and
+  // for every wavefront to be done with stage kt - 1.
+  auto enter = [&](int kt) {
+    if (kt + 1 < steps)
+      MOE_LN_WAIT_VMCNT(B::kLoads);
+    else
+      MOE_LN_WAIT_VMCNT(0);
+    lds_barrier();
+    asm volatile("" ::: "memory");
+  };
   // one K step; the weights of a slice of 16 columns are rebuilt, and its
   // activation fragments read, while the slice before it is multiplied
   int slot = 0;
   auto step = [&](auto fast_tag, int kt) {
     constexpr bool FAST = decltype(fast_tag)::value;
-    // stage kt has landed (only the DMA of stage kt + 1 may still be in flight);
-    // the barrier also tells that every wavefront is done with stage kt - 1
-    if (kt + 1 < ng)
-      MOE_LN_WAIT_VMCNT(kBgLoads);
-    else
-      MOE_LN_WAIT_VMCNT(0);
-    lds_barrier();
-    asm volatile("" ::: "memory");
-    if (kt % kBgChunk == kBgChunk - 1 && kt + 1 < ng) fetch(kt + 1);
-    const uint8_t *xs = smem + slot * kBgX + lrow;
-    uint32_t word[2][4];
-    DqGroup q[2];
-    float sc[2], bi[2];
+    if (kt % kBgChunk == kBgChunk - 1 && kt + 1 < steps) fetch(kt + 1);
+    const uint8_t *xs = lds + slot * B::kX + lrow;
+    uint32_t word[NB][4];
+    DqGroup q[NB];
+    float sc[NB], bi[NB];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const uint4 c = *(const uint4 *)(cring + slot * kBgCodes + b * 1024 + lane * 16);
+    for (int b = 0; b < NB; ++b) {
+      const uint4 c = *(const uint4 *)(cring + slot * B::kCodes + b * 1024 + lane * 16);
       word[b][0] = c.x, word[b][1] = c.y, word[b][2] = c.z, word[b][3] = c.w;
-      const uint32_t sb = table[(kt % kBgChunk) * kBgRows + b * 32 + (lane & 31)];
+      const uint32_t sb = table[(kt % kBgChunk) * B::kRows + b * 32 + (lane & 31)];
       if (FAST) {
         q[b] = dq_consts(sb);
       } else {
@@ -372,19 +378,19 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
         bi[b] = bf16_to_f32(sb >> 16);
       }
     }
-    auto weights = [&](int ks, bf16x8_t (&w)[2]) {
+    auto weights = [&](int ks, bf16x8_t (&w)[NB]) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < NB; ++b) {
         const uint4 v = FAST ? dequant8_fast(word[b][ks], q[b], dk) : dequant8(word[b][ks], sc[b], bi[b]);
         w[b] = __builtin_bit_cast(bf16x8_t, v);
       }
     };
-    auto fragments = [&](int ks, bf16x8_t (&x)[4]) {
+    auto fragments = [&](int ks, bf16x8_t (&x)[MB]) {
       const uint8_t *p = xs + (((lh + ks) ^ lx) << 4);
 #pragma unroll
-      for (int rb = 0; rb < 4; ++rb) x[rb] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(p + rb * 4096));
+      for (int rb = 0; rb < MB; ++rb) x[rb] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(p + rb * 4096));
     };
-    bf16x8_t w[2][2], x[2][4];
+    bf16x8_t w[2][NB], x[2][MB];
     fragments(0, x[0]);
     weights(0, w[0]);
 #pragma unroll
@@ -394,34 +400,46 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
         weights(ks + 1, w[(ks + 1) & 1]);
       }
 #pragma unroll
-      for (int rb = 0; rb < 4; ++rb)
+      for (int rb = 0; rb < MB; ++rb)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
           acc[rb][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[ks & 1][rb], w[ks & 1][b], acc[rb][b], 0, 0, 0);
       if (FAST && ks < 3) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);  // the next fragments' reads
+        __builtin_amdgcn_sched_group_barrier(0x100, MB, 0);  // the next fragments' reads
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA (32 cycles)
-          __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);  // five VALU operations (20)
+        for (int i = 0; i < MB * NB; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // one MFMA (32 cycles)
+          __builtin_amdgcn_sched_group_barrier(0x002, NB == 2 ? 5 : 9, 0);  // VALU operations of 4
         }
       }
       __builtin_amdgcn_sched_barrier(0);
       // a third of the DMA of stage kt + 2 behind each slice's MFMAs, whose time
       // covers its issue
-      if (ks < 3 && kt + 2 < ng) dma_part(kt + 2, slot == 0 ? 2 : slot - 1, ks);
+      if (ks < 3 && kt + 2 < steps) dma_part(kt + 2, slot == 0 ? 2 : slot - 1, ks);
     }
     slot = slot == kBgStages - 1 ? 0 : slot + 1;
   };
   // two whole loops, so that the accumulators meet no branch inside
   auto run = [&](auto fast_tag) {
-    for (int k0 = 0; k0 < ng; k0 += kBgChunk) {
+    for (int k0 = 0; k0 < common; k0 += kBgChunk) {
       if (k0 > 0) {
         MOE_LN_WAIT_VMCNT(0);
         fill();
       }
-      const int k1 = min(k0 + kBgChunk, ng);
-      for (int kt = k0; kt < k1; ++kt) step(fast_tag, kt);
+      const int k1 = min(k0 + kBgChunk, common);
+      for (int kt = k0; kt < k1; ++kt) {
+        enter(kt);
+        step(fast_tag, kt);
+      }
+    }
+    // the first team's steps over: every wavefront keeps the barriers
+    for (int kt = common; kt < common + left; ++kt) {
+      if (team == 0 && kt % kBgChunk == 0 && kt > 0) {
+        MOE_LN_WAIT_VMCNT(0);
+        fill();
+      }
+      enter(kt);
+      if (team == 0) step(fast_tag, kt);
     }
   };
   if (fast)
@@ -429,37 +447,45 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
   else
     run(std::false_type{});
 
-  // Epilogue. The sums go through the wavefront's quarter of the LDS, 64 tokens
-  // by 64 rows at a time, and leave a token's 64 outputs to a wavefront store.
-  // C layout: lane l holds weight row l % 32 of its block, register r token
+  // Epilogue. The sums go through LDS ([team][wavefront][token][32 NB rows]), in
+  // one or two passes; the teams share the tokens and add up their parts. C
+  // layout: lane l holds weight row l % 32 of its block, register r token
   // 8 (r / 4) + 4 (l / 32) + r % 4.
-  lds_barrier();
-  float *ep = (float *)(smem + wave * (64 * 64 * 4));
-  // lane l: outputs 8 (l % 8) .. +7 of token l / 8 (+ 8 a turn)
-  const int n = n0 + (lane & 7) * 8;
+  constexpr int kCols = B::kWaveRows, kLanesTok = kCols / 8, kPart = B::kPassTokens * kCols;
+  float *const ep = (float *)smem + wave * kPart;
+  // lane l: outputs 8 (l % kLanesTok) .. +7 of a token
+  const int c8 = (lane % kLanesTok) * 8, n = n0 + c8;
   // 16-byte (bf16) and 32-byte (fp32) accesses where rows keep their alignment
   const bool wide = n + 8 <= a.rows && a.y_stride % 8 == 0 && (!a.residual || a.r_stride % 8 == 0);
   float bias[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) bias[i] = a.bias && n + i < a.rows ? bf16_to_f32(a.bias[n + i]) : 0.f;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int pass = 0; pass < B::kPasses; ++pass) {
+    if (pass == 0) lds_barrier();  // the rings are done with
 #pragma unroll
-    for (int rb = 0; rb < 2; ++rb)
+    for (int rb = 0; rb < MB / B::kPasses; ++rb)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          ep[(rb * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * 64 + b * 32 + (lane & 31)] =
-              acc[half * 2 + rb][b][r];
+          ep[team * 4 * kPart + (rb * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * kCols + b * 32 + (lane & 31)] =
+              acc[pass * (MB / B::kPasses) + rb][b][r];
+    if (KS > 1) lds_barrier();
     with_act(a.act, [&](auto act) {
+      constexpr int kTurn = kWave / kLanesTok, kMine = B::kPassTokens / KS;  // tokens a turn, tokens a team
 #pragma unroll 2
-      for (int i = 0; i < 8; ++i) {
-        const int tl = i * 8 + (lane >> 3), t = t0 + half * 64 + tl;
+      for (int i = 0; i < kMine / kTurn; ++i) {
+        const int tl = team * kMine + i * kTurn + lane / kLanesTok, t = t0 + pass * B::kPassTokens + tl;
         if (t >= a.T) continue;
-        const float4 z0 = *(const float4 *)(ep + tl * 64 + (lane & 7) * 8);
-        const float4 z1 = *(const float4 *)(ep + tl * 64 + (lane & 7) * 8 + 4);
-        const float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+        float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const float4 z0 = *(const float4 *)(ep + k * 4 * kPart + tl * kCols + c8);
+          const float4 z1 = *(const float4 *)(ep + k * 4 * kPart + tl * kCols + c8 + 4);
+          z[0] += z0.x, z[1] += z0.y, z[2] += z0.z, z[3] += z0.w;
+          z[4] += z1.x, z[5] += z1.y, z[6] += z1.z, z[7] += z1.w;
+        }
         if (wide) {
           store_outputs8<act.value, F32>(a, t, n, z, bias);
         } else {
@@ -472,61 +498,71 @@ __global__ __launch_bounds__(kBgThreads, 2) void linear_tiles_kernel(LinearArgs 
   }
 }
 
-// Tiles of the large-batch kernel from which it is the faster one.
-constexpr int kBgMinTiles = 128;
+// Where the kernels change over.
+constexpr int kBgMinTiles = 256;
+constexpr int kMidMinT = 33;
 
+template <int MB, int NB, int KS>
 static long long bg_tiles(int T, int rows) {
-  return (long long)((T + kBgTokens - 1) / kBgTokens) * ((rows + kBgRows - 1) / kBgRows);
+  using B = Bg<MB, NB, KS>;
+  return (long long)((T + B::kTokens - 1) / B::kTokens) * ((rows + B::kRows - 1) / B::kRows);
 }
 
-static bool tiles_fit(const LinearArgs &a) {
-  // 32-bit byte offsets within a tile
-  return bg_tiles(a.T, a.rows) >= kBgMinTiles && a.x_stride < (1 << 23) && a.cols < (1 << 23);
-}
-
-template <int RB, int NT>
+template <int NT>
 static long long ln_blocks(int T, int rows) {
-  return (long long)((rows + 16 * RB - 1) / (16 * RB)) * ((T + 16 * NT - 1) / (16 * NT));
+  return (long long)((rows + 15) / 16) * ((T + 16 * NT - 1) / (16 * NT));
 }
 
-// A launch dimension holds fewer than 2^32 threads (512 to a workgroup).
-bool linear_grid_ok(int T, int rows) { return ln_blocks<1, 1>(T, rows) < (1ll << 23); }
-
-template <int RB, int NT>
-static void launch(const LinearArgs &a, int dtype, hipStream_t s) {
-  auto *kernel = dtype ? linear_kernel<RB, NT, true> : linear_kernel<RB, NT, false>;
-  kernel<<<(int)ln_blocks<RB, NT>(a.T, a.rows), kLnWaves * kWave, 0, s>>>(a);
+template <int NT>
+static hipError_t launch(const LinearArgs &a, int dtype, hipStream_t s) {
+  auto *kernel = dtype ? linear_kernel<NT, true> : linear_kernel<NT, false>;
+  kernel<<<(int)ln_blocks<NT>(a.T, a.rows), kLnWaves * kWave, 0, s>>>(a);
+  return hipGetLastError();
 }
 
+template <int MB, int NB, int KS>
 static hipError_t launch_tiles(const LinearArgs &a, int dtype, hipStream_t s) {
-  auto *kernel = dtype ? linear_tiles_kernel<true> : linear_tiles_kernel<false>;
+  using B = Bg<MB, NB, KS>;
+  auto *kernel = dtype ? linear_tiles_kernel<MB, NB, KS, true> : linear_tiles_kernel<MB, NB, KS, false>;
   static const hipError_t st = [] {  // more than 64 KB of LDS needs an opt-in, once per process
-    const hipError_t e = hipFuncSetAttribute((const void *)linear_tiles_kernel<true>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kBgLds);
+    const hipError_t e = hipFuncSetAttribute((const void *)linear_tiles_kernel<MB, NB, KS, true>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, B::kLds);
     return e != hipSuccess ? e
-                           : hipFuncSetAttribute((const void *)linear_tiles_kernel<false>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kBgLds);
+                           : hipFuncSetAttribute((const void *)linear_tiles_kernel<MB, NB, KS, false>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, B::kLds);
   }();
   if (st != hipSuccess) return st;
-  kernel<<<(int)((bg_tiles(a.T, a.rows) + 7) / 8 * 8), kBgThreads, kBgLds, s>>>(a);
+  kernel<<<(int)((bg_tiles<MB, NB, KS>(a.T, a.rows) + 7) / 8 * 8), B::kThreads, B::kLds, s>>>(a);
   return hipGetLastError();
+}
+
+// The kernel for a call: 0 large tiles, 1 middle tiles, 2 .. 5 the small one with
+// 1 .. 4 token tiles.
+static int linear_choice(const LinearArgs &a) {
+  // the tile kernels keep 32-bit byte offsets within a tile
+  const bool tiles = a.x_stride < (1 << 23) && a.cols < (1 << 23);
+  if (tiles && bg_tiles<4, 2, 1>(a.T, a.rows) >= kBgMinTiles) return 0;
+  if (tiles && a.T >= kMidMinT) return 1;
+  return a.T <= 16 ? 2 : a.T <= 32 ? 3 : a.T <= 48 ? 4 : 5;
+}
+
+bool linear_grid_ok(const LinearArgs &a) {
+  const int c = linear_choice(a);
+  const long long threads = c == 0   ? bg_tiles<4, 2, 1>(a.T, a.rows) * 256
+                            : c == 1 ? bg_tiles<2, 1, 2>(a.T, a.rows) * 512
+                                     : ln_blocks<4>(a.T, a.rows) * 512;
+  return threads < (1ll << 32) - 8 * 512;  // of one launch dimension
 }
 
 hipError_t launch_linear(const LinearArgs &a, int dtype, hipStream_t s) {
-  if (tiles_fit(a)) return launch_tiles(a, dtype, s);
-  if (a.T <= 16)
-    launch<1, 1>(a, dtype, s);
-  else if (a.T <= 32)
-    launch<1, 2>(a, dtype, s);
-  else if (a.T <= 48)
-    launch<1, 3>(a, dtype, s);
-  else if (ln_blocks<4, 4>(a.T, a.rows) >= 128)
-    launch<4, 4>(a, dtype, s);
-  else if (ln_blocks<2, 4>(a.T, a.rows) >= 128)
-    launch<2, 4>(a, dtype, s);
-  else
-    launch<1, 4>(a, dtype, s);
-  return hipGetLastError();
+  switch (linear_choice(a)) {
+    case 0: return launch_tiles<4, 2, 1>(a, dtype, s);
+    case 1: return launch_tiles<2, 1, 2>(a, dtype, s);
+    case 2: return launch<1>(a, dtype, s);
+    case 3: return launch<2>(a, dtype, s);
+    case 4: return launch<3>(a, dtype, s);
+    default: return launch<4>(a, dtype, s);
+  }
 }
 
 }  // namespace moe

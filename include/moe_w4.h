@@ -336,7 +336,7 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *             be y itself with the same stride (updated in place)
  *   y         bf16 or fp32 (dtype) [T][rows], rows y_stride elements apart, out
  * Limits: T >= 0, rows >= 1, cols >= 1 (MOE_E_INVALID otherwise); cols % 64 == 0,
- * x_stride % 8 == 0, rows * cols < 2^34, T * rows and T * cols < 2^40
+ * x_stride % 8 == 0, rows * cols < 2^34, T * rows < 2^36, T * cols < 2^40
  * (MOE_E_UNSUPPORTED); strides at least a row long (MOE_E_INVALID).
  */
 moe_status moe_linear_w4(int32_t T, int32_t rows, int32_t cols, const uint16_t *x, int64_t x_stride,
