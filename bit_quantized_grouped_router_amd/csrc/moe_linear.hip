@@ -498,9 +498,15 @@ __global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(Li
   }
 }
 
-// Where the kernels change over.
-constexpr int kBgMinTiles = 256;
-constexpr int kMidMinT = 33;
+// Where the kernels change over (5120 x 2048 weights unless said otherwise).
+// Large tiles from 220 of them: 1500 tokens (240 tiles) 49 us against 55 on
+// middle tiles, 1024 tokens (160) 49 against 44.
+constexpr int kBgMinTiles = 220;
+// Middle tiles above 16 tokens where the small kernel would need more than 384
+// workgroups of 32 tokens: 64 tokens (640) 16 us against 21; 32 tokens (320) 15
+// against 15; 64 tokens by 2048 rows (256) 15 against 9; 37 tokens by 2048 rows
+// and 4096 columns (256) 28 against 15.
+constexpr int kSmallMaxBlocks = 384;
 
 template <int MB, int NB, int KS>
 static long long bg_tiles(int T, int rows) {
@@ -536,21 +542,21 @@ static hipError_t launch_tiles(const LinearArgs &a, int dtype, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The kernel for a call: 0 large tiles, 1 middle tiles, 2 .. 5 the small one with
-// 1 .. 4 token tiles.
+// The kernel for a call: 0 large tiles, 1 middle tiles, 2 and 3 the small one with
+// 16 and 32 tokens.
 static int linear_choice(const LinearArgs &a) {
+  if (a.T <= 16) return 2;
   // the tile kernels keep 32-bit byte offsets within a tile
   const bool tiles = a.x_stride < (1 << 23) && a.cols < (1 << 23);
   if (tiles && bg_tiles<4, 2, 1>(a.T, a.rows) >= kBgMinTiles) return 0;
-  if (tiles && a.T >= kMidMinT) return 1;
-  return a.T <= 16 ? 2 : a.T <= 32 ? 3 : a.T <= 48 ? 4 : 5;
+  return tiles && ln_blocks<2>(a.T, a.rows) > kSmallMaxBlocks ? 1 : 3;
 }
 
 bool linear_grid_ok(const LinearArgs &a) {
   const int c = linear_choice(a);
   const long long threads = c == 0   ? bg_tiles<4, 2, 1>(a.T, a.rows) * 256
                             : c == 1 ? bg_tiles<2, 1, 2>(a.T, a.rows) * 512
-                                     : ln_blocks<4>(a.T, a.rows) * 512;
+                                     : ln_blocks<2>(a.T, a.rows) * 512;
   return threads < (1ll << 32) - 8 * 512;  // of one launch dimension
 }
 
@@ -559,9 +565,7 @@ hipError_t launch_linear(const LinearArgs &a, int dtype, hipStream_t s) {
     case 0: return launch_tiles<4, 2, 1>(a, dtype, s);
     case 1: return launch_tiles<2, 1, 2>(a, dtype, s);
     case 2: return launch<1>(a, dtype, s);
-    case 3: return launch<2>(a, dtype, s);
-    case 4: return launch<3>(a, dtype, s);
-    default: return launch<4>(a, dtype, s);
+    default: return launch<2>(a, dtype, s);
   }
 }
 
