@@ -125,6 +125,7 @@ struct Kv4Attn {
   float scale;
   bool causal;
   int window;
+  int most_rows;  // the row kernel's: sequences with more query rows a head are not its own
 };
 
 // Workgroups a call's keys are split over, and the bytes of their partial
@@ -132,6 +133,9 @@ struct Kv4Attn {
 int kv4_splits(const Kv4Dims &dm, int max_new, int window);
 size_t kv4_attention_ws(const Kv4Dims &dm, int max_new, int window);
 bool kv4_grid_ok(const Kv4Dims &dm, int max_new, int window);
+// Sequences of many query rows (n * G); those with at most `few` are skipped.
+hipError_t launch_kv4_prefill(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
+                              const Kv4Batch &bt, const Kv4Attn &at, int few, hipStream_t s);
 hipError_t launch_kv4_attention(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
                                 const Kv4Batch &bt, const Kv4Attn &at, void *ws, hipStream_t s);
 #endif

@@ -28,19 +28,11 @@
 // The order inside a contraction is free, so the nibbles of a word are taken
 // in the order 0 4 1 5 2 6 3 7 (one shift and one and-or give two of them),
 // and the query and the weights are laid out to match.
-#include "moe_device.h"
-#include "moe_kv4.h"
+#include "moe_kv4_device.h"
 
 namespace moe {
 
 constexpr int kAtRows = 16;  // query rows (token, head of the group) per workgroup; its wavefronts split the keys
-
-constexpr float kNegInf = -__builtin_huge_valf();
-
-// Scaled log2 units a score may exceed the running reference by before the
-// accumulators are rescaled: weights stay below 2^8, far from overflow, and
-// the rescale runs once or twice a row instead of at every new maximum.
-constexpr float kSlack = 8.0f;
 
 // Constants of the conversion, kept in registers and opaque to the compiler so
 // that it is one shift and one v_and_or_b32 (which takes no literals).
@@ -154,24 +146,6 @@ typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2_t kv_lds_i32x2;
 typedef __attribute__((address_space(3))) void kv_lds_void;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef const __attribute__((address_space(4))) int32_t kv_const_i32;
-
-// Pages of a tile's two halves (scalar loads; -1: no place).
-struct TilePages {
-  int page[2];
-};
-
-__device__ __forceinline__ TilePages tile_pages(const Kv4Dims &dm, const int32_t *table, int tile) {
-  TilePages p;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const long long t = (long long)tile * kKvTile + 16 * u;
-    const bool in = t < kv4_capacity(dm);
-    const int page = ((kv_const_i32 *)table)[in ? (int)(t >> dm.page_shift) : 0];
-    p.page[u] = in && kv4_page_ok(dm, page) ? page : -1;
-  }
-  return p;
-}
 
 // LDS DMA, 16 bytes a lane, to LDS address dst + 16 * lane (dst wave-uniform).
 // Written as assembly because the compiler, which cannot tell the ring's stages
@@ -420,24 +394,6 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
   }
 }
 
-// Query rows of a workgroup: row r of a sequence and cache head is new token
-// r / G, head (cache head) * G + r % G.
-struct RowTile {
-  int seq, head, row0, rows;  // rows: rows of this sequence and head (n * G)
-  Kv4Span sp;
-};
-
-__device__ __forceinline__ RowTile row_tile(const Kv4Dims &dm, const Kv4Batch &bt, int max_new,
-                                            int tile, int head, int seq) {
-  RowTile t;
-  t.head = head;
-  t.seq = seq;
-  t.row0 = tile * kAtRows;
-  t.sp = kv4_span(bt.cu[seq], bt.cu[seq + 1], bt.len[seq], bt.T);
-  t.rows = min(t.sp.n, max_new) * (dm.Hq / dm.Hkv);
-  return t;
-}
-
 // Keys the tile's rows can see.
 __device__ __forceinline__ Kv4Range tile_range(const Kv4Dims &dm, const RowTile &t, bool causal,
                                                int window) {
@@ -498,7 +454,8 @@ __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch
   const int cap = (int)kv4_capacity(dm);
   float total = 0.f, tasks = 0.f;  // rough figures will do
   for (int b = lane; b < dm.B; b += kWave) {
-    const int n = min(min(max(bt.cu[b + 1], 0), bt.T) - min(max(bt.cu[b], 0), bt.T), at.max_new);
+    int n = min(min(max(bt.cu[b + 1], 0), bt.T) - min(max(bt.cu[b], 0), bt.T), at.max_new);
+    if (n * G > at.most_rows) n = 0;
     float keys = (float)min(max(bt.len[b], 0), cap);
     if (at.window > 0) keys = fminf(keys, (float)at.window + (float)n);
     const float tiles = n > 0 ? ceilf((float)n * G * (1.0f / kAtRows)) : 0.f;
@@ -539,7 +496,7 @@ __device__ __forceinline__ bool work_item(const Kv4Dims &dm, const Kv4Batch &bt,
     const Kv4Span sp = kv4_span(bt.cu[b], bt.cu[b + 1], bt.len[b], bt.T);
     const int n = min(sp.n, at.max_new);
     const Kv4Range r = kv4_range(dm, sp.first, sp.first + max(n, 1) - 1, sp.len, at.causal, at.window);
-    const int used = b0 + lane < dm.B && n > 0 ? kv4_share(r, per, splits, 0).used : 0;
+    const int used = b0 + lane < dm.B && n > 0 && n * (dm.Hq / dm.Hkv) <= at.most_rows ? kv4_share(r, per, splits, 0).used : 0;
     const int upto = wave_scan(used * dm.Hkv);
     const uint64_t after = __builtin_amdgcn_ballot_w64(upto > item);
     if (after != 0) {
@@ -564,8 +521,8 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
                                             uint8_t *smem, float (*sm)[kAtRows], float (*sl)[kAtRows],
                                             float *__restrict__ part) {
   constexpr int NG = D / kGroup;
-  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, head, seq);
-  if (rt.row0 >= rt.rows) return;
+  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, head, seq, kAtRows);
+  if (rt.row0 >= rt.rows || rt.rows > at.most_rows) return;
   const int G = dm.Hq / dm.Hkv;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -753,8 +710,8 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
   const int tiles = gridDim.x / (kChunks * kAtRows);
   const long long task = ((long long)blockIdx.z * dm.Hkv + blockIdx.y) * tiles + tile_i;
   const long long tasks = (long long)gridDim.z * gridDim.y * tiles;
-  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z);
-  if (rt.row0 + r >= rt.rows) return;
+  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z, kAtRows);
+  if (rt.row0 + r >= rt.rows || rt.rows > at.most_rows) return;
   const Kv4Range range = tile_range(dm, rt, at.causal, at.window);
   const int used = kv4_share(range, tiles_per_split<D>(dm, bt, at), splits, 0).used;
   if (used <= 1) return;
@@ -793,68 +750,85 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
   }
 }
 
+// Query rows of a sequence and head above which the prefill kernel takes it: it
+// rebuilds the keys once for 128 rows, this one reads them once for 16.
+constexpr int kManyRows = 64;
+
+// The new tokens a sequence may have to be this file's kernel's: 0 if none is. A
+// batch of one with many rows goes to the other kernel whole, so that a prompt
+// takes one launch.
+static int few_new(const Kv4Dims &dm, int max_new) {
+  const int G = dm.Hq / dm.Hkv;
+  if ((long long)max_new * G <= kManyRows) return max_new;
+  return dm.B == 1 ? 0 : kManyRows / G;
+}
+
 // Row tiles of a sequence and head (an upper bound: it may have fewer new
-// tokens than max_new), and over all sequences and heads.
-static long long kv4_row_tiles(const Kv4Dims &dm, int max_new) {
-  const long long rows = (long long)max_new * (dm.Hq / dm.Hkv);
+// tokens), and over all sequences and heads.
+static long long kv4_row_tiles(const Kv4Dims &dm, int tokens) {
+  const long long rows = (long long)tokens * (dm.Hq / dm.Hkv);
   return (rows + kAtRows - 1) / kAtRows;
 }
-static long long kv4_tasks(const Kv4Dims &dm, int max_new) {
-  return kv4_row_tiles(dm, max_new) * dm.Hkv * dm.B;
+static long long kv4_tasks(const Kv4Dims &dm, int tokens) {
+  return kv4_row_tiles(dm, tokens) * dm.Hkv * dm.B;
 }
 
 // The most workgroups a sequence's keys are split over: as many as have
 // kMinTiles each (of the table's width: the host does not know the lengths),
 // and no more than twice the card's slots over all tasks.
-int kv4_splits(const Kv4Dims &dm, int max_new, int window) {
-  const long long tasks = kv4_tasks(dm, max_new);
+static int few_splits(const Kv4Dims &dm, int tokens, int window) {
+  const long long tasks = kv4_tasks(dm, tokens);
   const int slots = dm.D == 256 ? at_slots<256>() : dm.D == 128 ? at_slots<128>() : at_slots<64>();
   long long keys = kv4_capacity(dm);
-  if (window > 0 && (long long)window + max_new < keys) keys = (long long)window + max_new;
+  if (window > 0 && (long long)window + tokens < keys) keys = (long long)window + tokens;
   const long long most = keys / (kKvTile * kMinTiles);
   long long n = 2 * slots / tasks;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
 }
 
-// A launch dimension holds fewer than 2^32 threads (512 to a workgroup).
 bool kv4_grid_ok(const Kv4Dims &dm, int max_new, int window) {
-  return kv4_row_tiles(dm, max_new) * kv4_splits(dm, max_new, window) < (1ll << 23);
+  // a launch dimension holds fewer than 2^32 threads (256 a prefill workgroup
+  // of 128 rows; the other kernel's grids are small)
+  return (long long)max_new * (dm.Hq / dm.Hkv) < (1ll << 31) - 128;
 }
 
 size_t kv4_attention_ws(const Kv4Dims &dm, int max_new, int window) {
-  const int splits = kv4_splits(dm, max_new, window);
+  const int tokens = few_new(dm, max_new);
+  if (tokens == 0) return 0;
+  const int splits = few_splits(dm, tokens, window);
   if (splits == 1) return 0;
-  return (size_t)kv4_tasks(dm, max_new) * splits * kAtRows * (dm.D + 2) * sizeof(float);
+  return (size_t)kv4_tasks(dm, tokens) * splits * kAtRows * (dm.D + 2) * sizeof(float);
 }
 
 template <int D, int W>
-static hipError_t launch_main(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
-                              const Kv4Attn &at, int splits, float *part, hipStream_t s) {
+static hipError_t launch_rows(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
+                              const Kv4Attn &at, int tokens, int splits, float *part, hipStream_t s) {
   if constexpr (at_lds_bytes<D, W>() > 64 * 1024) {  // needs an opt-in, once per process
     static const hipError_t st =
         hipFuncSetAttribute((const void *)kv4_attention_kernel<D, W>,
                             hipFuncAttributeMaxDynamicSharedMemorySize, at_lds_bytes<D, W>());
     if (st != hipSuccess) return st;
   }
-  const long long tiles = kv4_row_tiles(dm, at.max_new);
+  const long long tiles = kv4_row_tiles(dm, tokens);
   const bool flat = splits > 1 && tiles == 1 && dm.B <= kEvenMaxB;
-  const dim3 grid = flat ? dim3((unsigned)(kv4_tasks(dm, at.max_new) * splits)) : dim3((unsigned)(tiles * splits), dm.Hkv, dm.B);
+  const dim3 grid = flat ? dim3((unsigned)(kv4_tasks(dm, tokens) * splits))
+                         : dim3((unsigned)(tiles * splits), dm.Hkv, dm.B);
   kv4_attention_kernel<D, W><<<grid, W * kWave, at_lds_bytes<D, W>(), s>>>(dm, kc, vc, bt, at, splits, flat, part);
   return hipGetLastError();
 }
 
 template <int D>
-static hipError_t launch(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
-                         const Kv4Attn &at, float *part, hipStream_t s) {
-  const int splits = kv4_splits(dm, at.max_new, at.window);
+static hipError_t launch_few(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
+                             const Kv4Attn &at, int tokens, float *part, hipStream_t s) {
+  const int splits = few_splits(dm, tokens, at.window);
   // Eight wavefronts where every workgroup has a CU to itself (a short sequence
   // ends sooner), four where there are more of them or keys are split.
-  const bool few = splits == 1 && kv4_tasks(dm, at.max_new) <= 256;
-  const hipError_t e = few ? launch_main<D, 8>(dm, kc, vc, bt, at, splits, part, s)
-                           : launch_main<D, 4>(dm, kc, vc, bt, at, splits, part, s);
+  const bool alone = splits == 1 && kv4_tasks(dm, tokens) <= 256;
+  const hipError_t e = alone ? launch_rows<D, 8>(dm, kc, vc, bt, at, tokens, splits, part, s)
+                             : launch_rows<D, 4>(dm, kc, vc, bt, at, tokens, splits, part, s);
   if (e != hipSuccess || splits == 1) return e;
-  const unsigned rows = (unsigned)(kv4_row_tiles(dm, at.max_new) * kAtRows);
+  const unsigned rows = (unsigned)(kv4_row_tiles(dm, tokens) * kAtRows);
   if (splits > 16)
     kv4_join_kernel<D, 32><<<dim3(rows * (D / 32), dm.Hkv, dm.B), 256, 0, s>>>(dm, bt, at, splits, part);
   else
@@ -863,10 +837,18 @@ static hipError_t launch(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &
 }
 
 hipError_t launch_kv4_attention(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
-                                const Kv4Batch &bt, const Kv4Attn &at, void *ws, hipStream_t s) {
-  if (dm.D == 64) return launch<64>(dm, kc, vc, bt, at, (float *)ws, s);
-  if (dm.D == 128) return launch<128>(dm, kc, vc, bt, at, (float *)ws, s);
-  return launch<256>(dm, kc, vc, bt, at, (float *)ws, s);
+                                const Kv4Batch &bt, const Kv4Attn &at_in, void *ws, hipStream_t s) {
+  Kv4Attn at = at_in;
+  const int tokens = few_new(dm, at.max_new);
+  const bool many = tokens < at.max_new;
+  if (many) {
+    const hipError_t e = launch_kv4_prefill(dm, kc, vc, bt, at, tokens > 0 ? kManyRows : 0, s);
+    if (e != hipSuccess || tokens == 0) return e;
+  }
+  at.most_rows = many ? kManyRows : 0x7FFFFFFF;
+  if (dm.D == 64) return launch_few<64>(dm, kc, vc, bt, at, tokens, (float *)ws, s);
+  if (dm.D == 128) return launch_few<128>(dm, kc, vc, bt, at, tokens, (float *)ws, s);
+  return launch_few<256>(dm, kc, vc, bt, at, tokens, (float *)ws, s);
 }
 
 }  // namespace moe

@@ -1,0 +1,53 @@
+// Device code shared by the two attention kernels over the 4-bit cache.
+#pragma once
+
+#include "moe_device.h"
+#include "moe_kv4.h"
+
+namespace moe {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// Scaled log2 units a score may exceed the running reference by before the
+// accumulators are rescaled: weights stay below 2^8, far from overflow, and
+// the rescale runs once or twice a row instead of at every new maximum.
+constexpr float kSlack = 8.0f;
+
+typedef const __attribute__((address_space(4))) int32_t kv_const_i32;
+
+// Pages of a tile's two halves (scalar loads; -1: no place).
+struct TilePages {
+  int page[2];
+};
+
+__device__ __forceinline__ TilePages tile_pages(const Kv4Dims &dm, const int32_t *table, int tile) {
+  TilePages p;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const long long t = (long long)tile * kKvTile + 16 * u;
+    const bool in = t < kv4_capacity(dm);
+    const int page = ((kv_const_i32 *)table)[in ? (int)(t >> dm.page_shift) : 0];
+    p.page[u] = in && kv4_page_ok(dm, page) ? page : -1;
+  }
+  return p;
+}
+
+// Query rows of a workgroup: row r of a sequence and cache head is new token
+// r / G, head (cache head) * G + r % G.
+struct RowTile {
+  int seq, head, row0, rows;  // rows: rows of this sequence and head (n * G)
+  Kv4Span sp;
+};
+
+__device__ __forceinline__ RowTile row_tile(const Kv4Dims &dm, const Kv4Batch &bt, int max_new,
+                                            int tile, int head, int seq, int rows_tile) {
+  RowTile t;
+  t.head = head;
+  t.seq = seq;
+  t.row0 = tile * rows_tile;
+  t.sp = kv4_span(bt.cu[seq], bt.cu[seq + 1], bt.len[seq], bt.T);
+  t.rows = min(t.sp.n, max_new) * (dm.Hq / dm.Hkv);
+  return t;
+}
+
+}  // namespace moe

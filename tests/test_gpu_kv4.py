@@ -245,6 +245,12 @@ ATTENTION = [  # new, past, Hq, Hkv, D, page, causal, window
     ([64, 9], [0, 80], 4, 4, 128, 16, False, 0),             # every token sees all
     ([20], [200], 4, 2, 64, 16, False, 50),
     ([150], [700], 20, 4, 256, 128, True, 333),
+    ([300], [0], 2, 2, 64, 16, True, 0),                     # one head a group, three tiles of 128 rows
+    ([257], [1000], 8, 2, 256, 64, True, 0),
+    ([129], [31], 3, 1, 128, 16, True, 40),
+    ([70], [333], 4, 2, 128, 32, False, 0),
+    ([700, 3, 0, 8, 1], [100, 2000, 50, 900, 5000], 16, 2, 128, 64, True, 0),  # prompts and single tokens
+    ([9, 2, 90], [300, 700, 0], 8, 1, 64, 16, True, 150),    # on both sides of 64 rows
 ]
 
 
@@ -347,6 +353,64 @@ def test_outlier_values_keep_their_neighbours():
     out = M.moe_kv4_attention(c, torch.from_numpy(x).cuda().to(BF16), *b.dev, max_new=1)
     want, tol = K.attention(x.astype(np.float64), K.Paged(*host_planes(c), b.table), b.cu, b.len, 0.125)
     check(out, want, tol, "outlier")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["large", "small", "query", "mixed"])
+def test_prompts_outside_fp16(D, kind):
+    """Prompts whose keys, values or queries leave fp16's range (the kernel turns to bf16
+    operands, whose rounding, 2^-8 of every key and value, is added to the bound)."""
+    rng = np.random.default_rng(D)
+    b = Batch(rng, [40, 33], [70, 0], 16)
+    T = sum(b.len)
+    f = {"large": 1e6, "small": 1e-6, "query": 1.0, "mixed": 1.0}[kind]
+    k = bf16_values(tokens(rng, T, 2, D, BF16) * (1.0 if kind == "large" else min(f, 1.0)))
+    v = bf16_values(tokens(rng, T, 2, D, BF16) * f)
+    if kind == "mixed":
+        v[95] *= 1e6  # far into the first sequence: the run starts over there
+    x = bf16_values(rng.standard_normal((b.T, 4, D)))
+    scale = D ** -0.5
+    if kind == "query":
+        x, scale = bf16_values(x * 1e5), scale * 1e-5
+    c = make_cache(b.num_pages, 2, 16, D)
+    M.moe_kv4_append(c, *(torch.from_numpy(a).cuda().to(BF16) for a in (k, v)), b.dev[0],
+                     i32([0] + list(np.cumsum(b.len))), b.dev[2])
+    out = M.moe_kv4_attention(c, torch.from_numpy(x).cuda().to(BF16), *b.dev, max_new=40, scale=scale)
+    scale = float(np.float32(scale))
+    want, tol = K.attention(x.astype(np.float64), K.Paged(*host_planes(c), b.table), b.cu, b.len, scale)
+    # scores off by 2^-8 scale sum |q k|, values by 2^-8 of themselves
+    extra = np.zeros_like(tol)
+    planes = K.Paged(*host_planes(c), b.table)
+    for s in range(b.B):
+        for h in range(2):
+            kc, ks, kb, _ = planes.rows("k", s, h, b.len[s])
+            vc, vs, vb, _ = planes.rows("v", s, h, b.len[s])
+            vmax = np.abs(vs * vc + vb).max(0)
+            for g in (2 * h, 2 * h + 1):
+                rows = slice(b.cu[s], b.cu[s + 1])
+                d = 2.0 ** -8 * scale * (np.abs(x[rows, g]).astype(np.float64) @ np.abs(ks * kc + kb).T).max(1)
+                extra[rows, g] = (2 * d[:, None] + 2.0 ** -8) * vmax
+    check(out, want, tol + extra, f"{kind} {D}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prompt_nan_reaches_only_those_who_see_it(D):
+    rng = np.random.default_rng(29)
+    b = Batch(rng, [80], [50], 16)
+    q64, q = queries(rng, 80, 2, D)
+    at = 50 + 37
+    for which in "kv":
+        c = filled(rng, b, 1, D)
+        m = getattr(c, which)
+        pg, sl = int(b.table[0, at // 16]), at % 16
+        m.scales[pg, 0, sl, -1] = float("nan")
+        m.biases[pg, 0, sl, -1] = float("nan")
+        out = M.moe_kv4_attention(c, q, *b.dev, max_new=80).float().cpu().numpy()
+        want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, D ** -0.5)
+        assert (np.isnan(out) == np.isnan(want)).all()
+        assert np.isfinite(out[:37]).all() and np.isnan(out[37:, :, -64:]).all()
+        ok = ~np.isnan(want)
+        assert np.abs(out[ok] - want[ok]).max() < 0.05 * np.abs(want[ok]).max()
 
 
 def test_offsets_past_32_bits():
