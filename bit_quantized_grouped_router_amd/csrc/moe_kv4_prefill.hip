@@ -45,13 +45,17 @@ template <int D>
 struct Pf {
   static constexpr int NG = D / kGroup, NM = D / 32, NK = D / 16;
   static constexpr int kWords = D / 32;        // code words (8 channels) a thread rebuilds
-  static constexpr int kRow = 2 * D;           // bytes of a rebuilt row
+  // A rebuilt row: its 16-byte chunks, those of the four threads that write it
+  // next to each other, and one more, so that in all three accesses (sixteen
+  // rows' equal chunks, four rows by four threads' chunks, four rows by four
+  // chunks of 32 channels) sixteen lanes meet sixteen different chunks of 256 bytes.
+  static constexpr int kRow = 2 * D + 16;
+  static constexpr __host__ __device__ int place(int chunk) {
+    return (chunk / kWords + 4 * (chunk % kWords)) * 16;
+  }
   static constexpr int kPlane = kKvTile * kRow;
-  static constexpr int kStage = 2 * kPlane;    // keys, then values
-  // D = 256: the queries lie in LDS, in operand order ([wavefront][k-step][lane]
-  // 16 bytes); with 128 registers of sums they do not fit beside them
-  static constexpr bool kQueriesInLds = D == 256;
-  static constexpr int kLds = 2 * kStage + (kQueriesInLds ? kPfRows * kRow : 0);
+  // two buffers of keys, three of values: the scores are one tile ahead
+  static constexpr int kValues = 2 * kPlane, kLds = 5 * kPlane;
 };
 
 // A thread's share of a tile as it lies in the cache: D / 4 channels of one key
@@ -59,18 +63,24 @@ struct Pf {
 template <int D>
 struct Packed {
   uint32_t c[D / 32];
-  uint32_t sb;  // scale | bias << 16
+  uint16_t s, b;
+  bool seen;  // by some row of the workgroup, and of a page that exists
 };
 
-// Can this group go through fp16? Its largest value stays below 2^15, and its
-// scale (or, without one, its bias) is large enough that a sixteenth of it is
-// exact (8 bits above 2^-24) and that fp16's smallest step is no more than
-// 2^-11 of it. False for NaN and infinities.
-__device__ __forceinline__ bool half_ok(uint32_t sb) {
-  const float s = bf16_to_f32(sb & 0xFFFFu), b = bf16_to_f32(sb >> 16);
-  const float big = fmaxf(fabsf(b), fabsf(fmaf(15.0f, s, b))), small = s != 0.f ? fabsf(s) : fabsf(b);
-  return big < 32768.0f && (big == 0.f || small >= 0x1p-13f) && s == s && b == b;
-}
+// Whether all groups so far can go through fp16: scales stay below 2^10 and
+// biases below 2^14, so that values stay below 2^15, and a scale (or, without
+// one, a bias) is at least 2^-13: its sixteenth is then exact (8 bits above
+// 2^-24) and fp16's smallest step is no more than 2^-11 of it. NaN and infinities
+// fail. Bits of the magnitudes are compared; a zero's, less one, are the largest.
+struct HalfRange {
+  uint32_t hi = 0, lo = ~0u;
+  __device__ __forceinline__ void add(uint32_t sb) {
+    const uint32_t s = sb & 0x7FFFu, b = (sb >> 16) & 0x7FFFu;
+    hi = max(max(hi, s + 0x200u), b);
+    lo = min(lo, (s != 0 ? s : b) - 1u);
+  }
+  __device__ __forceinline__ bool bad() const { return hi >= 0x4680u || lo < 0x38FFu; }
+};
 
 // Eight values of a code word as fp16, in the order 0 4 1 5 2 6 3 7: codes as
 // 1024 + q or 1024 + 16 q, exactly, then one packed FMA each.
@@ -132,13 +142,12 @@ __device__ __forceinline__ int prefill_tile(int i, int n, bool causal) {
 
 // Sequences with at most `few` rows are left to the other kernel.
 template <int D>
-__global__ __launch_bounds__(kPfWaves *kWave, 2) void kv4_prefill_kernel(Kv4Dims dm, Kv4Plane kc,
+__global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill_kernel(Kv4Dims dm, Kv4Plane kc,
                                                                                      Kv4Plane vc, Kv4Batch bt,
                                                                                      Kv4Attn at, int few) {
   using P = Pf<D>;
   constexpr int NG = P::NG, NM = P::NM, NK = P::NK;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ __attribute__((aligned(16))) int flags[2][kPfWaves];     // the buffer's tile needs bf16
   __shared__ __attribute__((aligned(4))) uint8_t vnan[2][kKvTile][4];  // its value groups that are NaN (bf16 run)
   const int tile_i = prefill_tile(blockIdx.x, gridDim.x, at.causal);
   const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z, kPfRows);
@@ -167,8 +176,7 @@ __global__ __launch_bounds__(kPfWaves *kWave, 2) void kv4_prefill_kernel(Kv4Dims
       large |= (w[i] & 0x7FFFu) >= 0x4700u || (w[i] & 0x7FFF0000u) >= 0x47000000u;
   }
   const bool any_large = __syncthreads_or(large);
-  uint4 q[P::kQueriesInLds ? 1 : NK];
-  uint4 *const ql = (uint4 *)(smem + 2 * P::kStage) + wave * (NK * kWave) + lane;  // read back by the same lane
+  uint4 q[NK];
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
     const uint4 x = *(const uint4 *)(qp + k * 16);
@@ -178,11 +186,7 @@ __global__ __launch_bounds__(kPfWaves *kWave, 2) void kv4_prefill_kernel(Kv4Dims
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = pack_half(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
-    const uint4 y = make_uint4(w[0], w[1], w[2], w[3]);
-    if constexpr (P::kQueriesInLds)
-      ql[k * kWave] = y;
-    else
-      q[k] = y;
+    q[k] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 
   // keys the first and the last token see, and this lane's row
@@ -197,18 +201,18 @@ __global__ __launch_bounds__(kPfWaves *kWave, 2) void kv4_prefill_kernel(Kv4Dims
     t0 = (int)(mine.lo < mine.hi ? mine.lo : 0);
     t1 = (int)(mine.lo < mine.hi ? mine.hi : 0);
   }
-  const long long all0 = r1.lo, all1 = r0.hi;
+  const int all0 = (int)r1.lo, all1 = (int)(tiles > 0 ? r0.hi : 0);  // what every row sees
 
   // rebuilding: wavefronts 0, 1 take the keys' halves, 2, 3 the values'; four
   // threads a row
   const int32_t *table = bt.table + (long long)rt.seq * dm.max_pages;
-  const int hf = wave & 1, plane = wave >> 1, part = lane & 3, key = 16 * hf + (lane >> 2);
+  const int hf = wave & 1, plane = wave >> 1, part = lane & 3, krow = ((lane >> 4) & 3) | ((lane & 12)), key = 16 * hf + krow;
   const Kv4Plane pl = plane ? vc : kc;
   const DqRegs dk = dq_regs();
   auto fetch = [&](int tile, const TilePages &pg, Packed<D> &r) {
     const int t = tile * kKvTile + key, page = hf ? pg.page[1] : pg.page[0];
     const long long row0 = kv4_row(dm, page < 0 ? 0 : page, rt.head, (tile * kKvTile + 16 * hf) & (dm.page - 1));
-    const uint8_t *c = pl.codes + row0 * (D / 2) + (uint32_t)((lane >> 2) * (D / 2) + part * (D / 8));
+    const uint8_t *c = pl.codes + row0 * (D / 2) + (uint32_t)(krow * (D / 2) + part * (D / 8));
     if constexpr (D == 64) {
       const uint2 x = *(const uint2 *)c;
       r.c[0] = x.x, r.c[1] = x.y;
@@ -219,56 +223,51 @@ __global__ __launch_bounds__(kPfWaves *kWave, 2) void kv4_prefill_kernel(Kv4Dims
         r.c[4 * i] = x.x, r.c[4 * i + 1] = x.y, r.c[4 * i + 2] = x.z, r.c[4 * i + 3] = x.w;
       }
     }
-    const uint32_t g = (uint32_t)((lane >> 2) * NG + part * NG / 4);
-    const uint32_t sb = (uint32_t)(pl.scales + row0 * NG)[g] | ((uint32_t)(pl.biases + row0 * NG)[g] << 16);
+    const uint32_t g = (uint32_t)(krow * NG + part * NG / 4);
+    r.s = (pl.scales + row0 * NG)[g];
+    r.b = (pl.biases + row0 * NG)[g];
+    r.seen = page >= 0 && t >= key_lo && t < key_hi;
+  };
+  // to buffer kb of the keys, the values' at byte vb
+  auto convert = [&](auto half_tag, const Packed<D> &r, int kb, int vb, HalfRange &seen) {
     // what no row of the workgroup sees may be anything: it becomes zeros
-    r.sb = page >= 0 && t >= key_lo && t < key_hi ? sb : 0u;
-  };
-  auto slot = [&](int buf, int w) -> uint4 * {
-    return (uint4 *)(smem + buf * P::kStage + plane * P::kPlane + key * P::kRow + (((part * P::kWords + w) ^ (key & 7)) << 4));
-  };
-  auto convert = [&](auto half_tag, const Packed<D> &r, int buf) {
+    const uint32_t sb = r.seen ? r.s | ((uint32_t)r.b << 16) : 0u;
+    const int at_row = (plane ? P::kValues + vb : kb * P::kPlane) + key * P::kRow + part * 16;
+    auto slot = [&](int w) { return (uint4 *)(smem + at_row + P::place(w)); };
     if constexpr (decltype(half_tag)::value) {
-      const _Float16 s = (_Float16)bf16_to_f32(r.sb & 0xFFFFu), b = (_Float16)bf16_to_f32(r.sb >> 16);
+      const _Float16 s = (_Float16)bf16_to_f32(sb & 0xFFFFu), b = (_Float16)bf16_to_f32(sb >> 16);
       const f16x2_t s2 = {s, s}, b2 = {b, b}, s16 = s2 * (_Float16)0.0625f;
 #pragma unroll
-      for (int w = 0; w < P::kWords; ++w) *slot(buf, w) = rebuild_half(r.c[w], s2, s16, b2, dk);
-      const uint64_t bad = __builtin_amdgcn_ballot_w64(!half_ok(r.sb));
-      if (lane == 0) flags[buf][wave] = bad != 0;
+      for (int w = 0; w < P::kWords; ++w) *slot(w) = rebuild_half(r.c[w], s2, s16, b2, dk);
+      seen.add(sb);
     } else {
-      float s = bf16_to_f32(r.sb & 0xFFFFu), b = bf16_to_f32(r.sb >> 16);
+      float s = bf16_to_f32(sb & 0xFFFFu), b = bf16_to_f32(sb >> 16);
       if (plane == 1) {
         const bool nan = !(fabsf(s) <= 3.402823466e38f) || !(fabsf(b) <= 3.402823466e38f);
-        if ((part * NG) % 4 == 0) vnan[buf][key][part * NG / 4] = nan;
+        if ((part * NG) % 4 == 0) vnan[kb][key][part * NG / 4] = nan;
         if (nan) s = b = 0.f;
       }
 #pragma unroll
-      for (int w = 0; w < P::kWords; ++w) *slot(buf, w) = rebuild_bf16(r.c[w], s, b);
+      for (int w = 0; w < P::kWords; ++w) *slot(w) = rebuild_bf16(r.c[w], s, b);
     }
   };
 
   const float scale2 = at.scale * 1.4426950408889634f;  // scores in log2 units
-  // LDS bytes in a stage. Keys: chunk 2 k + half of row l % 32, XORed with row %
-  // 8, is kbase ^ 32 (k % 4) and 128 (k / 4) on. Values: lane group member j
-  // supplies key j / 4 of a step of four, channels 4 (j % 4) .. +3; block i
-  // (chunks 4 i .. +3) is vbase ^ 64 (i % 2) and 128 (i / 2) on.
+  // Keys: chunk 2 k + half of row l % 32. Values: lane group member j supplies
+  // key j / 4 of a step of four, channels 4 (j % 4) .. +3.
   const int vk = 4 * half + ((lane >> 2) & 3);  // + 8 a step
-  const uint32_t kbase = (lane & 31) * P::kRow + ((half ^ (lane & 7)) << 4);
-  const uint32_t vbase = P::kPlane + vk * P::kRow + (((2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ vk) << 4) + (lane & 1) * 8;
+  const uint32_t kbase = (lane & 31) * P::kRow + P::place(half);
+  const uint32_t vbase = P::kValues + vk * P::kRow + P::place(2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) + (lane & 1) * 8;
 
-  auto attend = [&](auto half_tag, int buf, int key0, const TilePages &pg, f32x16_t (&o)[NM], float &m, float &l,
-                    uint32_t &nan) {
+  // scores of the tile in key buffer kb
+  auto scores = [&](auto half_tag, int kb) {
     constexpr bool HALF = decltype(half_tag)::value;
-    const uint8_t *st = smem + buf * P::kStage;
+    const uint8_t *st = smem + kb * P::kPlane;
     f32x16_t s = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      const uint4 a = *(const uint4 *)(st + (kbase ^ ((k & 3) << 5)) + (k >> 2) * 128);
-      uint4 b;
-      if constexpr (P::kQueriesInLds)
-        b = ql[k * kWave];
-      else
-        b = q[k];
+      const uint4 a = *(const uint4 *)(st + kbase + P::place(2 * k));
+      uint4 b = q[k];
       if constexpr (!HALF) {
         asm volatile("" : "+v"(b.x), "+v"(b.y), "+v"(b.z), "+v"(b.w));  // converted here, not kept
         b.x = any_large ? b.x : half_to_bf16x2(b.x);
@@ -279,18 +278,24 @@ __global__ __launch_bounds__(kPfWaves *kWave, 2) void kv4_prefill_kernel(Kv4Dims
       s = mfma32<HALF>(a, b, s);
       if (!HALF) __builtin_amdgcn_sched_barrier(0);
     }
-    if (D == 256 || !HALF) __builtin_amdgcn_sched_barrier(0);  // one product's operands at a time: registers
-    // register r: key 8 (r / 4) + 4 half + r % 4
-    const bool masked = key0 < all0 || key0 + (long long)kKvTile > all1 || pg.page[0] < 0 || pg.page[1] < 0;
+    return s;
+  };
+  // the scores that this lane's row must not see become -infinity
+  auto mask = [&](auto half_tag, int kb, int key0, const TilePages &pg, f32x16_t &s, uint32_t &nan) {
+    constexpr bool HALF = decltype(half_tag)::value;
+    const bool masked = key0 < all0 || key0 > all1 - kKvTile || (pg.page[0] | pg.page[1]) < 0;
     if (masked || !HALF) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
+      for (int r = 0; r < 16; ++r) {  // register r: key 8 (r / 4) + 4 half + r % 4
         const int k = 8 * (r >> 2) + 4 * half + (r & 3), t = key0 + k;
         const bool seen = pg.page[r >> 3] >= 0 && t >= t0 && t < t1;
         s[r] = seen ? s[r] : kNegInf;
-        if (!HALF) nan |= seen ? *(const uint32_t *)vnan[buf][k] : 0u;
+        if (!HALF) nan |= seen ? *(const uint32_t *)vnan[kb][k] : 0u;
       }
     }
+  };
+  // moves the reference m where the scores exceed it by too much
+  auto rescale = [&](const f32x16_t &s, f32x16_t (&o)[NM], float &m, float &l) {
     float mx = s[0];
 #pragma unroll
     for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
@@ -305,32 +310,6 @@ __global__ __launch_bounds__(kPfWaves *kWave, 2) void kv4_prefill_kernel(Kv4Dims
       l *= alpha;
       m = mn;
     }
-    const float ref = m == kNegInf ? 0.f : m;
-    uint32_t pw[8];
-#pragma unroll
-    for (int r = 0; r < 16; r += 2) {
-      const float p0 = __builtin_amdgcn_exp2f(fmaf(s[r], scale2, -ref));
-      const float p1 = __builtin_amdgcn_exp2f(fmaf(s[r + 1], scale2, -ref));
-      l += p0 + p1;
-      pw[r / 2] = HALF ? pack_half(p0, p1) : pack_bf16x2(p0, p1);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 p = make_uint4(pw[4 * j], pw[4 * j + 1], pw[4 * j + 2], pw[4 * j + 3]);
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        // keys 16 j + 4 half .. +3 and 8 more, channels 32 i + l % 32
-        uint2 v[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v[e] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                               (kv_lds_s16x4 *)(st + (vbase ^ ((i & 1) << 6)) + (i >> 1) * 128 +
-                                                                (16 * j + 8 * e) * P::kRow)));
-        }
-        o[i] = mfma32<HALF>(make_uint4(v[0].x, v[0].y, v[1].x, v[1].y), p, o[i]);
-        if (!HALF || (D == 256 && i % 4 == 3)) __builtin_amdgcn_sched_barrier(0);
-      }
-    }
   };
 
   // All tiles, and the rows' results; false where a tile asks for bf16.
@@ -340,34 +319,93 @@ __global__ __launch_bounds__(kPfWaves *kWave, 2) void kv4_prefill_kernel(Kv4Dims
 #pragma unroll
     for (int i = 0; i < NM; ++i) o[i] = f32x16_t{0};
     float m = kNegInf, l = 0.f;
+    HalfRange seen;
     uint32_t nan = 0;  // value groups (a byte each) that are NaN at a key this row sees
     if (tiles > 0) {
+      // Tile numbers are clamped to the last one, which is rebuilt, and scored,
+      // once or twice too often rather than branched around.
+      const int last_page = (key_hi - 1) >> dm.page_shift;
+      auto entries = [&](int t) {  // of the page table, not looked at until the tile after
+        const int p = (first + min(t, tiles - 1)) * kKvTile;
+        TilePages pg;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          pg.page[u] = ((kv_const_i32 *)table)[min((p + 16 * u) >> dm.page_shift, last_page)];
+        return pg;
+      };
+      auto pages = [&](TilePages pg) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) pg.page[u] = kv4_page_ok(dm, pg.page[u]) ? pg.page[u] : -1;
+        return pg;
+      };
+      auto load = [&](int t, const TilePages &pg, Packed<D> &r) { fetch(first + min(t, tiles - 1), pg, r); };
       Packed<D> r;
-      TilePages here = tile_pages(dm, table, first), next = tile_pages(dm, table, first + min(1, tiles - 1));
-      fetch(first, here, r);
-      convert(half_tag, r, 0);
-      fetch(first + min(1, tiles - 1), next, r);
+      TilePages pg1 = pages(entries(0)), pg2 = pages(entries(1)), pg3 = pages(entries(2)), pg4 = entries(3);
+      load(0, pg1, r);
+      convert(half_tag, r, 0, 0, seen);
+      load(1, pg2, r);
+      if (HALF && __syncthreads_or(seen.bad())) return false;  // most caches that need bf16 do so at once
       lds_barrier();
+      f32x16_t s = scores(half_tag, 0);
+      convert(half_tag, r, 1, P::kPlane, seen);
+      load(2, pg3, r);
+      mask(half_tag, 0, first * kKvTile, pg1, s, nan);
+      rescale(s, o, m, l);
+      pg1 = pg2, pg2 = pg3, pg3 = pages(pg4), pg4 = entries(4);
+      lds_barrier();
+      int vb = 0, wb = 2 * P::kPlane;
       for (int i = 0; i < tiles; ++i) {
-        const int buf = i & 1;
-        const TilePages after = tile_pages(dm, table, first + min(i + 2, tiles - 1));
-        if constexpr (HALF) {
-          // the same for every wavefront: the last barrier came after the flags
-          const int4 f = *(const int4 *)flags[buf];
-          if (__builtin_amdgcn_readfirstlane(f.x | f.y | f.z | f.w) != 0) return false;
+        const int kb = (i + 1) & 1;
+        // scores of tile i + 1 next to the weights of tile i
+        f32x16_t sn = scores(half_tag, kb);
+        if (!HALF || D == 256) __builtin_amdgcn_sched_barrier(0);  // registers
+        const float ref = m == kNegInf ? 0.f : m;
+        uint32_t pw[8];
+        const f16x2_t ones = {(_Float16)1.0f, (_Float16)1.0f};
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e], scale2, -ref));
+          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e + 1], scale2, -ref));
+          if constexpr (HALF) {
+            pw[e / 2] = pack_half(p0, p1);  // and the sum is that of the rounded weights
+            l = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_t, pw[e / 2]), ones, l, false);
+          } else {
+            l += p0 + p1;
+            pw[e / 2] = pack_bf16x2(p0, p1);
+          }
         }
-        if (i + 1 < tiles) {
-          convert(half_tag, r, buf ^ 1);
-          fetch(first + min(i + 2, tiles - 1), after, r);
+        __builtin_amdgcn_sched_barrier(0);
+        // the products of tile i next to the rebuilding of tile i + 2
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint4 p = make_uint4(pw[4 * j], pw[4 * j + 1], pw[4 * j + 2], pw[4 * j + 3]);
+#pragma unroll
+          for (int c = 0; c < NM; ++c) {
+            // keys 16 j + 4 half .. +3 and 8 more, channels 32 c + l % 32
+            uint2 v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              v[e] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                   (kv_lds_s16x4 *)(smem + vb + vbase + P::place(4 * c) +
+                                                                    (16 * j + 8 * e) * P::kRow)));
+            o[c] = mfma32<HALF>(make_uint4(v[0].x, v[0].y, v[1].x, v[1].y), p, o[c]);
+            if (!HALF) __builtin_amdgcn_sched_barrier(0);
+          }
         }
-        if (D == 256 || !HALF) __builtin_amdgcn_sched_barrier(0);
-        attend(half_tag, buf, (first + i) * kKvTile, here, o, m, l, nan);
-        here = next;
-        next = after;
+        convert(half_tag, r, i & 1, wb, seen);
+        __builtin_amdgcn_sched_barrier(0);
+        load(i + 3, pg3, r);
+        mask(half_tag, kb, (first + min(i + 1, tiles - 1)) * kKvTile, pg1, sn, nan);
+        rescale(sn, o, m, l);
+        s = sn;
+        pg1 = pg2, pg2 = pg3, pg3 = pages(pg4), pg4 = entries(i + 5);
+        vb = vb == 2 * P::kPlane ? 0 : vb + P::kPlane;
+        wb = wb == 2 * P::kPlane ? 0 : wb + P::kPlane;
         lds_barrier();
       }
     }
     // register 4 a + b of tile i: channels 32 i + 8 a + 0 4 1 5 (half 0) or 2 6 3 7
+    if (HALF && __syncthreads_or(seen.bad())) return false;
     l += __shfl_xor(l, 32, kWave);
     if (!HALF) nan |= __shfl_xor(nan, 32, kWave);
     if (!real) return true;
