@@ -36,6 +36,10 @@
 namespace moe {
 
 constexpr int kPfWaves = 4, kPfRows = 32 * kPfWaves;
+// Products whose LDS operands are on their way.
+template <bool HALF, int D>
+constexpr int ahead() { return !HALF ? 1 : D == 256 ? 2 : 4; }
+constexpr int kSalu = 0x4;  // sched_barrier: scalar instructions may pass
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -82,19 +86,15 @@ struct HalfRange {
   __device__ __forceinline__ bool bad() const { return hi >= 0x4680u || lo < 0x38FFu; }
 };
 
-// Eight values of a code word as fp16, in the order 0 4 1 5 2 6 3 7: codes as
-// 1024 + q or 1024 + 16 q, exactly, then one packed FMA each.
-__device__ __forceinline__ uint4 rebuild_half(uint32_t c, f16x2_t s, f16x2_t s16, f16x2_t b, const DqRegs &k) {
+// Values of a code word as fp16: those of codes 0 4 1 5, and of 2 6 3 7 from the
+// word shifted by 8. Codes become 1024 + q or 1024 + 16 q, exactly, and then one
+// packed FMA each.
+__device__ __forceinline__ uint2 rebuild_half(uint32_t c, f16x2_t s, f16x2_t s16, f16x2_t b, const DqRegs &k) {
   const f16x2_t off = {(_Float16)1024.0f, (_Float16)1024.0f};
-  const uint32_t y = c >> 8;
   const f16x2_t h0 = __builtin_bit_cast(f16x2_t, and_or(c, k.m_lo, k.magic)) - off;  // 0, 4
   const f16x2_t h1 = __builtin_bit_cast(f16x2_t, and_or(c, k.m_hi, k.magic)) - off;  // 1, 5 (times 16)
-  const f16x2_t h2 = __builtin_bit_cast(f16x2_t, and_or(y, k.m_lo, k.magic)) - off;  // 2, 6
-  const f16x2_t h3 = __builtin_bit_cast(f16x2_t, and_or(y, k.m_hi, k.magic)) - off;  // 3, 7 (times 16)
-  return make_uint4(__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(h0, s, b)),
-                    __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(h1, s16, b)),
-                    __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(h2, s, b)),
-                    __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(h3, s16, b)));
+  return make_uint2(__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(h0, s, b)),
+                    __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(h1, s16, b)));
 }
 
 // The same as bf16.
@@ -140,21 +140,22 @@ __device__ __forceinline__ int prefill_tile(int i, int n, bool causal) {
   return n - 1 - i;
 }
 
-// Sequences with at most `few` rows are left to the other kernel.
-template <int D>
-__global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill_kernel(Kv4Dims dm, Kv4Plane kc,
-                                                                                     Kv4Plane vc, Kv4Batch bt,
-                                                                                     Kv4Attn at, int few) {
+// Whether any thread of the workgroup says so: a barrier, and a scalar branch.
+__device__ __forceinline__ bool any_thread(bool x) {
+  return __builtin_amdgcn_readfirstlane(__syncthreads_or(x)) != 0;
+}
+
+// The tile's rows with fp16 or bf16 operands. False, with nothing written, where
+// fp16 will not do; the same for all threads of the workgroup.
+template <int D, bool HALF>
+__device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
+                                        const Kv4Attn &at, const RowTile &rt, int thread, uint8_t *smem,
+                                        uint8_t (*vnan)[4]) {
   using P = Pf<D>;
-  constexpr int NG = P::NG, NM = P::NM, NK = P::NK;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ __attribute__((aligned(4))) uint8_t vnan[2][kKvTile][4];  // its value groups that are NaN (bf16 run)
-  const int tile_i = prefill_tile(blockIdx.x, gridDim.x, at.causal);
-  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z, kPfRows);
-  if (rt.row0 >= rt.rows || rt.rows <= few) return;
+  constexpr int NG = P::NG, NM = P::NM, NK = P::NK, kAhead = ahead<HALF, D>();
   const int G = dm.Hq / dm.Hkv;
-  const int lane = threadIdx.x & (kWave - 1), half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = thread & (kWave - 1), half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(thread / kWave);
 
   // the tile's first and last token, and this lane's query row
   const int tok0 = rt.row0 / G, in0 = rt.row0 - tok0 * G;
@@ -163,38 +164,33 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
   const bool real = row <= last;
   const int rel = min(row, last) - rt.row0 + in0;
   const int tok = tok0 + rel / G, hd = rt.head * G + rel % G;
-  // its channels in the order rebuilt rows have, as fp16 unless some query of
-  // the workgroup is too large (read twice: cheaper than keeping them meanwhile)
+  // its channels in the order rebuilt rows have
   const uint16_t *qp = at.q + (rt.sp.begin + tok) * at.q_stride + (long long)hd * D + half * 8;
-  bool large = false;
-#pragma unroll
-  for (int k = 0; k < NK; ++k) {
-    const uint4 x = *(const uint4 *)(qp + k * 16);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)  // exponent of either half at least 2^15's, NaN and infinities among them
-      large |= (w[i] & 0x7FFFu) >= 0x4700u || (w[i] & 0x7FFF0000u) >= 0x47000000u;
-  }
-  const bool any_large = __syncthreads_or(large);
   uint4 q[NK];
+  bool large = false;
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
     const uint4 x = *(const uint4 *)(qp + k * 16);
     uint32_t w[4] = {(x.x & 0xFFFFu) | (x.z << 16), (x.x >> 16) | (x.z & 0xFFFF0000u),
                      (x.y & 0xFFFFu) | (x.w << 16), (x.y >> 16) | (x.w & 0xFFFF0000u)};
-    if (!any_large) {
+    if constexpr (HALF) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_half(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+      for (int i = 0; i < 4; ++i) {
+        const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xFFFF0000u);
+        large |= !(fmaxf(fabsf(a), fabsf(b)) < 32768.0f) || a != a || b != b;
+        w[i] = pack_half(a, b);
+      }
     }
     q[k] = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  if (HALF && any_thread(large)) return false;
 
   // keys the first and the last token see, and this lane's row
   const Kv4Range r0 = kv4_range(dm, rt.sp.first + tok0, rt.sp.first + tok0, rt.sp.len, at.causal, at.window);
   const Kv4Range r1 = kv4_range(dm, rt.sp.first + tok1, rt.sp.first + tok1, rt.sp.len, at.causal, at.window);
-  const Kv4Range range{r0.lo, r1.hi};
-  const int tiles = kv4_tiles(range), first = (int)(range.lo / kKvTile);
-  const int key_lo = (int)range.lo, key_hi = (int)(tiles > 0 ? range.hi : 0);  // positions fit 31 bits
+  const Kv4Range both{r0.lo, r1.hi};
+  const int tiles = kv4_tiles(both), first = (int)(both.lo / kKvTile);
+  const int key_lo = (int)both.lo, key_hi = (int)(tiles > 0 ? both.hi : 0);  // positions fit 31 bits
   int t0 = 0, t1 = 0;
   {
     const Kv4Range mine = kv4_range(dm, rt.sp.first + tok, rt.sp.first + tok, rt.sp.len, at.causal, at.window);
@@ -211,7 +207,8 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
   const DqRegs dk = dq_regs();
   auto fetch = [&](int tile, const TilePages &pg, Packed<D> &r) {
     const int t = tile * kKvTile + key, page = hf ? pg.page[1] : pg.page[0];
-    const long long row0 = kv4_row(dm, page < 0 ? 0 : page, rt.head, (tile * kKvTile + 16 * hf) & (dm.page - 1));
+    const uint64_t row0 = (((uint64_t)(uint32_t)max(page, 0) * (uint32_t)dm.Hkv + rt.head) << dm.page_shift) |
+                          (uint32_t)((tile * kKvTile + 16 * hf) & (dm.page - 1));
     const uint8_t *c = pl.codes + row0 * (D / 2) + (uint32_t)(krow * (D / 2) + part * (D / 8));
     if constexpr (D == 64) {
       const uint2 x = *(const uint2 *)c;
@@ -226,30 +223,49 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
     const uint32_t g = (uint32_t)(krow * NG + part * NG / 4);
     r.s = (pl.scales + row0 * NG)[g];
     r.b = (pl.biases + row0 * NG)[g];
-    r.seen = page >= 0 && t >= key_lo && t < key_hi;
+    r.seen = (page | (t - key_lo) | (key_hi - 1 - t)) >= 0;
   };
-  // to buffer kb of the keys, the values' at byte vb
-  auto convert = [&](auto half_tag, const Packed<D> &r, int kb, int vb, HalfRange &seen) {
+  // Rebuilding, to buffer kb of the keys, the values' at byte vb: what the groups
+  // of a row have in common, and then two steps a code word.
+  struct Rebuild {
+    uint8_t *row;
+    f16x2_t s2, s16, b2;
+    float s, b;
+    uint2 first;
+  };
+  auto begin = [&](const Packed<D> &r, int kb, int vb, HalfRange &range) {
     // what no row of the workgroup sees may be anything: it becomes zeros
     const uint32_t sb = r.seen ? r.s | ((uint32_t)r.b << 16) : 0u;
-    const int at_row = (plane ? P::kValues + vb : kb * P::kPlane) + key * P::kRow + part * 16;
-    auto slot = [&](int w) { return (uint4 *)(smem + at_row + P::place(w)); };
-    if constexpr (decltype(half_tag)::value) {
-      const _Float16 s = (_Float16)bf16_to_f32(sb & 0xFFFFu), b = (_Float16)bf16_to_f32(sb >> 16);
-      const f16x2_t s2 = {s, s}, b2 = {b, b}, s16 = s2 * (_Float16)0.0625f;
-#pragma unroll
-      for (int w = 0; w < P::kWords; ++w) *slot(w) = rebuild_half(r.c[w], s2, s16, b2, dk);
-      seen.add(sb);
-    } else {
-      float s = bf16_to_f32(sb & 0xFFFFu), b = bf16_to_f32(sb >> 16);
-      if (plane == 1) {
-        const bool nan = !(fabsf(s) <= 3.402823466e38f) || !(fabsf(b) <= 3.402823466e38f);
-        if ((part * NG) % 4 == 0) vnan[kb][key][part * NG / 4] = nan;
-        if (nan) s = b = 0.f;
-      }
-#pragma unroll
-      for (int w = 0; w < P::kWords; ++w) *slot(w) = rebuild_bf16(r.c[w], s, b);
+    Rebuild c;
+    c.row = smem + (plane ? P::kValues + vb : kb * P::kPlane) + key * P::kRow + part * 16;
+    c.s = bf16_to_f32(sb & 0xFFFFu), c.b = bf16_to_f32(sb >> 16);
+    if constexpr (HALF) {
+      const _Float16 s = (_Float16)c.s, b = (_Float16)c.b;
+      c.s2 = f16x2_t{s, s}, c.b2 = f16x2_t{b, b}, c.s16 = c.s2 * (_Float16)0.0625f;
+      range.add(sb);
+    } else if (plane == 1) {
+      const bool nan = !(fabsf(c.s) <= 3.402823466e38f) || !(fabsf(c.b) <= 3.402823466e38f);
+      if ((part * NG) % 4 == 0) vnan[key][part * NG / 4] = nan;
+      if (nan) c.s = c.b = 0.f;
     }
+    return c;
+  };
+  auto step = [&](const Packed<D> &r, Rebuild &c, int i) {
+    const int w = i / 2;
+    if constexpr (HALF) {
+      const uint2 y = rebuild_half(i % 2 ? r.c[w] >> 8 : r.c[w], c.s2, c.s16, c.b2, dk);
+      if (i % 2)
+        *(uint4 *)(c.row + P::place(w)) = make_uint4(c.first.x, c.first.y, y.x, y.y);
+      else
+        c.first = y;
+    } else if (i % 2) {
+      *(uint4 *)(c.row + P::place(w)) = rebuild_bf16(r.c[w], c.s, c.b);
+    }
+  };
+  auto convert = [&](const Packed<D> &r, int kb, int vb, HalfRange &range) {
+    Rebuild c = begin(r, kb, vb, range);
+#pragma unroll
+    for (int i = 0; i < 2 * P::kWords; ++i) step(r, c, i);
   };
 
   const float scale2 = at.scale * 1.4426950408889634f;  // scores in log2 units
@@ -259,48 +275,38 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
   const uint32_t kbase = (lane & 31) * P::kRow + P::place(half);
   const uint32_t vbase = P::kValues + vk * P::kRow + P::place(2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) + (lane & 1) * 8;
 
-  // scores of the tile in key buffer kb
-  auto scores = [&](auto half_tag, int kb) {
-    constexpr bool HALF = decltype(half_tag)::value;
-    const uint8_t *st = smem + kb * P::kPlane;
+  // Scores of the tile in key buffer kb; other(k) is what runs beside product k.
+  auto scores = [&](int kb, auto other) {
+    const uint8_t *st = smem + kb * P::kPlane + kbase;
     f32x16_t s = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint4 a[NK];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) a[k] = *(const uint4 *)(st + P::place(2 * k));
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      const uint4 a = *(const uint4 *)(st + kbase + P::place(2 * k));
-      uint4 b = q[k];
-      if constexpr (!HALF) {
-        asm volatile("" : "+v"(b.x), "+v"(b.y), "+v"(b.z), "+v"(b.w));  // converted here, not kept
-        b.x = any_large ? b.x : half_to_bf16x2(b.x);
-        b.y = any_large ? b.y : half_to_bf16x2(b.y);
-        b.z = any_large ? b.z : half_to_bf16x2(b.z);
-        b.w = any_large ? b.w : half_to_bf16x2(b.w);
-      }
-      s = mfma32<HALF>(a, b, s);
-      if (!HALF) __builtin_amdgcn_sched_barrier(0);
+      if (k + kAhead < NK) a[k + kAhead] = *(const uint4 *)(st + P::place(2 * (k + kAhead)));
+      s = mfma32<HALF>(a[k], q[k], s);
+      other(k);
+      __builtin_amdgcn_sched_barrier(kSalu);
     }
     return s;
   };
   // the scores that this lane's row must not see become -infinity
-  auto mask = [&](auto half_tag, int kb, int key0, const TilePages &pg, f32x16_t &s, uint32_t &nan) {
-    constexpr bool HALF = decltype(half_tag)::value;
-    const bool masked = key0 < all0 || key0 > all1 - kKvTile || (pg.page[0] | pg.page[1]) < 0;
-    if (masked || !HALF) {
+  auto mask = [&](int key0, const TilePages &pg, f32x16_t &s, uint32_t &nan) {
+    const bool all = (pg.page[0] | pg.page[1] | (key0 - all0) | (all1 - kKvTile - key0)) >= 0;
+    if (__builtin_expect(!all || !HALF, 0)) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {  // register r: key 8 (r / 4) + 4 half + r % 4
         const int k = 8 * (r >> 2) + 4 * half + (r & 3), t = key0 + k;
         const bool seen = pg.page[r >> 3] >= 0 && t >= t0 && t < t1;
         s[r] = seen ? s[r] : kNegInf;
-        if (!HALF) nan |= seen ? *(const uint32_t *)vnan[kb][k] : 0u;
+        if (!HALF) nan |= seen ? *(const uint32_t *)vnan[k] : 0u;
       }
     }
   };
-  // moves the reference m where the scores exceed it by too much
-  auto rescale = [&](const f32x16_t &s, f32x16_t (&o)[NM], float &m, float &l) {
-    float mx = s[0];
-#pragma unroll
-    for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
-    mx *= scale2;
-    if (__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0) {
+  // moves the reference m where a score exceeds it by too much
+  auto rescale = [&](float mx, f32x16_t (&o)[NM], float &m, float &l) {
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0, 0)) {
       const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32, kWave)));
       const float alpha = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - mn);
 #pragma unroll
@@ -312,105 +318,162 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
     }
   };
 
-  // All tiles, and the rows' results; false where a tile asks for bf16.
-  auto run = [&](auto half_tag) -> bool {
-    constexpr bool HALF = decltype(half_tag)::value;
-    f32x16_t o[NM];
-#pragma unroll
-    for (int i = 0; i < NM; ++i) o[i] = f32x16_t{0};
-    float m = kNegInf, l = 0.f;
-    HalfRange seen;
-    uint32_t nan = 0;  // value groups (a byte each) that are NaN at a key this row sees
-    if (tiles > 0) {
-      // Tile numbers are clamped to the last one, which is rebuilt, and scored,
-      // once or twice too often rather than branched around.
-      const int last_page = (key_hi - 1) >> dm.page_shift;
-      auto entries = [&](int t) {  // of the page table, not looked at until the tile after
-        const int p = (first + min(t, tiles - 1)) * kKvTile;
-        TilePages pg;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          pg.page[u] = ((kv_const_i32 *)table)[min((p + 16 * u) >> dm.page_shift, last_page)];
-        return pg;
-      };
-      auto pages = [&](TilePages pg) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) pg.page[u] = kv4_page_ok(dm, pg.page[u]) ? pg.page[u] : -1;
-        return pg;
-      };
-      auto load = [&](int t, const TilePages &pg, Packed<D> &r) { fetch(first + min(t, tiles - 1), pg, r); };
-      Packed<D> r;
-      TilePages pg1 = pages(entries(0)), pg2 = pages(entries(1)), pg3 = pages(entries(2)), pg4 = entries(3);
-      load(0, pg1, r);
-      convert(half_tag, r, 0, 0, seen);
-      load(1, pg2, r);
-      if (HALF && __syncthreads_or(seen.bad())) return false;  // most caches that need bf16 do so at once
-      lds_barrier();
-      f32x16_t s = scores(half_tag, 0);
-      convert(half_tag, r, 1, P::kPlane, seen);
-      load(2, pg3, r);
-      mask(half_tag, 0, first * kKvTile, pg1, s, nan);
-      rescale(s, o, m, l);
-      pg1 = pg2, pg2 = pg3, pg3 = pages(pg4), pg4 = entries(4);
-      lds_barrier();
-      int vb = 0, wb = 2 * P::kPlane;
-      for (int i = 0; i < tiles; ++i) {
-        const int kb = (i + 1) & 1;
-        // scores of tile i + 1 next to the weights of tile i
-        f32x16_t sn = scores(half_tag, kb);
-        if (!HALF || D == 256) __builtin_amdgcn_sched_barrier(0);  // registers
-        const float ref = m == kNegInf ? 0.f : m;
-        uint32_t pw[8];
-        const f16x2_t ones = {(_Float16)1.0f, (_Float16)1.0f};
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e], scale2, -ref));
-          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e + 1], scale2, -ref));
-          if constexpr (HALF) {
-            pw[e / 2] = pack_half(p0, p1);  // and the sum is that of the rounded weights
-            l = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_t, pw[e / 2]), ones, l, false);
-          } else {
-            l += p0 + p1;
-            pw[e / 2] = pack_bf16x2(p0, p1);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        // the products of tile i next to the rebuilding of tile i + 2
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 p = make_uint4(pw[4 * j], pw[4 * j + 1], pw[4 * j + 2], pw[4 * j + 3]);
-#pragma unroll
-          for (int c = 0; c < NM; ++c) {
-            // keys 16 j + 4 half .. +3 and 8 more, channels 32 c + l % 32
-            uint2 v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              v[e] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                   (kv_lds_s16x4 *)(smem + vb + vbase + P::place(4 * c) +
-                                                                    (16 * j + 8 * e) * P::kRow)));
-            o[c] = mfma32<HALF>(make_uint4(v[0].x, v[0].y, v[1].x, v[1].y), p, o[c]);
-            if (!HALF) __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-        convert(half_tag, r, i & 1, wb, seen);
-        __builtin_amdgcn_sched_barrier(0);
-        load(i + 3, pg3, r);
-        mask(half_tag, kb, (first + min(i + 1, tiles - 1)) * kKvTile, pg1, sn, nan);
-        rescale(sn, o, m, l);
-        s = sn;
-        pg1 = pg2, pg2 = pg3, pg3 = pages(pg4), pg4 = entries(i + 5);
-        vb = vb == 2 * P::kPlane ? 0 : vb + P::kPlane;
-        wb = wb == 2 * P::kPlane ? 0 : wb + P::kPlane;
-        lds_barrier();
-      }
+  // Weights of keys e, e + 1 and their sum.
+  auto weigh = [&](const f32x16_t &s, int e, float ref, float &l) {
+    const f16x2_t ones = {(_Float16)1.0f, (_Float16)1.0f};
+    const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e], scale2, -ref));
+    const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e + 1], scale2, -ref));
+    uint32_t w = HALF ? pack_half(p0, p1) : pack_bf16x2(p0, p1);
+    if constexpr (HALF) {
+      asm volatile("" : "+v"(w));  // in this place, not behind the next branch
+      l = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_t, w), ones, l, false);  // of the rounded weights
+    } else {
+      l += p0 + p1;
     }
-    // register 4 a + b of tile i: channels 32 i + 8 a + 0 4 1 5 (half 0) or 2 6 3 7
-    if (HALF && __syncthreads_or(seen.bad())) return false;
-    l += __shfl_xor(l, 32, kWave);
-    if (!HALF) nan |= __shfl_xor(nan, 32, kWave);
-    if (!real) return true;
-    const float sum_inv = l == 0.f ? 0.f : 1.0f / l;
-    uint16_t *out = at.out + (rt.sp.begin + tok) * at.out_stride + (long long)hd * D + 2 * half;
+    return w;
+  };
+  // Value operand of product n: keys 16 (n / NM) + 4 half .. +3 and 8 more, channels 32 (n % NM) + l % 32.
+  auto value = [&](int n, int vb) {
+    uint2 v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      v[e] = __builtin_bit_cast(
+          uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                     (kv_lds_s16x4 *)(smem + vb + vbase + P::place(4 * (n % NM)) + (16 * (n / NM) + 8 * e) * P::kRow)));
+    return make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
+  };
+  auto product = [&](int n, const uint4 &v, const uint32_t (&pw)[8], f32x16_t (&o)[NM]) {
+    const uint32_t *w = pw + n / NM * 4;
+    o[n % NM] = mfma32<HALF>(v, make_uint4(w[0], w[1], w[2], w[3]), o[n % NM]);
+  };
+
+  f32x16_t o[NM];
+#pragma unroll
+  for (int i = 0; i < NM; ++i) o[i] = f32x16_t{0};
+  float m = kNegInf, l = 0.f;
+  HalfRange range;
+  uint32_t nan = 0;  // value groups (a byte each) that are NaN at a key this row sees
+  // Page numbers of 32 tiles at a time lie in a register, two lanes a tile:
+  // scalar loads would return out of order with LDS reads, so that every tile
+  // waited for them. Tile numbers are clamped to the last tile's.
+  const int last_page = (key_hi - 1) >> dm.page_shift;
+  auto entries = [&](int t) {
+    const int p = (first + min(t + (lane >> 1), tiles - 1)) * kKvTile + (lane & 1) * 16;
+    return table[min(p >> dm.page_shift, last_page)];
+  };
+  auto checked = [&](int page) { return kv4_page_ok(dm, page) ? page : -1; };
+  auto pages = [&](int now, int t) {
+    TilePages pg;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) pg.page[u] = __builtin_amdgcn_readlane(now, 2 * (t & 31) + u);
+    return pg;
+  };
+  Packed<D> r;
+  if (HALF && tiles > 0) {
+    // A tile is loaded three tiles ahead of its weights, rebuilt two ahead and
+    // scored one ahead; past the last one it is the last that is rebuilt and
+    // scored again, rather than branched around.
+    auto load = [&](int t, const TilePages &pg) { fetch(first + min(t, tiles - 1), pg, r); };
+    int now = checked(entries(0)), later = entries(32);
+    TilePages pg1 = pages(now, 0), pg2 = pages(now, 1), pg3 = pages(now, 2);
+    load(0, pg1);
+    convert(r, 0, 0, range);
+    load(1, pg2);
+    if (any_thread(range.bad())) return false;  // most caches that need bf16 do so at once
+    lds_barrier();
+    f32x16_t s0 = scores(0, [](int) {}), s1;
+    convert(r, 1, P::kPlane, range);
+    load(2, pg3);
+    mask(first * kKvTile, pg1, s0, nan);
+    float mx = s0[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s0[e]);
+    rescale(mx * scale2, o, m, l);
+    pg1 = pg2, pg2 = pg3, pg3 = pages(now, 3);
+    lds_barrier();
+    int vb = 0, wb = 2 * P::kPlane;
+    // Tile i, whose scores are s, and the scores sn of tile i + 1.
+    auto tile = [&](int i, int kb, const f32x16_t &s, f32x16_t &sn) __attribute__((always_inline)) {
+      const float ref = m == kNegInf ? 0.f : m;
+      uint32_t pw[8];
+      sn = scores(kb, [&](int k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e * NK / 8 == k) pw[e] = weigh(s, 2 * e, ref, l);
+        asm volatile("" : "+v"(l));
+      });
+      mask((first + min(i + 1, tiles - 1)) * kKvTile, pg1, sn, nan);
+      __builtin_amdgcn_sched_barrier(0);
+      // the products of tile i next to the rebuilding of tile i + 2 and the
+      // largest of the new scores
+      uint4 v[2 * NM];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) v[n] = value(n, vb);
+      Rebuild c = begin(r, kb ^ 1, wb, range);
+      mx = kNegInf;
+#pragma unroll
+      for (int n = 0; n < 2 * NM; ++n) {
+        if (n + kAhead < 2 * NM) v[n + kAhead] = value(n + kAhead, vb);
+        product(n, v[n], pw, o);
+        step(r, c, n);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e * NM / 8 == n) mx = fmaxf(mx, sn[e]);
+        asm volatile("" : "+v"(mx));
+        __builtin_amdgcn_sched_barrier(kSalu);
+      }
+      load(i + 3, pg3);
+      if (((i + 4) & 31) == 0) {
+        now = checked(later);
+        later = entries(i + 36);
+      }
+      pg1 = pg2, pg2 = pg3, pg3 = pages(now, i + 4);
+      rescale(mx * scale2, o, m, l);
+      vb = vb == 2 * P::kPlane ? 0 : vb + P::kPlane;
+      wb = wb == 2 * P::kPlane ? 0 : wb + P::kPlane;
+      lds_barrier();
+    };
+    for (int i = 0;;) {
+      tile(i, 1, s0, s1);
+      if (++i == tiles) break;
+      tile(i, 0, s1, s0);
+      if (++i == tiles) break;
+    }
+  }
+  if (!HALF) {  // one tile after the other: with the above twice, registers spill
+    int now = 0;
+    for (int i = 0; i < tiles; ++i) {
+      if ((i & 31) == 0) now = checked(entries(i));
+      const TilePages pg = pages(now, i);
+      fetch(first + i, pg, r);
+      convert(r, 0, 0, range);
+      lds_barrier();
+      f32x16_t s = scores(0, [](int) {});
+      mask((first + i) * kKvTile, pg, s, nan);
+      float mx = s[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
+      rescale(mx * scale2, o, m, l);
+      uint32_t pw[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pw[e] = weigh(s, 2 * e, m == kNegInf ? 0.f : m, l);
+#pragma unroll
+      for (int n = 0; n < 2 * NM; ++n) {
+        product(n, value(n, 0), pw, o);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      lds_barrier();
+    }
+  }
+  if (HALF && any_thread(range.bad())) return false;
+  l += __shfl_xor(l, 32, kWave);
+  if (!HALF) nan |= __shfl_xor(nan, 32, kWave);
+  // register 4 a + b of tile i: channels 32 i + 8 a + 0 4 1 5 (half 0) or 2 6 3 7
+  // (no return from here for rows behind the last: a branch of lanes would have
+  // the second attempt's registers beside the first's)
+  const float sum_inv = l == 0.f ? 0.f : 1.0f / l;
+  uint16_t *out = at.out + (rt.sp.begin + tok) * at.out_stride + (long long)hd * D + 2 * half;
+  if (real) {
 #pragma unroll
     for (int i = 0; i < NM; ++i) {
       const float inv = !HALF && ((nan >> (8 * (i / 2))) & 0xFFu) ? __builtin_nanf("") : sum_inv;
@@ -420,11 +483,24 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
         *(uint32_t *)(out + 32 * i + 8 * a + 4) = pack_bf16x2(o[i][4 * a + 1] * inv, o[i][4 * a + 3] * inv);
       }
     }
-    return true;
-  };
-  if (!any_large && run(std::true_type{})) return;
-  __syncthreads();  // every wavefront has read the flags
-  run(std::false_type{});
+  }
+  return true;
+}
+
+// Sequences with at most `few` rows are left to the other kernel.
+template <int D>
+__global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill_kernel(Kv4Dims dm, Kv4Plane kc,
+                                                                                      Kv4Plane vc, Kv4Batch bt,
+                                                                                      Kv4Attn at, int few) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ __attribute__((aligned(4))) uint8_t vnan[kKvTile][4];  // value groups of a tile that are NaN (bf16)
+  const int tile = prefill_tile(blockIdx.x, gridDim.x, at.causal);
+  const RowTile rt = row_tile(dm, bt, at.max_new, tile, blockIdx.y, blockIdx.z, kPfRows);
+  if (rt.row0 >= rt.rows || rt.rows <= few) return;
+  int thread = threadIdx.x;
+  if (prefill<D, true>(dm, kc, vc, bt, at, rt, thread, smem, vnan)) return;
+  asm volatile("" : "+v"(thread));  // nothing of the first attempt is kept in registers for the second
+  prefill<D, false>(dm, kc, vc, bt, at, rt, thread, smem, vnan);
 }
 
 template <int D>
