@@ -155,10 +155,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: Optional[int] = None) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -536,8 +536,11 @@ def _rows(t: torch.Tensor, shape, name: str, dtypes) -> int:
     if t.dtype not in dtypes:
         raise MoeError(f"{name} has dtype {t.dtype}; expected one of "
                        f"{', '.join(str(d) for d in dtypes)}")
-    if shape[0] > 1 and t.is_contiguous():
-        return t.stride(0)
+    st = t.stride()
+    if shape[0] > 1 and st[-1] == 1:  # the usual cases first: host time counts for a single token
+        row = shape[-1] if len(shape) == 2 else shape[1] * shape[2]
+        if st[0] >= row and (len(shape) == 2 or st[1] == shape[2]):
+            return st[0]
     row = 1
     for i in range(t.dim() - 1, 0, -1):
         if t.shape[i] > 1 and t.stride(i) != row:
@@ -593,7 +596,7 @@ def moe_linear_w4(x: torch.Tensor, w: W4Matrix, bias=None, act: str = "none", re
     _need(w.biases, rows * (cols // GROUP) * 2, "biases", BF16)
     _check(lib().moe_linear_w4(T, rows, cols, x.data_ptr(), xs, w.c(), _ptr(bias),
                                ACTS[act], None if residual is None else residual.data_ptr(), rs,
-                               y.data_ptr(), ys, code, _stream(stream)), "moe_linear_w4")
+                               y.data_ptr(), ys, code, _stream(stream, cur)), "moe_linear_w4")
     return y
 
 
@@ -629,15 +632,10 @@ class KV4Cache:
                             torch.empty(g, dtype=torch.bfloat16, device=device))
         return KV4Cache(plane(), plane())
 
-    def c(self) -> MoeKv4Cache:
-        k, v = self.k, self.v
-        return MoeKv4Cache(_ptr(k.codes), _ptr(k.scales), _ptr(k.biases),
-                           _ptr(v.codes), _ptr(v.scales), _ptr(v.biases))
 
-
-def _kv4(cache: KV4Cache, page_table, cu, kv_len, tokens, Hq: int = 0):
-    """The C structs of a cache and a batch, after checking the batch's tensors and that
-    they, the cache and the token tensors are on the current GPU."""
+def _kv4(cache: KV4Cache, page_table, cu, kv_len, tokens, stream, Hq: int = 0):
+    """The C structs of a cache and a batch and the stream, after checking the batch's tensors
+    and that they, the cache and the token tensors are on the current GPU."""
     if page_table.dim() != 2 or cu.dim() != 1 or kv_len.dim() != 1:
         raise MoeError("page_table must be [B, max_pages], cu [B + 1] and kv_len [B]")
     B, width = page_table.shape
@@ -647,31 +645,39 @@ def _kv4(cache: KV4Cache, page_table, cu, kv_len, tokens, Hq: int = 0):
         raise MoeError(f"page_table, cu and kv_len are {page_table.dtype}, {cu.dtype} and {kv_len.dtype}; "
                        "expected torch.int32")
     cur = torch.cuda.current_device()
-    for t in (page_table, cu, kv_len, cache.k.codes, cache.v.codes, *tokens):
+    k, v = cache.k, cache.v
+    held = (k.codes, k.scales, k.biases, v.codes, v.scales, v.biases, page_table, cu, kv_len)
+    for t in held:
+        if t.get_device() != cur:
+            _wrong_device(**dict(zip(("k.codes", "k.scales", "k.biases", "v.codes", "v.scales", "v.biases",
+                                      "page_table", "cu", "kv_len"), held)))
+        if not t.is_contiguous():
+            raise MoeError("the cache's tensors, page_table, cu and kv_len must be contiguous")
+    for t in tokens:
         if t is not None and t.get_device() != cur:
-            _wrong_device(page_table=page_table, cu=cu, kv_len=kv_len, k_cache=cache.k.codes,
-                          v_cache=cache.v.codes, **{f"token tensor {i}": t for i, t in enumerate(tokens)})
-    return (MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, width), cache.c(),
-            MoeKv4Batch(_ptr(page_table), _ptr(cu), _ptr(kv_len)))
+            _wrong_device(**{f"token tensor {i}": t for i, t in enumerate(tokens)})
+    p = [t.data_ptr() for t in held]
+    return (MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, width), MoeKv4Cache(*p[:6]),
+            MoeKv4Batch(*p[6:]), _stream(stream, cur))
 
 
 def moe_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, page_table, cu, kv_len,
                    stream=None) -> None:
     """Quantise new keys and values [T, Hkv, D] (bf16 or fp32) into the cache. Rows
     cu[b] .. cu[b+1]-1 are the last tokens of sequence b, which then has kv_len[b]."""
-    dm, c, b = _kv4(cache, page_table, cu, kv_len, (k, v))
+    dm, c, b, s = _kv4(cache, page_table, cu, kv_len, (k, v), stream)
     T = k.shape[0]
     dt = _dtype(k.dtype)
     shape = (T, cache.Hkv, cache.D)
     ks, vs = _rows(k, shape, "k", (k.dtype,)), _rows(v, shape, "v", (k.dtype,))
-    _check(lib().moe_kv4_append(dm, c, T, k.data_ptr(), ks, v.data_ptr(), vs, dt, b, _stream(stream)),
+    _check(lib().moe_kv4_append(dm, c, T, k.data_ptr(), ks, v.data_ptr(), vs, dt, b, s),
            "moe_kv4_append")
 
 
 def moe_kv4_read(cache: KV4Cache, page_table, cu, kv_len, T: int, dtype=torch.bfloat16, k=None, v=None,
                  stream=None):
     """Keys and values [T, Hkv, D] of the last cu[b+1] - cu[b] tokens of each sequence."""
-    dm, c, b = _kv4(cache, page_table, cu, kv_len, (k, v))
+    dm, c, b, s = _kv4(cache, page_table, cu, kv_len, (k, v), stream)
     dt = _dtype(dtype)
     shape = (T, cache.Hkv, cache.D)
     ks = vs = cache.Hkv * cache.D
@@ -683,7 +689,7 @@ def moe_kv4_read(cache: KV4Cache, page_table, cu, kv_len, T: int, dtype=torch.bf
         v = _empty(shape, dtype, page_table.device, stream)
     else:
         vs = _rows(v, shape, "v", (dtype,))
-    _check(lib().moe_kv4_read(dm, c, T, k.data_ptr(), ks, v.data_ptr(), vs, dt, b, _stream(stream)),
+    _check(lib().moe_kv4_read(dm, c, T, k.data_ptr(), ks, v.data_ptr(), vs, dt, b, s),
            "moe_kv4_read")
     return k, v
 
@@ -705,7 +711,7 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
     T, Hq, D = q.shape
     if D != cache.D:
         raise MoeError(f"q has {D} channels a head; the cache {cache.D}")
-    dm, c, b = _kv4(cache, page_table, cu, kv_len, (q, out, ws), Hq)
+    dm, c, b, s = _kv4(cache, page_table, cu, kv_len, (q, out, ws), stream, Hq)
     qs = _rows(q, (T, Hq, D), "q", BF16)
     if out is None:
         out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
@@ -721,5 +727,5 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
         need = ws.numel() * ws.element_size()
     _check(L.moe_kv4_attention(dm, c, T, max_new, q.data_ptr(), qs, out.data_ptr(), os_, b,
                                D ** -0.5 if scale is None else scale, int(causal), window, _ptr(ws),
-                               need, _stream(stream)), "moe_kv4_attention")
+                               need, s), "moe_kv4_attention")
     return out

@@ -569,9 +569,12 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
   // pages of the tile in use, of the next one and (not loaded yet) of the one after
   TilePages here{}, next{}, after{};
   if (tile < end) {
-    here = tile_pages(dm, table, tile);
-    next = tile_pages(dm, table, min(tile + W, end - 1));
-    after = tile_pages(dm, table, min(tile + 2 * W, end - 1));
+    const int t1 = min(tile + W, end - 1);
+    here = tile_entries(dm, table, tile);
+    next = tile_entries(dm, table, t1);
+    after = tile_entries(dm, table, min(tile + 2 * W, end - 1));
+    here = tile_pages(dm, here, tile);
+    next = tile_pages(dm, next, t1);
     load_tile<D>(dm, kc, vc, here, rt.head, tile, ring_at, lp, lane);
     if (tile + W < end) load_tile<D>(dm, kc, vc, next, rt.head, tile + W, ring_at + Ring<D>::kStage, lp, lane);
   }
@@ -612,10 +615,10 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
     // every LDS read of this stage is done before the DMA refills it
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     here = next;
-    next = after;
     if (tile + 2 * W < end) {
-      load_tile<D>(dm, kc, vc, after, rt.head, tile + 2 * W, ring_at + stage * Ring<D>::kStage, lp, lane);
-      after = tile_pages(dm, table, min(tile + 3 * W, end - 1));
+      next = tile_pages(dm, after, tile + 2 * W);
+      load_tile<D>(dm, kc, vc, next, rt.head, tile + 2 * W, ring_at + stage * Ring<D>::kStage, lp, lane);
+      after = tile_entries(dm, table, min(tile + 3 * W, end - 1));
     }
   }
 

@@ -15,19 +15,29 @@ constexpr float kSlack = 8.0f;
 
 typedef const __attribute__((address_space(4))) int32_t kv_const_i32;
 
-// Pages of a tile's two halves (scalar loads; -1: no place).
+// Pages of a tile's two halves (-1: no place).
 struct TilePages {
   int page[2];
 };
 
-__device__ __forceinline__ TilePages tile_pages(const Kv4Dims &dm, const int32_t *table, int tile) {
+// The page table's entries (scalar loads), to be looked at a tile later, when
+// they have arrived.
+__device__ __forceinline__ TilePages tile_entries(const Kv4Dims &dm, const int32_t *table, int tile) {
   TilePages p;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const long long t = (long long)tile * kKvTile + 16 * u;
-    const bool in = t < kv4_capacity(dm);
-    const int page = ((kv_const_i32 *)table)[in ? (int)(t >> dm.page_shift) : 0];
-    p.page[u] = in && kv4_page_ok(dm, page) ? page : -1;
+    p.page[u] = ((kv_const_i32 *)table)[t < kv4_capacity(dm) ? (int)(t >> dm.page_shift) : 0];
+  }
+  return p;
+}
+
+__device__ __forceinline__ TilePages tile_pages(const Kv4Dims &dm, const TilePages &entries, int tile) {
+  TilePages p;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const bool in = (long long)tile * kKvTile + 16 * u < kv4_capacity(dm);
+    p.page[u] = in && kv4_page_ok(dm, entries.page[u]) ? entries.page[u] : -1;
   }
   return p;
 }
