@@ -193,7 +193,7 @@ moe_status check_kv4_attention(const moe_kv4_dims *dm, int32_t T, int32_t max_ne
   MOE_TRY(check_kv4_dims(dm, T, true));
   if (max_new < 0 || (max_new == 0 && T > 0) || window < 0) return MOE_E_INVALID;
   if ((long long)T * dm->Hq >= (1ll << 31) - 64) return MOE_E_UNSUPPORTED;
-  if (T > 0 && !kv4_grid_ok(to_kv4_dims(dm), kv4_max_new(T, max_new), window)) return MOE_E_UNSUPPORTED;
+  if (T > 0 && !kv4_grid_ok(to_kv4_dims(dm), kv4_max_new(T, max_new))) return MOE_E_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -514,7 +514,7 @@ moe_status moe_kv4_read(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int3
 size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int32_t max_new,
                                          int32_t window) {
   if (check_kv4_attention(dm, T, max_new, window) != MOE_OK || T == 0) return 0;
-  return kv4_attention_ws(to_kv4_dims(dm), kv4_max_new(T, max_new), window);
+  return kv4_attention_ws(to_kv4_dims(dm), T, kv4_max_new(T, max_new), window);
 }
 
 moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
@@ -532,12 +532,12 @@ moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
   MOE_TRY(check_ptr(out));
   const Kv4Dims d = to_kv4_dims(dm);
   const int n = kv4_max_new(T, max_new);
-  const size_t need = kv4_attention_ws(d, n, window);
+  const size_t need = kv4_attention_ws(d, T, n, window);
   if (need > 0) {
     if (ws_bytes < need) return MOE_E_WORKSPACE;
     MOE_TRY(check_ptr(ws));
   }
-  const Kv4Attn at{q, out, q_stride, out_stride, n, scale, causal != 0, window, 0};
+  const Kv4Attn at{q, out, q_stride, out_stride, n, scale, causal != 0, window, 0, 0};
   return hip_status(launch_kv4_attention(d, to_kv4_plane(cache->k), to_kv4_plane(cache->v),
                                          to_kv4_batch(batch, T), at, ws, as_stream(stream)));
 }

@@ -125,17 +125,17 @@ struct Kv4Attn {
   float scale;
   bool causal;
   int window;
-  int most_rows;  // the row kernel's: sequences with more query rows a head are not its own
+  int above, most;  // a kernel's own sequences: those with more query rows a head than above, and at most `most`
 };
 
-// Workgroups a call's keys are split over, and the bytes of their partial
-// results (0 when they are not split).
-int kv4_splits(const Kv4Dims &dm, int max_new, int window);
-size_t kv4_attention_ws(const Kv4Dims &dm, int max_new, int window);
-bool kv4_grid_ok(const Kv4Dims &dm, int max_new, int window);
-// Sequences of many query rows (n * G); those with at most `few` are skipped.
-hipError_t launch_kv4_prefill(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
-                              const Kv4Batch &bt, const Kv4Attn &at, int few, hipStream_t s);
+// Bytes of a call's partial results (0 when no keys are split), for T token rows
+// of which no sequence has more than max_new.
+size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window);
+bool kv4_grid_ok(const Kv4Dims &dm, int max_new);
+// Sequences of many query rows (n * G), `splits` workgroups to a tile of rows;
+// their partial results are joined by the other.
+hipError_t launch_kv4_prefill(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
+                              const Kv4Attn &at, int splits, float *part, hipStream_t s);
 hipError_t launch_kv4_attention(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
                                 const Kv4Batch &bt, const Kv4Attn &at, void *ws, hipStream_t s);
 #endif

@@ -395,10 +395,10 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
 }
 
 // Keys the tile's rows can see.
-__device__ __forceinline__ Kv4Range tile_range(const Kv4Dims &dm, const RowTile &t, bool causal,
+__device__ __forceinline__ Kv4Range tile_range(const Kv4Dims &dm, const RowTile &t, int rows, bool causal,
                                                int window) {
   const int G = dm.Hq / dm.Hkv;
-  const int last = min(t.row0 + kAtRows, t.rows) - 1;
+  const int last = min(t.row0 + rows, t.rows) - 1;
   return kv4_range(dm, t.sp.first + t.row0 / G, t.sp.first + last / G, t.sp.len, causal, window);
 }
 
@@ -455,7 +455,7 @@ __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch
   float total = 0.f, tasks = 0.f;  // rough figures will do
   for (int b = lane; b < dm.B; b += kWave) {
     int n = min(min(max(bt.cu[b + 1], 0), bt.T) - min(max(bt.cu[b], 0), bt.T), at.max_new);
-    if (n * G > at.most_rows) n = 0;
+    if (n * G > at.most) n = 0;
     float keys = (float)min(max(bt.len[b], 0), cap);
     if (at.window > 0) keys = fminf(keys, (float)at.window + (float)n);
     const float tiles = n > 0 ? ceilf((float)n * G * (1.0f / kAtRows)) : 0.f;
@@ -496,7 +496,7 @@ __device__ __forceinline__ bool work_item(const Kv4Dims &dm, const Kv4Batch &bt,
     const Kv4Span sp = kv4_span(bt.cu[b], bt.cu[b + 1], bt.len[b], bt.T);
     const int n = min(sp.n, at.max_new);
     const Kv4Range r = kv4_range(dm, sp.first, sp.first + max(n, 1) - 1, sp.len, at.causal, at.window);
-    const int used = b0 + lane < dm.B && n > 0 && n * (dm.Hq / dm.Hkv) <= at.most_rows ? kv4_share(r, per, splits, 0).used : 0;
+    const int used = b0 + lane < dm.B && n > 0 && n * (dm.Hq / dm.Hkv) <= at.most ? kv4_share(r, per, splits, 0).used : 0;
     const int upto = wave_scan(used * dm.Hkv);
     const uint64_t after = __builtin_amdgcn_ballot_w64(upto > item);
     if (after != 0) {
@@ -517,12 +517,12 @@ __device__ __forceinline__ bool work_item(const Kv4Dims &dm, const Kv4Batch &bt,
 template <int D, int W>
 __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
                                             const Kv4Batch &bt, const Kv4Attn &at, int seq, int head,
-                                            int tile_i, int tiles, int split, int splits, int per,
+                                            int tile_i, int split, int splits, int per,
                                             uint8_t *smem, float (*sm)[kAtRows], float (*sl)[kAtRows],
                                             float *__restrict__ part) {
   constexpr int NG = D / kGroup;
   const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, head, seq, kAtRows);
-  if (rt.row0 >= rt.rows || rt.rows > at.most_rows) return;
+  if (rt.row0 >= rt.rows || rt.rows > at.most) return;
   const int G = dm.Hq / dm.Hkv;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -647,7 +647,6 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
   }
   __syncthreads();
   constexpr int kThreadsRow = D / 4;
-  const long long task = ((long long)seq * dm.Hkv + head) * tiles + tile_i;
   for (int r = threadIdx.x / kThreadsRow; r < kAtRows && rt.row0 + r < rt.rows; r += W * kWave / kThreadsRow) {
     const int c = (threadIdx.x % kThreadsRow) * 4;
     float mr = kNegInf, l = 0.f;
@@ -661,11 +660,9 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
       l = fmaf(part_weight(sm[w][r], sl[w][r], mr), sl[w][r], l);
     }
     if (share.used > 1) {
-      // partial [task][split][16][D], then reference and sum [task][split][16][2]
-      const long long pr = (task * splits + split) * kAtRows + r;
+      const long long pr = part_index(dm, rt, r, splits, split);
       *(float4 *)(part + pr * D + c) = o;
-      if (c == 0)
-        *(float2 *)(part + (long long)dm.B * dm.Hkv * tiles * splits * kAtRows * D + pr * 2) = make_float2(mr, l);
+      if (c == 0) *(float2 *)(part_stats(dm, bt, splits, part) + pr * 2) = make_float2(mr, l);
     } else {
       const int x = r + in0, i = tok0 + x / G, h = rt.head * G + x % G;
       store_row(dm, at, rt.sp.begin + i, h, c, l, o);
@@ -682,7 +679,7 @@ __global__ __launch_bounds__(W *kWave, at_blocks<D>()) void kv4_attention_kernel
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ float sm[W][kAtRows], sl[W][kAtRows];
   const int per = splits > 1 ? tiles_per_split<D>(dm, bt, at) : 0;
-  int seq = blockIdx.z, head = blockIdx.y, tile_i = blockIdx.x, tiles = gridDim.x, split = 0;
+  int seq = blockIdx.z, head = blockIdx.y, tile_i = blockIdx.x, split = 0;
   if (flat) {
     // there are never more items than workgroups: a task has at most `splits`
     Item it;
@@ -691,80 +688,73 @@ __global__ __launch_bounds__(W *kWave, at_blocks<D>()) void kv4_attention_kernel
     head = it.head;
     split = it.split;
     tile_i = 0;
-    tiles = 1;
   } else if (splits > 1) {
-    tiles = gridDim.x / splits;
     tile_i = blockIdx.x / splits;
     split = blockIdx.x - tile_i * splits;
   }
-  attend_rows<D, W>(dm, kc, vc, bt, at, seq, head, tile_i, tiles, split, splits, per, smem, sm, sl, part);
+  attend_rows<D, W>(dm, kc, vc, bt, at, seq, head, tile_i, split, splits, per, smem, sm, sl, part);
 }
 
-// Joins the splits' partial results: one workgroup per row of a task and C of
-// its channels. C = D where splits are few; C = 32 where they are many, so that
-// 32 parts are read at a time and the card has more workgroups to run.
-template <int D, int C>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Attn at,
-                                                       int splits, const float *__restrict__ part) {
-  constexpr int kThreadsRow = C / 4, kParts = 256 / kThreadsRow, kChunks = D / C;
+// Joins the splits' partial results of a row tile of ROWS. Few splits (C = D): D /
+// 4 threads a row, each over all its splits. Many (C = 32): a workgroup for 32
+// channels of a row, 32 parts at a time.
+template <int D, int C, int ROWS>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Attn at, int splits,
+                                                       float *__restrict__ part) {
+  constexpr int kThreadsRow = C / 4, kGroups = 256 / kThreadsRow;
+  constexpr int kParts = C < D ? kGroups : 1, kRows = C < D ? 1 : kGroups, kChunks = D / C;
+  static_assert(ROWS % kRows == 0, "a workgroup's rows are of one tile");
   __shared__ float4 so[kParts][kThreadsRow];
   __shared__ float sl[kParts];
-  const int chunk = blockIdx.x % kChunks, r = blockIdx.x / kChunks % kAtRows, tile_i = blockIdx.x / (kChunks * kAtRows);
-  const int tiles = gridDim.x / (kChunks * kAtRows);
-  const long long task = ((long long)blockIdx.z * dm.Hkv + blockIdx.y) * tiles + tile_i;
-  const long long tasks = (long long)gridDim.z * gridDim.y * tiles;
-  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z, kAtRows);
-  if (rt.row0 + r >= rt.rows || rt.rows > at.most_rows) return;
-  const Kv4Range range = tile_range(dm, rt, at.causal, at.window);
-  const int used = kv4_share(range, tiles_per_split<D>(dm, bt, at), splits, 0).used;
-  if (used <= 1) return;
-  const float *ml = part + tasks * splits * kAtRows * D;
-  const long long pr0 = task * splits * kAtRows + r;
-  // the row's reference: every wavefront looks at all the splits'
-  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int tid = threadIdx.x, c = tid % kThreadsRow, group = tid / kThreadsRow;
+  const int chunk = blockIdx.x % kChunks, first = blockIdx.x / kChunks * kRows;
+  const int tile_i = first / ROWS, r = first - tile_i * ROWS + (C < D ? 0 : group), part_i = C < D ? group : 0;
+  const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z, ROWS);
+  if (rt.row0 + first - tile_i * ROWS >= rt.rows || rt.rows <= at.above || rt.rows > at.most) return;
+  const Kv4Range range = tile_range(dm, rt, ROWS, at.causal, at.window);
+  const int per = ROWS == kAtRows ? tiles_per_split<D>(dm, bt, at) : kPfMinTiles;
+  const int used = kv4_share(range, per, splits, 0).used;
+  if (used <= 1 || rt.row0 + r >= rt.rows) return;
+  const float *ml = part_stats(dm, bt, splits, part);
+  const long long pr0 = part_index(dm, rt, r, splits, 0);
+  // the row's reference
   float m = kNegInf;
-  for (int s = lane; s < used; s += kWave) m = fmaxf(m, ml[(pr0 + (long long)s * kAtRows) * 2]);
+  if constexpr (C < D) {  // every wavefront looks at all the splits'
+    for (int s = tid & (kWave - 1); s < used; s += kWave) m = fmaxf(m, ml[(pr0 + s) * 2]);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
-  const int c = tid % kThreadsRow, part_i = tid / kThreadsRow;
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+  } else {
+    for (int s = 0; s < used; ++s) m = fmaxf(m, ml[(pr0 + s) * 2]);
+  }
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = part_i; s < used; s += kParts) {
-    const long long pr = pr0 + (long long)s * kAtRows;
+    const long long pr = pr0 + s;
     const float2 mls = *(const float2 *)(ml + pr * 2);
     const float4 x = *(const float4 *)(part + pr * D + chunk * C + c * 4);
     const float f = part_weight(mls.x, mls.y, m);
     l = fmaf(f, mls.y, l);
     o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
   }
-  so[part_i][c] = o;
-  if (c == 0) sl[part_i] = l;
-  __syncthreads();
-  if (part_i == 0) {
+  if constexpr (kParts > 1) {
+    so[part_i][c] = o;
+    if (c == 0) sl[part_i] = l;
+    __syncthreads();
+    if (part_i != 0) return;
 #pragma unroll
     for (int i = 1; i < kParts; ++i) {
       const float4 x = so[i][c];
       o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
       l += sl[i];
     }
-    const int G = dm.Hq / dm.Hkv, x = rt.row0 + r;
-    store_row(dm, at, rt.sp.begin + x / G, rt.head * G + x % G, chunk * C + c * 4, l, o);
   }
+  const int G = dm.Hq / dm.Hkv, x = rt.row0 + r;
+  store_row(dm, at, rt.sp.begin + x / G, rt.head * G + x % G, chunk * C + c * 4, l, o);
 }
 
-// Query rows of a sequence and head above which the prefill kernel takes it: it
-// rebuilds the keys once for 128 rows, this one reads them once for 16.
+// Query rows of a sequence and head above which the prefill kernel can take it.
 constexpr int kManyRows = 64;
-
-// The new tokens a sequence may have to be this file's kernel's: 0 if none is. A
-// batch of one with many rows goes to the other kernel whole, so that a prompt
-// takes one launch.
-static int few_new(const Kv4Dims &dm, int max_new) {
-  const int G = dm.Hq / dm.Hkv;
-  if ((long long)max_new * G <= kManyRows) return max_new;
-  return dm.B == 1 ? 0 : kManyRows / G;
-}
 
 // Row tiles of a sequence and head (an upper bound: it may have fewer new
 // tokens), and over all sequences and heads.
@@ -776,32 +766,70 @@ static long long kv4_tasks(const Kv4Dims &dm, int tokens) {
   return kv4_row_tiles(dm, tokens) * dm.Hkv * dm.B;
 }
 
-// The most workgroups a sequence's keys are split over: as many as have
-// kMinTiles each (of the table's width: the host does not know the lengths),
-// and no more than twice the card's slots over all tasks.
+// Keys a row tile can see (of the table's width: the host does not know the lengths).
+static long long kv4_keys(const Kv4Dims &dm, int tokens, int window) {
+  const long long keys = kv4_capacity(dm);
+  return window > 0 && (long long)window + tokens < keys ? (long long)window + tokens : keys;
+}
+
+// The most workgroups a row tile's keys are split over: as many as have
+// kMinTiles each, and no more than the card's slots over all tasks, or twice
+// that where sequences have one row tile each (work_item() evens those out).
 static int few_splits(const Kv4Dims &dm, int tokens, int window) {
   const long long tasks = kv4_tasks(dm, tokens);
   const int slots = dm.D == 256 ? at_slots<256>() : dm.D == 128 ? at_slots<128>() : at_slots<64>();
-  long long keys = kv4_capacity(dm);
-  if (window > 0 && (long long)window + tokens < keys) keys = (long long)window + tokens;
-  const long long most = keys / (kKvTile * kMinTiles);
-  long long n = 2 * slots / tasks;
+  const long long most = kv4_keys(dm, tokens, window) / (kKvTile * kMinTiles);
+  long long n = (kv4_row_tiles(dm, tokens) == 1 ? 2 : 1) * slots / tasks;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
 }
 
-bool kv4_grid_ok(const Kv4Dims &dm, int max_new, int window) {
-  // a launch dimension holds fewer than 2^32 threads (256 a prefill workgroup
-  // of 128 rows; the other kernel's grids are small)
-  return (long long)max_new * (dm.Hq / dm.Hkv) < (1ll << 31) - 128;
+// How a call's sequences are shared between the two kernels.
+struct Kv4Plan {
+  bool many;       // the prefill kernel takes those with more than kManyRows rows
+  int few;         // new tokens a sequence of the row kernel can have; 0: it has none
+  int pre_splits, row_splits;
+};
+
+// The prefill kernel reads and rebuilds keys once for 128 rows instead of 16, but
+// starts slower and needs rows to fill its tiles. us of the prefill kernel / of
+// this one, D = 128, 16 query heads on 2 (and 8 on 8), by new tokens + earlier
+// ones: 128 + 0: 14 / 7 (15 / 7), 1024 + 0: 36 / 28 (37 / 19), 2048 + 0: 65 / 70
+// (48 / 45), 128 + 8000: 49 / 42 (45 / 28), 512 + 60000: 339 / 778 (215 / 398),
+// 1024 + 16000: 244 / 385 (136 / 223); D = 64 and 256 cross over at the same
+// products of rows and keys. Below 4096 rows it gains 20% at the most.
+static bool kv4_many(const Kv4Dims &dm, int T, long long keys) {
+  const long long rows = (long long)T * dm.Hq;
+  return rows >= 4096 && rows * keys >= 1ll << 25;
 }
 
-size_t kv4_attention_ws(const Kv4Dims &dm, int max_new, int window) {
-  const int tokens = few_new(dm, max_new);
-  if (tokens == 0) return 0;
-  const int splits = few_splits(dm, tokens, window);
-  if (splits == 1) return 0;
-  return (size_t)kv4_tasks(dm, tokens) * splits * kAtRows * (dm.D + 2) * sizeof(float);
+static Kv4Plan kv4_plan(const Kv4Dims &dm, int T, int max_new, int window) {
+  const int G = dm.Hq / dm.Hkv;
+  Kv4Plan p{false, max_new, 1, 1};
+  const long long keys = kv4_keys(dm, 128 / G, window);
+  if ((long long)max_new * G > kManyRows && kv4_many(dm, T, keys)) {
+    p.many = true;
+    p.few = dm.B == 1 ? 0 : kManyRows / G;
+    // enough workgroups for every slot (two a CU, one for D = 256)
+    const long long tiles = (long long)T * dm.Hq / 128 + (long long)(dm.B < T ? dm.B : T) * dm.Hkv;
+    long long n = ((dm.D == 256 ? 256 : 512) + tiles / 2) / tiles;
+    if (n > keys / (kKvTile * kPfMinTiles)) n = keys / (kKvTile * kPfMinTiles);
+    p.pre_splits = n < 1 ? 1 : (int)n;
+  }
+  if (p.few > 0) p.row_splits = few_splits(dm, p.few, window);
+  return p;
+}
+
+bool kv4_grid_ok(const Kv4Dims &dm, int max_new) {
+  // a launch dimension holds fewer than 2^32 threads: 256 for 16 rows, at the
+  // most (splits only multiply small grids)
+  return (long long)max_new * (dm.Hq / dm.Hkv) < (1ll << 28) - 128;
+}
+
+size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window) {
+  const Kv4Plan p = kv4_plan(dm, T, max_new, window);
+  const int splits = p.pre_splits > p.row_splits ? p.pre_splits : p.row_splits;
+  return splits == 1 ? 0 : (size_t)T * dm.Hq * splits * (dm.D + 2) * sizeof(float);
 }
 
 template <int D, int W>
@@ -821,37 +849,47 @@ static hipError_t launch_rows(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pl
   return hipGetLastError();
 }
 
-template <int D>
-static hipError_t launch_few(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
-                             const Kv4Attn &at, int tokens, float *part, hipStream_t s) {
-  const int splits = few_splits(dm, tokens, at.window);
-  // Eight wavefronts where every workgroup has a CU to itself (a short sequence
-  // ends sooner), four where there are more of them or keys are split.
-  const bool alone = splits == 1 && kv4_tasks(dm, tokens) <= 256;
-  const hipError_t e = alone ? launch_rows<D, 8>(dm, kc, vc, bt, at, tokens, splits, part, s)
-                             : launch_rows<D, 4>(dm, kc, vc, bt, at, tokens, splits, part, s);
-  if (e != hipSuccess || splits == 1) return e;
-  const unsigned rows = (unsigned)(kv4_row_tiles(dm, tokens) * kAtRows);
+template <int D, int ROWS>
+static hipError_t launch_join(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Attn &at, int tokens, int splits,
+                              float *part, hipStream_t s) {
+  const long long rows = (long long)tokens * (dm.Hq / dm.Hkv);
+  const unsigned all = (unsigned)((rows + ROWS - 1) / ROWS * ROWS);
   if (splits > 16)
-    kv4_join_kernel<D, 32><<<dim3(rows * (D / 32), dm.Hkv, dm.B), 256, 0, s>>>(dm, bt, at, splits, part);
+    kv4_join_kernel<D, 32, ROWS><<<dim3(all * (D / 32), dm.Hkv, dm.B), 256, 0, s>>>(dm, bt, at, splits, part);
   else
-    kv4_join_kernel<D, D><<<dim3(rows, dm.Hkv, dm.B), 256, 0, s>>>(dm, bt, at, splits, part);
+    kv4_join_kernel<D, D, ROWS><<<dim3(all / (1024 / D), dm.Hkv, dm.B), 256, 0, s>>>(dm, bt, at, splits, part);
   return hipGetLastError();
 }
 
-hipError_t launch_kv4_attention(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
-                                const Kv4Batch &bt, const Kv4Attn &at_in, void *ws, hipStream_t s) {
-  Kv4Attn at = at_in;
-  const int tokens = few_new(dm, at.max_new);
-  const bool many = tokens < at.max_new;
-  if (many) {
-    const hipError_t e = launch_kv4_prefill(dm, kc, vc, bt, at, tokens > 0 ? kManyRows : 0, s);
-    if (e != hipSuccess || tokens == 0) return e;
+template <int D>
+static hipError_t launch_all(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
+                             Kv4Attn at, float *part, hipStream_t s) {
+  const Kv4Plan p = kv4_plan(dm, bt.T, at.max_new, at.window);
+  hipError_t e = hipSuccess;
+  if (p.many) {
+    at.above = p.few > 0 ? kManyRows : 0;
+    at.most = 0x7FFFFFFF;
+    e = launch_kv4_prefill(dm, kc, vc, bt, at, p.pre_splits, part, s);
+    if (e == hipSuccess && p.pre_splits > 1) e = launch_join<D, 128>(dm, bt, at, at.max_new, p.pre_splits, part, s);
+    if (e != hipSuccess || p.few == 0) return e;
   }
-  at.most_rows = many ? kManyRows : 0x7FFFFFFF;
-  if (dm.D == 64) return launch_few<64>(dm, kc, vc, bt, at, tokens, (float *)ws, s);
-  if (dm.D == 128) return launch_few<128>(dm, kc, vc, bt, at, tokens, (float *)ws, s);
-  return launch_few<256>(dm, kc, vc, bt, at, tokens, (float *)ws, s);
+  // the partial results of the one above have been read when this one's come
+  at.above = 0;
+  at.most = p.many ? kManyRows : 0x7FFFFFFF;
+  // Eight wavefronts where every workgroup has a CU to itself (a short sequence
+  // ends sooner), four where there are more of them or keys are split.
+  const bool alone = p.row_splits == 1 && kv4_tasks(dm, p.few) <= 256;
+  e = alone ? launch_rows<D, 8>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s)
+            : launch_rows<D, 4>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s);
+  if (e == hipSuccess && p.row_splits > 1) e = launch_join<D, kAtRows>(dm, bt, at, p.few, p.row_splits, part, s);
+  return e;
+}
+
+hipError_t launch_kv4_attention(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
+                                const Kv4Batch &bt, const Kv4Attn &at, void *ws, hipStream_t s) {
+  if (dm.D == 64) return launch_all<64>(dm, kc, vc, bt, at, (float *)ws, s);
+  if (dm.D == 128) return launch_all<128>(dm, kc, vc, bt, at, (float *)ws, s);
+  return launch_all<256>(dm, kc, vc, bt, at, (float *)ws, s);
 }
 
 }  // namespace moe

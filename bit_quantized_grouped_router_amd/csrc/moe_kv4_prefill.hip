@@ -149,8 +149,8 @@ __device__ __forceinline__ bool any_thread(bool x) {
 // fp16 will not do; the same for all threads of the workgroup.
 template <int D, bool HALF>
 __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
-                                        const Kv4Attn &at, const RowTile &rt, int thread, uint8_t *smem,
-                                        uint8_t (*vnan)[4]) {
+                                        const Kv4Attn &at, const RowTile &rt, int split, int splits, float *part,
+                                        int thread, uint8_t *smem, uint8_t (*vnan)[4]) {
   using P = Pf<D>;
   constexpr int NG = P::NG, NM = P::NM, NK = P::NK, kAhead = ahead<HALF, D>();
   const int G = dm.Hq / dm.Hkv;
@@ -189,7 +189,9 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   const Kv4Range r0 = kv4_range(dm, rt.sp.first + tok0, rt.sp.first + tok0, rt.sp.len, at.causal, at.window);
   const Kv4Range r1 = kv4_range(dm, rt.sp.first + tok1, rt.sp.first + tok1, rt.sp.len, at.causal, at.window);
   const Kv4Range both{r0.lo, r1.hi};
-  const int tiles = kv4_tiles(both), first = (int)(both.lo / kKvTile);
+  const Kv4Share share = kv4_share(both, splits > 1 ? kPfMinTiles : 0, splits, split);
+  if (split >= share.used) return true;
+  const int tiles = share.end - share.begin, first = share.begin;
   const int key_lo = (int)both.lo, key_hi = (int)(tiles > 0 ? both.hi : 0);  // positions fit 31 bits
   int t0 = 0, t1 = 0;
   {
@@ -202,14 +204,14 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   // rebuilding: wavefronts 0, 1 take the keys' halves, 2, 3 the values'; four
   // threads a row
   const int32_t *table = bt.table + (long long)rt.seq * dm.max_pages;
-  const int hf = wave & 1, plane = wave >> 1, part = lane & 3, krow = ((lane >> 4) & 3) | ((lane & 12)), key = 16 * hf + krow;
+  const int hf = wave & 1, plane = wave >> 1, quarter = lane & 3, krow = ((lane >> 4) & 3) | ((lane & 12)), key = 16 * hf + krow;
   const Kv4Plane pl = plane ? vc : kc;
   const DqRegs dk = dq_regs();
   auto fetch = [&](int tile, const TilePages &pg, Packed<D> &r) {
     const int t = tile * kKvTile + key, page = hf ? pg.page[1] : pg.page[0];
     const uint64_t row0 = (((uint64_t)(uint32_t)max(page, 0) * (uint32_t)dm.Hkv + rt.head) << dm.page_shift) |
                           (uint32_t)((tile * kKvTile + 16 * hf) & (dm.page - 1));
-    const uint8_t *c = pl.codes + row0 * (D / 2) + (uint32_t)(krow * (D / 2) + part * (D / 8));
+    const uint8_t *c = pl.codes + row0 * (D / 2) + (uint32_t)(krow * (D / 2) + quarter * (D / 8));
     if constexpr (D == 64) {
       const uint2 x = *(const uint2 *)c;
       r.c[0] = x.x, r.c[1] = x.y;
@@ -220,7 +222,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
         r.c[4 * i] = x.x, r.c[4 * i + 1] = x.y, r.c[4 * i + 2] = x.z, r.c[4 * i + 3] = x.w;
       }
     }
-    const uint32_t g = (uint32_t)(krow * NG + part * NG / 4);
+    const uint32_t g = (uint32_t)(krow * NG + quarter * NG / 4);
     r.s = (pl.scales + row0 * NG)[g];
     r.b = (pl.biases + row0 * NG)[g];
     r.seen = (page | (t - key_lo) | (key_hi - 1 - t)) >= 0;
@@ -237,7 +239,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
     // what no row of the workgroup sees may be anything: it becomes zeros
     const uint32_t sb = r.seen ? r.s | ((uint32_t)r.b << 16) : 0u;
     Rebuild c;
-    c.row = smem + (plane ? P::kValues + vb : kb * P::kPlane) + key * P::kRow + part * 16;
+    c.row = smem + (plane ? P::kValues + vb : kb * P::kPlane) + key * P::kRow + quarter * 16;
     c.s = bf16_to_f32(sb & 0xFFFFu), c.b = bf16_to_f32(sb >> 16);
     if constexpr (HALF) {
       const _Float16 s = (_Float16)c.s, b = (_Float16)c.b;
@@ -245,7 +247,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
       range.add(sb);
     } else if (plane == 1) {
       const bool nan = !(fabsf(c.s) <= 3.402823466e38f) || !(fabsf(c.b) <= 3.402823466e38f);
-      if ((part * NG) % 4 == 0) vnan[key][part * NG / 4] = nan;
+      if ((quarter * NG) % 4 == 0) vnan[key][quarter * NG / 4] = nan;
       if (nan) c.s = c.b = 0.f;
     }
     return c;
@@ -471,7 +473,11 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   // register 4 a + b of tile i: channels 32 i + 8 a + 0 4 1 5 (half 0) or 2 6 3 7
   // (no return from here for rows behind the last: a branch of lanes would have
   // the second attempt's registers beside the first's)
-  const float sum_inv = l == 0.f ? 0.f : 1.0f / l;
+  const bool partial = share.used > 1;
+  const float sum_inv = partial ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
+  const long long pr = part_index(dm, rt, real ? row - rt.row0 : 0, splits, split);
+  float *sums = part + pr * D + 2 * half;
+  if (partial && real && half == 0) *(float2 *)(part_stats(dm, bt, splits, part) + pr * 2) = make_float2(m, l);
   uint16_t *out = at.out + (rt.sp.begin + tok) * at.out_stride + (long long)hd * D + 2 * half;
   if (real) {
 #pragma unroll
@@ -479,49 +485,65 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
       const float inv = !HALF && ((nan >> (8 * (i / 2))) & 0xFFu) ? __builtin_nanf("") : sum_inv;
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        *(uint32_t *)(out + 32 * i + 8 * a) = pack_bf16x2(o[i][4 * a] * inv, o[i][4 * a + 2] * inv);
-        *(uint32_t *)(out + 32 * i + 8 * a + 4) = pack_bf16x2(o[i][4 * a + 1] * inv, o[i][4 * a + 3] * inv);
+        const float c0 = o[i][4 * a] * inv, c1 = o[i][4 * a + 2] * inv;  // channels + 0, 1
+        const float c4 = o[i][4 * a + 1] * inv, c5 = o[i][4 * a + 3] * inv;
+        if (partial) {
+          *(float2 *)(sums + 32 * i + 8 * a) = make_float2(c0, c1);
+          *(float2 *)(sums + 32 * i + 8 * a + 4) = make_float2(c4, c5);
+        } else {
+          *(uint32_t *)(out + 32 * i + 8 * a) = pack_bf16x2(c0, c1);
+          *(uint32_t *)(out + 32 * i + 8 * a + 4) = pack_bf16x2(c4, c5);
+        }
       }
     }
   }
   return true;
 }
 
-// Sequences with at most `few` rows are left to the other kernel.
+// Grid: x = row tile * splits + split, y = cache head, z = sequence. Sequences
+// with at most at.above rows are left to the other kernel.
 template <int D>
 __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill_kernel(Kv4Dims dm, Kv4Plane kc,
                                                                                       Kv4Plane vc, Kv4Batch bt,
-                                                                                      Kv4Attn at, int few) {
+                                                                                      Kv4Attn at, int splits,
+                                                                                      float *__restrict__ part) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ __attribute__((aligned(4))) uint8_t vnan[kKvTile][4];  // value groups of a tile that are NaN (bf16)
-  const int tile = prefill_tile(blockIdx.x, gridDim.x, at.causal);
+  int tile, split = 0;
+  if (splits == 1) {
+    tile = prefill_tile(blockIdx.x, gridDim.x, at.causal);
+  } else {
+    tile = blockIdx.x / splits;
+    split = blockIdx.x - tile * splits;
+    if (at.causal) tile = gridDim.x / splits - 1 - tile;  // longest first
+  }
   const RowTile rt = row_tile(dm, bt, at.max_new, tile, blockIdx.y, blockIdx.z, kPfRows);
-  if (rt.row0 >= rt.rows || rt.rows <= few) return;
+  if (rt.row0 >= rt.rows || rt.rows <= at.above) return;
   int thread = threadIdx.x;
-  if (prefill<D, true>(dm, kc, vc, bt, at, rt, thread, smem, vnan)) return;
+  if (prefill<D, true>(dm, kc, vc, bt, at, rt, split, splits, part, thread, smem, vnan)) return;
   asm volatile("" : "+v"(thread));  // nothing of the first attempt is kept in registers for the second
-  prefill<D, false>(dm, kc, vc, bt, at, rt, thread, smem, vnan);
+  prefill<D, false>(dm, kc, vc, bt, at, rt, split, splits, part, thread, smem, vnan);
 }
 
 template <int D>
 static hipError_t launch_prefill(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
-                                 const Kv4Attn &at, int few, hipStream_t s) {
+                                 const Kv4Attn &at, int splits, float *part, hipStream_t s) {
   if constexpr (Pf<D>::kLds >= 64 * 1024) {  // needs an opt-in, once per process
     static const hipError_t st = hipFuncSetAttribute(
         (const void *)kv4_prefill_kernel<D>, hipFuncAttributeMaxDynamicSharedMemorySize, Pf<D>::kLds);
     if (st != hipSuccess) return st;
   }
   const long long rows = (long long)at.max_new * (dm.Hq / dm.Hkv);
-  const dim3 grid((unsigned)((rows + kPfRows - 1) / kPfRows), dm.Hkv, dm.B);
-  kv4_prefill_kernel<D><<<grid, kPfWaves * kWave, Pf<D>::kLds, s>>>(dm, kc, vc, bt, at, few);
+  const dim3 grid((unsigned)((rows + kPfRows - 1) / kPfRows * splits), dm.Hkv, dm.B);
+  kv4_prefill_kernel<D><<<grid, kPfWaves * kWave, Pf<D>::kLds, s>>>(dm, kc, vc, bt, at, splits, part);
   return hipGetLastError();
 }
 
 hipError_t launch_kv4_prefill(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
-                              const Kv4Attn &at, int few, hipStream_t s) {
-  if (dm.D == 64) return launch_prefill<64>(dm, kc, vc, bt, at, few, s);
-  if (dm.D == 128) return launch_prefill<128>(dm, kc, vc, bt, at, few, s);
-  return launch_prefill<256>(dm, kc, vc, bt, at, few, s);
+                              const Kv4Attn &at, int splits, float *part, hipStream_t s) {
+  if (dm.D == 64) return launch_prefill<64>(dm, kc, vc, bt, at, splits, part, s);
+  if (dm.D == 128) return launch_prefill<128>(dm, kc, vc, bt, at, splits, part, s);
+  return launch_prefill<256>(dm, kc, vc, bt, at, splits, part, s);
 }
 
 }  // namespace moe

@@ -49,11 +49,11 @@ def host_planes(c):
 class Batch:
     """Ragged sequences on shuffled pages."""
 
-    def __init__(self, rng, new, past, page, spare=2):
+    def __init__(self, rng, new, past, page, spare=2, width=0):
         self.new, self.len = list(new), [n + p for n, p in zip(new, past)]
         self.page, self.B, self.T = page, len(new), sum(new)
         self.cu = [0] + list(np.cumsum(new))
-        width = max(1, max(-(-t // page) for t in self.len)) + 1
+        width = max(width, max(1, max(-(-t // page) for t in self.len)) + 1)
         self.num_pages = self.B * width + spare
         self.table = rng.permutation(self.num_pages)[:self.B * width].reshape(self.B, width)
         self.dev = (i32(self.table), i32(self.cu), i32(self.len))
@@ -355,20 +355,120 @@ def test_outlier_values_keep_their_neighbours():
     check(out, want, tol, "outlier")
 
 
+# ------------------------------------------------------------------ prompts
+# Enough query rows (4096 in all, more than 64 a sequence and head), and a page
+# table of 8192 positions, for the kernel that prompts take.
+
+PROMPTS = [  # new, past, Hq, Hkv, D, page, causal, window
+    ([129], [31], 32, 1, 128, 16, True, 0),                  # 32 heads a group
+    ([70], [0], 64, 64, 64, 16, True, 0),                    # one
+    ([70], [0], 60, 20, 128, 32, True, 0),                   # three: tiles begin inside a token
+    ([300], [0], 16, 4, 64, 16, True, 0),
+    ([257], [1000], 16, 2, 256, 64, True, 0),
+    ([128], [333], 32, 4, 128, 32, False, 0),                # every token sees all
+    ([300, 3, 0, 8, 1], [100, 2000, 50, 900, 5000], 16, 2, 128, 64, True, 0),  # with single tokens
+    ([9, 2, 250], [300, 700, 0], 24, 3, 64, 16, True, 0),    # on both sides of 64 rows
+    ([1100], [500], 32, 1, 64, 16, True, 1000),              # sliding windows
+    ([520], [200], 128, 2, 64, 32, False, 550),
+    ([260], [3000], 16, 2, 128, 64, True, 0),                # keys split over workgroups
+    ([256], [2500], 16, 1, 256, 32, True, 0),
+    ([520], [1500], 8, 8, 64, 16, True, 0),
+    ([140, 126, 1], [4000, 900, 4095], 16, 2, 64, 64, True, 0),
+    ([130], [2200], 32, 1, 128, 128, False, 0),
+]
+
+
+def prompt_batch(rng, new, past, page):
+    return Batch(rng, new, past, page, width=8192 // page)
+
+
+@pytest.mark.parametrize("new,past,Hq,Hkv,D,page,causal,window", PROMPTS)
+def test_prompts(new, past, Hq, Hkv, D, page, causal, window):
+    rng = np.random.default_rng(Hq * 5 + D + len(new) + sum(past))
+    b = prompt_batch(rng, new, past, page)
+    assert b.T * Hq >= 4096 and max(new) * (Hq // Hkv) > 64
+    c = filled(rng, b, Hkv, D)
+    q64, q = queries(rng, b.T, Hq, D)
+    out = M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), causal=causal, window=window)
+    want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, D ** -0.5, causal, window)
+    check(out, want, tol, f"{new} {past} {Hq}/{Hkv}x{D}")
+    again = M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), causal=causal, window=window)
+    assert torch.equal(out, again)
+
+
+def test_prompt_scales_and_strides():
+    rng = np.random.default_rng(31)
+    b = prompt_batch(rng, [140], [90], 16)
+    c = filled(rng, b, 2, 128)
+    T = b.T + 2
+    x = bf16_values(rng.standard_normal((T, 40, 128)) * 4)
+    wide = torch.from_numpy(x).cuda().to(BF16)
+    room = torch.full((T, 34, 128), 3.0, dtype=BF16, device="cuda")
+    q, out = wide[:, 2:34], room[:, 1:33]
+    for scale in (0.5, 1e-3):
+        M.moe_kv4_attention(c, q, *b.dev, max_new=140, scale=scale, out=out)
+        want, tol = K.attention(x[:b.T, 2:34].astype(np.float64), K.Paged(*host_planes(c), b.table), b.cu,
+                                b.len, float(np.float32(scale)))
+        check(out[:b.T], want, tol, f"scale {scale}")
+        assert (room[b.T:] == 3).all() and (room[:, 0] == 3).all() and (room[:, 33] == 3).all()
+
+
+@pytest.mark.parametrize("past", [60, 3000])
+def test_prompt_rows_that_see_nothing(past):
+    """Positions before the start, a sequence of length zero and bad pages, among keys that are
+    split and not: zeros, and bad pages are skipped."""
+    rng = np.random.default_rng(32)
+    b = prompt_batch(rng, [140, 130, 70], [0, past, 0], 16)
+    c = filled(rng, b, 2, 64)
+    q64, q = queries(rng, b.T, 16, 64)
+    table = b.table.copy()
+    table[1, 1], table[1, 5], table[1, -1] = b.num_pages + 3, -1, 2 ** 31 - 1
+    lens = [20, b.len[1], 0]
+    out = M.moe_kv4_attention(c, q, i32(table), i32(b.cu), i32(lens), max_new=140)
+    want, tol = K.attention(q64, K.Paged(*host_planes(c), table), b.cu, lens, 64 ** -0.5)
+    check(out, want, tol, "holes")
+    assert not out[:120].any() and not out[270:].any() and out[120:270].any()
+
+
+def test_hostile_prompts_stay_in_their_buffers():
+    rng = np.random.default_rng(33)
+    b = prompt_batch(rng, [150, 150], [20, 2000], 16)
+    c = filled(rng, b, 2, 64)
+    _, q = queries(rng, b.T, 16, 64)
+    big = 2 ** 31 - 1
+    for cu, lens in (([-5, 100, 900], [23, 4300]), ([0, 300, 300], [big, -4]), ([300, 150, 0], [23, 43]),
+                     ([big, -big, 200], [5, 5]), ([0, 200, 300], [8193, 100000])):
+        out = torch.full((b.T, 16, 64), 5.0, dtype=BF16, device="cuda")
+        M.moe_kv4_attention(c, q, b.dev[0], i32(cu), i32(lens), max_new=b.T, out=out)
+    torch.cuda.synchronize()
+
+
+def test_prompt_max_new_bounds_what_is_computed():
+    rng = np.random.default_rng(34)
+    b = prompt_batch(rng, [300], [10], 16)
+    c = filled(rng, b, 1, 64)
+    _, q = queries(rng, 300, 16, 64)
+    whole = M.moe_kv4_attention(c, q, *b.dev, max_new=300)
+    assert torch.equal(whole, M.moe_kv4_attention(c, q, *b.dev, max_new=100000))
+    out = torch.full_like(whole, 9.0)
+    M.moe_kv4_attention(c, q, *b.dev, max_new=270, out=out)
+    assert torch.equal(out[:270], whole[:270]) and (out[270:] == 9).all()
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("kind", ["large", "small", "query", "mixed"])
+@pytest.mark.parametrize("kind", ["large", "small", "query", "mixed", "split"])
 def test_prompts_outside_fp16(D, kind):
     """Prompts whose keys, values or queries leave fp16's range (the kernel turns to bf16
     operands, whose rounding, 2^-8 of every key and value, is added to the bound)."""
     rng = np.random.default_rng(D)
-    b = Batch(rng, [40, 33], [70, 0], 16)
+    b = prompt_batch(rng, [40, 33], [3000 if kind == "split" else 70, 0], 16)
     T = sum(b.len)
-    f = {"large": 1e6, "small": 1e-6, "query": 1.0, "mixed": 1.0}[kind]
-    k = bf16_values(tokens(rng, T, 2, D, BF16) * (1.0 if kind == "large" else min(f, 1.0)))
+    f = 1e6 if kind == "large" else 1e-6 if kind == "small" else 1.0
+    k = bf16_values(tokens(rng, T, 2, D, BF16) * min(f, 1.0))
     v = bf16_values(tokens(rng, T, 2, D, BF16) * f)
-    if kind == "mixed":
+    if kind in ("mixed", "split"):
         v[95] *= 1e6  # far into the first sequence: the run starts over there
-    x = bf16_values(rng.standard_normal((b.T, 4, D)))
+    x = bf16_values(rng.standard_normal((b.T, 64, D)))
     scale = D ** -0.5
     if kind == "query":
         x, scale = bf16_values(x * 1e5), scale * 1e-5
@@ -377,16 +477,16 @@ def test_prompts_outside_fp16(D, kind):
                      i32([0] + list(np.cumsum(b.len))), b.dev[2])
     out = M.moe_kv4_attention(c, torch.from_numpy(x).cuda().to(BF16), *b.dev, max_new=40, scale=scale)
     scale = float(np.float32(scale))
-    want, tol = K.attention(x.astype(np.float64), K.Paged(*host_planes(c), b.table), b.cu, b.len, scale)
+    planes = K.Paged(*host_planes(c), b.table)
+    want, tol = K.attention(x.astype(np.float64), planes, b.cu, b.len, scale)
     # scores off by 2^-8 scale sum |q k|, values by 2^-8 of themselves
     extra = np.zeros_like(tol)
-    planes = K.Paged(*host_planes(c), b.table)
     for s in range(b.B):
         for h in range(2):
             kc, ks, kb, _ = planes.rows("k", s, h, b.len[s])
             vc, vs, vb, _ = planes.rows("v", s, h, b.len[s])
             vmax = np.abs(vs * vc + vb).max(0)
-            for g in (2 * h, 2 * h + 1):
+            for g in range(32 * h, 32 * h + 32):
                 rows = slice(b.cu[s], b.cu[s + 1])
                 d = 2.0 ** -8 * scale * (np.abs(x[rows, g]).astype(np.float64) @ np.abs(ks * kc + kb).T).max(1)
                 extra[rows, g] = (2 * d[:, None] + 2.0 ** -8) * vmax
@@ -394,11 +494,12 @@ def test_prompts_outside_fp16(D, kind):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_prompt_nan_reaches_only_those_who_see_it(D):
+@pytest.mark.parametrize("past", [50, 3000])
+def test_prompt_nan_reaches_only_those_who_see_it(D, past):
     rng = np.random.default_rng(29)
-    b = Batch(rng, [80], [50], 16)
-    q64, q = queries(rng, 80, 2, D)
-    at = 50 + 37
+    b = prompt_batch(rng, [80], [past], 16)
+    q64, q = queries(rng, 80, 64, D)
+    at = past + 37
     for which in "kv":
         c = filled(rng, b, 1, D)
         m = getattr(c, which)
