@@ -143,6 +143,44 @@ def test_activation_extremes(T):
         assert torch.isnan(got[1]).all() and not torch.isfinite(got[T - 1]).any()
 
 
+TILES = [(200, 2100), (2100, 3300)]  # the middle and the large tiles
+
+
+@pytest.mark.parametrize("T,rows", TILES)
+@pytest.mark.parametrize("dtype,pad", [(F32, 11), (BF16, 8), (BF16, 3)])
+def test_tiles_inside_wider_tensors_and_in_place(T, rows, dtype, pad):
+    rng = np.random.default_rng(T + pad)
+    w, w64 = make_w(rng, rows, 128)
+    wide = torch.from_numpy(rounded(rng.standard_normal((T, 192)))).cuda().to(BF16)
+    x = wide[:, 64:]
+    room = torch.from_numpy(rng.standard_normal((T, rows + pad)).astype(np.float32)).cuda().to(dtype)
+    before = room.double().cpu().numpy()
+    y = room[:, :rows]
+    M.moe_linear_w4(x, w, residual=y, y=y, act="relu")
+    xs = x.double().cpu().numpy()
+    z = xs @ w64.T
+    want = K.linear(xs, w64, act="relu", residual=before[:, :rows])
+    check(y, want, bound(xs, w64, z, want, dtype) + 2.0 ** -23 * np.abs(before[:, :rows]), f"{T} in place")
+    assert (room[:, rows:].double().cpu().numpy() == before[:, rows:]).all()
+
+
+@pytest.mark.parametrize("T,rows", TILES)
+def test_tiles_keep_tokens_apart(T, rows):
+    rng = np.random.default_rng(T)
+    w, w64 = make_w(rng, rows, 128)
+    x = rounded(rng.standard_normal((T, 128)) * 500)
+    xd = torch.from_numpy(x).cuda().to(BF16)
+    z = x @ w64.T
+    clean = M.moe_linear_w4(xd, w, act="silu", out_dtype=F32)
+    with np.errstate(over="ignore"):
+        check(clean, K.linear(x, w64, act="silu"), bound(x, w64, z, z, F32) + 1e-6, "silu")
+    xd[1, 5], xd[T - 1, 6] = float("nan"), float("inf")
+    got = M.moe_linear_w4(xd, w, act="silu", out_dtype=F32)
+    keep = [t for t in range(T) if t not in (1, T - 1)]
+    assert torch.equal(got[keep], clean[keep])
+    assert torch.isnan(got[1]).all() and not torch.isfinite(got[T - 1]).all()
+
+
 def test_matches_the_dequantised_matrix_and_repeats():
     rng = np.random.default_rng(8)
     w, w64 = make_w(rng, 96, 256, general=True)
