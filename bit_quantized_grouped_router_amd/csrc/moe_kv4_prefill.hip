@@ -39,6 +39,10 @@ constexpr int kPfWaves = 4, kPfRows = 32 * kPfWaves;
 // Products whose LDS operands are on their way.
 template <bool HALF, int D>
 constexpr int ahead() { return !HALF ? 1 : D == 256 ? 2 : 4; }
+// Weights are kept times 2^7: up to 2^15 (the reference lags by kSlack), and off
+// by no more than 2^-32 of the largest where fp16 runs out of exponents, so that
+// even a million keys in a faint tail lose less than 2^-12 of it together.
+constexpr float kShift = 7.0f;
 constexpr int kSalu = 0x4;  // sched_barrier: scalar instructions may pass
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -113,11 +117,6 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ uint32_t half_to_bf16x2(uint32_t w) {
-  const f16x2_t v = __builtin_bit_cast(f16x2_t, w);
-  return pack_bf16x2((float)v[0], (float)v[1]);
-}
-
 template <bool HALF>
 __device__ __forceinline__ f32x16_t mfma32(const uint4 &a, const uint4 &b, const f32x16_t &c) {
   if constexpr (HALF)
@@ -167,7 +166,8 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   // its channels in the order rebuilt rows have
   const uint16_t *qp = at.q + (rt.sp.begin + tok) * at.q_stride + (long long)hd * D + half * 8;
   uint4 q[NK];
-  bool large = false;
+  float most = 0.f;
+  bool nan_q = false;
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
     const uint4 x = *(const uint4 *)(qp + k * 16);
@@ -177,13 +177,18 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xFFFF0000u);
-        large |= !(fmaxf(fabsf(a), fabsf(b)) < 32768.0f) || a != a || b != b;
+        most = fmaxf(most, fmaxf(fabsf(a), fabsf(b)));
+        nan_q |= a != a || b != b;
         w[i] = pack_half(a, b);
       }
     }
     q[k] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  if (HALF && any_thread(large)) return false;
+  if constexpr (HALF) {
+    // a row whose largest channel is small would fall among fp16's subnormals
+    most = fmaxf(most, __shfl_xor(most, 32, kWave));
+    if (any_thread(nan_q || !(most < 32768.0f) || (most < 0x1p-8f && most != 0.f))) return false;
+  }
 
   // keys the first and the last token see, and this lane's row
   const Kv4Range r0 = kv4_range(dm, rt.sp.first + tok0, rt.sp.first + tok0, rt.sp.len, at.causal, at.window);
@@ -396,7 +401,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
     int vb = 0, wb = 2 * P::kPlane;
     // Tile i, whose scores are s, and the scores sn of tile i + 1.
     auto tile = [&](int i, int kb, const f32x16_t &s, f32x16_t &sn) __attribute__((always_inline)) {
-      const float ref = m == kNegInf ? 0.f : m;
+      const float ref = m == kNegInf ? 0.f : m - kShift;
       uint32_t pw[8];
       sn = scores(kb, [&](int k) {
 #pragma unroll
@@ -477,7 +482,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   const float sum_inv = partial ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
   const long long pr = part_index(dm, rt, real ? row - rt.row0 : 0, splits, split);
   float *sums = part + pr * D + 2 * half;
-  if (partial && real && half == 0) *(float2 *)(part_stats(dm, bt, splits, part) + pr * 2) = make_float2(m, l);
+  if (partial && real && half == 0) *(float2 *)(part_stats(dm, bt, splits, part) + pr * 2) = make_float2(HALF ? m - kShift : m, l);
   uint16_t *out = at.out + (rt.sp.begin + tok) * at.out_stride + (long long)hd * D + 2 * half;
   if (real) {
 #pragma unroll

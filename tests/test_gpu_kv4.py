@@ -456,7 +456,7 @@ def test_prompt_max_new_bounds_what_is_computed():
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("kind", ["large", "small", "query", "mixed", "split"])
+@pytest.mark.parametrize("kind", ["large", "small", "query", "faint query", "mixed", "split"])
 def test_prompts_outside_fp16(D, kind):
     """Prompts whose keys, values or queries leave fp16's range (the kernel turns to bf16
     operands, whose rounding, 2^-8 of every key and value, is added to the bound)."""
@@ -472,6 +472,9 @@ def test_prompts_outside_fp16(D, kind):
     scale = D ** -0.5
     if kind == "query":
         x, scale = bf16_values(x * 1e5), scale * 1e-5
+    if kind == "faint query":
+        x[:, :9], scale = bf16_values(x[:, :9] * 1e-7), scale * 1e5
+        x[:, 9:] = bf16_values(x[:, 9:] * 1e-5)
     c = make_cache(b.num_pages, 2, 16, D)
     M.moe_kv4_append(c, *(torch.from_numpy(a).cuda().to(BF16) for a in (k, v)), b.dev[0],
                      i32([0] + list(np.cumsum(b.len))), b.dev[2])
@@ -491,6 +494,25 @@ def test_prompts_outside_fp16(D, kind):
                 d = 2.0 ** -8 * scale * (np.abs(x[rows, g]).astype(np.float64) @ np.abs(ks * kc + kb).T).max(1)
                 extra[rows, g] = (2 * d[:, None] + 2.0 ** -8) * vmax
     check(out, want, tol + extra, f"{kind} {D}")
+
+
+@pytest.mark.parametrize("Hq", [4, 64])
+def test_long_faint_tail_is_not_lost(Hq):
+    """Keys that weigh 2^-27 of the largest each, whose value is all there is to see."""
+    rng = np.random.default_rng(35)
+    b = prompt_batch(rng, [72], [7900], 16)
+    k = np.zeros((7972, 1, 64), dtype=np.float32)
+    v = np.ones((7972, 1, 64), dtype=np.float32)
+    k[0], v[0] = 2.34375, 0.0   # 8 x 2.34 = 18.75 = 27.05 ln 2
+    c = make_cache(b.num_pages, 1, 16, 64)
+    M.moe_kv4_append(c, *(torch.from_numpy(a).cuda() for a in (k, v)), b.dev[0], i32([0, 7972]), b.dev[2])
+    x = np.ones((72, Hq, 64))
+    out = M.moe_kv4_attention(c, torch.from_numpy(x).cuda().to(BF16), *b.dev, max_new=72)
+    want, tol = K.attention(x, K.Paged(*host_planes(c), b.table), b.cu, b.len, 0.125)
+    # Prompts: weights are rounded to fp16 times 2^7. The reference they are relative to is a
+    # score of the row, so their sum is at least 1; below 2^-14 fp16 steps by 2^-24, so each is
+    # off by up to 2^-25 / 2^7 = 2^-32 beside what larger ones are. 7972 of them, of value 1:
+    check(out, want, tol + 7972 * 2.0 ** -32, "tail")  # 1.9e-6 of the 5.7e-5 that the tail adds up to
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
