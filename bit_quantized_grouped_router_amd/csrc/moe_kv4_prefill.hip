@@ -126,12 +126,16 @@ __device__ __forceinline__ f32x16_t mfma32(const uint4 &a, const uint4 &b, const
 }
 
 // The row tile of workgroup i of n, for causal calls longest first. Where all
-// workgroups are on the card at once (two a CU), every second round of 256 runs
-// the other way, so that a long tile shares its CU with a short one.
+// workgroups are on the card at once and two share a CU (not D = 256), every
+// second round of 256 runs the other way, so that a long tile shares its CU with
+// a short one (4096 tokens behind 1003, D = 128: 176 us against 198; D = 256,
+// whose second round comes as the shorter tiles of the first end, 4096 tokens: 218
+// us against 300).
+template <int D>
 __device__ __forceinline__ int prefill_tile(int i, int n, bool causal) {
   if (!causal) return i;
   const int heads = gridDim.y * gridDim.z;
-  if ((long long)n * heads <= 512) {
+  if (D < 256 && (long long)n * heads <= 512) {
     const int linear = i + n * (blockIdx.y + gridDim.y * blockIdx.z);
     if (n <= 256) return (linear >> 8) & 1 ? i : n - 1 - i;
     if (i >= 256) return i - 256;
@@ -516,7 +520,7 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
   __shared__ __attribute__((aligned(4))) uint8_t vnan[kKvTile][4];  // value groups of a tile that are NaN (bf16)
   int tile, split = 0;
   if (splits == 1) {
-    tile = prefill_tile(blockIdx.x, gridDim.x, at.causal);
+    tile = prefill_tile<D>(blockIdx.x, gridDim.x, at.causal);
   } else {
     tile = blockIdx.x / splits;
     split = blockIdx.x - tile * splits;
