@@ -28,7 +28,14 @@
 // The order inside a contraction is free, so the nibbles of a word are taken
 // in the order 0 4 1 5 2 6 3 7 (one shift and one and-or give two of them),
 // and the query and the weights are laid out to match.
+//
+// Bound by memory for many or long sequences, by its chain of dependent loads
+// (offsets, pages, codes) for few short ones. us, one new token a sequence, 16
+// heads on 2: 64 sequences of up to 8101, D = 256 (113 MB) 33.7 and 5.8 for the
+// join, 3.4 TB/s; one of 131,150, D = 128 (38 MB) 17.3 and 6.8; one of 500, D =
+// 256 11.7.
 #include "moe_kv4_device.h"
+#include "moe_lds.h"
 
 namespace moe {
 
@@ -835,10 +842,9 @@ size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window) {
 template <int D, int W>
 static hipError_t launch_rows(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
                               const Kv4Attn &at, int tokens, int splits, float *part, hipStream_t s) {
-  if constexpr (at_lds_bytes<D, W>() > 64 * 1024) {  // needs an opt-in, once per process
-    static const hipError_t st =
-        hipFuncSetAttribute((const void *)kv4_attention_kernel<D, W>,
-                            hipFuncAttributeMaxDynamicSharedMemorySize, at_lds_bytes<D, W>());
+  if constexpr (at_lds_bytes<D, W>() > 64 * 1024) {
+    static std::atomic<uint64_t> asked;
+    const hipError_t st = allow_lds((const void *)kv4_attention_kernel<D, W>, at_lds_bytes<D, W>(), asked);
     if (st != hipSuccess) return st;
   }
   const long long tiles = kv4_row_tiles(dm, tokens);

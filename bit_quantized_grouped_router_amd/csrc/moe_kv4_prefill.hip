@@ -11,27 +11,44 @@
 // so that the scores of a row stay in the two lanes (l, l ^ 32) that need them as
 // weights, and nothing but the row's maximum and sum ever crosses lanes. The
 // value operand is read with the transposing LDS read (4 keys by 16 channels a
-// lane group). Codes come straight from memory into registers one tile ahead;
-// the rebuilt tiles are double buffered, one barrier a tile.
+// lane group).
+//
+// A pass of the loop scores tile i + 1 while it turns tile i's scores into
+// weights, then multiplies tile i's weights and values while it rebuilds tile i
+// + 2, whose codes were loaded a pass before: matrix and vector instructions
+// alternate in the order written here (the compiler would put them one after
+// the other). One barrier a pass; two buffers of keys, three of values.
 //
 // fp16 rather than bf16 for the operands: keys, values and weights lose 2^-12 of
 // themselves at most instead of 2^-9, so that the result is as exact as its
 // own rounding to bf16 (rms error against fp64 1.7e-3 of the result, of which
 // the rounding is all; bf16 operands would make it 3.2e-3). Its range is the
 // price: where a tile has a value or key of 2^15 or more, or a scale so small
-// that codes would fall among fp16's subnormals, or a query is that large, the
-// workgroup starts over with bf16 operands. That run also takes NaN and
-// infinities: such values are replaced by zeros, and the rows that see their
-// key get NaN in the group's channels, so that a key no row may look at never
-// reaches one.
+// that codes would fall among fp16's subnormals, or a query is too large or
+// too small, the workgroup starts over with bf16 operands, one tile after the
+// other. That run also takes NaN and infinities: such values are replaced by
+// zeros, and the rows that see their key get NaN in the group's channels, so
+// that a key no row may look at never reaches one.
 //
-// Bound by the vector units: a 32-key tile costs a wavefront about 240 VALU
-// operations (16 exponentials at a quarter rate among them) next to 512 cycles
-// of MFMA; two workgroups share a CU, so one's softmax runs under the other's
-// products.
+// Keys are split over workgroups, as in the other kernel, where the row tiles
+// do not fill the card (512 tokens behind 60000, 16 heads on 2, D = 128: 1531 us
+// unsplit, 306 split eight ways: 826 TFLOP/s).
+//
+// Measured (us; TFLOP/s of the products that causality leaves), 16 heads on 2:
+//   4096 tokens behind 1003   D = 64 110 (463)  128 163-176 (582-628)
+//   8192 tokens               D = 128 343 (802)
+//   4096 tokens               D = 256 218 (629)
+// next to 1224 TFLOP/s of a library product of 8192^3. Bound by the vector
+// instructions that a tile needs besides its products (about 150 a wavefront,
+// 16 exponentials among them, next to 512 cycles of MFMA; matrix instructions
+// were busy 30% of the time, vector ones 42%) and, at 4096 tokens, by the long
+// tiles that end alone on their CU. Rows of 64 to a wavefront halve the
+// rebuilding per row but leave one wavefront a SIMD: the same time without a
+// mask (251 us against 254), longer with one (229 against 176).
 #include <type_traits>
 
 #include "moe_kv4_device.h"
+#include "moe_lds.h"
 
 namespace moe {
 
@@ -537,9 +554,9 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
 template <int D>
 static hipError_t launch_prefill(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
                                  const Kv4Attn &at, int splits, float *part, hipStream_t s) {
-  if constexpr (Pf<D>::kLds >= 64 * 1024) {  // needs an opt-in, once per process
-    static const hipError_t st = hipFuncSetAttribute(
-        (const void *)kv4_prefill_kernel<D>, hipFuncAttributeMaxDynamicSharedMemorySize, Pf<D>::kLds);
+  if constexpr (Pf<D>::kLds >= 64 * 1024) {
+    static std::atomic<uint64_t> asked;
+    const hipError_t st = allow_lds((const void *)kv4_prefill_kernel<D>, Pf<D>::kLds, asked);
     if (st != hipSuccess) return st;
   }
   const long long rows = (long long)at.max_new * (dm.Hq / dm.Hkv);

@@ -394,8 +394,8 @@ typedef struct {
 /*
  * Shape limits of the three calls: B, Hkv, page, num_pages, max_pages >= 1, D
  * and page as above, T >= 0 (MOE_E_INVALID for values < 1, MOE_E_UNSUPPORTED
- * for other D and page), max_pages * page < 2^31, B, Hq, Hkv <= 65535, T * Hq and
- * T * 2 Hkv D < 2^40. Token strides are in elements, multiples of 8
+ * for other D and page), max_pages * page < 2^31, B, Hq, Hkv <= 65535, T * Hq <
+ * 2^31 - 64, max_new * Hq / Hkv < 2^28 - 128 (attention), T * 2 Hkv D < 2^40. Token strides are in elements, multiples of 8
  * (MOE_E_UNSUPPORTED) and at least a token long (MOE_E_INVALID).
  */
 
@@ -432,7 +432,7 @@ size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int3
  * moe_kv4_attention - the new tokens' queries over the cache (their own keys and
  * values included, so append first).
  *   out[t][h] = sum_p softmax_p(scale * q[t][h] . k_p) v_p, with k_p, v_p =
- *   s * code + b not rounded, of cache head h / (Hq / Hkv), over the positions
+ *   s * code + b of cache head h / (Hq / Hkv), over the positions
  *   p < kv_len that the token at position i sees: p <= i if causal, and
  *   p > i - window if window > 0. A token that sees none gets zeros. Positions
  *   it does not see never reach its result, whatever the cache holds there.
@@ -443,9 +443,15 @@ size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int3
  *   window  >= 0 (0: none; MOE_E_INVALID when negative)
  *   ws      >= moe_kv4_attention_workspace_bytes of these dims; may be NULL when that
  *           is 0. Calls that may overlap need workspaces of their own.
- * Scores, softmax statistics and sums are fp32; a softmax weight times its
- * key's scale is rounded to bf16 for the matrix cores. Results repeat bit for
- * bit.
+ * Scores, softmax statistics and sums are fp32. What is rounded for the matrix
+ * cores, by the sizes of the call:
+ *   few query rows: a softmax weight times its key's scale, to bf16; keys and
+ *     values enter unrounded.
+ *   many (T * Hq >= 4096, T * Hq * positions of the page table or the window >=
+ *     2^25, and more than 64 rows max_new * Hq / Hkv of a cache head): keys, values and
+ *     weights, to fp16; to bf16 for a block of rows whose keys, values or
+ *     queries fp16's range does not hold (2^15 and more, or scales below 2^-13).
+ * Results repeat bit for bit. The calls are asynchronous and may be captured.
  */
 moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
                              int32_t max_new, const uint16_t *q, int64_t q_stride, uint16_t *out,

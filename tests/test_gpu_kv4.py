@@ -562,6 +562,10 @@ def test_offsets_past_32_bits():
     out = M.moe_kv4_attention(c, q, i32(table), i32([0, 2]), i32([n]), max_new=2)
     want, tol = K.attention(q64, K.Paged(*planes, np.array([[0, 1, 2]])), [0, 2], [n], D ** -0.5)
     check(out, want, tol, "far pages")
+    q64, q = queries(rng, n, 80, D)   # rows enough for the prompts' kernel
+    out = M.moe_kv4_attention(c, q, i32(table), i32([0, n]), i32([n]), max_new=n)
+    want, tol = K.attention(q64, K.Paged(*planes, np.array([[0, 1, 2]])), [0, n], [n], D ** -0.5)
+    check(out, want, tol, "far pages, prompt")
 
 
 def test_max_new_bounds_what_is_computed():
