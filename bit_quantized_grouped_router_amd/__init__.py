@@ -498,6 +498,7 @@ def moe_dequant_w4(m: W4Matrix, index: int = 0, out=None, stream=None):
 
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+INT32_MAX = 2 ** 31 - 1
 
 
 def _on(stream):
@@ -697,7 +698,7 @@ def moe_kv4_read(cache: KV4Cache, page_table, cu, kv_len, T: int, dtype=torch.bf
 def moe_kv4_attention_workspace_bytes(cache: KV4Cache, T: int, Hq: int, B: int, max_pages: int,
                                       max_new: int, window: int = 0) -> int:
     dm = MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, max_pages)
-    return lib().moe_kv4_attention_workspace_bytes(dm, T, max_new, window)
+    return lib().moe_kv4_attention_workspace_bytes(dm, T, min(max_new, T), min(window, INT32_MAX))
 
 
 def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, max_new: int,
@@ -705,7 +706,7 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
                       ws=None, stream=None):
     """Attention of queries q [T, Hq, D] (bf16) over the cache; rows cu[b] .. cu[b+1]-1 are
     the last tokens of sequence b. max_new: an upper bound of the new tokens of a sequence.
-    scale defaults to D ** -0.5."""
+    scale defaults to D ** -0.5. out may be q (in place)."""
     if q.dim() != 3:
         raise MoeError("q must be [T, Hq, D]")
     T, Hq, D = q.shape
@@ -718,6 +719,11 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
         os_ = Hq * D
     else:
         os_ = _rows(out, (T, Hq, D), "out", BF16)
+    if T > 0:  # the C ABI's integers are 32 bits wide
+        max_new = min(max_new, T)
+    window = min(window, INT32_MAX)
+    if max_new < 0 or window < 0:
+        raise MoeError(f"max_new {max_new} and window {window} must not be negative")
     L = lib()
     if ws is None:
         need = L.moe_kv4_attention_workspace_bytes(dm, T, max_new, window)

@@ -523,7 +523,7 @@ moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
                              int32_t causal, int32_t window, void *ws, size_t ws_bytes,
                              void *stream) {
   MOE_TRY(check_kv4_attention(dm, T, max_new, window));
-  if (!(scale > 0.0f) || !(scale <= 3.402823466e38f)) return MOE_E_INVALID;
+  if (!(scale > 0.0f) || !(scale <= 0x1p64f)) return MOE_E_INVALID;
   if (T == 0) return MOE_OK;
   MOE_TRY(check_stride(q_stride, (int64_t)dm->Hq * dm->D));
   MOE_TRY(check_stride(out_stride, (int64_t)dm->Hq * dm->D));

@@ -334,7 +334,8 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *   bias      bf16 [rows] or NULL
  *   residual  [T][rows] of y's type, rows residual_stride apart, or NULL; may
  *             be y itself with the same stride (updated in place)
- *   y         bf16 or fp32 (dtype) [T][rows], rows y_stride elements apart, out
+ *   y         bf16 or fp32 (dtype) [T][rows], rows y_stride elements apart, out;
+ *             overlaps neither x nor, but for the above, the residual
  * Limits: T >= 0, rows >= 1, cols >= 1 (MOE_E_INVALID otherwise); cols % 64 == 0,
  * x_stride % 8 == 0, rows * cols < 2^34, T * rows < 2^36, T * cols < 2^40
  * (MOE_E_UNSUPPORTED); strides at least a row long (MOE_E_INVALID).
@@ -437,9 +438,10 @@ size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int3
  *   p > i - window if window > 0. A token that sees none gets zeros. Positions
  *   it does not see never reach its result, whatever the cache holds there.
  *   q       bf16 [T][Hq][D], tokens q_stride apart
- *   out     bf16 [T][Hq][D], out, tokens out_stride apart
+ *   out     bf16 [T][Hq][D], out, tokens out_stride apart; may be q itself with the
+ *           same stride
  *   max_new an upper bound of every n_b; a sequence's tokens past it are not computed
- *   scale   > 0 and finite (MOE_E_INVALID otherwise)
+ *   scale   > 0 and <= 2^64 (MOE_E_INVALID otherwise)
  *   window  >= 0 (0: none; MOE_E_INVALID when negative)
  *   ws      >= moe_kv4_attention_workspace_bytes of these dims; may be NULL when that
  *           is 0. Calls that may overlap need workspaces of their own.

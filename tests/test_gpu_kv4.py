@@ -267,6 +267,38 @@ def test_attention(new, past, Hq, Hkv, D, page, causal, window):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("prompt", [0, 270])
+def test_hundreds_of_sequences(prompt):
+    """More than are spread by their lengths, keys split; and with a prompt among them."""
+    rng = np.random.default_rng(36)
+    new = [1] * 300
+    past = [int(x) for x in np.exp(rng.uniform(0, 7.9, 300))]
+    new[17], past[40] = max(prompt, 1), 2900
+    b = Batch(rng, new, past, 16, width=8192 // 16 if prompt else 0)
+    c = filled(rng, b, 1, 64)
+    q64, q = queries(rng, b.T, 16, 64)
+    out = M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new())
+    want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, 0.125)
+    check(out, want, tol, "300 sequences")
+
+
+def test_attention_in_place_and_wide_bounds():
+    rng = np.random.default_rng(37)
+    for new, past, width in (([1, 2], [3000, 40], 0), ([300], [3000], 512)):
+        b = Batch(rng, new, past, 16, width=width)
+        c = filled(rng, b, 2, 128)
+        _, q = queries(rng, b.T, 16, 128)
+        want = M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new())
+        for kw in (dict(max_new=2 ** 32 + 1), dict(max_new=b.T, window=2 ** 32 + 3)):
+            kw.setdefault("window", 0)
+            assert torch.allclose(M.moe_kv4_attention(c, q, *b.dev, **kw).float(), want.float(), atol=2e-2)
+        M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), out=q)
+        assert torch.equal(q, want)
+    for bad in (dict(max_new=-1), dict(max_new=1, window=-2 ** 32), dict(max_new=1, scale=2.0 ** 65)):
+        with pytest.raises(M.MoeError):
+            M.moe_kv4_attention(c, q, *b.dev, **bad)
+
+
 def test_attention_scales_and_strides():
     """Large scores, another scale, queries inside a wider row, an output of its own strides,
     rows past the last sequence left as they were."""
