@@ -117,16 +117,35 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
     xp[i] = a.x + min(t0 + i * 16 + (lane & 15), a.T - 1) * a.x_stride + c16;
     acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-  for (int g0 = wave; g0 < ng; g0 += kLnWaves * kBatch) {
+  // the epilogue's operands: of one output a thread, on their way meanwhile
+  static_assert(kTokens * 16 <= kLnWaves * kWave, "one output a thread");
+  const int te = t0 + threadIdx.x / 16, ne = n0 + threadIdx.x % 16;
+  const bool mine = threadIdx.x < kTokens * 16 && te < a.T && ne < a.rows;
+  const float bias = mine && a.bias ? bf16_to_f32(a.bias[ne]) : 0.f;
+  const float res = mine ? load_residual<F32>(a, te, ne) : 0.f;
+  // a wavefront takes kBatch groups in a row: whole lines of codes, and where rows
+  // of scales are 8-byte aligned one load for the four of them
+  const bool wide = ng % kBatch == 0;
+  for (int g0 = wave * kBatch; g0 < ng; g0 += kLnWaves * kBatch) {
     uint2 c[kBatch];
     uint32_t s[kBatch], b[kBatch];
     uint4 x[kBatch][NT][2];
+    if (wide) {
+      const uint2 s4 = *(const uint2 *)(sp + g0), b4 = *(const uint2 *)(bp + g0);
+      s[0] = s4.x & 0xFFFFu, s[1] = s4.x >> 16, s[2] = s4.y & 0xFFFFu, s[3] = s4.y >> 16;
+      b[0] = b4.x & 0xFFFFu, b[1] = b4.x >> 16, b[2] = b4.y & 0xFFFFu, b[3] = b4.y >> 16;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int g = min(g0 + j, ng - 1);
+        s[j] = sp[g];
+        b[j] = bp[g];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int g = min(g0 + j * kLnWaves, ng - 1);
+      const int g = min(g0 + j, ng - 1);
       c[j] = *(const uint2 *)(codes + g * 32);
-      s[j] = sp[g];
-      b[j] = bp[g];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         x[j][i][0] = *(const uint4 *)(xp[i] + g * kGroup);
@@ -136,7 +155,7 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
     __builtin_amdgcn_sched_barrier(0);  // all loads first
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      if (g0 + j * kLnWaves >= ng) break;
+      if (g0 + j >= ng) break;
       const float sc = bf16_to_f32(s[j]), bi = bf16_to_f32(b[j]);
       const bf16x8_t w0 = __builtin_bit_cast(bf16x8_t, dequant8(c[j].x, sc, bi));
       const bf16x8_t w1 = __builtin_bit_cast(bf16x8_t, dequant8(c[j].y, sc, bi));
@@ -152,17 +171,11 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
 #pragma unroll
     for (int r = 0; r < 4; ++r) part[wave][i * 16 + (lane & 15)][(lane >> 4) * 4 + r] = acc[i][r];
   __syncthreads();
-  with_act(a.act, [&](auto act) {
-    for (int e = threadIdx.x; e < kTokens * 16; e += kLnWaves * kWave) {
-      const int t = t0 + e / 16, n = n0 + e % 16;
-      if (t >= a.T || n >= a.rows) continue;
-      const float bias = a.bias ? bf16_to_f32(a.bias[n]) : 0.f, res = load_residual<F32>(a, t, n);
-      float z = 0.f;
+  if (!mine) return;
+  float z = 0.f;
 #pragma unroll
-      for (int w = 0; w < kLnWaves; ++w) z += part[w][e / 16][e % 16];
-      store_output<act.value, F32>(a, t, n, z, bias, res);
-    }
-  });
+  for (int w = 0; w < kLnWaves; ++w) z += part[w][threadIdx.x / 16][threadIdx.x % 16];
+  with_act(a.act, [&](auto act) { store_output<act.value, F32>(a, te, ne, z, bias, res); });
 }
 
 // ------------------------------------------------------------------ large batches
