@@ -88,7 +88,7 @@ struct Pf {
 template <int D>
 struct Packed {
   uint32_t c[D / 32];
-  uint16_t s, b;
+  uint32_t s, b;  // of this group and the one beside it (16-bit loads take longer)
   bool seen;  // by some row of the workgroup, and of a page that exists
 };
 
@@ -233,6 +233,8 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   const int hf = wave & 1, plane = wave >> 1, quarter = lane & 3, krow = ((lane >> 4) & 3) | ((lane & 12)), key = 16 * hf + krow;
   const Kv4Plane pl = plane ? vc : kc;
   const DqRegs dk = dq_regs();
+  const uint32_t g = (uint32_t)(krow * NG + quarter * NG / 4);  // its group in the half tile
+  const bool odd = g & 1;
   auto fetch = [&](int tile, const TilePages &pg, Packed<D> &r) {
     const int t = tile * kKvTile + key, page = hf ? pg.page[1] : pg.page[0];
     const uint64_t row0 = (((uint64_t)(uint32_t)max(page, 0) * (uint32_t)dm.Hkv + rt.head) << dm.page_shift) |
@@ -248,9 +250,8 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
         r.c[4 * i] = x.x, r.c[4 * i + 1] = x.y, r.c[4 * i + 2] = x.z, r.c[4 * i + 3] = x.w;
       }
     }
-    const uint32_t g = (uint32_t)(krow * NG + quarter * NG / 4);
-    r.s = (pl.scales + row0 * NG)[g];
-    r.b = (pl.biases + row0 * NG)[g];
+    r.s = *(const uint32_t *)(pl.scales + row0 * NG + (g & ~1u));
+    r.b = *(const uint32_t *)(pl.biases + row0 * NG + (g & ~1u));
     r.seen = (page | (t - key_lo) | (key_hi - 1 - t)) >= 0;
   };
   // Rebuilding, to buffer kb of the keys, the values' at byte vb: what the groups
@@ -263,7 +264,8 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   };
   auto begin = [&](const Packed<D> &r, int kb, int vb, HalfRange &range) {
     // what no row of the workgroup sees may be anything: it becomes zeros
-    const uint32_t sb = r.seen ? r.s | ((uint32_t)r.b << 16) : 0u;
+    const uint32_t pair = odd ? __builtin_amdgcn_perm(r.b, r.s, 0x07060302u) : __builtin_amdgcn_perm(r.b, r.s, 0x05040100u);
+    const uint32_t sb = r.seen ? pair : 0u;
     Rebuild c;
     c.row = smem + (plane ? P::kValues + vb : kb * P::kPlane) + key * P::kRow + quarter * 16;
     c.s = bf16_to_f32(sb & 0xFFFFu), c.b = bf16_to_f32(sb >> 16);

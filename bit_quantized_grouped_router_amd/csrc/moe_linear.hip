@@ -8,7 +8,7 @@
 // (lane l: row l % 16, columns 16 (l / 16) .. +15 of the group) against the
 // tokens' activations read straight from memory, and join their sums through
 // LDS, where the epilogue runs. Measured, rows x columns: 1 token by 5120 x 2048
-// 9.3 us, 37 by 2048 x 4096 with a residual 15.8 us. The tile kernels below: 777
+// 5.8 us in a graph, 37 by 2048 x 4096 11.9 us. The tile kernels below: 777
 // by 1001 x 2048 20 us, 8192 by 5120 x 2048 176 to 199 us (a library product of
 // bf16 weights of that size 175 to 177).
 #include <type_traits>
@@ -124,7 +124,8 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
   const float bias = mine && a.bias ? bf16_to_f32(a.bias[ne]) : 0.f;
   const float res = mine ? load_residual<F32>(a, te, ne) : 0.f;
   // a wavefront takes kBatch groups in a row: whole lines of codes, and where rows
-  // of scales are 8-byte aligned one load for the four of them
+  // of scales are 8-byte aligned one load for the four of them (eight 16-bit
+  // loads instead cost 1 x 5120 x 2048 3 us of 8.7)
   const bool wide = ng % kBatch == 0;
   for (int g0 = wave * kBatch; g0 < ng; g0 += kLnWaves * kBatch) {
     uint2 c[kBatch];
@@ -526,11 +527,11 @@ __global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(Li
 // Large tiles from 220 of them: 1500 tokens (240 tiles) 49 us against 55 on
 // middle tiles, 1024 tokens (160) 49 against 44.
 constexpr int kBgMinTiles = 220;
-// Middle tiles above 16 tokens where the small kernel would need more than 384
-// workgroups of 32 tokens: 64 tokens (640) 16 us against 21; 32 tokens (320) 15
-// against 15; 64 tokens by 2048 rows (256) 15 against 9; 37 tokens by 2048 rows
-// and 4096 columns (256) 28 against 15.
-constexpr int kSmallMaxBlocks = 384;
+// Middle tiles above 16 tokens where the small kernel would need more than 640
+// workgroups of 32 tokens: 96 tokens (960) 16 us against 21; 48 tokens by 8192 rows
+// (1024) 17 against 19; 64 tokens (640) 16 against 16; 128 tokens by 2048 rows
+// (512) 15 against 12; 64 tokens by 2048 rows and 4096 columns (256) 28 against 12.
+constexpr int kSmallMaxBlocks = 640;
 
 template <int MB, int NB, int KS>
 static long long bg_tiles(int T, int rows) {

@@ -72,13 +72,18 @@ CASES = [  # T, rows, cols, bias, act, residual, dtype
     (513, 769, 1088, False, "none", True, F32),
     (1000, 77, 640, True, "relu", False, BF16),
     (2, 300, 6400, True, "none", False, F32),                # more columns than a fused expert takes
-    # middle tiles (more than 384 blocks of 32 tokens by 16 rows): an odd number of groups
-    # (the first team's step over), one group, two, and more than one table of 8 a team
+    # 16 rows by 32 tokens a workgroup, up to 640 of them
     (70, 2100, 704, True, "gelu", True, BF16),
     (400, 520, 64, False, "none", True, F32),
     (257, 777, 128, True, "silu", False, F32),
     (90, 2200, 1216, False, "none", False, F32),
+    # middle tiles (more than 640): an odd number of groups (the first team's step over), one
+    # group, two, and more than one table of 8 a team
     (333, 1000, 2048, True, "relu", True, BF16),
+    (170, 2100, 704, True, "gelu", True, BF16),
+    (700, 520, 64, False, "none", True, F32),
+    (450, 777, 128, True, "silu", False, F32),
+    (170, 2200, 1216, False, "none", False, F32),
     # large tiles (220 of 128 x 256 and more): tails in both directions, few and many groups
     (2100, 3400, 64, True, "none", True, BF16),
     (3700, 2050, 576, False, "silu", False, F32),
