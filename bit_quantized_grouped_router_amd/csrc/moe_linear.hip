@@ -351,14 +351,13 @@ __global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(Li
     dma(0, 0);
     if (steps > 1) dma(1, 1);
 #pragma unroll 4
-    for (int g0 = 0; g0 < steps; g0 += kBgChunk) {
+    for (int g0 = (steps - 1) / kBgChunk * kBgChunk; g0 >= 0; g0 -= kBgChunk) {  // the first chunk's stay
       fetch(g0);
       const uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         ok &= (int)dq_fast_ok((s[i] & 0xFFFFu) | (b[i] << 16)) & (int)dq_fast_ok((s[i] >> 16) | (b[i] & 0xFFFF0000u));
     }
-    fetch(0);
     fill();
   }
   const bool fast = __builtin_amdgcn_ballot_w64(!ok) == 0;
