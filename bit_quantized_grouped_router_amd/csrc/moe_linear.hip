@@ -9,7 +9,7 @@
 // tokens' activations read straight from memory, and join their sums through
 // LDS, where the epilogue runs. Measured, rows x columns: 1 token by 5120 x 2048
 // 5.8 us in a graph, 37 by 2048 x 4096 11.9 us. The tile kernels below: 777
-// by 1001 x 2048 20 us, 8192 by 5120 x 2048 176 to 199 us (a library product of
+// by 1001 x 2048 13 us, 8192 by 5120 x 2048 176 to 199 us (a library product of
 // bf16 weights of that size 175 to 177).
 #include <type_traits>
 
@@ -181,12 +181,12 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
 
 // ------------------------------------------------------------------ large batches
 //
-// Four wavefronts take a tile of 32 MB tokens x 128 NB weight rows, each all the
+// WT wavefronts take a tile of 32 MB tokens x 32 NB WT weight rows, each all the
 // tokens and its own 32 NB rows, so every weight is rebuilt once per tile, in
 // registers, as the B operand of 32x32x16 MFMAs (C: lane = weight row,
 // registers = tokens). Per K step of 64 (one group):
 //   - activations (4 MB KB) come by LDS DMA into a ring of three stages shared by
-//     the four, 16-byte chunks XOR-swizzled by row so that fragment reads of 8
+//     the team, 16-byte chunks XOR-swizzled by row so that fragment reads of 8
 //     or 16 rows hit distinct banks;
 //   - codes come by LDS DMA too, into the wavefront's own ring, where each lane
 //     reads back the 16 bytes it fetched (32 columns of one row);
@@ -199,24 +199,25 @@ __global__ __launch_bounds__(kLnWaves *kWave, 2) void linear_kernel(LinearArgs a
 //                   registers), so one rebuilds weights while the other multiplies;
 //   middle ones     MB = 2, NB = 1 and KS = 2 teams of four wavefronts that split
 //                   the K steps and add up in LDS: there are few tiles then, and
-//                   a step takes its latency, not its work.
+//                   a step takes its latency, not its work;
+//   narrow ones     the same with KS = 4 teams of WT = 2, half as many rows a tile:
+//                   twice the workgroups where middle tiles leave CUs empty.
 constexpr int kBgStages = 3, kBgChunk = 8;
 
-template <int MB, int NB, int KS>
+template <int MB, int NB, int KS, int WT>
 struct Bg {
-  static constexpr int kTokens = 32 * MB, kRows = 128 * NB, kWaveRows = 32 * NB;
-  static constexpr int kThreads = KS * 4 * kWave;
+  static constexpr int kTokens = 32 * MB, kWaveRows = 32 * NB, kRows = WT * kWaveRows;
+  static constexpr int kThreads = KS * WT * kWave;
   static constexpr int kX = kTokens * kGroup * 2;      // bytes of activations a stage
   static constexpr int kCodes = kRows * kGroup / 2;    // bytes of codes a stage
   static constexpr int kTable = kBgChunk * kRows * 4;  // (scale | bias << 16) words
   static constexpr int kTeam = kBgStages * (kX + kCodes) + kTable;
   static constexpr int kLds = KS * kTeam;
-  static constexpr int kLoads = MB + NB;               // DMA instructions a wavefront and stage
+  static constexpr int kXLoads = 4 * MB / WT, kLoads = kXLoads + NB;  // DMA instructions a wavefront and stage
   static constexpr int kPasses = MB == 4 ? 2 : 1;      // of the epilogue
   static constexpr int kPassTokens = kTokens / kPasses;
-  static_assert(2 * kLds <= 160 * 1024, "two workgroups a CU");
-  static_assert(KS * 4 * kPassTokens * kWaveRows * 4 <= kLds, "the epilogue fits");
-  static_assert(kLoads % 3 == 0, "a third of the loads behind each of three slices");
+  static_assert((KS == 4 ? 1 : 2) * kLds <= 160 * 1024, "two workgroups a CU, one of four teams");
+  static_assert(KS * WT * kPassTokens * kWaveRows * 4 <= kLds, "the epilogue fits");
 };
 
 #define MOE_LN_WAIT_VMCNT(n) \
@@ -261,15 +262,15 @@ __device__ __forceinline__ bool bg_tile(int bid, int tt, int nn, int &t, int &n)
   return true;
 }
 
-template <int MB, int NB, int KS, bool F32>
-__global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(LinearArgs a) {
-  using B = Bg<MB, NB, KS>;
+template <int MB, int NB, int KS, int WT, bool F32>
+__global__ __launch_bounds__(KS * WT * kWave, KS == 1 ? 2 : 4) void linear_tiles_kernel(LinearArgs a) {
+  using B = Bg<MB, NB, KS, WT>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   int ti, ni;
   if (!bg_tile(blockIdx.x, (a.T + B::kTokens - 1) / B::kTokens, (a.rows + B::kRows - 1) / B::kRows, ti, ni)) return;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wave = wave8 & 3, team = wave8 >> 2;
+  const int wave = wave8 & (WT - 1), team = wave8 / WT;
   const int t0 = ti * B::kTokens, n0 = ni * B::kRows + wave * B::kWaveRows;
   const int ng = a.cols / kGroup;
   const int tokens = min(B::kTokens, a.T - t0);
@@ -279,14 +280,14 @@ __global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(Li
   const int steps = common + (team == 0 ? left : 0);
   uint8_t *const lds = smem + team * B::kTeam;
 
-  // activations: DMA instruction i of wavefront w fills rows 32 i + 8 w .. +7,
+  // activations: DMA instruction i of wavefront w fills rows 8 (WT i + w) .. +7,
   // lane l row l / 8 of those, LDS chunk l % 8, which holds the row's chunk
   // (l % 8) ^ (row % 8) ^ (row / 8 % 2). Rows past the last re-read it.
   const ln_u32x4 xr = ln_rsrc(a.x + t0 * a.x_stride, (uint32_t)(((tokens - 1) * a.x_stride + a.cols) * 2));
-  uint32_t x_off[MB];
+  uint32_t x_off[B::kXLoads];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int r = min(32 * i + 8 * wave + (lane >> 3), tokens - 1);
+  for (int i = 0; i < B::kXLoads; ++i) {
+    const int r = min(8 * (WT * i + wave) + (lane >> 3), tokens - 1);
     x_off[i] = (uint32_t)(r * (int)a.x_stride + first * kGroup + (((lane & 7) ^ (lane >> 3) ^ (wave & 1)) * 8)) * 2u;
   }
   // codes: instruction b fetches row 32 b + l % 32, columns 32 (l / 32) .. +31
@@ -303,11 +304,12 @@ __global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(Li
   // third i of a stage's DMA instructions: activations first, then codes
   auto dma_part = [&](int step, int slot, int i) {
 #pragma unroll
-    for (int j = i * (B::kLoads / 3); j < (i + 1) * (B::kLoads / 3); ++j) {
-      if (j < MB)
-        ln_dma(xr, x_off[j < MB ? j : 0], step * (kGroup * 2), x_lds + slot * B::kX + j * 4096);
+    for (int j = i * B::kLoads / 3; j < (i + 1) * B::kLoads / 3; ++j) {
+      constexpr int X = B::kXLoads;
+      if (j < X)
+        ln_dma(xr, x_off[j < X ? j : 0], step * (kGroup * 2), x_lds + slot * B::kX + j * (WT * 1024));
       else
-        ln_dma(cr, c_off[j < MB ? 0 : j - MB], step * (kGroup / 2), c_lds + slot * B::kCodes + (j - MB) * 1024);
+        ln_dma(cr, c_off[j < X ? 0 : j - X], step * (kGroup / 2), c_lds + slot * B::kCodes + (j - X) * 1024);
     }
   };
   auto dma = [&](int step, int slot) {
@@ -493,7 +495,7 @@ __global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(Li
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          ep[team * 4 * kPart + (rb * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * kCols + b * 32 + (lane & 31)] =
+          ep[team * WT * kPart + (rb * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * kCols + b * 32 + (lane & 31)] =
               acc[pass * (MB / B::kPasses) + rb][b][r];
     if (KS > 1) lds_barrier();
     with_act(a.act, [&](auto act) {
@@ -505,8 +507,8 @@ __global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(Li
         float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const float4 z0 = *(const float4 *)(ep + k * 4 * kPart + tl * kCols + c8);
-          const float4 z1 = *(const float4 *)(ep + k * 4 * kPart + tl * kCols + c8 + 4);
+          const float4 z0 = *(const float4 *)(ep + k * WT * kPart + tl * kCols + c8);
+          const float4 z1 = *(const float4 *)(ep + k * WT * kPart + tl * kCols + c8 + 4);
           z[0] += z0.x, z[1] += z0.y, z[2] += z0.z, z[3] += z0.w;
           z[4] += z1.x, z[5] += z1.y, z[6] += z1.z, z[7] += z1.w;
         }
@@ -526,15 +528,19 @@ __global__ __launch_bounds__(KS * 4 * kWave, 2 * KS) void linear_tiles_kernel(Li
 // Large tiles from 220 of them: 1500 tokens (240 tiles) 49 us against 55 on
 // middle tiles, 1024 tokens (160) 49 against 44.
 constexpr int kBgMinTiles = 220;
-// Middle tiles above 16 tokens where the small kernel would need more than 640
-// workgroups of 32 tokens: 96 tokens (960) 16 us against 21; 48 tokens by 8192 rows
-// (1024) 17 against 19; 64 tokens (640) 16 against 16; 128 tokens by 2048 rows
-// (512) 15 against 12; 64 tokens by 2048 rows and 4096 columns (256) 28 against 12.
-constexpr int kSmallMaxBlocks = 640;
+// The small kernel up to 16 tokens, and where its workgroups of 32 tokens do not
+// outnumber the CUs: 64 tokens by 2048 rows (256 of them) 7 us against 10 on
+// narrow tiles, 37 by 2048 x 4096 (256) 12 against 16, 32 tokens (320) 12
+// against 10, 64 tokens (640) 16 against 10.
+constexpr int kSmallMaxBlocks = 256;
+// Narrow tiles while each has a CU to itself: 777 tokens by 1001 rows (208) 13 us
+// against 19 on middle tiles, 512 by 2048 (256) 11 against 16, 300 tokens (400) 21
+// against 17, 1000 by 2048 (512) 23 against 20.
+constexpr int kNarrowMaxTiles = 256;
 
-template <int MB, int NB, int KS>
+template <int MB, int NB, int KS, int WT>
 static long long bg_tiles(int T, int rows) {
-  using B = Bg<MB, NB, KS>;
+  using B = Bg<MB, NB, KS, WT>;
   return (long long)((T + B::kTokens - 1) / B::kTokens) * ((rows + B::kRows - 1) / B::kRows);
 }
 
@@ -550,40 +556,43 @@ static hipError_t launch(const LinearArgs &a, int dtype, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MB, int NB, int KS>
+template <int MB, int NB, int KS, int WT>
 static hipError_t launch_tiles(const LinearArgs &a, int dtype, hipStream_t s) {
-  using B = Bg<MB, NB, KS>;
-  auto *kernel = dtype ? linear_tiles_kernel<MB, NB, KS, true> : linear_tiles_kernel<MB, NB, KS, false>;
+  using B = Bg<MB, NB, KS, WT>;
+  auto *kernel = dtype ? linear_tiles_kernel<MB, NB, KS, WT, true> : linear_tiles_kernel<MB, NB, KS, WT, false>;
   static std::atomic<uint64_t> asked[2];
   const hipError_t st = allow_lds((const void *)kernel, B::kLds, asked[dtype ? 1 : 0]);
   if (st != hipSuccess) return st;
-  kernel<<<(int)((bg_tiles<MB, NB, KS>(a.T, a.rows) + 7) / 8 * 8), B::kThreads, B::kLds, s>>>(a);
+  kernel<<<(int)((bg_tiles<MB, NB, KS, WT>(a.T, a.rows) + 7) / 8 * 8), B::kThreads, B::kLds, s>>>(a);
   return hipGetLastError();
 }
 
 // The kernel for a call: 0 large tiles, 1 middle tiles, 2 and 3 the small one with
 // 16 and 32 tokens.
 static int linear_choice(const LinearArgs &a) {
-  if (a.T <= 16) return 2;
+  if (a.T <= 16) return 3;
   // the tile kernels keep 32-bit byte offsets within a tile
   const bool tiles = a.x_stride < (1 << 23) && a.cols < (1 << 23);
-  if (tiles && bg_tiles<4, 2, 1>(a.T, a.rows) >= kBgMinTiles) return 0;
-  return tiles && ln_blocks<2>(a.T, a.rows) > kSmallMaxBlocks ? 1 : 3;
+  if (tiles && bg_tiles<4, 2, 1, 4>(a.T, a.rows) >= kBgMinTiles) return 0;
+  if (!tiles || ln_blocks<2>(a.T, a.rows) <= kSmallMaxBlocks) return 4;
+  return bg_tiles<2, 1, 4, 2>(a.T, a.rows) <= kNarrowMaxTiles ? 2 : 1;
 }
 
 bool linear_grid_ok(const LinearArgs &a) {
   const int c = linear_choice(a);
-  const long long threads = c == 0   ? bg_tiles<4, 2, 1>(a.T, a.rows) * 256
-                            : c == 1 ? bg_tiles<2, 1, 2>(a.T, a.rows) * 512
+  const long long threads = c == 0   ? bg_tiles<4, 2, 1, 4>(a.T, a.rows) * 256
+                            : c == 1 ? bg_tiles<2, 1, 2, 4>(a.T, a.rows) * 512
+                            : c == 2 ? bg_tiles<2, 1, 4, 2>(a.T, a.rows) * 512
                                      : ln_blocks<2>(a.T, a.rows) * 512;
   return threads < (1ll << 32) - 8 * 512;  // of one launch dimension
 }
 
 hipError_t launch_linear(const LinearArgs &a, int dtype, hipStream_t s) {
   switch (linear_choice(a)) {
-    case 0: return launch_tiles<4, 2, 1>(a, dtype, s);
-    case 1: return launch_tiles<2, 1, 2>(a, dtype, s);
-    case 2: return launch<1>(a, dtype, s);
+    case 0: return launch_tiles<4, 2, 1, 4>(a, dtype, s);
+    case 1: return launch_tiles<2, 1, 2, 4>(a, dtype, s);
+    case 2: return launch_tiles<2, 1, 4, 2>(a, dtype, s);
+    case 3: return launch<1>(a, dtype, s);
     default: return launch<2>(a, dtype, s);
   }
 }

@@ -72,18 +72,28 @@ CASES = [  # T, rows, cols, bias, act, residual, dtype
     (513, 769, 1088, False, "none", True, F32),
     (1000, 77, 640, True, "relu", False, BF16),
     (2, 300, 6400, True, "none", False, F32),                # more columns than a fused expert takes
-    # 16 rows by 32 tokens a workgroup, up to 640 of them
+    # narrow tiles (more than 256 blocks of 32 tokens by 16 rows): groups left over by four
+    # teams, fewer groups than teams, more than one table of 8 a team
     (70, 2100, 704, True, "gelu", True, BF16),
     (400, 520, 64, False, "none", True, F32),
     (257, 777, 128, True, "silu", False, F32),
     (90, 2200, 1216, False, "none", False, F32),
-    # middle tiles (more than 640): an odd number of groups (the first team's step over), one
-    # group, two, and more than one table of 8 a team
     (333, 1000, 2048, True, "relu", True, BF16),
     (170, 2100, 704, True, "gelu", True, BF16),
     (700, 520, 64, False, "none", True, F32),
     (450, 777, 128, True, "silu", False, F32),
     (170, 2200, 1216, False, "none", False, F32),
+    (100, 2100, 2240, True, "silu", False, BF16),
+    (64, 2049, 512, False, "none", False, BF16),             # 258 blocks, and 256 below
+    (64, 2048, 512, False, "none", False, BF16),
+    # middle tiles (more than 256 narrow ones): an odd number of groups, one, two, and more
+    # than one table of 8 a team
+    (1100, 1100, 704, True, "gelu", True, BF16),
+    (1300, 900, 64, False, "none", True, F32),
+    (1030, 1090, 128, True, "silu", False, F32),
+    (1200, 1000, 1216, False, "none", False, F32),
+    (1025, 1000, 256, False, "none", False, BF16),           # 272 narrow tiles, and 256 below
+    (1024, 1000, 256, False, "none", False, BF16),
     # large tiles (220 of 128 x 256 and more): tails in both directions, few and many groups
     (2100, 3400, 64, True, "none", True, BF16),
     (3700, 2050, 576, False, "silu", False, F32),
@@ -148,7 +158,7 @@ def test_activation_extremes(T):
         assert torch.isnan(got[1]).all() and not torch.isfinite(got[T - 1]).any()
 
 
-TILES = [(200, 2100), (2100, 3300)]  # the middle and the large tiles
+TILES = [(200, 2100), (1100, 1100), (2100, 3300)]  # narrow, middle and large tiles
 
 
 @pytest.mark.parametrize("T,rows", TILES)
