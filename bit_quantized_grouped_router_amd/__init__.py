@@ -565,19 +565,20 @@ def moe_linear_w4(x: torch.Tensor, w: W4Matrix, bias=None, act: str = "none", re
     """y [T, rows] = act(x [T, cols] W^T + bias) + residual for one int4-g64 matrix W
     [rows, cols]. act: none, relu, silu or gelu (erf form). y is bf16 unless out_dtype, y
     or the residual says fp32; y may be the residual itself (in place)."""
-    if x.dim() != 2 or w.codes.dim() not in (2, 3) or (w.codes.dim() == 3 and w.codes.shape[0] != 1):
+    codes, scales, biases = w.codes, w.scales, w.biases
+    shape = codes.shape
+    if x.dim() != 2 or len(shape) not in (2, 3) or (len(shape) == 3 and shape[0] != 1):
         raise MoeError("x must be [T, cols] and w one matrix: codes [1, rows, cols/2] or [rows, cols/2]")
     T, cols = x.shape
-    rows = w.codes.shape[-2]
-    if w.codes.shape[-1] * 2 != cols:
-        raise MoeError(f"w has {w.codes.shape[-1] * 2} columns; x has {cols}")
+    rows = shape[-2]
+    if shape[-1] * 2 != cols:
+        raise MoeError(f"w has {shape[-1] * 2} columns; x has {cols}")
     if act not in ACTS:
         raise MoeError(f"act {act!r}; expected one of {', '.join(ACTS)}")
     cur = torch.cuda.current_device()
-    for t in (x, w.codes, w.scales, w.biases, bias, residual, y):
+    for t in (x, codes, scales, biases, bias, residual, y):
         if t is not None and t.get_device() != cur:
-            _wrong_device(x=x, codes=w.codes, scales=w.scales, biases=w.biases, bias=bias,
-                          residual=residual, y=y)
+            _wrong_device(x=x, codes=codes, scales=scales, biases=biases, bias=bias, residual=residual, y=y)
     if out_dtype is not None:
         dtype = out_dtype
     else:
@@ -592,10 +593,16 @@ def moe_linear_w4(x: torch.Tensor, w: W4Matrix, bias=None, act: str = "none", re
         ys = _rows(y, (T, rows), "y", (dtype,))
     if bias is not None:
         _need(bias, rows * 2, "bias", BF16)
-    _need(w.codes, rows * cols // 2, "codes", U8)
-    _need(w.scales, rows * (cols // GROUP) * 2, "scales", BF16)
-    _need(w.biases, rows * (cols // GROUP) * 2, "biases", BF16)
-    _check(lib().moe_linear_w4(T, rows, cols, x.data_ptr(), xs, w.c(), _ptr(bias),
+    groups = rows * (cols // GROUP)
+    if (codes.dtype not in U8 or scales.dtype not in BF16 or biases.dtype not in BF16
+            or scales.numel() < groups or biases.numel() < groups):
+        _need(codes, rows * cols // 2, "codes", U8)
+        _need(scales, groups * 2, "scales", BF16)
+        _need(biases, groups * 2, "biases", BF16)
+    if not (codes.is_contiguous() and scales.is_contiguous() and biases.is_contiguous()):
+        raise MoeError("the weights' tensors must be contiguous")
+    _check(lib().moe_linear_w4(T, rows, cols, x.data_ptr(), xs,
+                               MoeW4Matrix(codes.data_ptr(), scales.data_ptr(), biases.data_ptr()), _ptr(bias),
                                ACTS[act], None if residual is None else residual.data_ptr(), rs,
                                y.data_ptr(), ys, code, _stream(stream, cur)), "moe_linear_w4")
     return y
