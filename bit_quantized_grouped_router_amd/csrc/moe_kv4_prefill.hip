@@ -32,12 +32,12 @@
 //
 // Keys are split over workgroups, as in the other kernel, where the row tiles
 // do not fill the card (512 tokens behind 60000, 16 heads on 2, D = 128: 1531 us
-// unsplit, 306 split eight ways: 826 TFLOP/s).
+// unsplit, 308 split eight ways: 821 TFLOP/s).
 //
 // Measured (us; TFLOP/s of the products that causality leaves), 16 heads on 2:
-//   4096 tokens behind 1003   D = 64 110 (463)  128 163-176 (582-628)
-//   8192 tokens               D = 128 343 (802)
-//   4096 tokens               D = 256 218 (629)
+//   4096 tokens behind 1003   D = 64 109 (472)  128 148-172 (596-690)
+//   8192 tokens               D = 128 345 (796)
+//   4096 tokens               D = 256 201 (685)
 // next to 1224 TFLOP/s of a library product of 8192^3. Bound by the vector
 // instructions that a tile needs besides its products (about 150 a wavefront,
 // 16 exponentials among them, next to 512 cycles of MFMA; matrix instructions
