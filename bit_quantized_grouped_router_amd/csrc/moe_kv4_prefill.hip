@@ -226,7 +226,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
     t0 = (int)(mine.lo < mine.hi ? mine.lo : 0);
     t1 = (int)(mine.lo < mine.hi ? mine.hi : 0);
   }
-  const int all0 = (int)r1.lo, all1 = (int)(tiles > 0 ? r0.hi : 0);  // what every row sees
+  const int all0 = (int)r1.lo, all1 = (int)(tiles > 0 && r0.hi > 0 ? r0.hi : 0);  // what every row sees
 
   // rebuilding: wavefronts 0, 1 take the keys' halves, 2, 3 the values'; four
   // threads a row
