@@ -108,6 +108,21 @@ def test_attention_workspace(L):
     assert L.moe_kv4_attention_workspace_bytes(None, 1, 1, 0) == 0
 
 
+def test_attention_limits(L):
+    """The largest scale and row counts, and the prompts' workspace: none where their rows fill
+    the card, and no more than a part for every row and split."""
+    assert attend(L, scale=2.0 ** 65) == INVALID
+    wide = dims(B=1, Hq=4, Hkv=1, D=64, page=128, max_pages=512, num_pages=512)
+    ws = lambda dm, T, new: L.moe_kv4_attention_workspace_bytes(ctypes.byref(dm), T, new, 0)
+    assert attend(L, dm=wide, T=2 ** 28, max_new=2 ** 28) == UNSUPPORTED   # 2^30 rows of a head
+    assert attend(L, dm=wide, T=2 ** 29, max_new=1) == UNSUPPORTED         # 2^31 rows in all
+    assert ws(wide, 2 ** 28, 2 ** 28) == 0
+    assert ws(wide, 2 ** 20, 2 ** 20) == 0
+    some = ws(wide, 2048, 2048)
+    part = 2048 * 4 * (64 + 2) * 4
+    assert some > part and some % part == 0 and some // part <= 8
+
+
 def project(L, T=3, rows=5, cols=128, x=FAKE, xs=128, w=None, bias=None, act=0, res=None, rs=0, y=FAKE,
             ys=5, dtype=0):
     return L.moe_linear_w4(T, rows, cols, x, xs, ctypes.byref(plane() if w is None else w), bias, act, res,
