@@ -108,6 +108,31 @@ MOE_HD Kv4Share kv4_share(const Kv4Range &r, int per, int splits, int split) {
   return s;
 }
 
+// Row tile and (cache head, sequence) that a prompt workgroup takes: the
+// workgroups are numbered x = 0 .. n - 1 of hs = 0 .. heads - 1. Every tile of
+// every hs is taken exactly once. Causal calls go from the longest tile to the
+// shortest; with `pair`, where all workgroups are on the card at once, two to a
+// CU, so that those from number 256 on share the CUs of the first 256: tiles of
+// all heads are put in one list, longest first, and its second part is turned
+// round, so that the longest tile shares its CU with the shortest (us without and
+// with, 16 heads on 2: 4096 tokens behind 1003, D = 128 173 and 144, D = 64 without
+// earlier ones 104 and 77; 3000 tokens, D = 128 92 and 80; 1500 tokens, 32 on 8 55
+// and 47).
+struct Kv4Place {
+  int tile;
+  long long hs;
+};
+
+constexpr int kPairCus = 256;
+
+MOE_HD Kv4Place kv4_prompt_place(int x, long long hs, int n, long long heads, bool causal, bool pair) {
+  if (!causal) return Kv4Place{x, hs};
+  if (!pair || n > 2 * kPairCus || heads > 2 * kPairCus || n * heads > 2 * kPairCus) return Kv4Place{n - 1 - x, hs};
+  const int all = n * (int)heads, at = (int)hs * n + x;
+  const int rank = at < kPairCus ? at : all - 1 - (at - kPairCus);
+  return Kv4Place{n - 1 - rank / (int)heads, rank % (int)heads};
+}
+
 #ifdef __HIPCC__
 // dtype: 0 bf16, 1 fp32
 hipError_t launch_kv4_append(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,

@@ -35,9 +35,10 @@
 // unsplit, 308 split eight ways: 821 TFLOP/s).
 //
 // Measured (us; TFLOP/s of the products that causality leaves), 16 heads on 2:
-//   4096 tokens behind 1003   D = 64 109 (472)  128 148-172 (596-690)
-//   8192 tokens               D = 128 345 (796)
-//   4096 tokens               D = 256 201 (685)
+//   4096 tokens behind 1003   D = 128 144 (712)
+//   3000 tokens               D = 64 59 (315)   128 80 (463)
+//   4096 tokens               D = 64 77 (446)   128 108 (637)   256 201 (683)
+//   8192 tokens               D = 128 322 (854)
 // next to 1224 TFLOP/s of a library product of 8192^3. Bound by the vector
 // instructions that a tile needs besides its products (about 150 a wavefront,
 // 16 exponentials among them, next to 512 cycles of MFMA; matrix instructions
@@ -141,24 +142,6 @@ __device__ __forceinline__ f32x16_t mfma32(const uint4 &a, const uint4 &b, const
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
   else
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-
-// The row tile of workgroup i of n, for causal calls longest first. Where all
-// workgroups are on the card at once and two share a CU (not D = 256), every
-// second round of 256 runs the other way, so that a long tile shares its CU with
-// a short one (4096 tokens behind 1003, D = 128: 176 us against 198; D = 256,
-// whose second round comes as the shorter tiles of the first end, 4096 tokens: 218
-// us against 300).
-template <int D>
-__device__ __forceinline__ int prefill_tile(int i, int n, bool causal) {
-  if (!causal) return i;
-  const int heads = gridDim.y * gridDim.z;
-  if (D < 256 && (long long)n * heads <= 512) {
-    const int linear = i + n * (blockIdx.y + gridDim.y * blockIdx.z);
-    if (n <= 256) return (linear >> 8) & 1 ? i : n - 1 - i;
-    if (i >= 256) return i - 256;
-  }
-  return n - 1 - i;
 }
 
 // Whether any thread of the workgroup says so: a barrier, and a scalar branch.
@@ -543,15 +526,14 @@ __global__ __launch_bounds__(kPfWaves *kWave, D == 256 ? 1 : 2) void kv4_prefill
                                                                                       float *__restrict__ part) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ __attribute__((aligned(4))) uint8_t vnan[kKvTile][4];  // value groups of a tile that are NaN (bf16)
-  int tile, split = 0;
-  if (splits == 1) {
-    tile = prefill_tile<D>(blockIdx.x, gridDim.x, at.causal);
-  } else {
-    tile = blockIdx.x / splits;
-    split = blockIdx.x - tile * splits;
-    if (at.causal) tile = gridDim.x / splits - 1 - tile;  // longest first
-  }
-  const RowTile rt = row_tile(dm, bt, at.max_new, tile, blockIdx.y, blockIdx.z, kPfRows);
+  // Pairs where two workgroups share a CU and no keys are split (D = 256, one a CU,
+  // 4096 tokens: 300 us with pairs, whose second round would come as the shorter
+  // tiles of the first end, and 218 without).
+  const int x = blockIdx.x / splits, split = blockIdx.x - x * splits;
+  const Kv4Place place = kv4_prompt_place(x, blockIdx.y + (long long)gridDim.y * blockIdx.z, gridDim.x / splits,
+                                          (long long)gridDim.y * gridDim.z, at.causal, D < 256 && splits == 1);
+  const int seq = (int)(place.hs / gridDim.y), head = (int)(place.hs - (long long)seq * gridDim.y);
+  const RowTile rt = row_tile(dm, bt, at.max_new, place.tile, head, seq, kPfRows);
   if (rt.row0 >= rt.rows || rt.rows <= at.above) return;
   int thread = threadIdx.x;
   if (prefill<D, true>(dm, kc, vc, bt, at, rt, split, splits, part, thread, smem, vnan)) return;

@@ -648,3 +648,42 @@ def test_binding_refusals():
     with pytest.raises(M.MoeError):
         M.moe_kv4_attention(long, q, table, dev[1], dev[2], max_new=2,
                             ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------------------------ prompts whose rows fill the card
+# No keys are split (no workspace), so a causal call's tiles go in the order that pairs
+# long ones with short ones: 257 to 512 tiles over several heads, of which some begin
+# before and end behind workgroup 256.
+
+UNSPLIT = [  # new, past, Hq, Hkv, D, page, causal
+    ([3000], [0], 16, 2, 128, 64, True),
+    ([3000], [40], 16, 2, 64, 16, True),
+    ([1500], [0], 32, 8, 128, 16, True),
+    ([1500], [7], 32, 4, 64, 32, True),
+    ([640, 640, 640], [0, 100, 33], 32, 8, 64, 16, True),
+    ([640, 411, 500], [0, 100, 33], 32, 8, 128, 64, True),
+    ([869, 800, 869, 869, 640, 750, 801, 777, 869], [0, 90, 3, 0, 200, 1, 20, 0, 4], 6, 2, 128, 16, True),
+    ([2049], [0], 24, 8, 64, 128, True),
+    ([2100], [300], 64, 2, 64, 16, True),                    # more tiles than are paired
+    ([1500], [0], 32, 8, 64, 16, False),
+    ([1500], [0], 32, 8, 256, 64, True),
+]
+
+
+@pytest.mark.parametrize("new,past,Hq,Hkv,D,page,causal", UNSPLIT)
+def test_prompts_that_fill_the_card(new, past, Hq, Hkv, D, page, causal):
+    rng = np.random.default_rng(Hq * 3 + D + len(new) + sum(past))
+    b = Batch(rng, new, past, page)
+    width = b.table.shape[1]
+    c = filled(rng, b, Hkv, D)
+    # rows and pairs enough for the prompts' kernel, and its keys in one piece
+    assert b.T * Hq >= 4096 and b.T * Hq * width * page >= 2 ** 25 and max(new) * (Hq // Hkv) > 64
+    assert M.moe_kv4_attention_workspace_bytes(c, b.T, Hq, b.B, width, b.max_new()) == 0
+    q64, q = queries(rng, b.T, Hq, D)
+    out = torch.full((b.T, Hq, D), float("nan"), dtype=BF16, device="cuda")
+    M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), causal=causal, out=out)
+    assert not torch.isnan(out).any()
+    want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, D ** -0.5, causal)
+    check(out, want, tol, f"{new} {past} {Hq}/{Hkv}x{D}")
+    M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), causal=causal, out=q)
+    assert torch.equal(out, q)

@@ -285,3 +285,49 @@ def test_binding_refuses_shapes_and_types():
                 t(3, 2, 32), t(3, 2, 64, dtype=bf)):
         with pytest.raises(M.MoeError):
             M._rows(bad, (3, 2, 64), "k", (torch.float32,))
+
+
+PLACE_SHIM = r"""
+#include "moe_kv4.h"
+using namespace moe;
+// how many (tile, head) of n x heads are not taken exactly once
+extern "C" long long lost(int n, long long heads, int causal, int pair, unsigned char *seen) {
+  for (long long i = 0; i < n * heads; ++i) seen[i] = 0;
+  long long bad = 0;
+  for (long long hs = 0; hs < heads; ++hs)
+    for (int x = 0; x < n; ++x) {
+      const Kv4Place p = kv4_prompt_place(x, hs, n, heads, causal, pair);
+      if (p.tile < 0 || p.tile >= n || p.hs < 0 || p.hs >= heads) return -1;
+      seen[p.hs * n + p.tile]++;
+    }
+  for (long long i = 0; i < n * heads; ++i) bad += seen[i] != 1;
+  return bad;
+}
+// the tile that shares a CU with workgroup 0's, of one head
+extern "C" int tile_of(int x, int n, int pair) { return kv4_prompt_place(x, 0, n, 1, true, pair).tile; }
+"""
+
+
+def test_prompt_tiles_are_taken_exactly_once(tmp_path):
+    """Every row tile of every head by one workgroup, for all shapes of up to 512 tiles and
+    heads, with and without a mask, in pairs and not; and past the sizes that pair."""
+    src, so = tmp_path / "place.cpp", tmp_path / "place.so"
+    src.write_text(PLACE_SHIM)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=undefined",
+                    "-static-libubsan", "-shared", "-fPIC",
+                    "-I", os.path.join(ROOT, "bit_quantized_grouped_router_amd", "csrc"), str(src), "-o", str(so)],
+                   check=True)
+    h = ctypes.CDLL(str(so))
+    h.lost.argtypes = [ctypes.c_int, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
+    h.lost.restype = ctypes.c_longlong
+    seen = ctypes.create_string_buffer(1 << 20)
+    shapes = [(n, k) for n in range(1, 513) for k in range(1, 513) if n * k <= 600]
+    shapes += [(513, 1), (512, 2), (700, 3), (3, 700), (512, 512), (1000, 1), (1, 1000)]
+    for n, heads in shapes:
+        for causal in (0, 1):
+            for pair in (0, 1):
+                assert h.lost(n, heads, causal, pair, seen) == 0, (n, heads, causal, pair)
+    # the longest tile is beside the shortest, and they come longest first
+    assert [h.tile_of(x, 512, 1) for x in (0, 1, 255, 256, 257, 511)] == [511, 510, 256, 0, 1, 255]
+    assert [h.tile_of(x, 300, 1) for x in (0, 43, 256, 299)] == [299, 256, 0, 43]
+    assert [h.tile_of(x, 300, 0) for x in (0, 299)] == [299, 0]
