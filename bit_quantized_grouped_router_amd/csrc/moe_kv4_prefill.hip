@@ -26,9 +26,10 @@
 // price: where a tile has a value or key of 2^15 or more, or a scale so small
 // that codes would fall among fp16's subnormals, or a query is too large or
 // too small, the workgroup starts over with bf16 operands, one tile after the
-// other. That run also takes NaN and infinities: such values are replaced by
-// zeros, and the rows that see their key get NaN in the group's channels, so
-// that a key no row may look at never reaches one.
+// other. That run also takes NaN and infinities: a group of values that holds one,
+// or that passes bf16's range at code 0 or 15, is replaced by zeros, and the rows
+// that see its key get NaN in the group's channels, so that a key no row may look
+// at never reaches one.
 //
 // Keys are split over workgroups, as in the other kernel, where the row tiles
 // do not fill the card (512 tokens behind 60000, 16 heads on 2, D = 128: 1531 us
@@ -258,7 +259,9 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
       c.s2 = f16x2_t{s, s}, c.b2 = f16x2_t{b, b}, c.s16 = c.s2 * (_Float16)0.0625f;
       range.add(sb);
     } else if (plane == 1) {
-      const bool nan = !(fabsf(c.s) <= 3.402823466e38f) || !(fabsf(c.b) <= 3.402823466e38f);
+      // values run from b to 15 s + b; a scale of 2e37 overflows there though it is finite
+      const float end = bf16_to_f32(to_bf16(fmaf(15.0f, c.s, c.b)));
+      const bool nan = !(fabsf(c.b) <= 3.402823466e38f) || !(fabsf(end) <= 3.402823466e38f);
       if ((quarter * NG) % 4 == 0) vnan[key][quarter * NG / 4] = nan;
       if (nan) c.s = c.b = 0.f;
     }

@@ -453,6 +453,9 @@ size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int3
  *     2^25, and more than 64 rows max_new * Hq / Hkv of a cache head): keys, values and
  *     weights, to fp16; to bf16 for a block of rows whose keys, values or
  *     queries fp16's range does not hold (2^15 and more, or scales below 2^-13).
+ * Sums are divided at the end: while scales and biases are below 2^80 they cannot
+ * overflow; larger values may come back as infinities or NaN, in their group of 64
+ * channels, for the tokens that see them.
  * Results repeat bit for bit. The calls are asynchronous and may be captured.
  */
 moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,

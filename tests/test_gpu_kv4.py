@@ -687,3 +687,32 @@ def test_prompts_that_fill_the_card(new, past, Hq, Hkv, D, page, causal):
     check(out, want, tol, f"{new} {past} {Hq}/{Hkv}x{D}")
     M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), causal=causal, out=q)
     assert torch.equal(out, q)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("past", [50, 3000])
+def test_prompt_values_past_the_range_stay_with_those_who_see_them(D, past):
+    """A finite scale whose rebuilt values (or keys) overflow, at a position that the first 37
+    tokens do not see, some of them in a block of rows with tokens that do: their results are
+    those beside a NaN there, bit for bit. Who sees it gets no finite number in its group."""
+    rng = np.random.default_rng(41)
+    b = prompt_batch(rng, [80], [past], 16)
+    q64, q = queries(rng, 80, 64, D)
+    at = past + 37
+    for which in "kv":
+        c = filled(rng, b, 1, D)
+        m = getattr(c, which)
+        pg, sl = int(b.table[0, at // 16]), at % 16
+        outs = []
+        for s, z in ((float("nan"), float("nan")), (2.5e37, 0.0), (-2.5e37, -1e38), (3e38, 3e38)):
+            m.codes[pg, 0, sl] = 0xFF      # 15 s + z is past 3.4e38
+            m.scales[pg, 0, sl, -1] = s
+            m.biases[pg, 0, sl, -1] = z
+            outs.append(M.moe_kv4_attention(c, q, *b.dev, max_new=80).float().cpu().numpy())
+        for i, out in enumerate(outs):
+            same = bool(np.isfinite(out[:37]).all() and (out[:37] == outs[0][:37]).all())
+            assert same, (which, i)
+            if which == "v":
+                kept = bool(np.isfinite(out[37:, :, -64:]).any())
+                others = bool(np.isfinite(out[37:, :, :-64]).all())
+                assert others and not kept, i
