@@ -286,7 +286,7 @@ struct RowSums {
   f32x4_t o[NG][4];  // [g][j]: register r
   float w[NG];       // sum of the rounded weights p s, this lane's keys only
   float c[NG];       // sum of p (b + 8 s), this lane's keys only
-  float m, l;        // reference maximum (scaled log2 units); sum of p, this lane's keys only
+  float m, l;        // reference score (unscaled); sum of p, this lane's keys only
 };
 
 // One 32-key tile. masked (wave-uniform): some row does not see some key (t0 ..
@@ -351,10 +351,9 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
   float mx = s[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
-  mx *= scale2;
-  if (__builtin_amdgcn_ballot_w64(mx > a.m + kSlack) != 0) {
+  if (__builtin_amdgcn_ballot_w64((mx - a.m) * scale2 > kSlack) != 0) {
     const float m = fmaxf(a.m, groups_max(mx));
-    const float alpha = a.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(a.m - m);
+    const float alpha = a.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((a.m - m) * scale2);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
@@ -371,7 +370,7 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
   float p[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale2, -ref));
+    p[i] = __builtin_amdgcn_exp2f((s[i] - ref) * scale2);  // see kSlack for this order
     a.l += p[i];
   }
 #pragma unroll
@@ -412,9 +411,9 @@ __device__ __forceinline__ Kv4Range tile_range(const Kv4Dims &dm, const RowTile 
 // What a part of a row (reference m_i, sum l_i) counts for at reference m: one
 // that saw no key (l_i = 0) nothing; one whose scores were all NaN has no
 // reference and passes its NaN on.
-__device__ __forceinline__ float part_weight(float m_i, float l_i, float m) {
+__device__ __forceinline__ float part_weight(float m_i, float l_i, float m, float scale2) {
   if (m_i == kNegInf) return l_i == 0.f ? 0.f : 1.f;
-  return __builtin_amdgcn_exp2f(m_i - m);
+  return __builtin_amdgcn_exp2f((m_i - m) * scale2);
 }
 
 // Channels c .. c + 3 of a token's head, divided by the row's sum; a row that
@@ -596,7 +595,7 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
 #pragma unroll
   for (int g = 0; g < NG; ++g) qsum[g] = groups_sum(qsum[g]);
   const bf16x8_t qaff = affine_query<NG>(qsum, lane >> 4);
-  const float scale2 = at.scale * 1.4426950408889634f;  // scores in log2 units
+  const float scale2 = at.scale * kLog2e;  // scores in log2 units
   RowSums<D> a;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
@@ -641,7 +640,7 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
   float m = kNegInf;
 #pragma unroll
   for (int w = 0; w < W; ++w) m = fmaxf(m, sm[w][lane & 15]);
-  const float f = part_weight(a.m, a.l, m);
+  const float f = part_weight(a.m, a.l, m, scale2);
   float *so = (float *)ring + (lane & 15) * (D + 4) + 4 * (lane >> 4);
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
@@ -664,7 +663,7 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
     for (int w = 0; w < W; ++w) {
       const float4 x = *(const float4 *)((float *)(smem + w * kStages * Ring<D>::kStage) + r * (D + 4) + c);
       o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-      l = fmaf(part_weight(sm[w][r], sl[w][r], mr), sl[w][r], l);
+      l = fmaf(part_weight(sm[w][r], sl[w][r], mr, scale2), sl[w][r], l);
     }
     if (share.used > 1) {
       const long long pr = part_index(dm, rt, r, splits, split);
@@ -740,7 +739,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
     const long long pr = pr0 + s;
     const float2 mls = *(const float2 *)(ml + pr * 2);
     const float4 x = *(const float4 *)(part + pr * D + chunk * C + c * 4);
-    const float f = part_weight(mls.x, mls.y, m);
+    const float f = part_weight(mls.x, mls.y, m, at.scale * kLog2e);
     l = fmaf(f, mls.y, l);
     o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
   }

@@ -8,9 +8,15 @@ namespace moe {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // Scaled log2 units a score may exceed the running reference by before the
 // accumulators are rescaled: weights stay below 2^8, far from overflow, and
-// the rescale runs once or twice a row instead of at every new maximum.
+// the rescale runs once or twice a row instead of at every new maximum. The
+// reference is kept unscaled and a weight is exp2((score - reference) * scale):
+// the difference to a near reference is exact, so this holds for scores of any
+// size, where the difference of two scaled scores would be off by a step of
+// theirs (128 from 2^31 on, an overflow).
 constexpr float kSlack = 8.0f;
 
 typedef const __attribute__((address_space(4))) int32_t kv_const_i32;

@@ -25,8 +25,8 @@
 // the rounding is all; bf16 operands would make it 3.2e-3). Its range is the
 // price: where a tile has a value or key of 2^15 or more, or a scale so small
 // that codes would fall among fp16's subnormals, or a query is too large or
-// too small, the workgroup starts over with bf16 operands, one tile after the
-// other. That run also takes NaN and infinities: a group of values that holds one,
+// too small, or scores pass kMostHalf, the workgroup starts over with bf16
+// operands, one tile after the other. That run also takes NaN and infinities: a group of values that holds one,
 // or that passes bf16's range at code 0 or 15, is replaced by zeros, and the rows
 // that see its key get NaN in the group's channels, so that a key no row may look
 // at never reaches one.
@@ -63,6 +63,9 @@ constexpr int ahead() { return !HALF ? 1 : D == 256 ? 2 : 3; }
 // by no more than 2^-32 of the largest where fp16 runs out of exponents, so that
 // even a million keys in a faint tail lose less than 2^-12 of it together.
 constexpr float kShift = 7.0f;
+// Scaled scores up to here take one FMA to their distance from the reference,
+// which is then off by half a step of theirs at most, 1/2: weights stay below 2^15.5.
+constexpr float kMostHalf = 0x1p23f;
 constexpr int kSalu = 0x4;  // sched_barrier: scalar instructions may pass
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -285,7 +288,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
     for (int i = 0; i < 2 * P::kWords; ++i) step(r, c, i);
   };
 
-  const float scale2 = at.scale * 1.4426950408889634f;  // scores in log2 units
+  const float scale2 = at.scale * kLog2e;  // scores in log2 units
   // Keys: chunk 2 k + half of row l % 32. Values: lane group member j supplies
   // key j / 4 of a step of four, channels 4 (j % 4) .. +3.
   const int vk = 4 * half + ((lane >> 2) & 3);  // + 8 a step
@@ -321,11 +324,13 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
       }
     }
   };
+  HalfRange range;
   // moves the reference m where a score exceeds it by too much
   auto rescale = [&](float mx, f32x16_t (&o)[NM], float &m, float &l) {
-    if (__builtin_expect(__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0, 0)) {
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64((mx - m) * scale2 > kSlack) != 0, 0)) {
       const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32, kWave)));
-      const float alpha = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+      const float alpha = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - mn) * scale2);
+      if (HALF && mn != kNegInf && !(fabsf(mn * scale2) < kMostHalf)) range.hi = ~0u;
 #pragma unroll
       for (int i = 0; i < NM; ++i)
 #pragma unroll
@@ -335,11 +340,12 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
     }
   };
 
-  // Weights of keys e, e + 1 and their sum.
+  // Weights of keys e, e + 1 and their sum. ref: the reference, for fp16 scaled and
+  // less kShift.
   auto weigh = [&](const f32x16_t &s, int e, float ref, float &l) {
     const f16x2_t ones = {(_Float16)1.0f, (_Float16)1.0f};
-    const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e], scale2, -ref));
-    const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e + 1], scale2, -ref));
+    const float p0 = __builtin_amdgcn_exp2f(HALF ? fmaf(s[e], scale2, -ref) : (s[e] - ref) * scale2);
+    const float p1 = __builtin_amdgcn_exp2f(HALF ? fmaf(s[e + 1], scale2, -ref) : (s[e + 1] - ref) * scale2);
     uint32_t w = HALF ? pack_half(p0, p1) : pack_bf16x2(p0, p1);
     if constexpr (HALF) {
       asm volatile("" : "+v"(w));  // in this place, not behind the next branch
@@ -368,7 +374,6 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
 #pragma unroll
   for (int i = 0; i < NM; ++i) o[i] = f32x16_t{0};
   float m = kNegInf, l = 0.f;
-  HalfRange range;
   uint32_t nan = 0;  // value groups (a byte each) that are NaN at a key this row sees
   // Page numbers of 32 tiles at a time lie in a register, two lanes a tile:
   // scalar loads would return out of order with LDS reads, so that every tile
@@ -405,13 +410,13 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
     float mx = s0[0];
 #pragma unroll
     for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s0[e]);
-    rescale(mx * scale2, o, m, l);
+    rescale(mx, o, m, l);
     pg1 = pg2, pg2 = pg3, pg3 = pages(now, 3);
     lds_barrier();
     int vb = 0, wb = 2 * P::kPlane;
     // Tile i, whose scores are s, and the scores sn of tile i + 1.
     auto tile = [&](int i, int kb, const f32x16_t &s, f32x16_t &sn) __attribute__((always_inline)) {
-      const float ref = m == kNegInf ? 0.f : m - kShift;
+      const float ref = m == kNegInf ? 0.f : fmaf(m, scale2, -kShift);
       uint32_t pw[8];
       // the wavefront that scores goes first, its neighbour's rebuilding can wait (4096
       // tokens by 5099 keys without a mask 248 -> 240 us, with one within 2%; D = 64
@@ -450,7 +455,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
         later = entries(i + 36);
       }
       pg1 = pg2, pg2 = pg3, pg3 = pages(now, i + 4);
-      rescale(mx * scale2, o, m, l);
+      rescale(mx, o, m, l);
       vb = vb == 2 * P::kPlane ? 0 : vb + P::kPlane;
       wb = wb == 2 * P::kPlane ? 0 : wb + P::kPlane;
       lds_barrier();
@@ -475,7 +480,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
       float mx = s[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
-      rescale(mx * scale2, o, m, l);
+      rescale(mx, o, m, l);
       uint32_t pw[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) pw[e] = weigh(s, 2 * e, m == kNegInf ? 0.f : m, l);
@@ -494,10 +499,11 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   // (no return from here for rows behind the last: a branch of lanes would have
   // the second attempt's registers beside the first's)
   const bool partial = share.used > 1;
-  const float sum_inv = partial ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
+  const float unit = HALF ? 0x1p-7f : 1.0f;  // parts leave without kShift
+  const float sum_inv = partial ? unit : l == 0.f ? 0.f : 1.0f / l;
   const long long pr = part_index(dm, rt, real ? row - rt.row0 : 0, splits, split);
   float *sums = part + pr * D + 2 * half;
-  if (partial && real && half == 0) *(float2 *)(part_stats(dm, bt, splits, part) + pr * 2) = make_float2(HALF ? m - kShift : m, l);
+  if (partial && real && half == 0) *(float2 *)(part_stats(dm, bt, splits, part) + pr * 2) = make_float2(m, l * unit);
   uint16_t *out = at.out + (rt.sp.begin + tok) * at.out_stride + (long long)hd * D + 2 * half;
   if (real) {
 #pragma unroll

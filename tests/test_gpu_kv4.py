@@ -716,3 +716,41 @@ def test_prompt_values_past_the_range_stay_with_those_who_see_them(D, past):
                 kept = bool(np.isfinite(out[37:, :, -64:]).any())
                 others = bool(np.isfinite(out[37:, :, :-64]).all())
                 assert others and not kept, i
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,past,Hq", [(2, 30, 4), (1, 5000, 4), (80, 50, 64), (80, 3000, 64)])
+def test_scores_of_any_size(D, new, past, Hq):
+    """Scores far past fp32's integers, and past fp32 once they are scaled (scales up to 2^64):
+    keys a_t u with u = +-1 a group, exact in the cache and in every product, where a token's own
+    key scores highest of all it sees; by 64 and more, its result is its own value."""
+    rng = np.random.default_rng(43)
+    b = prompt_batch(rng, [new], [past], 16)
+    n = new + past
+    u = rng.choice([-1.0, 1.0], D // 64).repeat(64)
+    back = np.arange(n - 1, -1, -1)              # tokens behind this one
+    far = np.exp2(rng.integers(3, 12, n)) * (1 + rng.integers(0, 128, n) / 128)
+    up = np.where(back < 128, 2.0 ** 13 * (1 - back / 256), far)
+    down = -np.where(back < 128, 1 + back / 128, far)
+    v = bf16_values(rng.standard_normal((n, 1, D)))
+    q, s, z = K.quantise(v)
+    val = K.values(K.pack(q), s, z)[:, 0]
+    s, z = (np.abs(np.repeat(bf16_to_f64(a)[:, 0], 64, -1)) for a in (s, z))
+    # 2^-8 each: the result, the values or weights as bf16 (few rows: weight times scale, on
+    # codes - 8), and weights beside a sum of unrounded ones; then the fp32 sums of n keys
+    tol = (2.0 ** -8 * (3 * np.abs(val) + 8 * s) + (n + 64) * 2.0 ** -24 * (55 * s + z))[past:, None]
+    for a in (up, down):
+        k = (a[:, None] * u).astype(np.float32)
+        assert (k == bf16_values(k)).all()
+        c = make_cache(b.num_pages, 1, 16, D)
+        M.moe_kv4_append(c, torch.from_numpy(k).cuda()[:, None], torch.from_numpy(v).cuda(),
+                         b.dev[0], i32([0, n]), b.dev[2])
+        for size in (0, 100):
+            x = torch.from_numpy(np.broadcast_to(u * 2.0 ** size, (new, Hq, D)).copy()).cuda().to(BF16)
+            for scale in (D ** -0.5, 2.0 ** 20, 2.0 ** 64):
+                out = M.moe_kv4_attention(c, x, *b.dev, max_new=new, scale=scale).double().cpu().numpy()
+                finite = bool(np.isfinite(out).all())
+                assert finite, (size, scale)
+                gap = 2.0 ** size * scale * D * (32 if a is up else 2.0 ** -7)
+                worst = float((np.abs(out - val[past:, None]) / tol).max())
+                assert gap < 64 or worst <= 1, (size, scale, worst)
