@@ -21,11 +21,13 @@ namespace moe {
 
 constexpr int kLnWaves = 8;
 
+// GELU by erfc: 1 + erf cancels below zero and leaves nothing from z = -5.6 on
+// (8192 x 5120 x 2048 with GELU 209 -> 223 us, small and middle batches the same).
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == kActRelu) return z > 0.f ? z : (z == z ? 0.f : z);
   if constexpr (ACT == kActSilu) return z / (1.0f + expf(-z));
-  if constexpr (ACT == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(z * -0.70710678118654752f);
   return z;
 }
 

@@ -318,7 +318,7 @@ moe_status moe_dequant_w4(const moe_w4_matrix *m, int32_t rows, int32_t cols, ui
 typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
 
 /* Activations of moe_linear_w4: z; max(z, 0); z / (1 + exp(-z));
- * z * (1 + erf(z / sqrt 2)) / 2. */
+ * z * erfc(-z / sqrt 2) / 2. */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
 
 /*

@@ -1,4 +1,6 @@
 """moe_linear_w4 on the GPU against the fp64 oracle, within the bound of its fp32 sums."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -221,3 +223,24 @@ def test_binding_refusals():
         with pytest.raises(M.MoeError):
             M.moe_linear_w4(a.pop("x"), w, **a)
     assert M.moe_linear_w4(x[:0], w).shape == (0, 32)
+
+
+@pytest.mark.parametrize("T,rows", [(1, 20), (40, 20)] + TILES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gelu_keeps_its_digits_far_from_zero(T, rows, dtype):
+    """z erfc(-z / sqrt 2) / 2 for z down to -12, relative to itself: the argument is off by 2^-23
+    of itself (its product and the constant), which z^2 + 1 takes into erfc, and erfc and the two
+    products by 16 steps of 2^-24 together; z itself is exact (one product of ones)."""
+    z = rounded(np.linspace(-12.0, 6.0, T) if T > 1 else np.array([-6.5]))
+    x = np.zeros((T, 64))
+    x[:, 5] = z
+    ones = M.W4Matrix(torch.zeros((1, rows, 32), dtype=torch.uint8, device="cuda"),
+                      torch.zeros((1, rows, 1), dtype=BF16, device="cuda"),
+                      torch.ones((1, rows, 1), dtype=BF16, device="cuda"))
+    got = M.moe_linear_w4(torch.from_numpy(x).cuda().to(BF16), ones, act="gelu", out_dtype=dtype)
+    got = got.double().cpu().numpy()
+    want = np.array([v * math.erfc(-v / math.sqrt(2.0)) / 2.0 for v in z])[:, None]
+    tol = ((z ** 2 + 1) * 2.0 ** -23 + 2.0 ** -20)[:, None] + (2.0 ** -8 if dtype == BF16 else 0)
+    worst = float((np.abs(got - want) / (tol * np.abs(want) + 1e-300)).max())
+    say(f"  gelu {T}: worst {worst:.3f} of the bound")
+    assert worst <= 1
