@@ -612,23 +612,33 @@ def moe_linear_w4(x: torch.Tensor, w: W4Matrix, bias=None, act: str = "none", re
 
 class KV4Cache:
     """A paged key/value cache in int4-g64: k and v hold codes uint8 [num_pages, Hkv, page,
-    D/2] and scales/biases bf16 [num_pages, Hkv, page, D/64]."""
+    D/2] and scales/biases bf16 [num_pages, Hkv, page, D/64]. The planes may be replaced;
+    sizes are always those of the planes there are, and every call checks them."""
 
     def __init__(self, k: W4Matrix, v: W4Matrix):
         self.k, self.v = k, v
+        self.sizes()
+
+    def sizes(self):
+        """(num_pages, Hkv, page, D); raises where the six tensors do not fit together."""
+        k, v = self.k, self.v
         shape = k.codes.shape
         if len(shape) != 4:
             raise MoeError("cache codes must be [num_pages, Hkv, page, D/2]")
-        self.num_pages, self.Hkv, self.page, half = shape
-        self.D = 2 * half
-        g = (self.num_pages, self.Hkv, self.page, self.D // GROUP)
-        for n, m in (("k", k), ("v", v)):
-            if m.codes.shape != shape or m.codes.dtype not in U8:
-                raise MoeError(f"{n}.codes is {m.codes.dtype} {tuple(m.codes.shape)}; expected "
-                               f"torch.uint8 {tuple(shape)}")
-            if m.scales.shape != g or m.scales.dtype not in BF16 or m.biases.shape != g or m.biases.dtype not in BF16:
-                raise MoeError(f"{n}.scales and biases are {m.scales.dtype} {tuple(m.scales.shape)} and "
-                               f"{m.biases.dtype} {tuple(m.biases.shape)}; expected bf16 {g}")
+        D = 2 * shape[3]
+        g = shape[:3] + (D // GROUP,)
+        for m in (k, v):
+            if (m.codes.shape != shape or m.scales.shape != g or m.biases.shape != g or m.codes.dtype not in U8
+                    or m.scales.dtype not in BF16 or m.biases.dtype not in BF16):
+                raise MoeError(f"cache planes of {m.codes.dtype} {tuple(m.codes.shape)}, {m.scales.dtype} "
+                               f"{tuple(m.scales.shape)} and {m.biases.dtype} {tuple(m.biases.shape)}; expected "
+                               f"uint8 {tuple(shape)} and twice bf16 {tuple(g)}")
+        return shape[0], shape[1], shape[2], D
+
+    num_pages = property(lambda self: self.k.codes.shape[0])
+    Hkv = property(lambda self: self.k.codes.shape[1])
+    page = property(lambda self: self.k.codes.shape[2])
+    D = property(lambda self: 2 * self.k.codes.shape[3])
 
     @staticmethod
     def empty(num_pages: int, Hkv: int, page: int, D: int, device="cuda") -> "KV4Cache":
@@ -642,8 +652,9 @@ class KV4Cache:
 
 
 def _kv4(cache: KV4Cache, page_table, cu, kv_len, tokens, stream, Hq: int = 0):
-    """The C structs of a cache and a batch and the stream, after checking the batch's tensors
-    and that they, the cache and the token tensors are on the current GPU."""
+    """The C structs of a cache and a batch and the stream, after checking the cache's planes,
+    the batch's tensors and that they and the token tensors are on the current GPU."""
+    num_pages, Hkv, page, D = cache.sizes()
     if page_table.dim() != 2 or cu.dim() != 1 or kv_len.dim() != 1:
         raise MoeError("page_table must be [B, max_pages], cu [B + 1] and kv_len [B]")
     B, width = page_table.shape
@@ -665,7 +676,7 @@ def _kv4(cache: KV4Cache, page_table, cu, kv_len, tokens, stream, Hq: int = 0):
         if t is not None and t.get_device() != cur:
             _wrong_device(**{f"token tensor {i}": t for i, t in enumerate(tokens)})
     p = [t.data_ptr() for t in held]
-    return (MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, width), MoeKv4Cache(*p[:6]),
+    return (MoeKv4Dims(B, Hq, Hkv, D, page, num_pages, width), MoeKv4Cache(*p[:6]),
             MoeKv4Batch(*p[6:]), _stream(stream, cur))
 
 

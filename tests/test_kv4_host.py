@@ -331,3 +331,44 @@ def test_prompt_tiles_are_taken_exactly_once(tmp_path):
     assert [h.tile_of(x, 512, 1) for x in (0, 1, 255, 256, 257, 511)] == [511, 510, 256, 0, 1, 255]
     assert [h.tile_of(x, 300, 1) for x in (0, 43, 256, 299)] == [299, 256, 0, 43]
     assert [h.tile_of(x, 300, 0) for x in (0, 299)] == [299, 0]
+
+
+def test_replaced_cache_planes_are_checked_by_every_call():
+    """The sizes a call passes on are those of the tensors it passes on."""
+    import torch
+
+    def plane(pages, heads, page, D):
+        g = torch.zeros(pages, heads, page, D // 64, dtype=torch.bfloat16)
+        return M.W4Matrix(torch.zeros(pages, heads, page, D // 2, dtype=torch.uint8), g, g.clone())
+
+    dev = [torch.zeros(s, dtype=torch.int32) for s in ((1, 2), (2,), (1,))]
+    kv = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    calls = (lambda c: M.moe_kv4_append(c, kv, kv, *dev), lambda c: M.moe_kv4_read(c, *dev, 1),
+             lambda c: M.moe_kv4_attention(c, q, *dev, max_new=1))
+
+    def changed():
+        for part in ("k", "v"):
+            for pages, heads, page, D in ((3, 2, 16, 64), (4, 1, 16, 64), (4, 2, 32, 64), (4, 2, 16, 128)):
+                c = M.KV4Cache(plane(4, 2, 16, 64), plane(4, 2, 16, 64))
+                setattr(c, part, plane(pages, heads, page, D))
+                yield c
+            for field, t in (("codes", torch.zeros(3, 2, 16, 32, dtype=torch.uint8)),
+                             ("scales", torch.zeros(4, 2, 16, 1)), ("biases", torch.zeros(1, dtype=torch.bfloat16))):
+                c = M.KV4Cache(plane(4, 2, 16, 64), plane(4, 2, 16, 64))
+                setattr(getattr(c, part), field, t)
+                yield c
+        c = M.KV4Cache(plane(4, 2, 16, 64), plane(4, 2, 16, 64))
+        c.v.codes.resize_(2, 2, 16, 32)
+        yield c
+
+    for c in changed():
+        for call in calls:
+            with pytest.raises(M.MoeError, match="cache"):
+                call(c)
+    # both planes replaced: their sizes count
+    c = M.KV4Cache(plane(4, 2, 16, 64), plane(4, 2, 16, 64))
+    c.k, c.v = plane(2, 1, 32, 128), plane(2, 1, 32, 128)
+    assert (c.num_pages, c.Hkv, c.page, c.D) == (2, 1, 32, 128) == tuple(c.sizes())
+    with pytest.raises(AttributeError):
+        c.num_pages = 100
