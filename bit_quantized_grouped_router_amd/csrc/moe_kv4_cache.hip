@@ -25,6 +25,12 @@
 namespace moe {
 
 constexpr int kCacheWaves = 4;  // wavefronts (tokens in flight) per workgroup
+constexpr int kGridRow = 1 << 20;
+
+// Token row of a wavefront; may be past the last.
+__device__ __forceinline__ long long token_row(int wave) {
+  return ((long long)blockIdx.y * kGridRow + blockIdx.x) * kCacheWaves + wave;
+}
 
 // Minimum and maximum over aligned groups of 8 lanes.
 template <int CTRL>
@@ -126,8 +132,9 @@ __global__ __launch_bounds__(kCacheWaves *kWave) void kv4_append_kernel(
     const void *__restrict__ v, long long k_stride, long long v_stride) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int tok = blockIdx.x * kCacheWaves + wave;
-  if (tok >= bt.T) return;
+  const long long t = token_row(wave);
+  if (t >= bt.T) return;
+  const int tok = (int)t;
   int page, slot;
   if (!find_slot(dm, bt, tok, &page, &slot) || page < 0) return;
   const int width = dm.Hkv * dm.D, total = 2 * width;
@@ -191,8 +198,9 @@ __global__ __launch_bounds__(kCacheWaves *kWave) void kv4_read_kernel(
     long long k_stride, long long v_stride) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int tok = blockIdx.x * kCacheWaves + wave;
-  if (tok >= bt.T) return;
+  const long long t = token_row(wave);
+  if (t >= bt.T) return;
+  const int tok = (int)t;
   int page, slot;
   if (!find_slot(dm, bt, tok, &page, &slot)) return;
   const int width = dm.Hkv * dm.D, total = 2 * width;
@@ -222,13 +230,18 @@ __global__ __launch_bounds__(kCacheWaves *kWave) void kv4_read_kernel(
   }
 }
 
-static int token_blocks(int T) { return (T + kCacheWaves - 1) / kCacheWaves; }
+// Workgroups of a call, in rows of kGridRow (a launch dimension holds fewer than
+// 2^32 threads, and T may be any int32).
+static dim3 token_grid(int T) {
+  const long long n = ((long long)T + kCacheWaves - 1) / kCacheWaves;
+  return n <= kGridRow ? dim3((unsigned)n) : dim3(kGridRow, (unsigned)((n + kGridRow - 1) / kGridRow));
+}
 
 hipError_t launch_kv4_append(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
                              const Kv4Batch &bt, const void *k, const void *v, long long k_stride,
                              long long v_stride, int dtype, hipStream_t s) {
   auto *kernel = dtype ? kv4_append_kernel<true> : kv4_append_kernel<false>;
-  kernel<<<token_blocks(bt.T), kCacheWaves * kWave, 0, s>>>(dm, kc, vc, bt, k, v, k_stride, v_stride);
+  kernel<<<token_grid(bt.T), kCacheWaves * kWave, 0, s>>>(dm, kc, vc, bt, k, v, k_stride, v_stride);
   return hipGetLastError();
 }
 
@@ -236,7 +249,7 @@ hipError_t launch_kv4_read(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane
                            const Kv4Batch &bt, void *k, void *v, long long k_stride,
                            long long v_stride, int dtype, hipStream_t s) {
   auto *kernel = dtype ? kv4_read_kernel<true> : kv4_read_kernel<false>;
-  kernel<<<token_blocks(bt.T), kCacheWaves * kWave, 0, s>>>(dm, kc, vc, bt, k, v, k_stride, v_stride);
+  kernel<<<token_grid(bt.T), kCacheWaves * kWave, 0, s>>>(dm, kc, vc, bt, k, v, k_stride, v_stride);
   return hipGetLastError();
 }
 

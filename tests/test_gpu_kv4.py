@@ -754,3 +754,28 @@ def test_scores_of_any_size(D, new, past, Hq):
                 gap = 2.0 ** size * scale * D * (32 if a is up else 2.0 ** -7)
                 worst = float((np.abs(out - val[past:, None]) / tol).max())
                 assert gap < 64 or worst <= 1, (size, scale, worst)
+
+
+def test_more_rows_than_a_launch_dimension_holds():
+    """2^26 rows and a few: those of a sequence without a place, then 100 that have one."""
+    rng = np.random.default_rng(45)
+    T, n = 2 ** 26 + 300, 100
+    b = Batch(rng, [n], [0], 16)
+    table = np.concatenate([b.table, b.table])
+    dev = (i32(table), i32([0, T - n, T]), i32([0, n]))
+    x = tokens(rng, n, 1, 64, BF16)
+    c = make_cache(b.num_pages, 1, 16, 64)
+    k, v = (torch.empty((T, 1, 64), dtype=BF16, device="cuda") for _ in range(2))
+    k[T - n:] = torch.from_numpy(x)
+    M.moe_kv4_append(c, k, k, *dev)
+    q, s, z = K.quantise(x)
+    at = np.arange(n)
+    for plane in host_planes(c):
+        for got, want in zip(plane, (K.pack(q), s, z)):
+            assert bool((got[b.table[0, at // 16], :, at % 16] == want).all())
+    k.fill_(1.0), v.fill_(1.0)
+    M.moe_kv4_read(c, *dev, T, k=k, v=v)
+    want = round_to_bf16_bits(K.values(K.pack(q), s, z).astype(np.float32))
+    for t in (k, v):
+        assert bool((host_bits(t[T - n:]) == want).all())
+        assert not bool(t[:T - n].view(torch.int16).any())
