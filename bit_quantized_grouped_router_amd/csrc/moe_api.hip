@@ -530,6 +530,7 @@ moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
   MOE_TRY(check_kv4_cache(cache, batch));
   MOE_TRY(check_ptr(q));
   MOE_TRY(check_ptr(out));
+  if (q == out && q_stride != out_stride && T > 1) return MOE_E_INVALID;  // rows would be written over others' queries
   const Kv4Dims d = to_kv4_dims(dm);
   const int n = kv4_max_new(T, max_new);
   const size_t need = kv4_attention_ws(d, T, n, window);

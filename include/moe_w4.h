@@ -439,7 +439,7 @@ size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int3
  *   it does not see never reach its result, whatever the cache holds there.
  *   q       bf16 [T][Hq][D], tokens q_stride apart
  *   out     bf16 [T][Hq][D], out, tokens out_stride apart; may be q itself with the
- *           same stride
+ *           same stride (MOE_E_INVALID with another), and overlaps nothing else
  *   max_new an upper bound of every n_b; a sequence's tokens past it are not computed
  *   scale   > 0 and <= 2^64 (MOE_E_INVALID otherwise)
  *   window  >= 0 (0: none; MOE_E_INVALID when negative)

@@ -372,3 +372,12 @@ def test_replaced_cache_planes_are_checked_by_every_call():
     assert (c.num_pages, c.Hkv, c.page, c.D) == (2, 1, 32, 128) == tuple(c.sizes())
     with pytest.raises(AttributeError):
         c.num_pages = 100
+
+
+def test_attention_onto_its_queries_keeps_their_stride(L):
+    assert attend(L, q=FAKE, out=FAKE, qs=2048, os_=4096) == INVALID
+    assert attend(L, q=FAKE, out=FAKE, qs=2056, os_=2048) == INVALID
+    assert attend(L, q=FAKE, out=FAKE, qs=4096, os_=4096, ws=FAKE + 8,
+                  dm=dims(B=1, page=128, max_pages=1024, num_pages=1024), T=1, max_new=1) == ALIGN  # past that check
+    assert attend(L, q=FAKE, out=FAKE, qs=2048, os_=4096, ws=FAKE + 8,
+                  dm=dims(B=1, page=128, max_pages=1024, num_pages=1024), T=1, max_new=1) == ALIGN  # one row has no stride
