@@ -570,34 +570,38 @@ static hipError_t launch_tiles(const LinearArgs &a, int dtype, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The kernel for a call: 0 large tiles, 1 middle tiles, 2 and 3 the small one with
-// 16 and 32 tokens.
-static int linear_choice(const LinearArgs &a) {
-  if (a.T <= 16) return 3;
+enum class LinearKind { kLargeTiles, kMiddleTiles, kNarrowTiles, kSmall16, kSmall32 };  // 16 and 32 tokens a workgroup
+
+static LinearKind linear_kind(const LinearArgs &a) {
+  if (a.T <= 16) return LinearKind::kSmall16;
   // the tile kernels keep 32-bit byte offsets within a tile
   const bool tiles = a.x_stride < (1 << 23) && a.cols < (1 << 23);
-  if (tiles && bg_tiles<4, 2, 1, 4>(a.T, a.rows) >= kBgMinTiles) return 0;
-  if (!tiles || ln_blocks<2>(a.T, a.rows) <= kSmallMaxBlocks) return 4;
-  return bg_tiles<2, 1, 4, 2>(a.T, a.rows) <= kNarrowMaxTiles ? 2 : 1;
+  if (tiles && bg_tiles<4, 2, 1, 4>(a.T, a.rows) >= kBgMinTiles) return LinearKind::kLargeTiles;
+  if (!tiles || ln_blocks<2>(a.T, a.rows) <= kSmallMaxBlocks) return LinearKind::kSmall32;
+  return bg_tiles<2, 1, 4, 2>(a.T, a.rows) <= kNarrowMaxTiles ? LinearKind::kNarrowTiles : LinearKind::kMiddleTiles;
 }
 
 bool linear_grid_ok(const LinearArgs &a) {
-  const int c = linear_choice(a);
-  const long long threads = c == 0   ? bg_tiles<4, 2, 1, 4>(a.T, a.rows) * 256
-                            : c == 1 ? bg_tiles<2, 1, 2, 4>(a.T, a.rows) * 512
-                            : c == 2 ? bg_tiles<2, 1, 4, 2>(a.T, a.rows) * 512
-                                     : ln_blocks<2>(a.T, a.rows) * 512;
+  long long threads = 0;
+  switch (linear_kind(a)) {
+    case LinearKind::kLargeTiles: threads = bg_tiles<4, 2, 1, 4>(a.T, a.rows) * 256; break;
+    case LinearKind::kMiddleTiles: threads = bg_tiles<2, 1, 2, 4>(a.T, a.rows) * 512; break;
+    case LinearKind::kNarrowTiles: threads = bg_tiles<2, 1, 4, 2>(a.T, a.rows) * 512; break;
+    case LinearKind::kSmall16: threads = ln_blocks<1>(a.T, a.rows) * 512; break;
+    case LinearKind::kSmall32: threads = ln_blocks<2>(a.T, a.rows) * 512; break;
+  }
   return threads < (1ll << 32) - 8 * 512;  // of one launch dimension
 }
 
 hipError_t launch_linear(const LinearArgs &a, int dtype, hipStream_t s) {
-  switch (linear_choice(a)) {
-    case 0: return launch_tiles<4, 2, 1, 4>(a, dtype, s);
-    case 1: return launch_tiles<2, 1, 2, 4>(a, dtype, s);
-    case 2: return launch_tiles<2, 1, 4, 2>(a, dtype, s);
-    case 3: return launch<1>(a, dtype, s);
-    default: return launch<2>(a, dtype, s);
+  switch (linear_kind(a)) {
+    case LinearKind::kLargeTiles: return launch_tiles<4, 2, 1, 4>(a, dtype, s);
+    case LinearKind::kMiddleTiles: return launch_tiles<2, 1, 2, 4>(a, dtype, s);
+    case LinearKind::kNarrowTiles: return launch_tiles<2, 1, 4, 2>(a, dtype, s);
+    case LinearKind::kSmall16: return launch<1>(a, dtype, s);
+    case LinearKind::kSmall32: break;
   }
+  return launch<2>(a, dtype, s);
 }
 
 }  // namespace moe

@@ -337,8 +337,10 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *   y         bf16 or fp32 (dtype) [T][rows], rows y_stride elements apart, out;
  *             overlaps neither x nor, but for the above, the residual
  * Limits: T >= 0, rows >= 1, cols >= 1 (MOE_E_INVALID otherwise); cols % 64 == 0,
- * x_stride % 8 == 0, rows * cols < 2^34, T * rows < 2^36, T * cols < 2^40
- * (MOE_E_UNSUPPORTED); strides at least a row long (MOE_E_INVALID).
+ * x_stride % 8 == 0, rows * cols < 2^34, T * rows < 2^36, T * cols < 2^40, T <=
+ * 2^31 - 2176, and fewer than 2^23 - 8 blocks of 16 rows (T <= 16) or of 16 rows by
+ * 32 tokens (x_stride or cols >= 2^23) (MOE_E_UNSUPPORTED); strides at least a row
+ * long (MOE_E_INVALID).
  */
 moe_status moe_linear_w4(int32_t T, int32_t rows, int32_t cols, const uint16_t *x, int64_t x_stride,
                          const moe_w4_matrix *w, const uint16_t *bias, int32_t act,

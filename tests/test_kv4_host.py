@@ -381,3 +381,15 @@ def test_attention_onto_its_queries_keeps_their_stride(L):
                   dm=dims(B=1, page=128, max_pages=1024, num_pages=1024), T=1, max_new=1) == ALIGN  # past that check
     assert attend(L, q=FAKE, out=FAKE, qs=2048, os_=4096, ws=FAKE + 8,
                   dm=dims(B=1, page=128, max_pages=1024, num_pages=1024), T=1, max_new=1) == ALIGN  # one row has no stride
+
+
+def test_linear_launch_limits(L):
+    """Sizes just past the limits that a launch dimension sets."""
+    def status(T, rows, xs=64):
+        return project(L, T=T, rows=rows, cols=64, xs=xs, ys=rows)
+
+    assert status(16, 2 ** 27 - 143) == UNSUPPORTED               # 2^23 - 8 blocks of 16 rows
+    assert status(1, 2 ** 27 - 143) == UNSUPPORTED
+    assert status(2 ** 31 - 2175, 16) == UNSUPPORTED
+    assert status(32 * 1024, 16 * 8192 - 15, xs=1 << 23) == UNSUPPORTED  # 2^23 blocks
+    assert status(2 ** 20, 2 ** 16) == UNSUPPORTED                # T * rows
