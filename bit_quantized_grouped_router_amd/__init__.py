@@ -622,18 +622,20 @@ class KV4Cache:
     def sizes(self):
         """(num_pages, Hkv, page, D); raises where the six tensors do not fit together."""
         k, v = self.k, self.v
-        shape = k.codes.shape
-        if len(shape) != 4:
+        codes = k.codes.shape
+        if len(codes) != 4:
             raise MoeError("cache codes must be [num_pages, Hkv, page, D/2]")
-        D = 2 * shape[3]
-        g = shape[:3] + (D // GROUP,)
-        for m in (k, v):
-            if (m.codes.shape != shape or m.scales.shape != g or m.biases.shape != g or m.codes.dtype not in U8
-                    or m.scales.dtype not in BF16 or m.biases.dtype not in BF16):
-                raise MoeError(f"cache planes of {m.codes.dtype} {tuple(m.codes.shape)}, {m.scales.dtype} "
-                               f"{tuple(m.scales.shape)} and {m.biases.dtype} {tuple(m.biases.shape)}; expected "
-                               f"uint8 {tuple(shape)} and twice bf16 {tuple(g)}")
-        return shape[0], shape[1], shape[2], D
+        n, heads, page, half = codes
+        g = (n, heads, page, 2 * half // GROUP)
+        if (v.codes.shape != codes or k.scales.shape != g or k.biases.shape != g or v.scales.shape != g
+                or v.biases.shape != g or k.codes.dtype not in U8 or v.codes.dtype not in U8
+                or k.scales.dtype not in BF16 or k.biases.dtype not in BF16 or v.scales.dtype not in BF16
+                or v.biases.dtype not in BF16):
+            have = "; ".join(f"{name}.{f} {getattr(m, f).dtype} {tuple(getattr(m, f).shape)}"
+                             for name, m in (("k", k), ("v", v)) for f in ("codes", "scales", "biases"))
+            raise MoeError(f"the cache's planes do not fit together: {have}; expected uint8 {tuple(codes)} codes, "
+                           f"bf16 {g} scales and biases")
+        return n, heads, page, 2 * half
 
     num_pages = property(lambda self: self.k.codes.shape[0])
     Hkv = property(lambda self: self.k.codes.shape[1])
@@ -652,8 +654,9 @@ class KV4Cache:
 
 
 def _kv4(cache: KV4Cache, page_table, cu, kv_len, tokens, stream, Hq: int = 0):
-    """The C structs of a cache and a batch and the stream, after checking the cache's planes,
-    the batch's tensors and that they and the token tensors are on the current GPU."""
+    """The C structs of a cache and a batch, the stream, and the cache's Hkv and D, after checking
+    the cache's planes, the batch's tensors and that they and the token tensors are on the
+    current GPU."""
     num_pages, Hkv, page, D = cache.sizes()
     if page_table.dim() != 2 or cu.dim() != 1 or kv_len.dim() != 1:
         raise MoeError("page_table must be [B, max_pages], cu [B + 1] and kv_len [B]")
@@ -677,17 +680,17 @@ def _kv4(cache: KV4Cache, page_table, cu, kv_len, tokens, stream, Hq: int = 0):
             _wrong_device(**{f"token tensor {i}": t for i, t in enumerate(tokens)})
     p = [t.data_ptr() for t in held]
     return (MoeKv4Dims(B, Hq, Hkv, D, page, num_pages, width), MoeKv4Cache(*p[:6]),
-            MoeKv4Batch(*p[6:]), _stream(stream, cur))
+            MoeKv4Batch(*p[6:]), _stream(stream, cur), Hkv, D)
 
 
 def moe_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, page_table, cu, kv_len,
                    stream=None) -> None:
     """Quantise new keys and values [T, Hkv, D] (bf16 or fp32) into the cache. Rows
     cu[b] .. cu[b+1]-1 are the last tokens of sequence b, which then has kv_len[b]."""
-    dm, c, b, s = _kv4(cache, page_table, cu, kv_len, (k, v), stream)
+    dm, c, b, s, Hkv, D = _kv4(cache, page_table, cu, kv_len, (k, v), stream)
     T = k.shape[0]
     dt = _dtype(k.dtype)
-    shape = (T, cache.Hkv, cache.D)
+    shape = (T, Hkv, D)
     ks, vs = _rows(k, shape, "k", (k.dtype,)), _rows(v, shape, "v", (k.dtype,))
     _check(lib().moe_kv4_append(dm, c, T, k.data_ptr(), ks, v.data_ptr(), vs, dt, b, s),
            "moe_kv4_append")
@@ -696,10 +699,10 @@ def moe_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, page_table
 def moe_kv4_read(cache: KV4Cache, page_table, cu, kv_len, T: int, dtype=torch.bfloat16, k=None, v=None,
                  stream=None):
     """Keys and values [T, Hkv, D] of the last cu[b+1] - cu[b] tokens of each sequence."""
-    dm, c, b, s = _kv4(cache, page_table, cu, kv_len, (k, v), stream)
+    dm, c, b, s, Hkv, D = _kv4(cache, page_table, cu, kv_len, (k, v), stream)
     dt = _dtype(dtype)
-    shape = (T, cache.Hkv, cache.D)
-    ks = vs = cache.Hkv * cache.D
+    shape = (T, Hkv, D)
+    ks = vs = Hkv * D
     if k is None:
         k = _empty(shape, dtype, page_table.device, stream)
     else:
@@ -715,7 +718,8 @@ def moe_kv4_read(cache: KV4Cache, page_table, cu, kv_len, T: int, dtype=torch.bf
 
 def moe_kv4_attention_workspace_bytes(cache: KV4Cache, T: int, Hq: int, B: int, max_pages: int,
                                       max_new: int, window: int = 0) -> int:
-    dm = MoeKv4Dims(B, Hq, cache.Hkv, cache.D, cache.page, cache.num_pages, max_pages)
+    num_pages, Hkv, page, D = cache.sizes()
+    dm = MoeKv4Dims(B, Hq, Hkv, D, page, num_pages, max_pages)
     return lib().moe_kv4_attention_workspace_bytes(dm, T, min(max_new, T), min(window, INT32_MAX))
 
 
@@ -728,9 +732,9 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
     if q.dim() != 3:
         raise MoeError("q must be [T, Hq, D]")
     T, Hq, D = q.shape
-    if D != cache.D:
-        raise MoeError(f"q has {D} channels a head; the cache {cache.D}")
-    dm, c, b, s = _kv4(cache, page_table, cu, kv_len, (q, out, ws), stream, Hq)
+    dm, c, b, s, _, channels = _kv4(cache, page_table, cu, kv_len, (q, out, ws), stream, Hq)
+    if D != channels:
+        raise MoeError(f"q has {D} channels a head; the cache {channels}")
     qs = _rows(q, (T, Hq, D), "q", BF16)
     if out is None:
         out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
