@@ -741,8 +741,7 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
         os_ = Hq * D
     else:
         os_ = _rows(out, (T, Hq, D), "out", BF16)
-    if T > 0:  # the C ABI's integers are 32 bits wide
-        max_new = min(max_new, T)
+    max_new = min(max_new, T if T > 0 else INT32_MAX)  # the C ABI's integers are 32 bits wide
     window = min(window, INT32_MAX)
     if max_new < 0 or window < 0:
         raise MoeError(f"max_new {max_new} and window {window} must not be negative")

@@ -779,3 +779,10 @@ def test_more_rows_than_a_launch_dimension_holds():
     for t in (k, v):
         assert bool((host_bits(t[T - n:]) == want).all())
         assert not bool(t[:T - n].view(torch.int16).any())
+
+
+def test_empty_attention_with_a_wide_bound():
+    c = make_cache(2, 1, 16, 64)
+    e = torch.empty((0, 1, 64), dtype=BF16, device="cuda")
+    for bound in (0, 5, 2 ** 31, 2 ** 32 + 7):
+        assert M.moe_kv4_attention(c, e, i32([[0]]), i32([0, 0]), i32([5]), max_new=bound).shape == (0, 1, 64)
