@@ -412,8 +412,8 @@ __device__ __forceinline__ Kv4Range tile_range(const Kv4Dims &dm, const RowTile 
 // that saw no key (l_i = 0) nothing; one whose scores were all NaN has no
 // reference and passes its NaN on.
 __device__ __forceinline__ float part_weight(float m_i, float l_i, float m, float scale2) {
-  if (m_i == kNegInf) return l_i == 0.f ? 0.f : 1.f;
-  return __builtin_amdgcn_exp2f((m_i - m) * scale2);
+  const float none = l_i == 0.f ? kNegInf : 0.f;
+  return __builtin_amdgcn_exp2f(m_i == kNegInf ? none : (m_i - m) * scale2);
 }
 
 // Channels c .. c + 3 of a token's head, divided by the row's sum; a row that
