@@ -27,9 +27,10 @@ namespace moe {
 constexpr int kCacheWaves = 4;  // wavefronts (tokens in flight) per workgroup
 constexpr int kGridRow = 1 << 20;
 
-// Token row of a wavefront; may be past the last.
-__device__ __forceinline__ long long token_row(int wave) {
-  return ((long long)blockIdx.y * kGridRow + blockIdx.x) * kCacheWaves + wave;
+// Token row of a wavefront; may be past the last (by kGridRow workgroups at the most,
+// so below 2^32).
+__device__ __forceinline__ uint32_t token_row(int wave) {
+  return (blockIdx.y * kGridRow + blockIdx.x) * kCacheWaves + wave;
 }
 
 // Minimum and maximum over aligned groups of 8 lanes.
@@ -132,8 +133,8 @@ __global__ __launch_bounds__(kCacheWaves *kWave) void kv4_append_kernel(
     const void *__restrict__ v, long long k_stride, long long v_stride) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const long long t = token_row(wave);
-  if (t >= bt.T) return;
+  const uint32_t t = token_row(wave);
+  if (t >= (uint32_t)bt.T) return;
   const int tok = (int)t;
   int page, slot;
   if (!find_slot(dm, bt, tok, &page, &slot) || page < 0) return;
@@ -198,8 +199,8 @@ __global__ __launch_bounds__(kCacheWaves *kWave) void kv4_read_kernel(
     long long k_stride, long long v_stride) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const long long t = token_row(wave);
-  if (t >= bt.T) return;
+  const uint32_t t = token_row(wave);
+  if (t >= (uint32_t)bt.T) return;
   const int tok = (int)t;
   int page, slot;
   if (!find_slot(dm, bt, tok, &page, &slot)) return;
