@@ -538,7 +538,7 @@ moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
     if (ws_bytes < need) return MOE_E_WORKSPACE;
     MOE_TRY(check_ptr(ws));
   }
-  const Kv4Attn at{q, out, q_stride, out_stride, n, scale, causal != 0, window, 0, 0};
+  const Kv4Attn at{q, out, q_stride, out_stride, n, scale, causal != 0, window, 0, 0, 0};
   return hip_status(launch_kv4_attention(d, to_kv4_plane(cache->k), to_kv4_plane(cache->v),
                                          to_kv4_batch(batch, T), at, ws, as_stream(stream)));
 }

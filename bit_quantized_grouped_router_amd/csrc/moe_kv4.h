@@ -151,6 +151,7 @@ struct Kv4Attn {
   bool causal;
   int window;
   int above, most;  // a kernel's own sequences: those with more query rows a head than above, and at most `most`
+  int room;         // partial results lie by sequence, this many tokens each; 0: by row of the call
 };
 
 // Bytes of a call's partial results (0 when no keys are split), for T token rows

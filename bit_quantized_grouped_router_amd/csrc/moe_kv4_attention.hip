@@ -666,9 +666,9 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
       l = fmaf(part_weight(sm[w][r], sl[w][r], mr, scale2), sl[w][r], l);
     }
     if (share.used > 1) {
-      const long long pr = part_index(dm, rt, r, splits, split);
+      const long long pr = part_index(dm, at, rt, r, splits, split);
       *(float4 *)(part + pr * D + c) = o;
-      if (c == 0) *(float2 *)(part_stats(dm, bt, splits, part) + pr * 2) = make_float2(mr, l);
+      if (c == 0) *(float2 *)(part_stats(dm, bt, at, splits, part) + pr * 2) = make_float2(mr, l);
     } else {
       const int x = r + in0, i = tok0 + x / G, h = rt.head * G + x % G;
       store_row(dm, at, rt.sp.begin + i, h, c, l, o);
@@ -721,8 +721,8 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
   const int per = ROWS == kAtRows ? tiles_per_split<D>(dm, bt, at) : kPfMinTiles;
   const int used = kv4_share(range, per, splits, 0).used;
   if (used <= 1 || rt.row0 + r >= rt.rows) return;
-  const float *ml = part_stats(dm, bt, splits, part);
-  const long long pr0 = part_index(dm, rt, r, splits, 0);
+  const float *ml = part_stats(dm, bt, at, splits, part);
+  const long long pr0 = part_index(dm, at, rt, r, splits, 0);
   // the row's reference
   float m = kNegInf;
   if constexpr (C < D) {  // every wavefront looks at all the splits'
@@ -795,6 +795,7 @@ struct Kv4Plan {
   bool many;       // the prefill kernel takes those with more than kManyRows rows
   int few;         // new tokens a sequence of the row kernel can have; 0: it has none
   int pre_splits, row_splits;
+  int room;        // Kv4Attn::room of the row kernel
 };
 
 // The prefill kernel reads and rebuilds keys once for 128 rows instead of 16, but
@@ -811,7 +812,7 @@ static bool kv4_many(const Kv4Dims &dm, int T, long long keys) {
 
 static Kv4Plan kv4_plan(const Kv4Dims &dm, int T, int max_new, int window) {
   const int G = dm.Hq / dm.Hkv;
-  Kv4Plan p{false, max_new, 1, 1};
+  Kv4Plan p{false, max_new, 1, 1, 0};
   const long long keys = kv4_keys(dm, 128 / G, window);
   if ((long long)max_new * G > kManyRows && kv4_many(dm, T, keys)) {
     p.many = true;
@@ -823,6 +824,9 @@ static Kv4Plan kv4_plan(const Kv4Dims &dm, int T, int max_new, int window) {
     p.pre_splits = n < 1 ? 1 : (int)n;
   }
   if (p.few > 0) p.row_splits = few_splits(dm, p.few, window);
+  // beside a prompt few of the call's rows are the row kernel's (32768 tokens and one
+  // sequence of a single one, 64 heads on 8, D = 128: 12 GB of workspace by row, 6 MB so)
+  if ((long long)dm.B * p.few < T) p.room = p.few;
   return p;
 }
 
@@ -834,8 +838,10 @@ bool kv4_grid_ok(const Kv4Dims &dm, int max_new) {
 
 size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window) {
   const Kv4Plan p = kv4_plan(dm, T, max_new, window);
-  const int splits = p.pre_splits > p.row_splits ? p.pre_splits : p.row_splits;
-  return splits == 1 ? 0 : (size_t)T * dm.Hq * splits * (dm.D + 2) * sizeof(float);
+  const size_t row = (size_t)dm.Hq * (dm.D + 2) * sizeof(float);  // bytes of a token and split
+  const size_t pre = p.pre_splits > 1 ? row * T * p.pre_splits : 0;
+  const size_t few = p.row_splits > 1 ? row * p.row_splits * (p.room > 0 ? (size_t)dm.B * p.room : T) : 0;
+  return pre > few ? pre : few;
 }
 
 template <int D, int W>
@@ -874,6 +880,7 @@ static hipError_t launch_all(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pla
   if (p.many) {
     at.above = p.few > 0 ? kManyRows : 0;
     at.most = 0x7FFFFFFF;
+    at.room = 0;
     e = launch_kv4_prefill(dm, kc, vc, bt, at, p.pre_splits, part, s);
     if (e == hipSuccess && p.pre_splits > 1) e = launch_join<D, 128>(dm, bt, at, at.max_new, p.pre_splits, part, s);
     if (e != hipSuccess || p.few == 0) return e;
@@ -881,6 +888,7 @@ static hipError_t launch_all(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pla
   // the partial results of the one above have been read when this one's come
   at.above = 0;
   at.most = p.many ? kManyRows : 0x7FFFFFFF;
+  at.room = p.room;
   // Eight wavefronts where every workgroup has a CU to itself (a short sequence
   // ends sooner), four where there are more of them or keys are split.
   const bool alone = p.row_splits == 1 && kv4_tasks(dm, p.few) <= 256;

@@ -68,13 +68,17 @@ __device__ __forceinline__ RowTile row_tile(const Kv4Dims &dm, const Kv4Batch &b
 
 // Partial results of row r of a row tile, split `split` of `splits`: D sums at
 // part + index * D; reference and sum of weights, all rows' after all sums.
-__device__ __forceinline__ long long part_index(const Kv4Dims &dm, const RowTile &t, int r, int splits, int split) {
+__device__ __forceinline__ long long part_index(const Kv4Dims &dm, const Kv4Attn &at, const RowTile &t, int r,
+                                                int splits, int split) {
   const int G = dm.Hq / dm.Hkv, x = t.row0 + r;
-  return ((long long)(t.sp.begin + x / G) * dm.Hq + t.head * G + x % G) * splits + split;
+  const long long first = at.room > 0 ? (long long)t.seq * at.room : t.sp.begin;
+  return ((first + x / G) * dm.Hq + t.head * G + x % G) * splits + split;
 }
 
-__device__ __forceinline__ float *part_stats(const Kv4Dims &dm, const Kv4Batch &bt, int splits, float *part) {
-  return part + (long long)bt.T * dm.Hq * splits * dm.D;
+__device__ __forceinline__ float *part_stats(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Attn &at, int splits,
+                                             float *part) {
+  const long long tokens = at.room > 0 ? (long long)dm.B * at.room : bt.T;
+  return part + tokens * dm.Hq * splits * dm.D;
 }
 
 // Fewest tiles a split of the prefill kernel's keys has.

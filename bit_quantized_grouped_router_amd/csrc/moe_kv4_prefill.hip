@@ -501,9 +501,9 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   const bool partial = share.used > 1;
   const float unit = HALF ? 0x1p-7f : 1.0f;  // parts leave without kShift
   const float sum_inv = partial ? unit : l == 0.f ? 0.f : 1.0f / l;
-  const long long pr = part_index(dm, rt, real ? row - rt.row0 : 0, splits, split);
+  const long long pr = part_index(dm, at, rt, real ? row - rt.row0 : 0, splits, split);
   float *sums = part + pr * D + 2 * half;
-  if (partial && real && half == 0) *(float2 *)(part_stats(dm, bt, splits, part) + pr * 2) = make_float2(m, l * unit);
+  if (partial && real && half == 0) *(float2 *)(part_stats(dm, bt, at, splits, part) + pr * 2) = make_float2(m, l * unit);
   uint16_t *out = at.out + (rt.sp.begin + tok) * at.out_stride + (long long)hd * D + 2 * half;
   if (real) {
 #pragma unroll

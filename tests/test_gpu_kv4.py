@@ -786,3 +786,21 @@ def test_empty_attention_with_a_wide_bound():
     e = torch.empty((0, 1, 64), dtype=BF16, device="cuda")
     for bound in (0, 5, 2 ** 31, 2 ** 32 + 7):
         assert M.moe_kv4_attention(c, e, i32([[0]]), i32([0, 0]), i32([5]), max_new=bound).shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("new,past,Hq,Hkv,D", [([300, 1, 2], [0, 8000, 5000], 16, 2, 128), ([1, 300, 1], [7000, 20, 0], 16, 1, 64),
+                                                ([2, 3, 260, 1], [8100, 900, 5, 4000], 24, 2, 256)])
+def test_single_tokens_beside_a_prompt_in_their_own_workspace(new, past, Hq, Hkv, D):
+    """Split keys of the few rows, parts kept by sequence: within the bytes asked for."""
+    rng = np.random.default_rng(47)
+    b = prompt_batch(rng, new, past, 32)
+    c = filled(rng, b, Hkv, D)
+    q64, q = queries(rng, b.T, Hq, D)
+    need = M.moe_kv4_attention_workspace_bytes(c, b.T, Hq, b.B, b.table.shape[1], b.max_new())
+    assert 0 < need
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((b.T, Hq, D), float("nan"), dtype=BF16, device="cuda")
+    M.moe_kv4_attention(c, q, *b.dev, max_new=b.max_new(), out=out, ws=ws[:need])
+    assert bool((ws[need:] == 0xA5).all())
+    want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, D ** -0.5)
+    check(out, want, tol, f"{new} {past}")

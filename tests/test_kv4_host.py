@@ -393,3 +393,15 @@ def test_linear_launch_limits(L):
     assert status(2 ** 31 - 2175, 16) == UNSUPPORTED
     assert status(32 * 1024, 16 * 8192 - 15, xs=1 << 23) == UNSUPPORTED  # 2^23 blocks
     assert status(2 ** 20, 2 ** 16) == UNSUPPORTED                # T * rows
+
+
+def test_workspace_of_a_prompt_beside_single_tokens(L):
+    """The parts of the few rows are kept for those sequences, not for every row of the prompt."""
+    for T, Hq, Hkv, D, B in ((8193, 16, 2, 128, 2), (100001, 16, 2, 128, 2), (32769, 64, 8, 128, 2),
+                             (32776, 16, 2, 256, 9), (20300, 32, 1, 64, 300)):
+        dm = dims(B=B, Hq=Hq, Hkv=Hkv, D=D, page=128, max_pages=1024, num_pages=1 << 20)
+        need = L.moe_kv4_attention_workspace_bytes(ctypes.byref(dm), T, T, 0)
+        few = 64 // (Hq // Hkv)   # tokens of a sequence that has few rows
+        slots = 2 * 5 * 256       # twice the workgroups that the card holds
+        assert need <= B * few * Hq * (D + 2) * 4 * max(1, slots // (B * Hkv * (few * Hq // Hkv // 16))), (T, need)
+        assert need < 1 << 28
