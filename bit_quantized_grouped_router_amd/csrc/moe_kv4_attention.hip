@@ -31,8 +31,8 @@
 //
 // Bound by memory for many or long sequences, by its chain of dependent loads
 // (offsets, pages, codes) for few short ones. us, one new token a sequence, 16
-// heads on 2: 64 sequences of up to 8101, D = 256 (113 MB) 33.7 and 5.8 for the
-// join, 3.4 TB/s; one of 131,150, D = 128 (38 MB) 17.3 and 6.8; one of 500, D =
+// heads on 2: 64 sequences of up to 8101, D = 256 (113 MB) 33.2 and 5.4 for the
+// join, 3.4 TB/s; one of 131,150, D = 128 (38 MB) 16.9 and 6.8; one of 500, D =
 // 256 11.7.
 #include "moe_kv4_device.h"
 #include "moe_lds.h"
@@ -439,7 +439,7 @@ constexpr int at_lds_bytes() {
 // instead of 512 took a batch of 64 mixed sequences from 33 to 57 us.
 constexpr int kMinTiles = 16;
 // Workgroups of 4 wavefronts a CU holds: wavefronts a SIMD by their registers
-// (216, 130 and 90; a 4-wavefront limit at D = 128 spills a pointer of the loop,
+// (214, 130 and 90; a 4-wavefront limit at D = 128 spills a pointer of the loop,
 // and its reload waits for the DMA in flight).
 template <int D>
 constexpr int at_blocks() { return D == 256 ? 2 : D == 128 ? 3 : 5; }

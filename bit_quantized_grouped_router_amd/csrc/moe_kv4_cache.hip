@@ -18,7 +18,7 @@
 // per step; 8 lanes share a group and reduce its minimum and maximum with
 // three DPP steps. Measured: 72,400 tokens of 4 x 128 channels read to bf16 (190
 // MB) in 39 us, 4.9 TB/s; 7480 tokens of 8 x 128 channels written from fp32 (70 MB)
-// in 20 us and read back in 16; 8 tokens in 4.2 and 3.1, three dependent loads.
+// in 19 us and read back in 16; 8 tokens in 4.2 and 3.1, three dependent loads.
 #include "moe_device.h"
 #include "moe_kv4.h"
 

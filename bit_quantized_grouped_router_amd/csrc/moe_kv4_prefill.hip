@@ -36,17 +36,18 @@
 // unsplit, 308 split eight ways: 821 TFLOP/s).
 //
 // Measured (us; TFLOP/s of the products that causality leaves), 16 heads on 2:
-//   4096 tokens behind 1003   D = 128 144 (712)
-//   3000 tokens               D = 64 59 (315)   128 80 (463)
-//   4096 tokens               D = 64 77 (446)   128 108 (637)   256 201 (683)
-//   8192 tokens               D = 128 322 (854)
+//   4096 tokens behind 1003   D = 128 147 (696)
+//   3000 tokens               D = 64 60 (307)   128 82 (450)
+//   4096 tokens               D = 64 79 (435)   128 110 (625)   256 203 (677)
+//   8192 tokens               D = 128 329 (836)
+//   4096 tokens, values past fp16, D = 128 331
 // next to 1224 TFLOP/s of a library product of 8192^3. Bound by the vector
 // instructions that a tile needs besides its products (about 150 a wavefront,
-// 16 exponentials among them, next to 512 cycles of MFMA; matrix instructions
-// were busy 30% of the time, vector ones 42%) and, at 4096 tokens, by the long
-// tiles that end alone on their CU. Rows of 64 to a wavefront halve the
-// rebuilding per row but leave one wavefront a SIMD: the same time without a
-// mask (251 us against 254), longer with one (229 against 176).
+// 16 exponentials among them, next to 512 cycles of MFMA; of the SIMDs' time at
+// 4096 tokens behind 1003, matrix instructions took 28%, vector ones 42%). Rows of
+// 64 to a wavefront halve the rebuilding per row but leave one wavefront a SIMD:
+// the same time without a mask (251 us against 254, as first written), longer
+// with one (229 against 176).
 #include <type_traits>
 
 #include "moe_kv4_device.h"

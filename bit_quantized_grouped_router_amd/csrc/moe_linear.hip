@@ -2,16 +2,18 @@
 //   y[t][n] = act(sum_c x[t][c] W[n][c] + bias[n]) + residual[t][n],
 //   W = bf16(fp32(s q + b)), products of bf16 values exact, sums in fp32.
 //
-// Small batches are bound by the latency of one or two rounds of loads. One
+// Small batches are bound by the latency of one or two rounds of loads, and from 17
+// tokens on by activations too, which every 16 weight rows read again (37 by 2048 x
+// 4096: 64 MB from the L2 for 5 MB of operands; 52% of the time is waiting). One
 // workgroup takes 16 weight rows and 16 NT tokens; its 8 wavefronts take four
 // 64-column groups at a time, rebuild the rows' weights in registers as the A operand of 16x16x32 MFMAs
 // (lane l: row l % 16, columns 16 (l / 16) .. +15 of the group) against the
 // tokens' activations read straight from memory, and join their sums through
 // LDS, where the epilogue runs. Measured, rows x columns: 1 token by 5120 x 2048
-// 5.8 us in a graph, 37 by 2048 x 4096 11.9 us. (Activations brought in whole
+// 6.0 us in a graph, 37 by 2048 x 4096 12.1 us. (Activations brought in whole
 // lines and turned in LDS took 13 and 27 us.) The tile kernels below: 777
-// by 1001 x 2048 13 us, 8192 by 5120 x 2048 176 to 199 us (a library product of
-// bf16 weights of that size 175 to 177).
+// by 1001 x 2048 14 us, 8192 by 5120 x 2048 173 to 180 us (a library product of
+// bf16 weights of that size 175 to 178).
 #include <type_traits>
 
 #include "moe_lds.h"
