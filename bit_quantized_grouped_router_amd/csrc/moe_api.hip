@@ -476,6 +476,7 @@ moe_status moe_linear_w4(int32_t T, int32_t rows, int32_t cols, const uint16_t *
   if (residual == y && residual_stride != y_stride) return MOE_E_INVALID;
   const LinearArgs a{T, rows, cols, x, x_stride, to_w4(*w), bias, act, residual, residual_stride, y, y_stride};
   if (!linear_grid_ok(a)) return MOE_E_UNSUPPORTED;
+  if (x == y) return MOE_E_INVALID;  // other workgroups still read x
   return hip_status(launch_linear(a, dtype, as_stream(stream)));
 }
 
@@ -506,6 +507,7 @@ moe_status moe_kv4_read(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int3
   MOE_TRY(check_kv4_cache(cache, batch));
   MOE_TRY(check_ptr(k));
   MOE_TRY(check_ptr(v));
+  if (k == v) return MOE_E_INVALID;  // one would be written over the other
   return hip_status(launch_kv4_read(to_kv4_dims(dm), to_kv4_plane(cache->k), to_kv4_plane(cache->v),
                                     to_kv4_batch(batch, T), k, v, k_stride, v_stride, dtype,
                                     as_stream(stream)));

@@ -335,7 +335,8 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *   residual  [T][rows] of y's type, rows residual_stride apart, or NULL; may
  *             be y itself with the same stride (updated in place)
  *   y         bf16 or fp32 (dtype) [T][rows], rows y_stride elements apart, out;
- *             overlaps neither x nor, but for the above, the residual
+ *             overlaps neither x (MOE_E_INVALID at its address) nor, but for the
+ *             above, the residual
  * Limits: T >= 0, rows >= 1, cols >= 1 (MOE_E_INVALID otherwise); cols % 64 == 0,
  * x_stride % 8 == 0, rows * cols < 2^34, T * rows < 2^36, T * cols < 2^40, T <=
  * 2^31 - 2176, and fewer than 2^23 - 8 blocks of 16 rows (T <= 16) or of 16 rows by
@@ -421,7 +422,8 @@ moe_status moe_kv4_append(const moe_kv4_dims *dm, const moe_kv4_cache *cache, in
  * moe_kv4_read - rebuild the same tokens' keys and values, scale * code + bias,
  * rounded to fp32 and for bf16 once more (n_b = kv_len[b] reads a whole
  * sequence).
- *   k, v  bf16 or fp32 (dtype) [T][Hkv][D], out, tokens k_stride / v_stride apart
+ *   k, v  bf16 or fp32 (dtype) [T][Hkv][D], out, tokens k_stride / v_stride apart; they
+ *         do not overlap (MOE_E_INVALID at one address)
  */
 moe_status moe_kv4_read(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T, void *k,
                         int64_t k_stride, void *v, int64_t v_stride, int32_t dtype,
@@ -437,7 +439,8 @@ size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int3
  *   out[t][h] = sum_p softmax_p(scale * q[t][h] . k_p) v_p, with k_p, v_p =
  *   s * code + b of cache head h / (Hq / Hkv), over the positions
  *   p < kv_len that the token at position i sees: p <= i if causal, and
- *   p > i - window if window > 0. A token that sees none gets zeros. Positions
+ *   p > i - window if window > 0. A token that sees none gets zeros (and so does one
+ *   whose scores are all -infinity in fp32). Positions
  *   it does not see never reach its result, whatever the cache holds there.
  *   q       bf16 [T][Hq][D], tokens q_stride apart
  *   out     bf16 [T][Hq][D], out, tokens out_stride apart; may be q itself with the
@@ -454,7 +457,8 @@ size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int3
  *   many (T * Hq >= 4096, T * Hq * positions of the page table or the window >=
  *     2^25, and more than 64 rows max_new * Hq / Hkv of a cache head): keys, values and
  *     weights, to fp16; to bf16 for a block of rows whose keys, values or
- *     queries fp16's range does not hold (2^15 and more, or scales below 2^-13).
+ *     queries fp16's range does not hold (2^15 and more, or scales below 2^-13), or
+ *     whose scores times scale log2(e) pass 2^23.
  * Sums are divided at the end: while scales and biases are below 2^80 they cannot
  * overflow; larger values may come back as infinities or NaN, in their group of 64
  * channels, for the tokens that see them.

@@ -405,3 +405,9 @@ def test_workspace_of_a_prompt_beside_single_tokens(L):
         slots = 2 * 5 * 256       # twice the workgroups that the card holds
         assert need <= B * few * Hq * (D + 2) * 4 * max(1, slots // (B * Hkv * (few * Hq // Hkv // 16))), (T, need)
         assert need < 1 << 28
+
+
+def test_outputs_onto_what_is_still_read_or_written(L):
+    assert project(L, rows=128, ys=128, y=FAKE) == INVALID           # y onto x
+    assert project(L, T=1, rows=128, ys=128, y=FAKE, dtype=1) == INVALID
+    assert move(L, "moe_kv4_read", k=FAKE, v=FAKE) == INVALID        # keys and values in one place
