@@ -804,3 +804,22 @@ def test_single_tokens_beside_a_prompt_in_their_own_workspace(new, past, Hq, Hkv
     assert bool((ws[need:] == 0xA5).all())
     want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, D ** -0.5)
     check(out, want, tol, f"{new} {past}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_split_keys_in_a_padded_batch(D):
+    """More rows than the sequences have tokens for: parts are kept by sequence."""
+    rng = np.random.default_rng(49)
+    b = Batch(rng, [1, 2, 0, 1], [5000, 900, 40, 2500], 32)
+    c = filled(rng, b, 2, D)
+    T = b.T + 200
+    x = bf16_values(rng.standard_normal((T, 8, D)))
+    q = torch.from_numpy(x).cuda().to(BF16)
+    need = M.moe_kv4_attention_workspace_bytes(c, T, 8, b.B, b.table.shape[1], 2)
+    assert 0 < need
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((T, 8, D), 5.0, dtype=BF16, device="cuda")
+    M.moe_kv4_attention(c, q, *b.dev, max_new=2, out=out, ws=ws[:need])
+    assert bool((ws[need:] == 0xA5).all()) and bool((out[b.T:] == 5).all())
+    want, tol = K.attention(x[:b.T].astype(np.float64), K.Paged(*host_planes(c), b.table), b.cu, b.len, D ** -0.5)
+    check(out[:b.T], want, tol, f"padded {D}")
