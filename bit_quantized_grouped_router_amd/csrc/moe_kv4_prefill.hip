@@ -26,10 +26,10 @@
 // price: where a tile has a value or key of 2^15 or more, or a scale so small
 // that codes would fall among fp16's subnormals, or a query is too large or
 // too small, or scores pass kMostHalf, the workgroup starts over with bf16
-// operands, one tile after the other. That run also takes NaN and infinities: a group of values that holds one,
-// or that passes bf16's range at code 0 or 15, is replaced by zeros, and the rows
-// that see its key get NaN in the group's channels, so that a key no row may look
-// at never reaches one.
+// operands, one tile after the other. That run also takes NaN and infinities: a
+// group of values that holds one, or that passes bf16's range at code 0 or 15, is
+// replaced by zeros, and the rows that see its key get NaN in the group's
+// channels, so that a key no row may look at never reaches one.
 //
 // Keys are split over workgroups, as in the other kernel, where the row tiles
 // do not fill the card (512 tokens behind 60000, 16 heads on 2, D = 128: 1531 us
@@ -64,8 +64,10 @@ constexpr int ahead() { return !HALF ? 1 : D == 256 ? 2 : 3; }
 // by no more than 2^-32 of the largest where fp16 runs out of exponents, so that
 // even a million keys in a faint tail lose less than 2^-12 of it together.
 constexpr float kShift = 7.0f;
-// Scaled scores up to here take one FMA to their distance from the reference,
-// which is then off by half a step of theirs at most, 1/2: weights stay below 2^15.5.
+// Scaled scores up to here take one FMA to their distance from the scaled
+// reference. That is off by half a step of theirs, 1/2 at most, so weights stay below
+// 2^15.5; the same for all of a reference's weights, and taken into account where
+// they meet those of another.
 constexpr float kMostHalf = 0x1p23f;
 constexpr int kSalu = 0x4;  // sched_barrier: scalar instructions may pass
 
@@ -326,11 +328,13 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
     }
   };
   HalfRange range;
+  // what a score is scaled and then taken from, as fp16 weights have it
+  auto scaled = [&](float m) { return fmaf(m, scale2, -kShift); };
   // moves the reference m where a score exceeds it by too much
   auto rescale = [&](float mx, f32x16_t (&o)[NM], float &m, float &l) {
     if (__builtin_expect(__builtin_amdgcn_ballot_w64((mx - m) * scale2 > kSlack) != 0, 0)) {
       const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32, kWave)));
-      const float alpha = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((m - mn) * scale2);
+      const float alpha = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(HALF ? scaled(m) - scaled(mn) : (m - mn) * scale2);
       if (HALF && mn != kNegInf && !(fabsf(mn * scale2) < kMostHalf)) range.hi = ~0u;
 #pragma unroll
       for (int i = 0; i < NM; ++i)
@@ -417,7 +421,7 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
     int vb = 0, wb = 2 * P::kPlane;
     // Tile i, whose scores are s, and the scores sn of tile i + 1.
     auto tile = [&](int i, int kb, const f32x16_t &s, f32x16_t &sn) __attribute__((always_inline)) {
-      const float ref = m == kNegInf ? 0.f : fmaf(m, scale2, -kShift);
+      const float ref = m == kNegInf ? 0.f : scaled(m);
       uint32_t pw[8];
       // the wavefront that scores goes first, its neighbour's rebuilding can wait (4096
       // tokens by 5099 keys without a mask 248 -> 240 us, with one within 2%; D = 64
@@ -500,7 +504,8 @@ __device__ __forceinline__ bool prefill(const Kv4Dims &dm, const Kv4Plane &kc, c
   // (no return from here for rows behind the last: a branch of lanes would have
   // the second attempt's registers beside the first's)
   const bool partial = share.used > 1;
-  const float unit = HALF ? 0x1p-7f : 1.0f;  // parts leave without kShift
+  // parts leave relative to m itself, without kShift and the rounding of scaled(m)
+  const float unit = HALF && m != kNegInf ? __builtin_amdgcn_exp2f(-fmaf(m, scale2, -scaled(m))) : 1.0f;
   const float sum_inv = partial ? unit : l == 0.f ? 0.f : 1.0f / l;
   const long long pr = part_index(dm, at, rt, real ? row - rt.row0 : 0, splits, split);
   float *sums = part + pr * D + 2 * half;

@@ -823,3 +823,44 @@ def test_split_keys_in_a_padded_batch(D):
     assert bool((ws[need:] == 0xA5).all()) and bool((out[b.T:] == 5).all())
     want, tol = K.attention(x[:b.T].astype(np.float64), K.Paged(*host_planes(c), b.table), b.cu, b.len, D ** -0.5)
     check(out[:b.T], want, tol, f"padded {D}")
+
+
+@pytest.mark.parametrize("scale", [2.0, 90.0, 700.0, 1500.0])
+@pytest.mark.parametrize("new,past,Hq,width", [(2, 5000, 4, 8192), (80, 2000, 64, 8192), (1500, 600, 16, 2112)])
+def test_close_scores_far_from_zero(new, past, Hq, width, scale):
+    """Scores of 2^13 and small multiples of 2^-9 more, exact in the cache and in every product: a
+    softmax over small differences of scaled scores of up to 2^24, whose reference moves within
+    a workgroup and differs between splits."""
+    rng = np.random.default_rng(51)
+    n, D = new + past, 128
+    b = Batch(rng, [new], [past], 16, width=width // 16)
+    t = np.arange(n)
+    j = np.where(t % 512 < 256, (t // 512) % 3, 0.0)
+    j = np.where(np.isin(t % 512, (300, 400)), 9.0 + (t // 512) % 3, j) * (355 / max(scale, 16.0))
+    j = np.clip(np.round(j), 0, 255)
+    k = np.zeros((n, 1, D), dtype=np.float32)
+    k[:, :, :64], k[:, :, 64:] = 2.0 ** 13, (j * 2.0 ** -9)[:, None, None]
+    assert (k == bf16_values(k)).all()
+    v = bf16_values(rng.standard_normal((n, 1, D)))
+    q, s, z = K.quantise(v)
+    code, val = q[:, 0].astype(np.float64), K.values(K.pack(q), s, z)[:, 0]
+    s = np.repeat(bf16_to_f64(s)[:, 0], 64, -1)
+    c = make_cache(b.num_pages, 1, 16, D)
+    M.moe_kv4_append(c, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), b.dev[0], i32([0, n]), b.dev[2])
+    x = torch.zeros((new, Hq, D), dtype=BF16, device="cuda")
+    x[:, :, 3], x[:, :, 70] = 1.0, 1.0
+    out = torch.full((new, Hq, D), float("nan"), dtype=BF16, device="cuda")
+    M.moe_kv4_attention(c, x, *b.dev, max_new=new, scale=scale, out=out)
+    out = out.double().cpu().numpy()
+    w = np.exp(scale * (j - j.max()) * 2.0 ** -9)
+    total = np.cumsum(w)[past:, None]
+    mean = lambda a: np.cumsum(w[:, None] * a, axis=0)[past:] / total  # noqa: E731  over what a token sees
+    # the result's rounding and weight times scale as bf16 (few rows), or weights and values as
+    # fp16, or both as bf16 (scaled scores past 2^23); arguments of up to 60 off by 2^-22 of
+    # themselves, and fp32 sums of n keys
+    bf16 = 2.0 ** 13 * scale * 1.45 > 2.0 ** 23 and new > 2
+    tol = (2.0 ** -8 * (np.abs(mean(val)) + mean(np.abs(s * (code - 8)))) + (2.0 ** -7 if bf16 else 2.0 ** -10) * mean(np.abs(val))
+           + (2 * 60 * 2.0 ** -22 + (n + 64) * 2.0 ** -24) * mean(55 * s + np.abs(val)))
+    worst = float((np.abs(out - mean(val)[:, None]) / tol[:, None]).max())
+    say(f"  scale {scale}: worst {worst:.3f} of the bound")
+    assert worst <= 1
