@@ -26,7 +26,8 @@ EXPORTS = [
     "moe_dequant_w4", "moe_status_string", "moe_last_hip_error", "moe_router_logits",
     "moe_layer_forward_hidden", "moe_route_permute", "moe_layer_forward_noalloc",
     "moe_linear_w4", "moe_kv4_append", "moe_kv4_read", "moe_kv4_attention_workspace_bytes",
-    "moe_kv4_attention",
+    "moe_kv4_attention", "moe_rmsnorm", "moe_rope", "moe_kv4_rope_append", "moe_kv4_bounds",
+    "moe_kv4_sparse_attention_workspace_bytes", "moe_kv4_sparse_attention",
 ]
 
 
@@ -61,6 +62,19 @@ class MoeKv4Batch(ctypes.Structure):
                 ("kv_len", ctypes.c_void_p)]
 
 
+class MoeRopeSpec(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
+class MoeHeadNorm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("plus_one", ctypes.c_int32)]
+
+
+class MoeKv4Pages(ctypes.Structure):
+    _fields_ = [("top", ctypes.c_int32), ("first", ctypes.c_int32), ("recent", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     pass
 
@@ -78,7 +92,8 @@ def load(path: str) -> ctypes.CDLL:
     W = ctypes.POINTER(MoeW4Weights)
     KD, KC, KB = (ctypes.POINTER(MoeKv4Dims), ctypes.POINTER(MoeKv4Cache),
                   ctypes.POINTER(MoeKv4Batch))
-    I64 = ctypes.c_int64
+    I64, FL = ctypes.c_int64, ctypes.c_float
+    RS, HN, KP = (ctypes.POINTER(MoeRopeSpec), ctypes.POINTER(MoeHeadNorm), ctypes.POINTER(MoeKv4Pages))
     sig = {
         "moe_route": ([P, I32, I32, I32, P, P, P], I32),
         "moe_block_m": ([], I32),
@@ -103,6 +118,12 @@ def load(path: str) -> ctypes.CDLL:
         "moe_kv4_attention_workspace_bytes": ([KD, I32, I32, I32], SZ),
         "moe_kv4_attention": ([KD, KC, I32, I32, P, I64, P, I64, KB, ctypes.c_float, I32, I32, P,
                                SZ, P], I32),
+        "moe_rmsnorm": ([I32, I32, P, I64, I32, P, I64, P, I64, I32, P, I32, FL, P, I64, I32, P, I32, P], I32),
+        "moe_rope": ([I32, I32, I32, P, I64, I32, P, RS, HN, P, I64, I32, P], I32),
+        "moe_kv4_rope_append": ([KD, KC, I32, P, I64, P, I64, P, I64, I32, RS, HN, HN, P, I64, KB, P], I32),
+        "moe_kv4_bounds": ([KD, KC, I32, P, KB, P], I32),
+        "moe_kv4_sparse_attention_workspace_bytes": ([KD, I32, I32, KP], SZ),
+        "moe_kv4_sparse_attention": ([KD, KC, P, I32, I32, P, I64, P, I64, KB, KP, FL, P, P, SZ, P], I32),
         "moe_status_string": ([I32], ctypes.c_char_p),
         "moe_last_hip_error": ([], I32),
     }
@@ -755,4 +776,246 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
     _check(L.moe_kv4_attention(dm, c, T, max_new, q.data_ptr(), qs, out.data_ptr(), os_, b,
                                D ** -0.5 if scale is None else scale, int(causal), window, _ptr(ws),
                                need, s), "moe_kv4_attention")
+    return out
+
+
+# ------------------------------------------------------------------ norms and rotary positions
+
+DTYPES8 = {torch.float8_e4m3fn: 2, torch.int8: 3}
+
+
+def _here(cur: int, tensors: Dict[str, Optional[torch.Tensor]]) -> None:
+    """Raise unless every tensor there is lives on device cur, the current one."""
+    for t in tensors.values():
+        if t is not None and t.get_device() != cur:
+            _wrong_device(**tensors)
+
+
+def _row_stride(t: torch.Tensor, shape, name: str, dtypes) -> int:
+    """As _rows, for rows of any alignment (a single row's stride is its length)."""
+    st = _rows(t, shape, name, dtypes)
+    return st if shape[0] > 1 else shape[1]
+
+
+def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None, h=None, y=None,
+                out_dtype=None, plus_one: bool = False, group: int = 0, scales=None, stream=None):
+    """Root-mean-square norm of rows x [T, d] (bf16 or fp32): y = s / sqrt(mean s^2 + eps) * w
+    with s = x + residual and w the weight (bf16 [d]) or 1 + weight (plus_one). y is bf16
+    unless out_dtype or y says fp32, float8_e4m3fn or int8; the 8-bit types come with fp32
+    scales [T, d / group], group being 64, 128 or 0 for whole rows. With a residual the sum,
+    in its type, is stored to h (the residual itself: in place). Returns y, then scales, then
+    h, where there are such."""
+    if x.dim() != 2:
+        raise MoeError("x must be [T, d]")
+    T, d = x.shape
+    shape = (T, d)
+    cur = torch.cuda.current_device()
+    _here(cur, dict(x=x, weight=weight, residual=residual, h=h, y=y, scales=scales))
+    dtype = out_dtype if out_dtype is not None else y.dtype if y is not None else torch.bfloat16
+    eight = dtype in DTYPES8
+    code = DTYPES8[dtype] if eight else _dtype(dtype)
+    xs = _row_stride(x, shape, "x", (x.dtype,))
+    xd = _dtype(x.dtype)
+    _need(weight, d * 2, "weight", BF16)
+    rs = hs = hd = 0
+    if residual is not None:
+        hd = _dtype(residual.dtype)
+        rs = _row_stride(residual, shape, "residual", (residual.dtype,))
+        if h is None:
+            h = _empty(shape, residual.dtype, x.device, stream)
+            hs = d
+        else:
+            hs = _row_stride(h, shape, "h", (residual.dtype,))
+    elif h is not None:
+        raise MoeError("h is the sum with a residual; there is none")
+    if y is None:
+        y = _empty(shape, dtype, x.device, stream)
+        ys = d
+    else:
+        ys = _row_stride(y, shape, "y", (dtype,))
+    if eight:
+        if group < 0 or (group and d % group):
+            raise MoeError(f"group {group} does not divide d = {d}")
+        group = group or d
+        if scales is None:
+            scales = _empty((T, d // group), torch.float32, x.device, stream)
+        elif scales.shape != (T, d // group) or scales.dtype != torch.float32:
+            raise MoeError(f"scales are {scales.dtype} {tuple(scales.shape)}; expected float32 {(T, d // group)}")
+    elif group or scales is not None:
+        raise MoeError(f"group and scales belong to 8-bit outputs; y is {dtype}")
+    _check(lib().moe_rmsnorm(T, d, x.data_ptr(), xs, xd, None if residual is None else residual.data_ptr(), rs,
+                             None if h is None else h.data_ptr(), hs, hd, _ptr(weight), int(plus_one), eps,
+                             y.data_ptr(), ys, code, _ptr(scales), group, _stream(stream, cur)), "moe_rmsnorm")
+    if not eight and h is None:
+        return y
+    return tuple(t for t in (y, scales, h) if t is not None)
+
+
+class Rope:
+    """Rotary positions: freqs fp32 [rot / 2] on the GPU, radians a position, turn the first rot
+    channels of a head, in pairs (2i, 2i + 1) if interleaved and (i, i + rot / 2) otherwise;
+    cosines and sines are multiplied by magnitude."""
+
+    def __init__(self, freqs: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0):
+        if freqs.dim() != 1 or freqs.dtype != torch.float32 or not freqs.is_contiguous():
+            raise MoeError("freqs must be a contiguous float32 vector")
+        self.freqs, self.interleaved, self.magnitude = freqs, bool(interleaved), float(magnitude)
+
+    def c(self) -> MoeRopeSpec:
+        return MoeRopeSpec(self.freqs.data_ptr(), 2 * self.freqs.shape[0], self.interleaved, self.magnitude)
+
+    @staticmethod
+    def make(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, trained: int = 0,
+             fast: float = 32.0, slow: float = 1.0, interleaved: bool = False, device="cuda") -> "Rope":
+        """The frequencies base ** (-2i / rot), for contexts `factor` times as long as the one
+        trained on:
+          none    as they are;
+          linear  all divided by factor (positions interpolated);
+          base    the base raised so that the slowest pair is divided by factor and the fastest
+                  stays: base * factor ** (rot / (rot - 2));
+          ramp    pairs that turn at least `fast` times in the `trained` positions stay, those that
+                  turn at most `slow` times are divided by factor, between them a linear ramp over
+                  the pair's index; the magnitude is 0.1 ln(factor) + 1."""
+        if rot < 2 or rot % 2 or not base > 1.0 or not factor >= 1.0:
+            raise MoeError(f"rot {rot} must be even and positive, base {base} above 1 and factor {factor} at least 1")
+        import math
+        n, magnitude = rot // 2, 1.0
+        if scaling == "base" and rot > 2:
+            base = base * factor ** (rot / (rot - 2))
+        f = [base ** (-2.0 * i / rot) for i in range(n)]
+        if scaling == "linear" or (scaling == "base" and rot == 2):
+            f = [v / factor for v in f]
+        elif scaling == "ramp":
+            if trained < 1 or not fast > slow > 0.0:
+                raise MoeError(f"a ramp needs trained >= 1 and fast > slow > 0; got {trained}, {fast} and {slow}")
+            # index of the pair that turns so many times in the trained positions
+            at = lambda turns: rot * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+            lo, hi = max(math.floor(at(fast)), 0), math.ceil(at(slow))
+            keep = [1.0 - min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(n)]
+            f = [v * k + v / factor * (1.0 - k) for v, k in zip(f, keep)]
+            magnitude = 0.1 * math.log(factor) + 1.0
+        elif scaling not in ("none", "base"):
+            raise MoeError(f"scaling {scaling!r}; expected none, linear, base or ramp")
+        return Rope(torch.tensor(f, dtype=torch.float64).float().to(device), interleaved, magnitude)
+
+
+def _head_norm(weight, D: int, eps: float, plus_one: bool, name: str):
+    if weight is None:
+        return None
+    _need(weight, D * 2, name, BF16)
+    return MoeHeadNorm(_ptr(weight), eps, plus_one)
+
+
+def moe_rope(x: torch.Tensor, rope: Rope, positions: torch.Tensor, weight=None, eps: float = 1e-6,
+             plus_one: bool = False, out=None, out_dtype=None, stream=None):
+    """Rotary positions of heads x [T, H, D] (bf16 or fp32) at positions int32 [T], after a norm
+    of each head if weight (bf16 [D]) is given. out has x's type unless it or out_dtype says
+    otherwise; it may be x (in place)."""
+    if x.dim() != 3:
+        raise MoeError("x must be [T, H, D]")
+    T, H, D = x.shape
+    cur = torch.cuda.current_device()
+    _here(cur, dict(x=x, freqs=rope.freqs, positions=positions, weight=weight, out=out))
+    if positions.shape != (T,) or positions.dtype != torch.int32:
+        raise MoeError(f"positions are {positions.dtype} {tuple(positions.shape)}; expected int32 {(T,)}")
+    dtype = out_dtype if out_dtype is not None else out.dtype if out is not None else x.dtype
+    xs = _rows(x, (T, H, D), "x", (x.dtype,))
+    if out is None:
+        out = _empty((T, H, D), dtype, x.device, stream)
+        os_ = H * D
+    else:
+        os_ = _rows(out, (T, H, D), "out", (dtype,))
+    _check(lib().moe_rope(T, H, D, x.data_ptr(), xs, _dtype(x.dtype), _ptr(positions), rope.c(),
+                          _head_norm(weight, D, eps, plus_one, "weight"), out.data_ptr(), os_, _dtype(dtype),
+                          _stream(stream, cur)), "moe_rope")
+    return out
+
+
+def moe_kv4_rope_append(cache: KV4Cache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: Rope,
+                        page_table, cu, kv_len, q_weight=None, k_weight=None, eps: float = 1e-6,
+                        plus_one: bool = False, q_out=None, stream=None):
+    """moe_rope on the new tokens' queries [T, Hq, D] and keys [T, Hkv, D] at their positions in
+    the batch's sequences (with norms of the heads if q_weight or k_weight is given), and
+    moe_kv4_append of those keys and the values, in one pass. q, k and v are all bf16 or all
+    fp32. Returns the queries in bf16; q_out may be q (in place)."""
+    if q.dim() != 3:
+        raise MoeError("q must be [T, Hq, D]")
+    T, Hq, _ = q.shape
+    dm, c, b, s, Hkv, D = _kv4(cache, page_table, cu, kv_len, (q, k, v, q_weight, k_weight, q_out, rope.freqs),
+                               stream, Hq)
+    dt = _dtype(q.dtype)
+    qs = _rows(q, (T, Hq, D), "q", (q.dtype,))
+    ks, vs = _rows(k, (T, Hkv, D), "k", (q.dtype,)), _rows(v, (T, Hkv, D), "v", (q.dtype,))
+    if q_out is None:
+        q_out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
+        os_ = Hq * D
+    else:
+        os_ = _rows(q_out, (T, Hq, D), "q_out", BF16)
+    _check(lib().moe_kv4_rope_append(dm, c, T, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, dt, rope.c(),
+                                     _head_norm(q_weight, D, eps, plus_one, "q_weight"),
+                                     _head_norm(k_weight, D, eps, plus_one, "k_weight"), q_out.data_ptr(), os_, b, s),
+           "moe_kv4_rope_append")
+    return q_out
+
+
+# ------------------------------------------------------------------ attention over selected pages
+
+def _bounds(cache: KV4Cache, bounds: torch.Tensor) -> int:
+    n, heads, _, D = cache.sizes()
+    if bounds.shape != (n, heads, 2, D) or bounds.dtype not in BF16 or not bounds.is_contiguous():
+        raise MoeError(f"bounds are {bounds.dtype} {tuple(bounds.shape)}; expected a contiguous bf16 tensor "
+                       f"{(n, heads, 2, D)}")
+    return bounds.data_ptr()
+
+
+def moe_kv4_bounds(cache: KV4Cache, bounds: torch.Tensor, page_table, cu, kv_len, T: int, stream=None) -> None:
+    """Bring bounds (bf16 [num_pages, Hkv, 2, D]: smallest and largest key of each channel) up to
+    date for the pages that the batch's T new tokens lie in. Call it after every write."""
+    dm, c, b, s, _, _ = _kv4(cache, page_table, cu, kv_len, (bounds,), stream)
+    _check(lib().moe_kv4_bounds(dm, c, T, _bounds(cache, bounds), b, s), "moe_kv4_bounds")
+
+
+def moe_kv4_sparse_attention_workspace_bytes(cache: KV4Cache, T: int, Hq: int, B: int, max_pages: int, max_new: int,
+                                             top: int, first: int = 1, recent: int = 1) -> int:
+    num_pages, Hkv, page, D = cache.sizes()
+    dm = MoeKv4Dims(B, Hq, Hkv, D, page, num_pages, max_pages)
+    return lib().moe_kv4_sparse_attention_workspace_bytes(dm, T, min(max_new, T), MoeKv4Pages(top, first, recent))
+
+
+def moe_kv4_sparse_attention(cache: KV4Cache, bounds: torch.Tensor, q: torch.Tensor, page_table, cu, kv_len,
+                             max_new: int, top: int, first: int = 1, recent: int = 1, scale: Optional[float] = None,
+                             blocks=None, out=None, ws=None, stream=None):
+    """Causal attention of queries q [T, Hq, D] (bf16) over the pages that each token and cache
+    head selects: the sequence's first `first` and last `recent` pages, and of the others the
+    `top` whose bounds (moe_kv4_bounds) allow the best scores. blocks, if given (int32 [T, Hkv,
+    top + first + recent]), gets the pages' numbers in the sequence, ascending, -1 behind them.
+    Otherwise as moe_kv4_attention."""
+    if q.dim() != 3:
+        raise MoeError("q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    dm, c, b, s, Hkv, channels = _kv4(cache, page_table, cu, kv_len, (q, bounds, blocks, out, ws), stream, Hq)
+    if D != channels:
+        raise MoeError(f"q has {D} channels a head; the cache {channels}")
+    qs = _rows(q, (T, Hq, D), "q", BF16)
+    if out is None:
+        out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
+        os_ = Hq * D
+    else:
+        os_ = _rows(out, (T, Hq, D), "out", BF16)
+    if not (0 <= top <= INT32_MAX and 0 <= first <= INT32_MAX and 1 <= recent <= INT32_MAX and max_new >= 0):
+        raise MoeError(f"top {top}, first {first} and max_new {max_new} must not be negative, recent {recent} at least 1")
+    if blocks is not None and (blocks.shape != (T, Hkv, top + first + recent) or blocks.dtype != torch.int32):
+        raise MoeError(f"blocks are {blocks.dtype} {tuple(blocks.shape)}; expected int32 {(T, Hkv, top + first + recent)}")
+    max_new = min(max_new, T if T > 0 else INT32_MAX)
+    pages = MoeKv4Pages(top, first, recent)
+    L = lib()
+    if ws is None:
+        need = L.moe_kv4_sparse_attention_workspace_bytes(dm, T, max_new, pages)
+        if need:
+            ws = _empty((need,), torch.uint8, q.device, stream)
+    else:
+        need = ws.numel() * ws.element_size()
+    _check(L.moe_kv4_sparse_attention(dm, c, _bounds(cache, bounds), T, max_new, q.data_ptr(), qs, out.data_ptr(), os_, b,
+                                      pages, D ** -0.5 if scale is None else scale, _ptr(blocks), _ptr(ws), need, s),
+           "moe_kv4_sparse_attention")
     return out

@@ -3,13 +3,17 @@
 // host synchronisation, no exceptions across the interface.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
 #include "../../include/moe_w4.h"
 #include "moe_kv4.h"
+#include "moe_kv4_sparse.h"
 #include "moe_launch.h"
 #include "moe_linear.h"
+#include "moe_norm.h"
+#include "moe_rope.h"
 
 using namespace moe;
 
@@ -182,7 +186,7 @@ moe_status check_kv4_cache(const moe_kv4_cache *c, const moe_kv4_batch *b) {
 Kv4Plane to_kv4_plane(const moe_kv4_plane &p) { return Kv4Plane{p.codes, p.scales, p.biases}; }
 
 Kv4Batch to_kv4_batch(const moe_kv4_batch *b, int32_t T) {
-  return Kv4Batch{b->page_table, b->cu, b->kv_len, T};
+  return Kv4Batch{b->page_table, b->cu, b->kv_len, T, false};
 }
 
 // max_new as the kernels take it: no sequence has more new tokens than there
@@ -194,6 +198,33 @@ moe_status check_kv4_attention(const moe_kv4_dims *dm, int32_t T, int32_t max_ne
   if (max_new < 0 || (max_new == 0 && T > 0) || window < 0) return MOE_E_INVALID;
   if ((long long)T * dm->Hq >= (1ll << 31) - 64) return MOE_E_UNSUPPORTED;
   if (T > 0 && !kv4_grid_ok(to_kv4_dims(dm), kv4_max_new(T, max_new))) return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_rope(const moe_rope_spec *r, int32_t D) {
+  if (r == nullptr || r->rot < 2 || r->rot > D || r->rot % 2 != 0) return MOE_E_INVALID;
+  return check_ptr(r->freqs);
+}
+
+bool eps_ok(float eps) { return eps > 0.0f && std::isfinite(eps); }
+
+moe_status check_head_norm(const moe_head_norm *n) {
+  if (n == nullptr) return MOE_OK;
+  if (!eps_ok(n->eps)) return MOE_E_INVALID;
+  return check_ptr(n->weight);
+}
+
+Rope to_rope(const moe_rope_spec *r) { return Rope{r->freqs, r->rot, r->interleaved != 0, r->magnitude}; }
+
+HeadNorm to_head_norm(const moe_head_norm *n) {
+  return n == nullptr ? HeadNorm{nullptr, 1.0f, false} : HeadNorm{n->weight, n->eps, n->plus_one != 0};
+}
+
+moe_status check_kv4_sparse(const moe_kv4_dims *dm, int32_t T, int32_t max_new, const moe_kv4_pages *p) {
+  MOE_TRY(check_kv4_attention(dm, T, max_new, 0));
+  if (p == nullptr || p->top < 0 || p->first < 0 || p->recent < 1) return MOE_E_INVALID;
+  if ((long long)p->top + p->first + p->recent > kSelectMostTaken) return MOE_E_UNSUPPORTED;
+  if (dm->max_pages > kSelectMostPages || dm->Hq / dm->Hkv > 64) return MOE_E_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -543,6 +574,133 @@ moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
   const Kv4Attn at{q, out, q_stride, out_stride, n, scale, causal != 0, window, 0, 0, 0};
   return hip_status(launch_kv4_attention(d, to_kv4_plane(cache->k), to_kv4_plane(cache->v),
                                          to_kv4_batch(batch, T), at, ws, as_stream(stream)));
+}
+
+moe_status moe_rmsnorm(int32_t T, int32_t d, const void *x, int64_t x_stride, int32_t x_dtype,
+                       const void *residual, int64_t residual_stride, void *h, int64_t h_stride,
+                       int32_t h_dtype, const uint16_t *weight, int32_t plus_one, float eps, void *y,
+                       int64_t y_stride, int32_t y_dtype, float *scales, int32_t group, void *stream) {
+  if (T < 0 || d <= 0 || !eps_ok(eps)) return MOE_E_INVALID;
+  MOE_TRY(check_dtype(x_dtype));
+  if (residual != nullptr) MOE_TRY(check_dtype(h_dtype));
+  if (residual == nullptr && h != nullptr) return MOE_E_INVALID;
+  if (y_dtype < MOE_BF16 || y_dtype > MOE_INT8) return MOE_E_INVALID;
+  if (d > kNormMaxD) return MOE_E_UNSUPPORTED;
+  const bool eight = y_dtype == MOE_E4M3 || y_dtype == MOE_INT8;
+  if (eight && (group <= 0 || d % group != 0)) return MOE_E_INVALID;
+  if (eight && group != d && group != 64 && group != 128) return MOE_E_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (x_stride < d || y_stride < d || (residual != nullptr && residual_stride < d) || (h != nullptr && h_stride < d))
+    return MOE_E_INVALID;
+  MOE_TRY(check_ptr(x));
+  if (residual != nullptr) MOE_TRY(check_ptr(residual));
+  if (h != nullptr) MOE_TRY(check_ptr(h));
+  MOE_TRY(check_ptr(weight));
+  MOE_TRY(check_ptr(y));
+  if (eight) MOE_TRY(check_ptr(scales));
+  // rows would be written over others that are still read
+  if (y == x && (y_dtype != x_dtype || (y_stride != x_stride && T > 1))) return MOE_E_INVALID;
+  if (h != nullptr && h == residual && h_stride != residual_stride && T > 1) return MOE_E_INVALID;
+  if (y == weight || (residual != nullptr && y == residual)) return MOE_E_INVALID;
+  if (h != nullptr && (h == x || h == y || h == weight)) return MOE_E_INVALID;
+  if (eight && (scales == x || scales == residual || scales == h || scales == y || (const void *)scales == weight))
+    return MOE_E_INVALID;
+  const NormArgs a{T, d, x, x_stride, residual, residual ? residual_stride : 0, h, h ? h_stride : 0, weight, eps,
+                   plus_one != 0, y, y_stride, y_dtype, eight ? scales : nullptr, eight ? group : d};
+  return hip_status(launch_rmsnorm(a, x_dtype, h_dtype, as_stream(stream)));
+}
+
+moe_status moe_rope(int32_t T, int32_t H, int32_t D, const void *x, int64_t x_stride, int32_t x_dtype,
+                    const int32_t *positions, const moe_rope_spec *rope, const moe_head_norm *norm,
+                    void *out, int64_t out_stride, int32_t out_dtype, void *stream) {
+  if (T < 0 || H <= 0 || D <= 0) return MOE_E_INVALID;
+  MOE_TRY(check_dtype(x_dtype));
+  MOE_TRY(check_dtype(out_dtype));
+  if (D % 8 != 0 || D > kRopeMaxD || (long long)H * D >= (1ll << 31)) return MOE_E_UNSUPPORTED;
+  if ((long long)T * H >= (1ll << 40) / D) return MOE_E_UNSUPPORTED;
+  MOE_TRY(check_rope(rope, D));
+  MOE_TRY(check_head_norm(norm));
+  if (T == 0) return MOE_OK;
+  MOE_TRY(check_stride(x_stride, (int64_t)H * D));
+  MOE_TRY(check_stride(out_stride, (int64_t)H * D));
+  MOE_TRY(check_ptr(x));
+  MOE_TRY(check_ptr(positions));
+  MOE_TRY(check_ptr(out));
+  if (out == x && (x_dtype != out_dtype || (x_stride != out_stride && T > 1))) return MOE_E_INVALID;
+  if (out == positions || out == rope->freqs || (norm != nullptr && out == norm->weight)) return MOE_E_INVALID;
+  return hip_status(launch_rope(T, H, D, x, x_stride, x_dtype, positions, to_rope(rope), to_head_norm(norm), out,
+                                out_stride, out_dtype, as_stream(stream)));
+}
+
+moe_status moe_kv4_rope_append(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
+                               const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                               const void *v, int64_t v_stride, int32_t dtype,
+                               const moe_rope_spec *rope, const moe_head_norm *q_norm,
+                               const moe_head_norm *k_norm, uint16_t *q_out, int64_t q_out_stride,
+                               const moe_kv4_batch *batch, void *stream) {
+  MOE_TRY(check_kv4_dims(dm, T, true));
+  if ((long long)T * dm->Hq >= (1ll << 31) - 64) return MOE_E_UNSUPPORTED;
+  MOE_TRY(check_dtype(dtype));
+  MOE_TRY(check_rope(rope, dm->D));
+  MOE_TRY(check_head_norm(q_norm));
+  MOE_TRY(check_head_norm(k_norm));
+  if (T == 0) return MOE_OK;
+  MOE_TRY(check_stride(q_stride, (int64_t)dm->Hq * dm->D));
+  MOE_TRY(check_stride(k_stride, (int64_t)dm->Hkv * dm->D));
+  MOE_TRY(check_stride(v_stride, (int64_t)dm->Hkv * dm->D));
+  MOE_TRY(check_stride(q_out_stride, (int64_t)dm->Hq * dm->D));
+  MOE_TRY(check_kv4_cache(cache, batch));
+  MOE_TRY(check_ptr(q));
+  MOE_TRY(check_ptr(k));
+  MOE_TRY(check_ptr(v));
+  MOE_TRY(check_ptr(q_out));
+  if (q == q_out && (dtype != MOE_BF16 || (q_stride != q_out_stride && T > 1))) return MOE_E_INVALID;
+  if (q_out == k || q_out == v) return MOE_E_INVALID;  // other wavefronts still read them
+  const RopeAppend a{q, k, v, q_stride, k_stride, v_stride, q_out, q_out_stride, to_head_norm(q_norm),
+                     to_head_norm(k_norm)};
+  return hip_status(launch_kv4_rope_append(to_kv4_dims(dm), to_kv4_plane(cache->k), to_kv4_plane(cache->v),
+                                           to_kv4_batch(batch, T), to_rope(rope), a, dtype, as_stream(stream)));
+}
+
+moe_status moe_kv4_bounds(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
+                          uint16_t *bounds, const moe_kv4_batch *batch, void *stream) {
+  MOE_TRY(check_kv4_dims(dm, T, false));
+  if (T == 0) return MOE_OK;
+  MOE_TRY(check_kv4_cache(cache, batch));
+  MOE_TRY(check_ptr(bounds));
+  return hip_status(launch_kv4_bounds(to_kv4_dims(dm), to_kv4_plane(cache->k), to_kv4_batch(batch, T), bounds,
+                                      as_stream(stream)));
+}
+
+size_t moe_kv4_sparse_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int32_t max_new,
+                                                const moe_kv4_pages *pages) {
+  if (check_kv4_sparse(dm, T, max_new, pages) != MOE_OK || T == 0) return 0;
+  const Kv4Select sel{nullptr, nullptr, 0, kv4_max_new(T, max_new), pages->top, pages->first, pages->recent, nullptr};
+  return kv4_sparse_ws(to_kv4_dims(dm), T, sel);
+}
+
+moe_status moe_kv4_sparse_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
+                                    const uint16_t *bounds, int32_t T, int32_t max_new, const uint16_t *q,
+                                    int64_t q_stride, uint16_t *out, int64_t out_stride,
+                                    const moe_kv4_batch *batch, const moe_kv4_pages *pages, float scale,
+                                    int32_t *blocks, void *ws, size_t ws_bytes, void *stream) {
+  MOE_TRY(check_kv4_sparse(dm, T, max_new, pages));
+  if (!(scale > 0.0f) || !(scale <= 0x1p64f)) return MOE_E_INVALID;
+  if (T == 0) return MOE_OK;
+  MOE_TRY(check_stride(q_stride, (int64_t)dm->Hq * dm->D));
+  MOE_TRY(check_stride(out_stride, (int64_t)dm->Hq * dm->D));
+  MOE_TRY(check_kv4_cache(cache, batch));
+  MOE_TRY(check_ptr(bounds));
+  MOE_TRY(check_ptr(q));
+  MOE_TRY(check_ptr(out));
+  if (blocks != nullptr) MOE_TRY(check_ptr(blocks));
+  if (q == out && q_stride != out_stride && T > 1) return MOE_E_INVALID;  // rows would be written over others' queries
+  const Kv4Select sel{bounds, q, q_stride, kv4_max_new(T, max_new), pages->top, pages->first, pages->recent, blocks};
+  const Kv4Dims d = to_kv4_dims(dm);
+  if (ws_bytes < kv4_sparse_ws(d, T, sel)) return MOE_E_WORKSPACE;
+  MOE_TRY(check_ptr(ws));
+  return hip_status(launch_kv4_sparse(d, to_kv4_plane(cache->k), to_kv4_plane(cache->v), to_kv4_batch(batch, T), sel,
+                                      out, out_stride, scale, ws, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -35,6 +35,9 @@ struct Kv4Batch {
   const int32_t *cu;     // [B+1] first row of each sequence's new tokens
   const int32_t *len;    // [B] tokens of each sequence, the new ones included
   int T;
+  // Each row is a sequence of its own (B = T, cu unused): table is [T][Hkv][max_pages], a
+  // list of pages for each cache head, and len[t] the keys in them; negative: left out.
+  bool rows;
 };
 
 // The new tokens of one sequence: rows begin .. begin + n - 1 of the token
@@ -53,6 +56,20 @@ MOE_HD Kv4Span kv4_span(int cu0, int cu1, int len, int T) {
   s.len = len < 0 ? 0 : len;
   s.first = s.len - s.n;
   return s;
+}
+
+// A row that is a sequence of its own.
+MOE_HD Kv4Span kv4_row_span(int row, int len) {
+  Kv4Span s;
+  s.begin = row;
+  s.n = len < 0 ? 0 : 1;
+  s.len = len < 0 ? 0 : len;
+  s.first = s.len - s.n;
+  return s;
+}
+
+MOE_HD Kv4Span kv4_seq_span(const Kv4Batch &bt, int seq) {
+  return bt.rows ? kv4_row_span(seq, bt.len[seq]) : kv4_span(bt.cu[seq], bt.cu[seq + 1], bt.len[seq], bt.T);
 }
 
 // Positions a sequence's page table row covers.

@@ -460,7 +460,8 @@ __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch
   const int cap = (int)kv4_capacity(dm);
   float total = 0.f, tasks = 0.f;  // rough figures will do
   for (int b = lane; b < dm.B; b += kWave) {
-    int n = min(min(max(bt.cu[b + 1], 0), bt.T) - min(max(bt.cu[b], 0), bt.T), at.max_new);
+    int n = bt.rows ? (bt.len[b] < 0 ? 0 : 1)
+                    : min(min(max(bt.cu[b + 1], 0), bt.T) - min(max(bt.cu[b], 0), bt.T), at.max_new);
     if (n * G > at.most) n = 0;
     float keys = (float)min(max(bt.len[b], 0), cap);
     if (at.window > 0) keys = fminf(keys, (float)at.window + (float)n);
@@ -472,17 +473,6 @@ __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch
   tasks = wave_sum_dpp(tasks) * dm.Hkv;
   const float room = fmaxf(at_slots<D>() - tasks, at_slots<D>() / 4);
   return max(kMinTiles, (int)fminf(ceilf(total / room), 67108864.0f));
-}
-
-// Inclusive sum over the wavefront's lanes (six DPP steps).
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);  // row_shr:2
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);  // row_shr:4
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);  // row_shr:8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
-  return v;
 }
 
 // Work item `item` of a call whose sequences have one row tile each: the
@@ -499,7 +489,7 @@ __device__ __forceinline__ bool work_item(const Kv4Dims &dm, const Kv4Batch &bt,
   const int lane = threadIdx.x & (kWave - 1);
   for (int b0 = 0; b0 < dm.B; b0 += kWave) {
     const int b = min(b0 + lane, dm.B - 1);
-    const Kv4Span sp = kv4_span(bt.cu[b], bt.cu[b + 1], bt.len[b], bt.T);
+    const Kv4Span sp = kv4_seq_span(bt, b);
     const int n = min(sp.n, at.max_new);
     const Kv4Range r = kv4_range(dm, sp.first, sp.first + max(n, 1) - 1, sp.len, at.causal, at.window);
     const int used = b0 + lane < dm.B && n > 0 && n * (dm.Hq / dm.Hkv) <= at.most ? kv4_share(r, per, splits, 0).used : 0;
@@ -566,7 +556,8 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
   const Kv4Share share = kv4_share(Kv4Range{r0.lo, r1.hi}, per, splits, split);
   if (split >= share.used) return;
 
-  const int32_t *table = bt.table + (long long)rt.seq * dm.max_pages;
+  const int32_t *table =
+      bt.table + (bt.rows ? (long long)rt.seq * dm.Hkv + rt.head : (long long)rt.seq) * dm.max_pages;
   uint8_t *ring = smem + wave * kStages * Ring<D>::kStage;
   const uint32_t ring_at = lds_address(ring);
   LaneParts<D> lp = lane_parts<D>(kc, vc, lane);

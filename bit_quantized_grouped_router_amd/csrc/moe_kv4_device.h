@@ -61,7 +61,7 @@ __device__ __forceinline__ RowTile row_tile(const Kv4Dims &dm, const Kv4Batch &b
   t.head = head;
   t.seq = seq;
   t.row0 = tile * rows_tile;
-  t.sp = kv4_span(bt.cu[seq], bt.cu[seq + 1], bt.len[seq], bt.T);
+  t.sp = kv4_seq_span(bt, seq);
   t.rows = min(t.sp.n, max_new) * (dm.Hq / dm.Hkv);
   return t;
 }
@@ -79,6 +79,17 @@ __device__ __forceinline__ float *part_stats(const Kv4Dims &dm, const Kv4Batch &
                                              float *part) {
   const long long tokens = at.room > 0 ? (long long)dm.B * at.room : bt.T;
   return part + tokens * dm.Hq * splits * dm.D;
+}
+
+// Inclusive sum over the wavefront's lanes (six DPP steps).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);  // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
 }
 
 // Fewest tiles a split of the prefill kernel's keys has.

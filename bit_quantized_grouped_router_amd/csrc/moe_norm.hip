@@ -1,0 +1,266 @@
+// Root-mean-square norm of rows, with the residual's addition before it.
+//
+//   s = x + r,   h = s rounded to r's type,   y = s / sqrt(mean s^2 + eps) * w
+// with w the weight or 1 + the weight. To 8 bits: per group of channels a = max
+// |y|, scale = a / 448 (e4m3) or a / 127 (int8), q = y / scale rounded to
+// nearest, ties to even. Everything up to the last rounding is fp32; the norm
+// is that of the unrounded sum.
+//
+// Bound by memory: one pass, a row stays in registers between the sum of its
+// squares and its output. L threads take a row, 8 channels (one 16-byte or two)
+// at a time and C times, so that a group of 64 or 128 channels is 8 or 16
+// neighbouring lanes and its maximum three or four DPP steps.
+#include "moe_norm.h"
+
+namespace moe {
+
+constexpr int kNormThreads = 256;
+
+// Channels at .. at + 7 of a row, those from n on as 0.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void norm_load8(const void *row, int at, int n, float (&x)[8]) {
+  if constexpr (VEC) {
+    if (F32) {
+      const float4 a = *(const float4 *)((const float *)row + at);
+      const float4 b = *(const float4 *)((const float *)row + at + 4);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+      const uint4 a = *(const uint4 *)((const uint16_t *)row + at);
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = 0.f;
+      if (at + i < n) x[i] = F32 ? ((const float *)row)[at + i] : bf16_to_f32(((const uint16_t *)row)[at + i]);
+    }
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void norm_store8(void *row, bool f32, int at, int n, const float (&x)[8]) {
+  if constexpr (VEC) {
+    if (f32) {
+      *(float4 *)((float *)row + at) = make_float4(x[0], x[1], x[2], x[3]);
+      *(float4 *)((float *)row + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      *(uint4 *)((uint16_t *)row + at) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                    pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (at + i < n) {
+        if (f32)
+          ((float *)row)[at + i] = x[i];
+        else
+          ((uint16_t *)row)[at + i] = to_bf16(x[i]);
+      }
+  }
+}
+
+// Sum of the L threads of a row, the same in each; sm is the row's own.
+template <int L>
+__device__ __forceinline__ float row_sum(float v, float *sm) {
+  v = wave_sum_dpp(v);
+  if constexpr (L > kWave) {
+    __syncthreads();  // what the row before left has been read
+    if ((threadIdx.x & (kWave - 1)) == 0) sm[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < L / kWave; ++i) v += sm[i];
+  }
+  return v;
+}
+
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *sm) {
+  v = wave_max_u32(v);
+  if constexpr (L > kWave) {
+    __syncthreads();
+    if ((threadIdx.x & (kWave - 1)) == 0) sm[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < L / kWave; ++i) v = max(v, sm[i]);
+  }
+  return v;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
+}
+
+// Bit pattern of a group's largest |y| (an infinity's or a NaN's is larger than
+// any finite one's) as its scale, NaN where the group is not finite.
+__device__ __forceinline__ float group_scale(uint32_t top, float largest) {
+  return top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / largest;
+}
+
+// Eight values over their scale, rounded; zeros where that is 0 or NaN.
+__device__ __forceinline__ uint2 to_8bit(const float (&y)[8], float scale, bool e4m3) {
+  const float largest = e4m3 ? 448.f : 127.f;
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = scale > 0.f ? fminf(fmaxf(y[i] / scale, -largest), largest) : 0.f;
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float *p = t + 4 * i;
+    if (e4m3) {
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(p[0], p[1], 0, false);
+      w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(p[2], p[3], lo, true);
+    } else {
+      w[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)(int)rintf(p[j]) & 0xFFu) << (8 * j);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// RK: the residual's type, 0 none, 1 bf16, 2 fp32. A workgroup takes its rows in
+// steps of the grid (launch_norm bounds it).
+template <int L, int C, bool X32, int RK, bool VEC>
+__global__ __launch_bounds__(L > kNormThreads ? L : kNormThreads) void rmsnorm_kernel(NormArgs a) {
+  constexpr int kThreads = L > kNormThreads ? L : kNormThreads, kRows = kThreads / L;
+  __shared__ uint32_t sm[kThreads / kWave];
+  const int lane = threadIdx.x % L;
+  const float largest = a.out == kOutE4m3 ? 448.f : 127.f;
+  for (long long row = (long long)blockIdx.x * kRows + threadIdx.x / L; row < a.T; row += (long long)gridDim.x * kRows) {
+    const char *x = (const char *)a.x + row * a.x_stride * (X32 ? 4 : 2);
+    const char *r = (const char *)a.r + row * a.r_stride * (RK == 2 ? 4 : 2);
+    float s[C][8], w[C][8];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int at = (lane + j * L) * 8;
+      if (at < a.d) norm_load8<X32, VEC>(x, at, a.d, s[j]);
+    }
+    if constexpr (RK != 0) {
+      float v[C][8];
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int at = (lane + j * L) * 8;
+        if (at < a.d) norm_load8<RK == 2, VEC>(r, at, a.d, v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] += v[j][i];
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int at = (lane + j * L) * 8;
+      if (at < a.d) norm_load8<false, VEC>(a.weight, at, a.d, w[j]);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int at = (lane + j * L) * 8;
+      if (at >= a.d) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] = w[j][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(s[j][i], s[j][i], sum);
+    }
+    sum = row_sum<L>(sum, (float *)sm);
+    if (RK != 0 && a.h != nullptr) {
+      char *h = (char *)a.h + row * a.h_stride * (RK == 2 ? 4 : 2);
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int at = (lane + j * L) * 8;
+        if (at < a.d) norm_store8<VEC>(h, RK == 2, at, a.d, s[j]);
+      }
+    }
+    const float inv = 1.0f / sqrtf(sum / (float)a.d + a.eps), one = a.plus_one ? 1.f : 0.f;
+    uint32_t top[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      top[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[j][i] = s[j][i] * inv * (w[j][i] + one);
+        top[j] = max(top[j], __float_as_uint(s[j][i]) & 0x7FFFFFFFu);
+      }
+    }
+    if (a.out <= kOutF32) {
+      char *y = (char *)a.y + row * a.y_stride * (a.out == kOutF32 ? 4 : 2);
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int at = (lane + j * L) * 8;
+        if (at < a.d) norm_store8<VEC>(y, a.out == kOutF32, at, a.d, s[j]);
+      }
+      continue;
+    }
+    uint8_t *y = (uint8_t *)a.y + row * a.y_stride;
+    uint32_t all = 0;
+    if (a.group == a.d) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) all = max(all, top[j]);
+      all = row_max<L>(all, sm);
+    }
+    float *scales = a.scales + row * (a.d / a.group);
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int at = (lane + j * L) * 8;
+      uint32_t m = all;
+      if (a.group != a.d) {
+        m = dpp_max<0x141>(dpp_max<0x4e>(dpp_max<0xb1>(top[j])));  // 8 lanes
+        if (a.group == 128) m = dpp_max<0x140>(m);                 // 16 lanes
+      }
+      if (at >= a.d) continue;
+      const float scale = group_scale(m, largest);
+      if (at % a.group == 0) scales[at / a.group] = scale;
+      const uint2 q = to_8bit(s[j], scale, a.out == kOutE4m3);
+      if constexpr (VEC) {
+        *(uint2 *)(y + at) = q;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at + i < a.d) y[at + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+      }
+    }
+  }
+}
+
+template <int L, int C, bool X32, int RK>
+static hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
+  constexpr int kThreads = L > kNormThreads ? L : kNormThreads, kRows = kThreads / L;
+  const long long need = ((long long)a.T + kRows - 1) / kRows;
+  const unsigned grid = (unsigned)(need < (1 << 20) ? need : 1 << 20);
+  const bool vec = a.d % 8 == 0 && ((a.x_stride | a.r_stride | a.h_stride | a.y_stride) & 7) == 0;
+  if (vec)
+    rmsnorm_kernel<L, C, X32, RK, true><<<grid, kThreads, 0, s>>>(a);
+  else
+    rmsnorm_kernel<L, C, X32, RK, false><<<grid, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool X32, int RK>
+static hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
+  const int chunks = (a.d + 7) / 8;
+  if (chunks <= 64) return launch_norm<64, 1, X32, RK>(a, s);
+  if (chunks <= 256 && a.T > 2048)
+    return chunks <= 128 ? launch_norm<64, 2, X32, RK>(a, s) : launch_norm<64, 4, X32, RK>(a, s);
+  if (chunks <= 256) return launch_norm<256, 1, X32, RK>(a, s);
+  if (chunks <= 512) return launch_norm<256, 2, X32, RK>(a, s);
+  if (chunks <= 1024) return launch_norm<256, 4, X32, RK>(a, s);
+  return launch_norm<1024, 4, X32, RK>(a, s);
+}
+
+hipError_t launch_rmsnorm(const NormArgs &a, int x_dtype, int r_dtype, hipStream_t s) {
+  if (a.r == nullptr) return x_dtype ? launch_rows<true, 0>(a, s) : launch_rows<false, 0>(a, s);
+  if (r_dtype) return x_dtype ? launch_rows<true, 2>(a, s) : launch_rows<false, 2>(a, s);
+  return x_dtype ? launch_rows<true, 1>(a, s) : launch_rows<false, 1>(a, s);
+}
+
+}  // namespace moe

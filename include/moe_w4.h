@@ -470,6 +470,139 @@ moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
                              int32_t causal, int32_t window, void *ws, size_t ws_bytes,
                              void *stream);
 
+/*
+ * moe_rmsnorm - root-mean-square norm of rows, with the residual's addition before
+ * it (a block's input norm, the norm between attention and the experts):
+ *   s = x + residual;  h = s in the residual's type;
+ *   y = s / sqrt(sum_c s[c]^2 / d + eps) * w,  w = weight, or 1 + weight (plus_one)
+ * in fp32 (the norm is that of the unrounded sum), each output rounded once.
+ * 8-bit outputs hold y / scale: for each row and `group` channels a = max |y|, scale
+ * = a / 448 (MOE_E4M3, without infinities, bias 7) or a / 127 (MOE_INT8), the quotient
+ * rounded to nearest, ties to even; a group of zeros has scale 0, one that holds a
+ * NaN or an infinity scale NaN and codes 0.
+ *   x         bf16 or fp32 (x_dtype) [T][d]
+ *   residual  bf16 or fp32 (h_dtype) [T][d], or NULL
+ *   h         h_dtype [T][d], out, or NULL (not stored; MOE_E_INVALID without a
+ *             residual); may be the residual itself with the same stride
+ *   weight    bf16 [d]
+ *   y         MOE_BF16, MOE_F32, MOE_E4M3 or MOE_INT8 (y_dtype) [T][d], out; may be x
+ *             itself with the same type and stride
+ *   scales    fp32 [T][d / group], out, for 8-bit outputs (NULL otherwise)
+ *   group     64 or 128 (d a multiple), or d: one scale a row; 8-bit outputs only
+ * Other overlaps of outputs are not allowed (MOE_E_INVALID at one address). Strides
+ * are in elements and at least a row long (MOE_E_INVALID); any d and any strides
+ * run, multiples of 8 fast. Squares are summed in fp32: a row whose sum of squares
+ * passes its range has norm infinity.
+ * Limits: 1 <= d <= 32768, eps > 0 and finite (MOE_E_INVALID otherwise).
+ */
+typedef enum { MOE_E4M3 = 2, MOE_INT8 = 3 } moe_dtype8;
+
+moe_status moe_rmsnorm(int32_t T, int32_t d, const void *x, int64_t x_stride, int32_t x_dtype,
+                       const void *residual, int64_t residual_stride, void *h, int64_t h_stride,
+                       int32_t h_dtype, const uint16_t *weight, int32_t plus_one, float eps, void *y,
+                       int64_t y_stride, int32_t y_dtype, float *scales, int32_t group, void *stream);
+
+/*
+ * Rotary positions: the first rot channels of a head turn in pairs (a, b) =
+ * channels (2i, 2i + 1) if interleaved, (i, i + rot / 2) otherwise, by t = position
+ * * freqs[i]:  (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t).
+ * The other channels pass. t is taken in 64 bits, the rest in fp32.
+ *   freqs  fp32 [rot / 2], radians a position, in device memory
+ *   rot    even, 2 .. D
+ */
+typedef struct {
+  const float *freqs;
+  int32_t rot;
+  int32_t interleaved;
+  float magnitude;
+} moe_rope_spec;
+
+/* A norm of every head before it turns: x / sqrt(mean x^2 + eps) * w over its D channels,
+ * w = weight (bf16 [D]) or 1 + weight. eps > 0 and finite. */
+typedef struct {
+  const uint16_t *weight;
+  float eps;
+  int32_t plus_one;
+} moe_head_norm;
+
+/*
+ * moe_rope - norm (if norm is not NULL) and rotary positions of heads.
+ *   x          bf16 or fp32 (x_dtype) [T][H][D], tokens x_stride elements apart
+ *   positions  int32 [T], any values
+ *   out        bf16 or fp32 (out_dtype) [T][H][D], out; may be x itself with the same
+ *              type and stride (MOE_E_INVALID with another), and overlaps nothing else
+ * Limits: D % 8 == 0, 8 <= D <= 512, H >= 1, T * H * D < 2^40; strides multiples of 8
+ * (MOE_E_UNSUPPORTED) and at least a token long (MOE_E_INVALID).
+ */
+moe_status moe_rope(int32_t T, int32_t H, int32_t D, const void *x, int64_t x_stride, int32_t x_dtype,
+                    const int32_t *positions, const moe_rope_spec *rope, const moe_head_norm *norm,
+                    void *out, int64_t out_stride, int32_t out_dtype, void *stream);
+
+/*
+ * moe_kv4_rope_append - moe_rope on the new tokens' queries and keys at their
+ * positions in the batch's sequences, and moe_kv4_append of the turned keys and the
+ * values, in one pass: what the cache holds is bit for bit what moe_kv4_append makes
+ * of moe_rope's keys in fp32.
+ *   q, k, v   bf16 or fp32 (dtype) [T][Hq][D], [T][Hkv][D], [T][Hkv][D]
+ *   q_norm, k_norm  may be NULL
+ *   q_out     bf16 [T][Hq][D], out; may be q itself if that is bf16, with the same
+ *             stride (MOE_E_INVALID with another), and overlaps nothing else
+ * A token without a place in the cache has its queries turned and nothing written;
+ * rows of no sequence are left as they are. Precondition as for moe_kv4_append.
+ */
+moe_status moe_kv4_rope_append(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
+                               const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                               const void *v, int64_t v_stride, int32_t dtype,
+                               const moe_rope_spec *rope, const moe_head_norm *q_norm,
+                               const moe_head_norm *k_norm, uint16_t *q_out, int64_t q_out_stride,
+                               const moe_kv4_batch *batch, void *stream);
+
+/*
+ * moe_kv4_bounds - the smallest and the largest key of every channel, for each page
+ * that holds one of the call's new tokens, over the page's slots up to the sequence's
+ * last token; other pages' bounds are left as they are. Call it after every write (the
+ * attention below relies on the bounds of full pages).
+ *   bounds  bf16 [num_pages][Hkv][2][D]: smallest, then largest, of the keys as
+ *           moe_kv4_read gives them in bf16 (a zero is +0); NaN where a key is
+ */
+moe_status moe_kv4_bounds(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
+                          uint16_t *bounds, const moe_kv4_batch *batch, void *stream);
+
+/* Which pages a token attends to: its own page and those before it, of which the first
+ * `first`, the last `recent` (its own among them) and, of the others, the `top` with the
+ * best scores. first, top >= 0, recent >= 1 (MOE_E_INVALID otherwise), together at most
+ * 4096 (MOE_E_UNSUPPORTED). */
+typedef struct {
+  int32_t top, first, recent;
+} moe_kv4_pages;
+
+/* Bytes of workspace moe_kv4_sparse_attention needs (0 for arguments out of range). */
+size_t moe_kv4_sparse_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int32_t max_new,
+                                                const moe_kv4_pages *pages);
+
+/*
+ * moe_kv4_sparse_attention - causal attention of the new tokens' queries over the pages
+ * that each token and cache head selects. The score of a page is the most that any
+ * key inside its bounds could score, summed over the query heads of the cache head:
+ *   sum_h sum_c max(q[t][h][c] * lo[c], q[t][h][c] * hi[c])
+ * summed in 64 bits and rounded to fp32; ties go to the lower page of the sequence, a
+ * NaN ranks below every number. Pages that do not exist are not taken.
+ *   out[t][h] = moe_kv4_attention's, over the keys of those pages at positions up to the
+ *   token's own. Where nothing is left out it is causal attention without a window.
+ *   bounds  as moe_kv4_bounds leaves them
+ *   blocks  int32 [T][Hkv][first + recent + top], out, or NULL: the pages taken, as their
+ *           numbers 0, 1, .. in the sequence, ascending, -1 behind them
+ *   other arguments as for moe_kv4_attention; a token past max_new of its sequence, or of
+ *   no sequence, is left out (its rows of out and blocks stay as they are)
+ * Limits, besides moe_kv4_attention's: max_pages <= 2^20, Hq / Hkv <= 64
+ * (MOE_E_UNSUPPORTED).
+ */
+moe_status moe_kv4_sparse_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
+                                    const uint16_t *bounds, int32_t T, int32_t max_new, const uint16_t *q,
+                                    int64_t q_stride, uint16_t *out, int64_t out_stride,
+                                    const moe_kv4_batch *batch, const moe_kv4_pages *pages, float scale,
+                                    int32_t *blocks, void *ws, size_t ws_bytes, void *stream);
+
 const char *moe_status_string(int32_t status);
 
 /* hipError_t of the last MOE_E_HIP on this thread (0 if none). */

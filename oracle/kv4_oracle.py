@@ -103,8 +103,8 @@ class Paged:
                 np.repeat(bf16_to_f64(z), GROUP, -1), ok)
 
 
-def attention(q, cache, cu, kv_len, scale, causal=True, window=0):
-    """out fp64 [T, Hq, D], and what an implementation may be off by, element by element:
+def attention(q, cache, cu, kv_len, scale, causal=True, window=0, taken=None):
+    """taken, if given (bool [T, heads, pages of the table]): the pages a token attends to. out fp64 [T, Hq, D], and what an implementation may be off by, element by element:
       2^-8 |out|                     the result's rounding to bf16,
       2^-8 sum p s |code - 8|        each weight p s rounded to bf16,
       (n + 64) 2^-24 sum p (55 s + |b|)   fp32 sums of n keys with codes kept as 16 + code,
@@ -128,6 +128,8 @@ def attention(q, cache, cu, kv_len, scale, causal=True, window=0):
                 see &= pos <= at
             if window:
                 see &= pos > at - window
+            if taken is not None:
+                see &= taken[cu[b]:cu[b] + n, h][:, np.minimum(pos // cache.page, taken.shape[2] - 1)]
             some = see.any(1)
             # what no query sees is dropped before any arithmetic
             keep = see.any(0)
