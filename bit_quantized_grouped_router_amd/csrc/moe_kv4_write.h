@@ -8,6 +8,9 @@
 
 namespace moe {
 
+// A wavefront's own LDS accesses are done, and none is moved across.
+__device__ __forceinline__ void wave_lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // Minimum and maximum over aligned groups of 8 lanes.
 template <int CTRL>
 __device__ __forceinline__ float dpp_get(float v) {

@@ -4,9 +4,11 @@
 // for each pair of the first rot channels of a head: (2i, 2i + 1) interleaved,
 // (i, i + rot / 2) otherwise; the other channels pass. A norm of the head, x /
 // sqrt(mean x^2 + eps) * w, may come before. fp32 throughout, rounded once at
-// the end; only the angle is taken in 64 bits, as a number of turns whose whole
-// part is dropped there: in fp32 the angle of position 131,072 would be off by
-// 2^-8 radians.
+// the end; only angle, sine and cosine are taken in 64 bits (in fp32 the angle of
+// position 131,072 would be off by 2^-8 radians), as a number of turns whose
+// whole part is dropped, and rounded to fp32. The two products are rounded one by
+// one and not fused, so that a and b are treated alike and a key next to a border of
+// the quantisation falls on the side that the formula in fp32 says.
 //
 // Bound by memory for many tokens, by launch and latency for few. P lanes take
 // a head, 8 channels each, and a wavefront 64 / P heads at a time, up to
@@ -29,9 +31,6 @@ struct RopeLds {
   float stage[kWave * 8];
 };
 
-// A wavefront's own LDS accesses are done, and none is moved across.
-__device__ __forceinline__ void wave_lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
 // Sum over the P lanes of a head.
 template <int P>
 __device__ __forceinline__ float head_sum(float v) {
@@ -51,9 +50,9 @@ __device__ __forceinline__ void lane_turn(const Rope &rope, int position, int at
   const int lane = threadIdx.x & (kWave - 1), half = rope.rot / 2;
   for (int i = lane; i < half; i += kWave) {
     const double turns = (double)position * (double)rope.freqs[i] * 0.15915494309189533577;
-    float sn, cs;
-    sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-    lds.turn[i] = make_float2(cs * rope.magnitude, sn * rope.magnitude);
+    double sn, cs;
+    sincospi(2.0 * (turns - rint(turns)), &sn, &cs);
+    lds.turn[i] = make_float2((float)(cs * rope.magnitude), (float)(sn * rope.magnitude));
   }
   wave_lds_sync();
 #pragma unroll
@@ -98,7 +97,7 @@ __device__ __forceinline__ void rotate8(const Rope &rope, const LaneTurn &t, int
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = fmaf(y[i], t.s[i], x[i] * t.c[i]);
+    const float v = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(y[i], t.s[i]));
     x[i] = at + i < rope.rot ? v : x[i];
   }
 }
