@@ -547,7 +547,7 @@ moe_status moe_kv4_read(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int3
 size_t moe_kv4_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t T, int32_t max_new,
                                          int32_t window) {
   if (check_kv4_attention(dm, T, max_new, window) != MOE_OK || T == 0) return 0;
-  return kv4_attention_ws(to_kv4_dims(dm), T, kv4_max_new(T, max_new), window);
+  return kv4_attention_ws(to_kv4_dims(dm), T, kv4_max_new(T, max_new), window, false);
 }
 
 moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
@@ -566,7 +566,7 @@ moe_status moe_kv4_attention(const moe_kv4_dims *dm, const moe_kv4_cache *cache,
   if (q == out && q_stride != out_stride && T > 1) return MOE_E_INVALID;  // rows would be written over others' queries
   const Kv4Dims d = to_kv4_dims(dm);
   const int n = kv4_max_new(T, max_new);
-  const size_t need = kv4_attention_ws(d, T, n, window);
+  const size_t need = kv4_attention_ws(d, T, n, window, false);
   if (need > 0) {
     if (ws_bytes < need) return MOE_E_WORKSPACE;
     MOE_TRY(check_ptr(ws));

@@ -172,8 +172,8 @@ struct Kv4Attn {
 };
 
 // Bytes of a call's partial results (0 when no keys are split), for T token rows
-// of which no sequence has more than max_new.
-size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window);
+// of which no sequence has more than max_new; rows: Kv4Batch::rows.
+size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window, bool rows);
 bool kv4_grid_ok(const Kv4Dims &dm, int max_new);
 // Sequences of many query rows (n * G), `splits` workgroups to a tile of rows;
 // their partial results are joined by the other.

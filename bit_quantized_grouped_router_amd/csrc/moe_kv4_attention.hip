@@ -438,6 +438,11 @@ constexpr int at_lds_bytes() {
 // 256 CUs hold at a time. A workgroup too many runs alone after the others: 516
 // instead of 512 took a batch of 64 mixed sequences from 33 to 57 us.
 constexpr int kMinTiles = 16;
+// Of rows that are sequences, which have few keys: two a wavefront (us of this kernel and
+// the join for 2048 keys of one token, 16 heads on 2, D = 128: 10.9 + 3.9 with four,
+// 8.7 + 4.1 with two, 7.6 + 5.2 with one).
+constexpr int kMinTilesRows = 8;
+__host__ __device__ constexpr int min_tiles(bool rows) { return rows ? kMinTilesRows : kMinTiles; }
 // Workgroups of 4 wavefronts a CU holds: wavefronts a SIMD by their registers
 // (214, 130 and 90; a 4-wavefront limit at D = 128 spills a pointer of the loop,
 // and its reload waits for the DMA in flight).
@@ -455,7 +460,7 @@ constexpr int kEvenMaxB = 256;
 // tasks. (kv4_share raises it where `splits` are too few.)
 template <int D>
 __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Attn &at) {
-  if (dm.B > kEvenMaxB) return kMinTiles;
+  if (dm.B > kEvenMaxB) return min_tiles(bt.rows);
   const int lane = threadIdx.x & (kWave - 1), G = dm.Hq / dm.Hkv;
   const int cap = (int)kv4_capacity(dm);
   float total = 0.f, tasks = 0.f;  // rough figures will do
@@ -472,7 +477,7 @@ __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch
   total = wave_sum_dpp(total) * dm.Hkv;
   tasks = wave_sum_dpp(tasks) * dm.Hkv;
   const float room = fmaxf(at_slots<D>() - tasks, at_slots<D>() / 4);
-  return max(kMinTiles, (int)fminf(ceilf(total / room), 67108864.0f));
+  return max(min_tiles(bt.rows), (int)fminf(ceilf(total / room), 67108864.0f));
 }
 
 // Work item `item` of a call whose sequences have one row tile each: the
@@ -772,10 +777,10 @@ static long long kv4_keys(const Kv4Dims &dm, int tokens, int window) {
 // The most workgroups a row tile's keys are split over: as many as have
 // kMinTiles each, and no more than the card's slots over all tasks, or twice
 // that where sequences have one row tile each (work_item() evens those out).
-static int few_splits(const Kv4Dims &dm, int tokens, int window) {
+static int few_splits(const Kv4Dims &dm, int tokens, int window, bool rows) {
   const long long tasks = kv4_tasks(dm, tokens);
   const int slots = dm.D == 256 ? at_slots<256>() : dm.D == 128 ? at_slots<128>() : at_slots<64>();
-  const long long most = kv4_keys(dm, tokens, window) / (kKvTile * kMinTiles);
+  const long long most = kv4_keys(dm, tokens, window) / (kKvTile * min_tiles(rows));
   long long n = (kv4_row_tiles(dm, tokens) == 1 ? 2 : 1) * slots / tasks;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
@@ -801,7 +806,7 @@ static bool kv4_many(const Kv4Dims &dm, int T, long long keys) {
   return rows >= 4096 && rows * keys >= 1ll << 25;
 }
 
-static Kv4Plan kv4_plan(const Kv4Dims &dm, int T, int max_new, int window) {
+static Kv4Plan kv4_plan(const Kv4Dims &dm, int T, int max_new, int window, bool rows) {
   const int G = dm.Hq / dm.Hkv;
   Kv4Plan p{false, max_new, 1, 1, 0};
   const long long keys = kv4_keys(dm, 128 / G, window);
@@ -814,7 +819,7 @@ static Kv4Plan kv4_plan(const Kv4Dims &dm, int T, int max_new, int window) {
     if (n > keys / (kKvTile * kPfMinTiles)) n = keys / (kKvTile * kPfMinTiles);
     p.pre_splits = n < 1 ? 1 : (int)n;
   }
-  if (p.few > 0) p.row_splits = few_splits(dm, p.few, window);
+  if (p.few > 0) p.row_splits = few_splits(dm, p.few, window, rows);
   // beside a prompt few of the call's rows are the row kernel's (32768 tokens and one
   // sequence of a single one, 64 heads on 8, D = 128: 12 GB of workspace by row, 6 MB so)
   if ((long long)dm.B * p.few < T) p.room = p.few;
@@ -827,8 +832,8 @@ bool kv4_grid_ok(const Kv4Dims &dm, int max_new) {
   return (long long)max_new * (dm.Hq / dm.Hkv) < (1ll << 28) - 128;
 }
 
-size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window) {
-  const Kv4Plan p = kv4_plan(dm, T, max_new, window);
+size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window, bool rows) {
+  const Kv4Plan p = kv4_plan(dm, T, max_new, window, rows);
   const size_t row = (size_t)dm.Hq * (dm.D + 2) * sizeof(float);  // bytes of a token and split
   const size_t pre = p.pre_splits > 1 ? row * T * p.pre_splits : 0;
   const size_t few = p.row_splits > 1 ? row * p.row_splits * (p.room > 0 ? (size_t)dm.B * p.room : T) : 0;
@@ -866,7 +871,7 @@ static hipError_t launch_join(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4At
 template <int D>
 static hipError_t launch_all(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
                              Kv4Attn at, float *part, hipStream_t s) {
-  const Kv4Plan p = kv4_plan(dm, bt.T, at.max_new, at.window);
+  const Kv4Plan p = kv4_plan(dm, bt.T, at.max_new, at.window, bt.rows);
   hipError_t e = hipSuccess;
   if (p.many) {
     at.above = p.few > 0 ? kManyRows : 0;

@@ -147,6 +147,8 @@ struct ScorePart {
   uint32_t *most;  // [rows][Hkv][chunks * kScoreWaves]
   int row0, rows;
   int pitch, chunks, steps;  // a chunk is `steps` tiles of 16 pages for each wavefront
+  int tiles;                 // token tiles of a sequence
+  void *queries;             // prompts: QueryTile [slots][Hkv]; null otherwise
 };
 
 // What a score may be off by, over the sum of its terms' magnitudes, in units of
@@ -171,67 +173,22 @@ __device__ __forceinline__ void score_operand(float v, uint16_t (&part)[3]) {
   }
 }
 
-// The bounds of 16 pages as they are loaded: lane l has 16 bytes of each 64 of page l /
-// 4, so that four lanes' addresses follow on each other (with a page a lane, as the
-// matrix instruction wants them, the L1 cache takes 16 bytes at a time: 46 us, not
-// 20, for 1500 tokens behind 60,000). They change lanes through LDS, 4 KB at a time.
-// Which 16 bytes: swapped by l / 16, so that no banks collide there.
+// A token tile's q- and q+ as the matrix instruction takes them: part p of terms 32 m +
+// 8 (l / 16) .. + 7 of token l % 16 for lane l in step m, the first half of the steps
+// being q-'s.
 template <int D>
-struct PageBounds {
-  static constexpr int kLoads = 2 * D / 32;
-  uint4 v[kLoads];
+struct QueryTile {
+  static constexpr int kSteps = 2 * D / 32;
+  uint4 v[3][kSteps][kWave];
 };
 
+// The tile of `tokens` rows from q on (rows of a head, D channels of G heads), by all
+// threads, two channels at a time. Columns without a token are left as they are.
 template <int D>
-__device__ __forceinline__ void load_bounds(const Kv4Dims &dm, const uint16_t *bounds, int entry, int head, int lane,
-                                            PageBounds<D> &b) {
-  const bool ok = kv4_page_ok(dm, entry);
-  const uint16_t *p = bounds + ((long long)(ok ? entry : 0) * dm.Hkv + head) * 2 * D + ((lane & 3) ^ (lane >> 4)) * 8;
-#pragma unroll
-  for (int m = 0; m < PageBounds<D>::kLoads; ++m) {
-    b.v[m] = make_uint4(0, 0, 0, 0);
-    if (ok) b.v[m] = *(const uint4 *)(p + m * 32);
-  }
-}
-
-// Grid: x = token tile * chunks + chunk of pages, y = cache head, z = sequence.
-// 16 pages by 16 tokens a wavefront at a time; the tokens' q- and q+ lie in LDS as
-// the matrix instruction takes them. What bounds it: for few tokens the chain
-// offsets - table - bounds, for many the bounds' way from the L2.
-template <int D>
-__global__ __launch_bounds__(kScoreWaves *kWave) void kv4_score_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Select sel,
-                                                                       ScorePart part) {
-  constexpr int kSteps = 2 * D / 32;
-  __shared__ uint4 sq[3][kSteps][kWave];
-  __shared__ uint4 turned[kScoreWaves][4][kWave];
-  const int head = blockIdx.y, seq = blockIdx.z;
-  const int tile = blockIdx.x / part.chunks, chunk = blockIdx.x - tile * part.chunks;
-  const Kv4Span sp = kv4_seq_span(bt, seq);
-  const int n = min(sp.n, sel.max_new), i0 = tile * kScoreTile;
-  if (i0 >= n) return;
-  const int last = min(i0 + kScoreTile, n) - 1;
-  if (sp.begin + last < part.row0 || sp.begin + i0 >= part.row0 + part.rows) return;
-  const Kv4Scored sc = kv4_scored(dm, sp.first + last, sel.first, sel.recent);
-  const int span = part.steps * kScoreWaves * kScoreTile, c0 = chunk * span;
-  if (c0 > sc.hi || c0 + span <= sc.lo) return;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int G = dm.Hq / dm.Hkv;
-  const int32_t *table = bt.table + (long long)seq * dm.max_pages;
-  // page of this lane in the wavefront's tile st (hi is inside the table)
-  const auto entry_of = [&](int st) {
-    const int c = c0 + (st * kScoreWaves + wave) * kScoreTile + (lane >> 2);
-    return st < part.steps && c <= sc.hi ? table[c] : -1;
-  };
-  int entry = entry_of(0), next_entry = entry_of(1);
-  PageBounds<D> here;
-  load_bounds<D>(dm, sel.bounds, entry, head, lane, here);
-
-  // q- and q+ of the tile's tokens, two channels at a time: terms 32 m + 8 (l / 16) .. + 7
-  // of token l % 16 for lane l in step m. Columns without a token are not looked at.
-  for (int at = threadIdx.x; at < (last - i0 + 1) * (D / 2); at += kScoreWaves * kWave) {
+__device__ __forceinline__ void fill_queries(QueryTile<D> &t, const uint16_t *rows, long long stride, int tokens, int G) {
+  for (int at = threadIdx.x; at < tokens * (D / 2); at += blockDim.x) {
     const int j = at / (D / 2), c2 = at % (D / 2);
-    const uint16_t *q = sel.q + (long long)(sp.begin + i0 + j) * sel.q_stride + (long long)head * G * D + c2 * 2;
+    const uint16_t *q = rows + j * stride + c2 * 2;
     float neg[2] = {0.f, 0.f}, pos[2] = {0.f, 0.f};
 #pragma unroll 8
     for (int g = 0; g < G; ++g) {
@@ -253,74 +210,296 @@ __global__ __launch_bounds__(kScoreWaves *kWave) void kv4_score_kernel(Kv4Dims d
     const int m = c2 / 16, l = (c2 / 4 % 4) * 16 + j;
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
-      ((uint32_t *)&sq[p][m][l])[c2 % 4] = a[0][p] | (uint32_t)a[1][p] << 16;
-      ((uint32_t *)&sq[p][D / 32 + m][l])[c2 % 4] = b[0][p] | (uint32_t)b[1][p] << 16;
+      ((uint32_t *)&t.v[p][m][l])[c2 % 4] = a[0][p] | (uint32_t)a[1][p] << 16;
+      ((uint32_t *)&t.v[p][D / 32 + m][l])[c2 % 4] = b[0][p] | (uint32_t)b[1][p] << 16;
     }
   }
+}
+
+// The bounds of 16 pages as they are loaded: lane l has 16 bytes of each 64 of page l /
+// 4, so that four lanes' addresses follow on each other. They change lanes in LDS.
+// Which 16 bytes: swapped by l / 16, so that no banks collide there. A page that does
+// not exist reads page 0: its scores are not looked at.
+template <int D>
+__device__ __forceinline__ const uint16_t *page_bounds(const Kv4Dims &dm, const uint16_t *bounds, int entry, int head,
+                                                       int lane) {
+  return bounds + ((long long)(kv4_page_ok(dm, entry) ? entry : 0) * dm.Hkv + head) * 2 * D +
+         ((lane & 3) ^ (lane >> 4)) * 8;
+}
+
+// (Copied as a struct, an array of these would go to scratch memory.)
+__device__ __forceinline__ uint4 load16(const uint16_t *p) {
+  typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+  const u32x4_t v = *(const u32x4_t *)p;
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Where lane l finds terms 8 (l / 16) .. + 7 of page l % 16 among the 64 lanes' loads.
+__device__ __forceinline__ int turned_lane(int lane) { return (lane & 15) * 4 + ((lane >> 4) ^ (lane >> 2 & 3)); }
+
+// Sums of a page tile by a token tile: register r is page 4 (l / 16) + r, token l % 16.
+struct ScoreSums {
+  f32x4_t score, rest[2], most;  // rest: of the second and third parts; most: of magnitudes
+};
+
+__device__ __forceinline__ f32x4_t mfma_bf16(const uint4 &a, const uint4 &b, const f32x4_t &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                 0, 0);
+}
+
+// One step, whose sum of products is returned. q- is negative and q+ is not: with q's
+// sign the bounds' magnitudes make all terms positive.
+__device__ __forceinline__ f32x4_t score_step(ScoreSums &s, const uint4 &b, const uint4 (&q)[3], bool negative) {
+  const uint4 mag = negative ? make_uint4(b.x | 0x80008000u, b.y | 0x80008000u, b.z | 0x80008000u, b.w | 0x80008000u)
+                             : make_uint4(b.x & 0x7FFF7FFFu, b.y & 0x7FFF7FFFu, b.z & 0x7FFF7FFFu, b.w & 0x7FFF7FFFu);
+  s.most = mfma_bf16(mag, q[0], s.most);
+  s.rest[0] = mfma_bf16(b, q[1], s.rest[0]);
+  s.rest[1] = mfma_bf16(b, q[2], s.rest[1]);
+  return mfma_bf16(b, q[0], f32x4_t{0.f, 0.f, 0.f, 0.f});
+}
+
+// Keys of the tile's pages cb .. cb + 15 for this lane's token (out: its keys; null: none),
+// and the largest sum of magnitudes so far. valid: bit BIT i, page i exists.
+template <int BIT>
+__device__ __forceinline__ void put_scores(const ScoreSums &s, uint64_t valid, int lane, uint32_t *out, uint32_t &most) {
+  const uint32_t mine = (uint32_t)(valid >> (4 * BIT * (lane >> 4)));
+  uint32_t key[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const bool there = mine >> (BIT * r) & 1;
+    const uint32_t k = logit_key(s.score[r] + (s.rest[0][r] + s.rest[1][r]));
+    key[r] = there ? k : 0u;
+    most = max(most, there ? __float_as_uint(s.most[r]) & 0x7FFFFFFFu : 0u);
+  }
+  if (out != nullptr) *(uint4 *)(out + 4 * (lane >> 4)) = make_uint4(key[0], key[1], key[2], key[3]);
+}
+
+// The token tile and the pages c0 .. c0 + span - 1 of a workgroup.
+struct ScoreTile {
+  Kv4Span sp;
+  Kv4Scored sc;  // of the tile's last token
+  int i0, last;  // its tokens in the sequence
+};
+
+// False where there is nothing to score. kTokens: of a workgroup.
+template <int kTokens>
+__device__ __forceinline__ bool score_tile(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Select &sel,
+                                           const ScorePart &part, int seq, int tile, int c0, int span, ScoreTile &t) {
+  t.sp = kv4_seq_span(bt, seq);
+  const int n = min(t.sp.n, sel.max_new);
+  t.i0 = tile * kTokens;
+  t.last = min(t.i0 + kTokens, n) - 1;
+  if (t.i0 >= n || t.sp.begin + t.last < part.row0 || t.sp.begin + t.i0 >= part.row0 + part.rows) return false;
+  t.sc = kv4_scored(dm, t.sp.first + t.last, sel.first, sel.recent);
+  return c0 <= t.sc.hi && c0 + span > t.sc.lo;
+}
+
+// Few tokens a sequence. Grid: x = sequence, y = cache head, z = token tile + tiles *
+// chunk of pages (chunks that shorter sequences do not have come last: 64 sequences of
+// up to 32,000 tokens, D = 256, 24 us with them in between, ... without). 16 pages by
+// 16 tokens a wavefront at a time; as a chunk of four loads goes to LDS to change
+// lanes, the next tile's takes its registers. Bound by the chain offsets - table -
+// bounds.
+template <int D>
+__device__ __forceinline__ void score_pages(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Select &sel,
+                                            const ScorePart &part, int chunk, int tile, QueryTile<D> &sq,
+                                            uint4 (&turned)[kScoreWaves][4][kWave]) {
+  constexpr int kSteps = QueryTile<D>::kSteps;
+  const int head = blockIdx.y, seq = blockIdx.x;
+  const int span = part.steps * kScoreWaves * kScoreTile, c0 = chunk * span;
+  ScoreTile t;
+  if (!score_tile<kScoreTile>(dm, bt, sel, part, seq, tile, c0, span, t)) return;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int G = dm.Hq / dm.Hkv;
+  const int32_t *table = bt.table + (long long)seq * dm.max_pages;
+  // this lane's page in the wavefront's tile st (hi is inside the table)
+  const auto entry_of = [&](int st) {
+    const int c = c0 + (st * kScoreWaves + wave) * kScoreTile + (lane >> 2);
+    return st < part.steps && c <= t.sc.hi ? table[c] : -1;
+  };
+  int entry = entry_of(0), next_entry = entry_of(1);
+  uint4 raw[kSteps];
+  const uint16_t *page = page_bounds<D>(dm, sel.bounds, entry, head, lane);
+#pragma unroll
+  for (int m = 0; m < kSteps; ++m) raw[m] = load16(page + m * 32);
+  fill_queries<D>(sq, sel.q + (long long)(t.sp.begin + t.i0) * sel.q_stride + (long long)head * G * D, sel.q_stride,
+                  t.last - t.i0 + 1, G);
   __syncthreads();
 
   const int j = lane & 15;
-  const int row = sp.begin + i0 + j - part.row0;
-  const bool mine = i0 + j <= last && row >= 0 && row < part.rows;
-  uint32_t *out = part.keys + ((long long)row * dm.Hkv + head) * part.pitch;
+  const int row = t.sp.begin + t.i0 + j - part.row0;
+  const bool mine = t.i0 + j <= t.last && row >= 0 && row < part.rows;
+  const long long item = (long long)row * dm.Hkv + head;
   uint32_t most = 0;
   for (int st = 0; st < part.steps; ++st) {
     const int cb = c0 + (st * kScoreWaves + wave) * kScoreTile;
-    if (cb > sc.hi) break;
-    const uint64_t valid = __builtin_amdgcn_ballot_w64(kv4_page_ok(dm, entry));  // bit 4 i: page i of the tile
-    PageBounds<D> now = here;
+    if (cb > t.sc.hi) break;
+    const uint64_t valid = __builtin_amdgcn_ballot_w64(kv4_page_ok(dm, entry));
     entry = next_entry;
-    load_bounds<D>(dm, sel.bounds, entry, head, lane, here);
+    page = page_bounds<D>(dm, sel.bounds, entry, head, lane);
     next_entry = entry_of(st + 2);
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4_t step[kSteps], rest[2] = {zero, zero}, sum = zero;
+    ScoreSums s{zero, {zero, zero}, zero};
+    f32x4_t four[kSteps / 4];
 #pragma unroll
-    for (int m = 0; m < kSteps; ++m) {
-      if (m % 4 == 0) {
-        wave_lds_sync();  // what was there has been read
+    for (int k = 0; k < kSteps / 4; ++k) {
+      wave_lds_sync();  // what was there has been read
 #pragma unroll
-        for (int i = 0; i < 4; ++i) turned[wave][i][lane] = now.v[m + i];
-        wave_lds_sync();
+      for (int i = 0; i < 4; ++i) turned[wave][i][lane] = raw[4 * k + i];
+      wave_lds_sync();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) now.v[m + i] = turned[wave][i][(lane & 15) * 4 + ((lane >> 4) ^ (lane >> 2 & 3))];
+      for (int i = 0; i < 4; ++i) raw[4 * k + i] = load16(page + (4 * k + i) * 32);
+      f32x4_t one[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = 4 * k + i;
+        const uint4 q[3] = {sq.v[0][m][lane], sq.v[1][m][lane], sq.v[2][m][lane]};
+        one[i] = score_step(s, turned[wave][i][turned_lane(lane)], q, m < kSteps / 2);
       }
-      const bf16x8_t b = __builtin_bit_cast(bf16x8_t, now.v[m]);
-      // q- is negative and q+ is not: with the sign of q the bounds' magnitudes make all terms positive
-      const uint4 mag = m < kSteps / 2 ? make_uint4(now.v[m].x | 0x80008000u, now.v[m].y | 0x80008000u,
-                                                    now.v[m].z | 0x80008000u, now.v[m].w | 0x80008000u)
-                                       : make_uint4(now.v[m].x & 0x7FFF7FFFu, now.v[m].y & 0x7FFF7FFFu,
-                                                    now.v[m].z & 0x7FFF7FFFu, now.v[m].w & 0x7FFF7FFFu);
-      const bf16x8_t q = __builtin_bit_cast(bf16x8_t, sq[0][m][lane]);
-      step[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, q, zero, 0, 0, 0);
-      sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, mag), q, sum, 0, 0, 0);
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        rest[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, __builtin_bit_cast(bf16x8_t, sq[p + 1][m][lane]), rest[p],
-                                                          0, 0, 0);
+      four[k] = (one[0] + one[1]) + (one[2] + one[3]);
     }
+    s.score = four[0];
+    if constexpr (kSteps == 8) s.score = four[0] + four[1];
+    if constexpr (kSteps == 16) s.score = (four[0] + four[1]) + (four[2] + four[3]);
+    put_scores<4>(s, valid, lane, mine ? part.keys + item * part.pitch + cb : nullptr, most);
+  }
+  most = max(most, (uint32_t)__shfl_xor((int)most, 16, kWave));
+  most = max(most, (uint32_t)__shfl_xor((int)most, 32, kWave));
+  if (mine && lane < 16) part.most[item * part.chunks * kScoreWaves + chunk * kScoreWaves + wave] = most;
+}
+
+template <int D>
+__global__ __launch_bounds__(kScoreWaves *kWave) void kv4_score_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Select sel,
+                                                                       ScorePart part) {
+  __shared__ QueryTile<D> sq;
+  __shared__ uint4 turned[kScoreWaves][4][kWave];
+  const long long all = (long long)part.tiles * part.chunks;
+  for (long long z = blockIdx.z; z < all; z += gridDim.z) {
+    const int chunk = (int)(z / part.tiles);
+    score_pages<D>(dm, bt, sel, part, chunk, (int)(z - (long long)chunk * part.tiles), sq, turned);
+    if (z + gridDim.z < all) __syncthreads();  // the queries have been read
+  }
+}
+
+// Prompts: the token tiles' operands are worked out once, for all pages, and lie in
+// memory; tile `tile` of a sequence in slot query_slot.
+__device__ __forceinline__ long long query_slot(const Kv4Span &sp, const ScorePart &part, int seq, int tile) {
+  return (long long)(sp.begin >> 4) + tile + seq - (part.row0 >> 4) + 2;
+}
+
+template <int D>
+__global__ __launch_bounds__(1024) void kv4_query_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Select sel, ScorePart part) {
+  __shared__ QueryTile<D> sq;
+  const int head = blockIdx.y, seq = blockIdx.z, tile = blockIdx.x, G = dm.Hq / dm.Hkv;
+  ScoreTile t;
+  if (!score_tile<kScoreTile>(dm, bt, sel, part, seq, tile, 0, 0x7FFFFFFF, t)) return;
+  uint4 *all = &sq.v[0][0][0];
+  constexpr int kAll = sizeof(sq) / 16;
+  if (t.last - t.i0 + 1 < kScoreTile) {  // columns without a token
+    for (int i = threadIdx.x; i < kAll; i += blockDim.x) all[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
+  fill_queries<D>(sq, sel.q + (long long)(t.sp.begin + t.i0) * sel.q_stride + (long long)head * G * D, sel.q_stride,
+                  t.last - t.i0 + 1, G);
+  __syncthreads();
+  uint4 *out = (uint4 *)part.queries + (query_slot(t.sp, part, seq, tile) * dm.Hkv + head) * kAll;
+  for (int i = threadIdx.x; i < kAll; i += blockDim.x) out[i] = all[i];
+}
+
+// 64 pages by 64 tokens a workgroup at a time: each wavefront loads 16 of the pages
+// and has 16 of the tokens, whose operands stay in registers. Grid: x = token tile of 64
+// * chunks + chunk of pages, y = cache head, z = sequence.
+template <int D>
+__global__ __launch_bounds__(kScoreWaves *kWave) void kv4_score_prompt_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Select sel,
+                                                                              ScorePart part) {
+  constexpr int kSteps = QueryTile<D>::kSteps, kTokens = kScoreWaves * kScoreTile;
+  __shared__ uint4 turned[kScoreWaves][kSteps][kWave];
+  const int head = blockIdx.y, seq = blockIdx.z;
+  const int tile = blockIdx.x / part.chunks, chunk = blockIdx.x - tile * part.chunks;
+  const int span = part.steps * kScoreWaves * kScoreTile, c0 = chunk * span;
+  ScoreTile t;
+  if (!score_tile<kTokens>(dm, bt, sel, part, seq, tile, c0, span, t)) return;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int32_t *table = bt.table + (long long)seq * dm.max_pages;
+  const auto entry_of = [&](int st) {
+    const int c = c0 + (st * kScoreWaves + wave) * kScoreTile + (lane >> 2);
+    return st < part.steps && c <= t.sc.hi ? table[c] : -1;
+  };
+  const auto entry_at = [&](int st) {  // lane's page of the 64
+    const int c = c0 + st * kScoreWaves * kScoreTile + lane;
+    return st < part.steps && c <= t.sc.hi ? table[c] : -1;
+  };
+  int all_entry = entry_at(0);
+  int next_entry = entry_of(1);
+  uint4 raw[kSteps];
+  const uint16_t *page = page_bounds<D>(dm, sel.bounds, entry_of(0), head, lane);
 #pragma unroll
-    for (int w = 1; w < kSteps; w *= 2)
+  for (int m = 0; m < kSteps; ++m) raw[m] = load16(page + m * 32);
+  // this wavefront's tokens; a tile without any takes the first one's operands and stores nothing
+  const int i0 = t.i0 + wave * kScoreTile, j = lane & 15;
+  const int at = i0 <= t.last && t.sp.begin + min(i0 + kScoreTile - 1, t.last) >= part.row0 &&
+                         t.sp.begin + i0 < part.row0 + part.rows ? tile * kScoreWaves + wave : -1;
+  uint4 q[kSteps][3];
+  {
+    // some tile of the workgroup is inside the part: its last token is not before it, its first not behind
+    const int inside = at >= 0 ? at : max(tile * kScoreWaves, (part.row0 - t.sp.begin) >> 4);
+    const QueryTile<D> *qt = (const QueryTile<D> *)part.queries + query_slot(t.sp, part, seq, inside) * dm.Hkv + head;
 #pragma unroll
-      for (int m = 0; m + w < kSteps; m += 2 * w) step[m] += step[m + w];
-    step[0] += rest[0] + rest[1];
-    // register r: page 4 (l / 16) + r, token l % 16
-    uint32_t key[4];
+    for (int m = 0; m < kSteps; ++m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      key[r] = (valid >> (4 * (4 * (lane >> 4) + r)) & 1) ? logit_key(step[0][r]) : 0u;
-      most = max(most, __float_as_uint(sum[r]) & 0x7FFFFFFFu);
+      for (int p = 0; p < 3; ++p) q[m][p] = qt->v[p][m][lane];
+  }
+  const int row = t.sp.begin + i0 + j - part.row0;
+  const bool mine = at >= 0 && i0 + j <= t.last && row >= 0 && row < part.rows;
+  const long long item = (long long)row * dm.Hkv + head;
+  uint32_t most = 0;
+  for (int st = 0; st < part.steps; ++st) {
+    const int cb = c0 + st * kScoreWaves * kScoreTile;
+    if (cb > t.sc.hi) break;
+    const uint64_t valid = __builtin_amdgcn_ballot_w64(kv4_page_ok(dm, all_entry));  // of the 64 pages
+    lds_barrier();  // the tiles before have been read
+#pragma unroll
+    for (int m = 0; m < kSteps; ++m) turned[wave][m][lane] = raw[m];
+    lds_barrier();
+    page = page_bounds<D>(dm, sel.bounds, next_entry, head, lane);
+#pragma unroll
+    for (int m = 0; m < kSteps; ++m) raw[m] = load16(page + m * 32);
+    next_entry = entry_of(st + 2);
+    all_entry = entry_at(st + 1);
+#pragma unroll  // not a loop: hipcc would wait for the loads above before it
+    for (int w = 0; w < kScoreWaves; ++w) {
+      if (cb + w * kScoreTile > t.sc.hi) break;
+      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+      ScoreSums s{zero, {zero, zero}, zero};
+      f32x4_t four[kSteps / 4];
+#pragma unroll
+      for (int k = 0; k < kSteps / 4; ++k) {
+        f32x4_t one[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = 4 * k + i;
+          one[i] = score_step(s, turned[w][m][turned_lane(lane)], q[m], m < kSteps / 2);
+        }
+        four[k] = (one[0] + one[1]) + (one[2] + one[3]);
+      }
+      s.score = four[0];
+      if constexpr (kSteps == 8) s.score = four[0] + four[1];
+      if constexpr (kSteps == 16) s.score = (four[0] + four[1]) + (four[2] + four[3]);
+      put_scores<1>(s, valid >> (16 * w), lane, mine ? part.keys + item * part.pitch + cb + w * kScoreTile : nullptr, most);
     }
-    if (mine) *(uint4 *)(out + cb + 4 * (lane >> 4)) = make_uint4(key[0], key[1], key[2], key[3]);
   }
   most = max(most, (uint32_t)__shfl_xor((int)most, 16, kWave));
   most = max(most, (uint32_t)__shfl_xor((int)most, 32, kWave));
   if (mine && lane < 16)
-    part.most[((long long)row * dm.Hkv + head) * part.chunks * kScoreWaves + chunk * kScoreWaves + wave] = most;
+    *(uint4 *)(part.most + (item * part.chunks + chunk) * kScoreWaves) = make_uint4(most, most, most, most);
 }
 
 // ---- selection
 
 constexpr int kSelectMostWaves = 16;
+constexpr uint32_t kTaken = 0xFFFFFFFFu;  // key of a page that is taken whatever the others are
 
 // Sum over the first 16 lanes (the others hold 0), wave-uniform.
 __device__ __forceinline__ int first16_sum(int v) {
@@ -399,13 +578,16 @@ struct ExactScore {
 };
 
 // One workgroup for a token and cache head. A page that is always taken has the
-// largest key, one that does not exist 0. The key of the last one taken is found 8
-// bits at a time, from the first bit on in which keys differ; pages whose scores
-// lie within their error of it are scored again in 64 bits: up to 64 of them are
-// ranked at once, for more the search is repeated. Each wavefront then lists what it takes of its own pages.
-// Bound by latency: three rounds of loads, then barriers. R: pages of a lane, their
-// keys and places held in registers, so that a workgroup of W wavefronts takes 64 R W
-// pages; 0: any number, read each time from the scores.
+// largest key, one that does not exist 0. The key of the last one taken, but for its
+// last 8 bits or fewer, is found 8 bits at a time from the first bit on in which keys
+// differ, with counts in LDS. Pages above those bits and their error are taken, those below are not, and if
+// that leaves a choice the ones between are scored again in 64 bits: up to 64 are
+// ranked at once, for more the search is repeated to the last bit. Then each wavefront
+// lists what it takes of its own pages.
+// Bound by latency (three rounds of loads, then barriers) for few lists, by vector
+// instructions for many. R: pages of a lane, their keys and places held in registers,
+// so that a workgroup of W wavefronts takes 64 R W pages; 0: any number, read each
+// time from the scores.
 template <int D, int R>
 __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4Dims dm, Kv4Batch bt, Kv4Select sel,
                                                                              ScorePart part, SelectOut out) {
@@ -414,7 +596,7 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
   __shared__ uint32_t found[2];
   __shared__ int listed, list_page[kWave], list_place[kWave];
   __shared__ uint32_t list_key[kWave];
-  __shared__ uint32_t shared[kSelectMostWaves][2];
+  __shared__ __attribute__((aligned(16))) uint4 shared[kSelectMostWaves];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
   const int r = blockIdx.x, tok = part.row0 + r, head = blockIdx.y, G = dm.Hq / dm.Hkv;
@@ -435,23 +617,10 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
   const int seg = R > 0 ? R * kWave : ((pages + waves - 1) / waves + kWave - 1) / kWave * kWave;
   const int begin = min(wave * seg, pages), end = min(begin + seg, pages);
 
-  if (threadIdx.x == 0) listed = 0;
-  if (sel.top > 0) {  // in case scores have to be worked out again
-    const uint16_t *q = sel.q + tok * sel.q_stride + (long long)head * G * D;
-    for (int i = threadIdx.x; i < G * (D / 8); i += blockDim.x) queries[i] = *(const uint4 *)(q + i * 8);
-  }
-  // the largest sum of magnitudes of the scored pages
-  uint32_t most = 0;
-  if (sel.top > 0 && sc.hi >= sc.lo) {
-    const int span = part.steps * kScoreWaves * kScoreTile;
-    const uint32_t *m = part.most + item * part.chunks * kScoreWaves;
-    for (int i = sc.lo / span * kScoreWaves + lane; i < (sc.hi / span + 1) * kScoreWaves; i += kWave)
-      most = max(most, m[i]);
-  }
   const auto first_key = [&](int c, int entry) -> uint32_t {
     if (c >= end) return 0u;
     if (c >= sc.lo && c <= sc.hi) return sel.top > 0 ? keys[c] : 0u;
-    return kv4_page_ok(dm, entry) ? 0xFFFFFFFFu : 0u;
+    return kv4_page_ok(dm, entry) ? kTaken : 0u;
   };
   uint32_t held[R > 0 ? R : 1];
   int place[R > 0 ? R : 1];
@@ -461,6 +630,18 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
       const int c = begin + i * kWave + lane;
       place[i] = c < end ? table[c] : -1;
       held[i] = first_key(c, place[i]);
+    }
+  }
+  uint32_t most = 0;  // the largest sum of magnitudes of the scored pages
+  if (sel.top > 0) {
+    // in case scores have to be worked out again
+    const uint16_t *q = sel.q + tok * sel.q_stride + (long long)head * G * D;
+    for (int i = threadIdx.x; i < G * (D / 8); i += blockDim.x) queries[i] = *(const uint4 *)(q + i * 8);
+    if (sc.hi >= sc.lo) {
+      const int span = part.steps * kScoreWaves * kScoreTile;
+      const uint32_t *m = part.most + item * part.chunks * kScoreWaves;
+      for (int i = sc.lo / span * kScoreWaves + lane; i < (sc.hi / span + 1) * kScoreWaves; i += kWave)
+        most = max(most, m[i]);
     }
   }
   // f(page, its place, key) for this wavefront's pages, 64 at a time; keys past its last are 0
@@ -476,107 +657,121 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
       }
     }
   };
-  // sums over the workgroup of two wave-uniform counts
-  const auto add_up = [&](int &a, int &b) {
-    __syncthreads();
-    if (lane == 0) shared[wave][0] = a, shared[wave][1] = b;
-    __syncthreads();
-    a = lane < waves ? shared[lane][0] : 0;
-    b = lane < waves ? shared[lane][1] : 0;
-    a = first16_sum(a);
-    b = first16_sum(b);
-  };
+  const auto count_of = [](bool b) { return (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(b)); };
 
-  int all = 0, always = 0;  // pages there are; those always taken
-  each([&](int, int, uint32_t k) {
-    all += __builtin_popcountll(__builtin_amdgcn_ballot_w64(k != 0));
-    always += __builtin_popcountll(__builtin_amdgcn_ballot_w64(k == 0xFFFFFFFFu));
-  });
-  add_up(all, always);
-  const int want = sel.top + always;
+  // pages there are, those always taken, and the range of the others' keys
+  int all = 0, certain = 0;
+  uint32_t hi = 0, lo = 0xFFFFFFFFu;
+  const auto range = [&]() {
+    all = certain = 0;
+    hi = 0;
+    lo = 0xFFFFFFFFu;
+    each([&](int, int, uint32_t k) {
+      all += count_of(k != 0);
+      certain += count_of(k == kTaken);
+      hi = max(hi, k == kTaken ? 0u : k);
+      lo = min(lo, k == 0 ? 0xFFFFFFFFu : k);
+    });
+    hi = wave_max_u32(hi);
+    lo = wave_max_u32(~lo);
+    __syncthreads();  // what was there has been read
+    if (lane == 0) shared[wave] = make_uint4(all, certain, hi, lo);
+    for (int i = threadIdx.x; i < 256; i += blockDim.x) hist[i] = 0;
+    if (threadIdx.x == 0) listed = 0;
+    __syncthreads();
+    const uint4 x = lane < waves ? shared[lane] : make_uint4(0, 0, 0, 0);
+    all = first16_sum((int)x.x);
+    certain = first16_sum((int)x.y);
+    hi = wave_max_u32(x.z);
+    lo = ~wave_max_u32(x.w);
+  };
+  range();
+  const int want = sel.top + certain;
 
   // taken: keys above `least`, and the first `ties` of those equal to it
   uint32_t least = 0;
   int ties = 0;
-  if (want == 0) {
-    least = 0xFFFFFFFFu;
-  } else if (all > want) {
-    int certain = always;  // keys 0xFFFFFFFF: taken whatever the others are
-    for (int exact = 0; exact < 2; ++exact) {
-      // of the others the (want - certain)-th largest
-      uint32_t hi = 0, lo = 0xFFFFFFFFu;
+  // The left-th largest key that is not kTaken: its `prefix` but for the last `rest` bits or
+  // fewer, and how many of the keys that share it are among the left largest.
+  uint32_t prefix;
+  int left, bits;
+  const auto search = [&](int rest) {
+    left = want - certain;
+    // one bit at least, which spares a choice that hipcc 7.2 compiles to a vector
+    // compare and a scalar select on another condition
+    bits = 32 - __builtin_clz((hi ^ lo) | 1u);
+    prefix = 0;  // of all keys up to that bit
+    bool first = true;
+    do {
+      const int take = min(bits, 8), shift = bits - take;
+      const uint32_t mask = (1u << take) - 1;
       each([&](int, int, uint32_t k) {
-        if (k != 0 && k != 0xFFFFFFFFu) hi = max(hi, k), lo = min(lo, k);
+        if (k - 1 < kTaken - 1 && (first || k >> bits == prefix)) atomicAdd(&hist[k >> shift & mask], 1u);
       });
-      hi = wave_max_u32(hi);
-      lo = ~wave_max_u32(~lo);
       __syncthreads();
-      if (lane == 0) shared[wave][0] = hi, shared[wave][1] = ~lo;
-      if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-      __syncthreads();
-      hi = wave_max_u32(lane < waves ? shared[lane][0] : 0u);
-      lo = ~wave_max_u32(lane < waves ? shared[lane][1] : 0u);
-      // bits not known yet: one at least, which spares a choice that hipcc 7.2 compiles
-      // to a vector compare and a scalar select on another condition
-      int left = want - certain, bits = 32 - __builtin_clz((hi ^ lo) | 1u);
-      uint64_t prefix = (uint64_t)hi >> bits;
-      while (true) {
-        const int take = min(bits, 8);
-        each([&](int, int, uint32_t k) {
-          if (k != 0 && k != 0xFFFFFFFFu && (uint64_t)k >> bits == prefix)
-            atomicAdd(&hist[k >> (bits - take) & ((1u << take) - 1)], 1u);
-        });
-        __syncthreads();
-        if (wave == 0) {
-          // lane l: digits 255 - 4 l down to 252 - 4 l
-          const uint4 x = *(const uint4 *)&hist[252 - 4 * lane];
-          const uint32_t h[4] = {x.w, x.z, x.y, x.x}, sum = x.x + x.y + x.z + x.w;
-          uint32_t before = (uint32_t)wave_scan((int)sum) - sum;
-          if (before < (uint32_t)left && before + sum >= (uint32_t)left) {
-            int i = 0;
+      if (wave == 0) {
+        // lane l: digits 255 - 4 l down to 252 - 4 l
+        const uint4 x = *(const uint4 *)&hist[252 - 4 * lane];
+        const uint32_t h[4] = {x.w, x.z, x.y, x.x}, sum = x.x + x.y + x.z + x.w;
+        uint32_t before = (uint32_t)wave_scan((int)sum) - sum;
+        if (before < (uint32_t)left && before + sum >= (uint32_t)left) {
+          int i = 0;
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-              if (i == k && before + h[k] < (uint32_t)left) before += h[k], ++i;
-            found[0] = 255 - 4 * lane - i;
-            found[1] = before;
-          }
-          *(uint4 *)&hist[252 - 4 * lane] = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 3; ++k)
+            if (i == k && before + h[k] < (uint32_t)left) before += h[k], ++i;
+          found[0] = 255 - 4 * lane - i;
+          found[1] = before;
         }
-        __syncthreads();
-        bits -= take;
-        prefix = prefix << take | __builtin_amdgcn_readfirstlane(found[0]);
-        left -= (int)__builtin_amdgcn_readfirstlane(found[1]);
-        if (bits == 0) break;
+        *(uint4 *)&hist[252 - 4 * lane] = make_uint4(0, 0, 0, 0);
       }
-      least = (uint32_t)prefix;
-      ties = left;
-      if (exact) break;
+      __syncthreads();
+      // the digits above the first one looked at are the largest key's
+      if (first) prefix = bits < 32 ? hi >> bits : 0u;
+      prefix = prefix << take | __builtin_amdgcn_readfirstlane(found[0]);
+      left -= (int)__builtin_amdgcn_readfirstlane(found[1]);
+      bits = shift;
+      first = false;
+    } while (bits > rest);
+  };
 
-      // scores that may be on the other side of the border
-      most = wave_max_u32(most);
-      const bool finite = most < 0x7F800000u;
-      const float off = 2.0f * (score_error(G) * __uint_as_float(most) + kScoreFlushed);
-      const float border = key_logit(least);
-      const float above = (border + off) * (1.0f + 0x1p-22f * (border + off > 0.f ? 1.f : -1.f));
-      const float below = (border - off) * (1.0f - 0x1p-22f * (border - off > 0.f ? 1.f : -1.f));
-      const auto surely = [&](uint32_t k) { return k == 0xFFFFFFFFu || (k != 0 && finite && key_logit(k) > above); };
-      const auto maybe = [&](uint32_t k) { return k != 0 && !surely(k) && !(finite && key_logit(k) < below); };
-      int near = 0;
-      certain = 0;
-      each([&](int, int, uint32_t k) {
-        certain += __builtin_popcountll(__builtin_amdgcn_ballot_w64(surely(k)));
-        near += __builtin_popcountll(__builtin_amdgcn_ballot_w64(maybe(k)));
-      });
-      add_up(certain, near);
-      if (finite && certain + near == want) break;  // all of those near it are taken: keys from least on
+  int more = 0, same = 0;  // of this wavefront: keys above least, and equal to it
+  bool counted = false;
+  if (want == 0) {
+    least = kTaken;
+  } else if (all > want) {
+    search(8);
+    most = wave_max_u32(most);
+    const float off = 2.0f * (score_error(G) * __uint_as_float(most) + kScoreFlushed);
+    // the keys of border + off and border - off, rounded away; all scored pages where sums are not finite
+    const float top = key_logit(prefix << bits | ((1u << bits) - 1)), bottom = key_logit(prefix << bits);
+    const float x = top + off, y = bottom - off;
+    uint32_t above = logit_key(x * (1.0f + (x > 0.f ? 0x1p-22f : -0x1p-22f)));
+    uint32_t below = logit_key(y * (1.0f - (y > 0.f ? 0x1p-22f : -0x1p-22f)));
+    if (most >= 0x7F800000u) above = kTaken - 1, below = 1;
+    int sure = 0, near = 0;
+    each([&](int, int, uint32_t k) {
+      sure += count_of(k > above);
+      near += count_of(k >= below && k <= above);
+    });
+    more = sure + near;
+    __syncthreads();
+    if (lane == 0) shared[wave] = make_uint4(sure, near, 0, 0);
+    __syncthreads();
+    const uint4 n = lane < waves ? shared[lane] : make_uint4(0, 0, 0, 0);
+    sure = first16_sum((int)n.x);
+    near = first16_sum((int)n.y);
+    if (sure + near == want) {
+      least = below - 1;
+      counted = true;
+    } else {
       ExactScore<D> score;
       uint32_t words[D / 64];
       if (near <= kWave) {
         each([&](int c, int entry, uint32_t k) {
-          if (maybe(k)) {
+          if (k >= below && k <= above) {
             const int i = atomicAdd(&listed, 1);
             list_page[i] = c;
-            list_place[i] = entry;
+            list_place[i] = entry;  // it has a key, so it exists
           }
         });
         __syncthreads();
@@ -597,51 +792,55 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
           const int c = __builtin_amdgcn_readlane(lc, i);
           rank += k > lk || (k == lk && c < lc);
         }
-        const uint64_t taken = __builtin_amdgcn_ballot_w64(lane < near && rank < want - certain);
+        const uint64_t taken = __builtin_amdgcn_ballot_w64(lane < near && rank < want - sure);
         each([&](int c, int, uint32_t &k) {
-          bool take = surely(k);
+          bool take = k > above;
           for (uint64_t todo = taken; todo != 0; todo &= todo - 1)
             take |= c == __builtin_amdgcn_readlane(lc, __builtin_ctzll(todo));
-          k = take ? 0xFFFFFFFFu : 0u;
+          k = take ? kTaken : 0u;
           if constexpr (R == 0) {
             if (c < end && c >= sc.lo && c <= sc.hi) keys[c] = k;
           }
         });
-        least = 0xFFFFFFFEu;
-        ties = 0;
-        break;
+      } else {
+        score.load((const uint16_t *)queries, G, lane);
+        each([&](int c, int entry, uint32_t &k) {
+          uint64_t todo = __builtin_amdgcn_ballot_w64(k >= below && k <= above);
+          k = k > above ? kTaken : 0u;
+          while (todo != 0) {
+            const int w = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            const int pg = __builtin_amdgcn_readlane(entry, w);
+            score.words(sel.bounds + ((long long)pg * dm.Hkv + head) * 2 * D + lane * (D / 32), words);
+            const uint32_t e = score.key(words);
+            k = lane == w ? e : k;
+          }
+          if constexpr (R == 0) {
+            if (c < end && c >= sc.lo && c <= sc.hi) keys[c] = k;
+          }
+        });
+        range();
+        search(0);
+        least = prefix;
+        ties = left;
       }
-      score.load((const uint16_t *)queries, G, lane);
-      each([&](int c, int entry, uint32_t &k) {
-        uint64_t todo = __builtin_amdgcn_ballot_w64(maybe(k));
-        k = surely(k) ? 0xFFFFFFFFu : 0u;
-        while (todo != 0) {
-          const int w = __builtin_ctzll(todo);
-          todo &= todo - 1;
-          const int pg = __builtin_amdgcn_readlane(entry, w);  // it has a key, so it exists
-          score.words(sel.bounds + ((long long)pg * dm.Hkv + head) * 2 * D + lane * (D / 32), words);
-          const uint32_t e = score.key(words);
-          k = lane == w ? e : k;
-        }
-        if constexpr (R == 0) {
-          if (c < end && c >= sc.lo && c <= sc.hi) keys[c] = k;
-        }
-      });
     }
   }
 
-  int more = 0, same = 0;
-  each([&](int, int, uint32_t k) {
-    more += __builtin_popcountll(__builtin_amdgcn_ballot_w64(k > least));
-    same += __builtin_popcountll(__builtin_amdgcn_ballot_w64(k != 0 && k == least));
-  });
-  __syncthreads();  // what was there has been read
-  if (lane == 0) shared[wave][0] = more, shared[wave][1] = same;
+  if (!counted) {
+    more = same = 0;
+    each([&](int, int, uint32_t k) {
+      more += count_of(k > least);
+      same += count_of(k != 0 && k == least);
+    });
+  }
   __syncthreads();
-  // of all wavefronts up to lane's: keys taken above least, and equal to it
-  more = lane < waves ? (int)shared[lane][0] : 0;
-  same = lane < waves ? (int)shared[lane][1] : 0;
-  const int seen_upto = wave_scan(same), at_upto = wave_scan(more + min(same, max(ties - (seen_upto - same), 0)));
+  if (lane == 0) shared[wave] = make_uint4(more, same, 0, 0);
+  __syncthreads();
+  // of all wavefronts up to lane's: keys equal to least, and taken
+  const uint4 n = lane < waves ? shared[lane] : make_uint4(0, 0, 0, 0);
+  const int seen_upto = wave_scan((int)n.y);
+  const int at_upto = wave_scan((int)n.x + min((int)n.y, max(ties - (seen_upto - (int)n.y), 0)));
   int seen = wave > 0 ? __builtin_amdgcn_readlane(seen_upto, wave > 0 ? wave - 1 : 0) : 0;  // ties before this one's
   int at = wave > 0 ? __builtin_amdgcn_readlane(at_upto, wave > 0 ? wave - 1 : 0) : 0;      // its first place
   const int total = __builtin_amdgcn_readlane(at_upto, kWave - 1);
@@ -677,11 +876,13 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
 // their lengths, and what the attention over them needs.
 struct SparseWs {
   int rows;  // of a part
-  int pitch, chunks, steps;  // of the scores
-  size_t keys, most, table, len, attention, bytes;
+  int pitch, chunks, steps, tiles;  // of the scores
+  bool prompt;
+  size_t keys, most, queries, table, len, attention, bytes;
 };
 
-constexpr size_t kKeysBytes = 256u << 20;  // score keys of a part, while it has more than one row
+// Score keys of a part, while it has more than one row; prompts' query operands have up to the same again.
+constexpr size_t kPartBytes = 256u << 20;
 
 static size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -696,27 +897,36 @@ static SparseWs sparse_ws(const Kv4Dims &dm, int T, const Kv4Select &sel) {
   SparseWs w;
   const int size = sel.top + sel.first + sel.recent;
   w.pitch = (dm.max_pages + kScoreTile - 1) / kScoreTile * kScoreTile;
-  // the queries are brought to LDS once for a workgroup's pages: few workgroups
-  // where there are enough of them for the card
-  const long long tiles = ((long long)sel.max_new + kScoreTile - 1) / kScoreTile;
+  // The prompt's kernels need 64 tokens a sequence and rows for its token tiles (us for
+  // the scores of 1500 tokens behind 60,000, D = 128: ... with, 39 without).
+  const size_t slot = (size_t)dm.Hkv * 3 * 2 * dm.D * 16 * 2;
+  w.prompt = sel.top > 0 && sel.max_new >= 64 && sel.max_new <= 1 << 20 && (long long)dm.B * 16 <= T &&
+             dm.B * slot <= kPartBytes / 2;
+  const int tokens = w.prompt ? kScoreWaves * kScoreTile : kScoreTile;
+  w.tiles = (int)(((long long)sel.max_new + tokens - 1) / tokens);
+  // a workgroup's tokens are brought to it once for all its pages: no more workgroups
+  // than the card holds at once (two a CU)
   const long long all = (w.pitch + kScoreWaves * kScoreTile - 1) / (kScoreWaves * kScoreTile);
-  long long steps = tiles * dm.B * dm.Hkv * all / 768;
-  if (steps > 16) steps = 16;
+  long long steps = ((long long)w.tiles * dm.B * dm.Hkv * all + 511) / 512;
+  if (!w.prompt && steps > 16) steps = 16;
+  if (steps > all) steps = all;
   if (steps < 1) steps = 1;
-  while (steps < all && tiles * ((all + steps - 1) / steps) >= 1 << 24) steps *= 2;
+  while (w.prompt && steps < all && w.tiles * ((all + steps - 1) / steps) >= 1 << 24) steps *= 2;  // a grid's x
   w.steps = (int)steps;
   w.chunks = (int)((all + steps - 1) / steps);
   const size_t row = (size_t)dm.Hkv * w.pitch * 4;
-  size_t rows = kKeysBytes / row;
+  size_t rows = kPartBytes / row;
   if (rows > 32768) rows = 32768;
+  if (w.prompt && rows > kPartBytes / 2 / (slot / 16)) rows = kPartBytes / 2 / (slot / 16);
   if (rows < 1) rows = 1;
   w.rows = rows < (size_t)T ? (int)rows : T;
-  const size_t full = kv4_attention_ws(selected_dims(dm, w.rows, size), w.rows, 1, 0);
+  const size_t full = kv4_attention_ws(selected_dims(dm, w.rows, size), w.rows, 1, 0, true);
   const int rest = T % w.rows;
-  const size_t last = rest ? kv4_attention_ws(selected_dims(dm, rest, size), rest, 1, 0) : 0;
+  const size_t last = rest ? kv4_attention_ws(selected_dims(dm, rest, size), rest, 1, 0, true) : 0;
   w.keys = 0;
   w.most = align256(w.keys + w.rows * row);
-  w.table = align256(w.most + (size_t)w.rows * dm.Hkv * w.chunks * kScoreWaves * 4);
+  w.queries = align256(w.most + (size_t)w.rows * dm.Hkv * w.chunks * kScoreWaves * 4);
+  w.table = align256(w.queries + (w.prompt ? slot * (w.rows / 16 + 4 + dm.B) : 0));
   w.len = align256(w.table + (size_t)w.rows * dm.Hkv * size * 4);
   w.attention = align256(w.len + (size_t)w.rows * 4);
   w.bytes = w.attention + (full > last ? full : last);
@@ -726,13 +936,28 @@ static SparseWs sparse_ws(const Kv4Dims &dm, int T, const Kv4Select &sel) {
 size_t kv4_sparse_ws(const Kv4Dims &dm, int T, const Kv4Select &sel) { return sparse_ws(dm, T, sel).bytes; }
 
 template <int D>
+static hipError_t launch_score(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Select &sel, const ScorePart &part,
+                               hipStream_t s) {
+  if (part.queries == nullptr) {
+    const long long z = (long long)part.tiles * part.chunks;
+    kv4_score_kernel<D><<<dim3(dm.B, dm.Hkv, z < 65535 ? (unsigned)z : 65535), kScoreWaves * kWave, 0, s>>>(dm, bt, sel,
+                                                                                                            part);
+    return hipGetLastError();
+  }
+  const int tiles = (sel.max_new + kScoreTile - 1) / kScoreTile;
+  kv4_query_kernel<D><<<dim3(tiles, dm.Hkv, dm.B), 1024, 0, s>>>(dm, bt, sel, part);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  kv4_score_prompt_kernel<D><<<dim3(part.tiles * part.chunks, dm.Hkv, dm.B), kScoreWaves * kWave, 0, s>>>(dm, bt, sel,
+                                                                                                          part);
+  return hipGetLastError();
+}
+
+template <int D>
 static hipError_t launch_selection(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Select &sel, const ScorePart &part,
                                    const SelectOut &so, hipStream_t s) {
-  const long long tiles = ((long long)sel.max_new + kScoreTile - 1) / kScoreTile;
   if (sel.top > 0) {
-    kv4_score_kernel<D><<<dim3((unsigned)(tiles * part.chunks), dm.Hkv, dm.B), kScoreWaves * kWave, 0, s>>>(dm, bt, sel,
-                                                                                                            part);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_score<D>(dm, bt, sel, part, s);
     if (e != hipSuccess) return e;
   }
   // Few lists: two pages a lane of as many wavefronts as that takes, for the shortest
@@ -757,7 +982,8 @@ hipError_t launch_kv4_sparse(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pla
   const SelectOut so{(int32_t *)((char *)ws + w.table), (int32_t *)((char *)ws + w.len), size};
   for (int row0 = 0; row0 < bt.T; row0 += w.rows) {
     const ScorePart part{(uint32_t *)((char *)ws + w.keys), (uint32_t *)((char *)ws + w.most), row0,
-                         bt.T - row0 < w.rows ? bt.T - row0 : w.rows, w.pitch, w.chunks, w.steps};
+                         bt.T - row0 < w.rows ? bt.T - row0 : w.rows, w.pitch, w.chunks, w.steps, w.tiles,
+                         w.prompt ? (char *)ws + w.queries : nullptr};
     hipError_t e = dm.D == 64    ? launch_selection<64>(dm, bt, sel, part, so, s)
                    : dm.D == 128 ? launch_selection<128>(dm, bt, sel, part, so, s)
                                  : launch_selection<256>(dm, bt, sel, part, so, s);
