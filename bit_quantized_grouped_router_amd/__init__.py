@@ -784,11 +784,15 @@ def moe_kv4_attention(cache: KV4Cache, q: torch.Tensor, page_table, cu, kv_len, 
 DTYPES8 = {torch.float8_e4m3fn: 2, torch.int8: 3}
 
 
-def _here(cur: int, tensors: Dict[str, Optional[torch.Tensor]]) -> None:
+def _here(cur: int, names, tensors) -> None:
     """Raise unless every tensor there is lives on device cur, the current one."""
-    for t in tensors.values():
+    for t in tensors:
         if t is not None and t.get_device() != cur:
-            _wrong_device(**tensors)
+            _wrong_device(**dict(zip(names, tensors)))
+
+
+_NORM_TENSORS = ("x", "weight", "residual", "h", "y", "scales")
+_ROPE_TENSORS = ("x", "freqs", "positions", "weight", "out")
 
 
 def _row_stride(t: torch.Tensor, shape, name: str, dtypes) -> int:
@@ -805,12 +809,12 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     scales [T, d / group], group being 64, 128 or 0 for whole rows. With a residual the sum,
     in its type, is stored to h (the residual itself: in place). Returns y, then scales, then
     h, where there are such."""
-    if x.dim() != 2:
-        raise MoeError("x must be [T, d]")
+    if x.dim() != 2 or x.shape[1] == 0:
+        raise MoeError("x must be [T, d], d at least 1")
     T, d = x.shape
     shape = (T, d)
     cur = torch.cuda.current_device()
-    _here(cur, dict(x=x, weight=weight, residual=residual, h=h, y=y, scales=scales))
+    _here(cur, _NORM_TENSORS, (x, weight, residual, h, y, scales))
     dtype = out_dtype if out_dtype is not None else y.dtype if y is not None else torch.bfloat16
     eight = dtype in DTYPES8
     code = DTYPES8[dtype] if eight else _dtype(dtype)
@@ -915,7 +919,7 @@ def moe_rope(x: torch.Tensor, rope: Rope, positions: torch.Tensor, weight=None, 
         raise MoeError("x must be [T, H, D]")
     T, H, D = x.shape
     cur = torch.cuda.current_device()
-    _here(cur, dict(x=x, freqs=rope.freqs, positions=positions, weight=weight, out=out))
+    _here(cur, _ROPE_TENSORS, (x, rope.freqs, positions, weight, out))
     if positions.shape != (T,) or positions.dtype != torch.int32:
         raise MoeError(f"positions are {positions.dtype} {tuple(positions.shape)}; expected int32 {(T,)}")
     dtype = out_dtype if out_dtype is not None else out.dtype if out is not None else x.dtype

@@ -30,21 +30,22 @@ namespace moe {
 
 constexpr int kBoundWaves = 4;
 
-// Pages of new tokens: one wavefront looks at `run` token rows, and for each that
-// is the first of the call in its page it goes over the page's keys, up to the
-// sequence's last. D / 8 lanes take a key, 8 channels each.
+// Pages of new tokens: a workgroup looks at `run` token rows (a lane each, every
+// wavefront all of them), and for each that is the first of the call in its page it
+// goes over the page's keys, up to the sequence's last. D / 8 lanes take a key, 8
+// channels each, and 64 keys are loaded at once. Bound by a chain of four loads
+// (offsets, page, codes, and the sums' way through LDS).
 template <int D>
 __global__ __launch_bounds__(kBoundWaves *kWave) void kv4_bounds_kernel(Kv4Dims dm, Kv4Plane kc, Kv4Batch bt,
                                                                         uint16_t *__restrict__ bounds, int run) {
-  constexpr int kLanes = D / 8, kKeys = kWave / kLanes;
+  constexpr int kLanes = D / 8, kKeys = kWave / kLanes, kLoads = 64 / (kBoundWaves * kKeys);
+  __shared__ float part[kBoundWaves][2][D];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const long long r0 = ((long long)blockIdx.x * kBoundWaves + wave) * run;
-  if (r0 >= bt.T) return;
+  const long long row = (long long)blockIdx.x * run + lane;
   const int head = blockIdx.y;
-  // this lane's row: the last sequence that begins at or before it
+  // the last sequence that begins at or before this lane's row
   int page = -1, keys = 0;
-  const long long row = r0 + lane;
   if (lane < run && row < bt.T) {
     int lo = 0, hi = dm.B;
     while (hi - lo > 1) {
@@ -63,51 +64,42 @@ __global__ __launch_bounds__(kBoundWaves *kWave) void kv4_bounds_kernel(Kv4Dims 
       }
     }
   }
-  uint64_t todo = __builtin_amdgcn_ballot_w64(page >= 0);
-  while (todo != 0) {
+  const int at = (lane % kLanes) * 8;
+  for (uint64_t todo = __builtin_amdgcn_ballot_w64(page >= 0); todo != 0; todo &= todo - 1) {
     const int w = __builtin_ctzll(todo);
-    todo &= todo - 1;
     const int pg = __builtin_amdgcn_readlane(page, w), n = __builtin_amdgcn_readlane(keys, w);
     const long long base = kv4_row(dm, pg, head, 0);
     float mn[8], mx[8];
-    bool bad = false;
+    uint32_t nan = 0;  // channels that hold one
 #pragma unroll
     for (int i = 0; i < 8; ++i) mn[i] = __builtin_huge_valf(), mx[i] = kNegInf;
-    const int at = (lane % kLanes) * 8;
-    for (int k0 = 0; k0 < n; k0 += 4 * kKeys) {
-      uint32_t word[4], sb[4];
+    for (int k0 = 0; k0 < n; k0 += 64) {
+      uint32_t word[kLoads], sb[kLoads];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kLoads; ++u) {
         // keys past the last repeat it
-        const long long r = base + min(k0 + u * kKeys + lane / kLanes, n - 1);
+        const long long r = base + min(k0 + (u * kBoundWaves + wave) * kKeys + lane / kLanes, n - 1);
         word[u] = *(const uint32_t *)(kc.codes + r * (D / 2) + at / 2);
         const long long g = r * (D / kGroup) + at / kGroup;
         sb[u] = kc.scales[g] | (uint32_t)kc.biases[g] << 16;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kLoads; ++u) {
         const float s = __uint_as_float(sb[u] << 16), b = __uint_as_float(sb[u] & 0xFFFF0000u);
+        float any = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = fmaf(s, (float)((word[u] >> (4 * i)) & 15u), b);
           mn[i] = fminf(mn[i], v);
           mx[i] = fmaxf(mx[i], v);
-          bad |= v != v;
+          any = fmaf(v, 0.f, any);
         }
-      }
-    }
-    // a channel that holds a NaN has NaN bounds; the lane looks again at which
-    uint32_t nan = 0;
-    if (__builtin_amdgcn_ballot_w64(bad) != 0) {
-      for (int k = lane / kLanes; k < n; k += kKeys) {
-        const long long r = base + k;
-        const uint32_t word = *(const uint32_t *)(kc.codes + r * (D / 2) + at / 2);
-        const long long g = r * (D / kGroup) + at / kGroup;
-        const float s = bf16_to_f32(kc.scales[g]), b = bf16_to_f32(kc.biases[g]);
+        if (any != any) {  // an infinity or a NaN
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = fmaf(s, (float)((word >> (4 * i)) & 15u), b);
-          nan |= (uint32_t)(v != v) << i;
+          for (int i = 0; i < 8; ++i) {
+            const float v = fmaf(s, (float)((word[u] >> (4 * i)) & 15u), b);
+            nan |= (uint32_t)(v != v) << i;
+          }
         }
       }
     }
@@ -122,15 +114,34 @@ __global__ __launch_bounds__(kBoundWaves *kWave) void kv4_bounds_kernel(Kv4Dims 
     }
     if (lane < kLanes) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (nan >> i & 1) mn[i] = mx[i] = __uint_as_float(0x7FC00000u);
-      uint16_t *o = bounds + ((long long)pg * dm.Hkv + head) * 2 * D + at;
-      // adding 0 makes a zero +0
-      *(uint4 *)o = make_uint4(pack_bf16x2(mn[0] + 0.f, mn[1] + 0.f), pack_bf16x2(mn[2] + 0.f, mn[3] + 0.f),
-                               pack_bf16x2(mn[4] + 0.f, mn[5] + 0.f), pack_bf16x2(mn[6] + 0.f, mn[7] + 0.f));
-      *(uint4 *)(o + D) = make_uint4(pack_bf16x2(mx[0] + 0.f, mx[1] + 0.f), pack_bf16x2(mx[2] + 0.f, mx[3] + 0.f),
-                                     pack_bf16x2(mx[4] + 0.f, mx[5] + 0.f), pack_bf16x2(mx[6] + 0.f, mx[7] + 0.f));
+      for (int i = 0; i < 8; ++i) {
+        part[wave][0][at + i] = nan >> i & 1 ? __uint_as_float(0x7FC00000u) : mn[i];
+        part[wave][1][at + i] = mx[i];
+      }
     }
+    __syncthreads();
+    uint16_t *out = bounds + ((long long)pg * dm.Hkv + head) * 2 * D;
+    for (int c = threadIdx.x; c < D / 2; c += kBoundWaves * kWave) {
+      float lo[2], hi[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        lo[e] = __builtin_huge_valf(), hi[e] = kNegInf;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kBoundWaves; ++i) {
+          const float v = part[i][0][2 * c + e];
+          bad |= v != v;
+          lo[e] = fminf(lo[e], v);
+          hi[e] = fmaxf(hi[e], part[i][1][2 * c + e]);
+        }
+        // adding 0 makes a zero +0
+        lo[e] = bad ? __uint_as_float(0x7FC00000u) : lo[e] + 0.f;
+        hi[e] = bad ? __uint_as_float(0x7FC00000u) : hi[e] + 0.f;
+      }
+      *(uint32_t *)(out + 2 * c) = pack_bf16x2(lo[0], lo[1]);
+      *(uint32_t *)(out + D + 2 * c) = pack_bf16x2(hi[0], hi[1]);
+    }
+    __syncthreads();
   }
 }
 
@@ -999,11 +1010,10 @@ hipError_t launch_kv4_sparse(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pla
 
 hipError_t launch_kv4_bounds(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Batch &bt, uint16_t *bounds,
                              hipStream_t s) {
-  // rows a wavefront looks at: one while that many wavefronts fit the card
+  // rows a workgroup looks at: one while the card holds that many workgroups
   int run = 1;
-  while (run < kWave && (long long)bt.T * dm.Hkv / run > 8192) run *= 2;
-  const long long per = (long long)run * kBoundWaves;
-  const dim3 grid((unsigned)((bt.T + per - 1) / per), dm.Hkv);
+  while (run < kWave && (long long)bt.T * dm.Hkv / run > 2048) run *= 2;
+  const dim3 grid((unsigned)(((long long)bt.T + run - 1) / run), dm.Hkv);
   auto *kernel = dm.D == 64 ? kv4_bounds_kernel<64> : dm.D == 128 ? kv4_bounds_kernel<128> : kv4_bounds_kernel<256>;
   kernel<<<grid, kBoundWaves * kWave, 0, s>>>(dm, kc, bt, bounds, run);
   return hipGetLastError();

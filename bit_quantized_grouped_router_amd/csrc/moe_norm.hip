@@ -105,12 +105,25 @@ __device__ __forceinline__ float group_scale(uint32_t top, float largest) {
   return top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / largest;
 }
 
-// Eight values over their scale, rounded; zeros where that is 0 or NaN.
+// Eight values over their scale, rounded; zeros where that is 0 or NaN. With the
+// rounded reciprocal and one step of the remainder a quotient is the rounded one, in
+// three operations instead of a division's ten, while nothing under- or overflows.
 __device__ __forceinline__ uint2 to_8bit(const float (&y)[8], float scale, bool e4m3) {
   const float largest = e4m3 ? 448.f : 127.f;
   float t[8];
+  if (scale >= 0x1p-60f && scale <= 0x1p60f) {
+    const float inv = 1.0f / scale;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = scale > 0.f ? fminf(fmaxf(y[i] / scale, -largest), largest) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      const float q = y[i] * inv;
+      t[i] = fmaf(fmaf(-q, scale, y[i]), inv, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = scale > 0.f ? y[i] / scale : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = fminf(fmaxf(t[i], -largest), largest);
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -248,11 +261,12 @@ static hipError_t launch_norm(const NormArgs &a, hipStream_t s) {
 template <bool X32, int RK>
 static hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
   const int chunks = (a.d + 7) / 8;
+  // 256 threads a row rather than a wavefront with four times the steps: 8192 x 2048 in
+  // fp32 with an fp32 residual, 42 us and 52
   if (chunks <= 64) return launch_norm<64, 1, X32, RK>(a, s);
-  if (chunks <= 256 && a.T > 2048)
-    return chunks <= 128 ? launch_norm<64, 2, X32, RK>(a, s) : launch_norm<64, 4, X32, RK>(a, s);
   if (chunks <= 256) return launch_norm<256, 1, X32, RK>(a, s);
   if (chunks <= 512) return launch_norm<256, 2, X32, RK>(a, s);
+  if (chunks <= 768) return launch_norm<256, 3, X32, RK>(a, s);
   if (chunks <= 1024) return launch_norm<256, 4, X32, RK>(a, s);
   return launch_norm<1024, 4, X32, RK>(a, s);
 }
