@@ -57,8 +57,7 @@ __device__ __forceinline__ void sincos_turns(double t, double &sn, double &cs) {
   s = fma(s, y, -1.0 / 6.0), c = fma(c, y, 1.0 / 24.0);
   c = fma(c, y, -0.5);
   s = fma(s * y, x, x), c = fma(c, y, 1.0);
-  // of the quarters only those left after whole turns count (below 2^31 turns)
-  const int q = (int)(long long)quarter & 3;
+  const int q = (int)(quarter - 4.0 * floor(0.25 * quarter));  // the quarters left after whole turns
   sn = q & 1 ? c : s;
   cs = q & 1 ? s : c;
   sn = q & 2 ? -sn : sn;

@@ -261,3 +261,43 @@ def test_oracle_bounds():
     assert (b[0] == [[1, 0], [2, 0]]).all() and not np.signbit(b[0]).any()
     assert np.isnan(b[1, :, 0]).all() and (b[1, :, 1] == [5, 7]).all()
     assert (B.bounds(v, 3)[1] == [[-3, 5], [-3, 5]]).all() and (B.bounds(v, 2)[1] == 0).all()
+
+
+def test_index_arithmetic_on_hostile_positions(tmp_path):
+    """kv4_scored and the spans of rows, compiled for the host: what is scored lies before the token's
+    own page and inside the table, whatever the position."""
+    src, so = tmp_path / "scored.cpp", tmp_path / "scored.so"
+    src.write_text('''
+#include "moe_kv4_sparse.h"
+using namespace moe;
+extern "C" void scored(int page_shift, int max_pages, long long pos, int first, int recent, int *out) {
+  Kv4Dims dm{1, 1, 1, 64, 1 << page_shift, page_shift, 1, max_pages};
+  const Kv4Scored s = kv4_scored(dm, pos, first, recent);
+  out[0] = s.lo, out[1] = s.hi, out[2] = s.own;
+}
+extern "C" void row_span(int row, int len, long long *out) {
+  const Kv4Span s = kv4_row_span(row, len);
+  out[0] = s.begin, out[1] = s.n, out[2] = s.first, out[3] = s.len;
+}
+''')
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    import subprocess
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=undefined",
+                    "-static-libubsan", "-shared", "-fPIC", "-I",
+                    os.path.join(root, "bit_quantized_grouped_router_amd", "csrc"), str(src), "-o", str(so)], check=True)
+    h = ctypes.CDLL(str(so))
+    h.scored.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
+    out = (ctypes.c_int * 3)()
+    for shift, pages in ((4, 1), (4, 100), (16, 32767), (10, 1 << 20)):
+        cap = pages << shift
+        for pos in (-2 ** 31, -1, 0, 1, (1 << shift) - 1, 1 << shift, cap - 1, cap, cap + 1, 2 ** 31 - 1):
+            for first in (0, 1, 3, 4095):
+                for recent in (1, 2, 4096):
+                    h.scored(shift, pages, pos, first, recent, out)
+                    lo, hi, own = out
+                    assert own == (-1 if pos < 0 else min(pos, cap - 1) >> shift)
+                    assert lo == first and hi == own - recent and hi < own < pages
+    span = (ctypes.c_longlong * 4)()
+    for row, n in ((0, -1), (5, -2 ** 31), (7, 0), (9, 12)):
+        h.row_span(row, n, span)
+        assert list(span) == ([row, 0, 0, 0] if n < 0 else [row, 1, n - 1, n])

@@ -314,3 +314,48 @@ def test_rope_append_refusals():
         with pytest.raises(M.MoeError):
             M.moe_kv4_rope_append(**{**ok, **bad})
     M.moe_kv4_rope_append(**ok)
+
+
+def test_far_rows():
+    """Rows so far apart that their offsets pass 32 bits: the norm and the rotation."""
+    wide = torch.empty((1030, 1 << 22), dtype=BF16, device="cuda")
+    x = torch.randn((1030, 64), device="cuda").to(BF16)
+    wide[:, :64] = x
+    w = torch.ones(64, dtype=BF16, device="cuda")
+    assert torch.equal(M.moe_rmsnorm(wide[:, :64], w), M.moe_rmsnorm(x, w))
+    pos, r = i32(np.arange(1030)), M.Rope.make(32)
+    heads = wide[:, :64].unflatten(1, (2, 32))
+    want = M.moe_rope(x.view(1030, 2, 32), r, pos)
+    assert torch.equal(M.moe_rope(heads, r, pos), want)
+    M.moe_rope(heads, r, pos, out=heads)
+    assert torch.equal(heads, want)
+
+
+def test_rope_against_differences():
+    """A score of two turned vectors depends on their distance alone, near and far."""
+    rng = np.random.default_rng(3)
+    _, x = values(rng, (2, 1, 128), F32)
+    for inter in (False, True):
+        r = M.Rope.make(128, interleaved=inter)
+        dots = []
+        for p in (0, 1000, 130000, 1 << 24):
+            y = M.moe_rope(x, r, i32([p + 77, p]))
+            dots.append(float((y[0].double() * y[1].double()).sum()))
+        # the frequencies' products with positions are exact, so the angles' distance is
+        assert max(abs(d - dots[0]) for d in dots) <= 128 * 8 * 5 * U * 4
+
+
+def test_stream_argument():
+    """Work on a stream given as argument, outputs and workspaces allocated for it."""
+    s = torch.cuda.Stream()
+    x, w = torch.randn((4096, 2048), device="cuda"), torch.ones(2048, dtype=BF16, device="cuda")
+    want = M.moe_rmsnorm(x, w, residual=x)
+    heads = x.view(4096, 16, 128)
+    pos, r = i32(np.arange(4096)), M.Rope.make(128)
+    turned = M.moe_rope(heads, r, pos)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a = M.moe_rmsnorm(x, w, residual=x, stream=s)
+        b = M.moe_rope(heads, r, pos, stream=s)
+        s.synchronize()
+        assert torch.equal(a[0], want[0]) and torch.equal(a[1], want[1]) and torch.equal(b, turned)

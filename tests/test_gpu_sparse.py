@@ -348,3 +348,105 @@ def test_refusals():
     with pytest.raises(M.MoeError):
         M.moe_kv4_bounds(c, bounds, *b.dev, -1)
     assert M.moe_kv4_sparse_attention(**{**ok, "q": q[:0], "cu": i(2)}).shape == (0, 2, 64)
+
+
+MORE = [  # prompts and rows of several kinds: new, earlier, Hq, Hkv, D, page, top, first, recent
+    ([100], [5000], 8, 2, 256, 32, 6, 1, 2),
+    ([64], [3000], 5, 1, 128, 16, 9, 0, 1),
+    ([80] + [1] * 69, [900] + list(range(10, 1390, 20)), 4, 2, 64, 16, 3, 1, 1),   # many sequences, one of them a prompt
+    ([150, 0, 65, 1], [0, 40, 2000, 700], 64, 1, 64, 16, 4, 2, 1),
+    ([300], [0], 4, 4, 128, 16, 5, 1, 1),
+]
+
+
+@pytest.mark.parametrize("new,past,Hq,Hkv,D,page,top,first,recent", MORE)
+def test_sparse_prompts(new, past, Hq, Hkv, D, page, top, first, recent):
+    test_sparse_attention(new, past, Hq, Hkv, D, page, top, first, recent)
+
+
+@pytest.mark.parametrize("W", [3000, 9000])
+def test_ties_in_long_tables(W):
+    """Lists from tables whose keys are held eight a lane, or not held: the border inside ties of more
+    and of fewer pages than are ranked at once."""
+    rng = np.random.default_rng(W)
+    b = Batch(rng, [1], [W * 16 - 1], 16)
+    c = filled(rng, b, 1, 64)
+    level = np.where(rng.random(W) < 0.01, 3, rng.integers(0, 3, W))
+    bounds = torch.zeros((c.num_pages, 1, 2, 64), dtype=BF16, device="cuda")
+    bounds[b.dev[0][0, :W].long()] = torch.from_numpy(level).cuda().to(BF16)[:, None, None, None]
+    q = torch.ones((1, 2, 64), dtype=BF16, device="cuda")
+    many = int((level[1:-1] == 3).sum())
+    for top in (1, many - 1, many, many + 1, many + 300):
+        blocks = torch.empty((1, 1, top + 2), dtype=torch.int32, device="cuda")
+        M.moe_kv4_sparse_attention(c, bounds, q, *b.dev, 1, top, blocks=blocks)
+        order = sorted(range(1, W - 1), key=lambda i: (-level[i], i))[:top]
+        assert blocks[0, 0].tolist() == sorted([0, W - 1] + order), top
+
+
+@pytest.mark.parametrize("new", [[3], [70]])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 66, 2.0 ** -100, 2.0 ** 120])
+def test_queries_of_any_size(scale, new):
+    """Queries outside the range that the fast scores are bounded for, zeros, infinities and NaN: the
+    pages are still those of the scores in 64 bits, and other tokens' do not change."""
+    rng = np.random.default_rng(31)
+    b = Batch(rng, new, [1500], 16)
+    c = filled(rng, b, 2, 128)
+    bounds = all_bounds(c, b)
+    q64, q = queries(rng, b.T, 6, 128)
+    q64, q = q64 * scale, q * scale
+    q64[1, :, :64] = 0
+    q[1, :, :64] = 0
+    blocks = torch.empty((b.T, 2, 12), dtype=torch.int32, device="cuda")
+    out = M.moe_kv4_sparse_attention(c, bounds, q, *b.dev, b.T, 10, blocks=blocks)
+    with np.errstate(over="ignore", invalid="ignore"):
+        bb = bf16_to_f64(host_bits(bounds))
+        for t in range(b.T):
+            for h in range(2):
+                p = B.select(q64[t, 3 * h:3 * h + 3], bb[b.table[0], h, 0], bb[b.table[0], h, 1],
+                             np.ones(b.table.shape[1], bool), 1500 + t, 16, 10, 1, 1)
+                assert blocks[t, h].tolist() == p.tolist() + [-1] * (12 - len(p)), (t, h)
+    q[0, 0, 5], q[2, 3, 7] = float("nan"), float("inf")
+    more = torch.empty_like(blocks)
+    again = M.moe_kv4_sparse_attention(c, bounds, q, *b.dev, b.T, 10, blocks=more)
+    rest = [t for t in range(b.T) if t not in (0, 2)]
+    assert torch.equal(again[rest].nan_to_num(7.0), out[rest].nan_to_num(7.0)) and torch.equal(more[rest], blocks[rest])
+    # a NaN query's scores are all NaN: its pages are the first ones
+    assert more[0, 0].tolist() == list(range(11)) + [(b.len[0] - b.T) // 16]
+    assert torch.equal(more[0, 1], blocks[0, 1]) and torch.equal(more[2, 0], blocks[2, 0])
+
+
+def test_far_pages():
+    """Cache offsets past 2^32: the write, the bounds and attention on the last pages of a large cache,
+    against a small one."""
+    rng = np.random.default_rng(33)
+    n, Hkv, page, D = 70000, 8, 64, 256
+    big, small = M.KV4Cache.empty(n, Hkv, page, D), M.KV4Cache.empty(9, Hkv, page, D)
+    assert big.k.codes.numel() > 2 ** 32
+    bb = torch.empty((n, Hkv, 2, D), dtype=BF16, device="cuda")
+    bs = torch.empty((9, Hkv, 2, D), dtype=BF16, device="cuda")
+    T = 500
+    _, x = queries(rng, T, 3 * Hkv, D)
+    order = rng.permutation(9)[:8]
+    rope = M.Rope.make(128)
+    outs = []
+    for cache, bounds, table in ((big, bb, n - 1 - order), (small, bs, order)):
+        batch = (i32(table[None]), i32([0, T]), i32([T]))
+        q = M.moe_kv4_rope_append(cache, x[:, :Hkv], x[:, Hkv:2 * Hkv], x[:, 2 * Hkv:], rope, *batch)
+        M.moe_kv4_bounds(cache, bounds, *batch, T)
+        outs.append((q, M.moe_kv4_sparse_attention(cache, bounds, q, *batch, T, 2), bounds[i32(table).long()],
+                     *M.moe_kv4_read(cache, *batch, T)))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_bounds_follow_a_rejected_draft():
+    """A sequence cut back and refilled: its pages' bounds are those of the tokens it has now."""
+    rng = np.random.default_rng(34)
+    b = Batch(rng, [5], [30], 16)
+    c = filled(rng, b, 1, 64)
+    got = all_bounds(c, b)
+    x = torch.from_numpy(100 * rng.standard_normal((2, 1, 64))).cuda().to(BF16)
+    M.moe_kv4_append(c, x, x, b.dev[0], i32([0, 2]), i32([33]))  # tokens 31 and 32 anew, 33 and 34 gone
+    M.moe_kv4_bounds(c, got, b.dev[0], i32([0, 2]), i32([33]), 2)
+    keys = whole(c)
+    want = B.bounds(keys[b.table[0, :3], 0], 33)
+    assert (host_bits(got)[b.table[0, :3], 0] == round_to_bf16_bits(want)).all()
