@@ -33,7 +33,9 @@
 // (offsets, pages, codes) for few short ones. us, one new token a sequence, 16
 // heads on 2: 64 sequences of up to 8101, D = 256 (113 MB) 33.2 and 5.4 for the
 // join, 3.4 TB/s; one of 131,150, D = 128 (38 MB) 16.9 and 6.8; one of 500, D =
-// 256 11.7.
+// 256 11.7. 3000 lists of 1024 keys of their own, 8 heads, D = 128: 75.6 (90.1 with
+// half the columns empty), 90% of it vector instructions: the codes' conversion is 128
+// of 214 a tile, and a workgroup's start and end cost as much as three tiles.
 #include "moe_kv4_device.h"
 #include "moe_lds.h"
 
@@ -79,32 +81,29 @@ __device__ __forceinline__ float sum_bf16x2(uint32_t w, float a) {
 // the first group for NG = 1.
 template <int NG>
 __device__ __forceinline__ bf16x8_t affine_query(const float (&qsum)[NG], int group) {
-  uint16_t v[6][NG];
+  float v[6 * NG];  // [slot][g]
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     float rest = qsum[g];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      v[i][g] = to_bf16(rest);
-      const float part = bf16_to_f32(v[i][g]);
-      v[3 + i][g] = to_bf16(-16.0f * part);
+      const float part = bf16_to_f32(to_bf16(rest));
+      v[i * NG + g] = part;
+      v[(3 + i) * NG + g] = -16.0f * part;
       rest -= part;
     }
   }
-  constexpr int kPer = 8 / NG;  // slots of NG values a lane group
-  uint16_t e[8];
+  uint32_t e[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint16_t x = 0;
+  for (int i = 0; i < 4; ++i) {
+    e[i] = 0;
 #pragma unroll
     for (int lg = 0; lg < 4; ++lg) {
-      const int slot = lg * kPer + i / NG;
-      if (slot < 6) x = group == lg ? v[slot][i % NG] : x;
+      const int at = lg * 8 + i * 2;
+      if (at < 6 * NG) e[i] = group == lg ? pack_bf16x2(v[at], v[at + 1]) : e[i];
     }
-    e[i] = x;
   }
-  return __builtin_bit_cast(bf16x8_t, make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                                                 e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16));
+  return __builtin_bit_cast(bf16x8_t, make_uint4(e[0], e[1], e[2], e[3]));
 }
 
 // Sum and maximum over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
@@ -191,7 +190,7 @@ struct LaneParts {
   uint32_t affine0, affine1;   // and of what affine_keys reads
 };
 
-template <int D>
+template <int D, bool HALF>
 __device__ __forceinline__ LaneParts<D> lane_parts(const Kv4Plane &kc, const Kv4Plane &vc, int lane) {
   using R = Ring<D>;
   constexpr int NG = R::NG, kChunks = R::kRow / 16;
@@ -203,10 +202,11 @@ __device__ __forceinline__ LaneParts<D> lane_parts(const Kv4Plane &kc, const Kv4
            (lane % (2 * NG)) * 8;
   p.key = (lane & 15) * R::kRow + (lane >> 4) * 8 + (((lane >> 2) & (NG - 1)) << 5);
   // lane k % 8 of a lane group supplies the row of the group's k-th key (4 of
-  // the first half, 4 of the second), lanes 8 .. 15 the next 16 channels
-  p.value = R::kCodes + (4 * (lane >> 4) + (lane & 3) + 4 * (lane & 4)) * R::kRow + (lane & 8) +
-            (((lane >> 4) & (NG - 1)) << 5);
-  p.scale = 2 * R::kCodes + (lane >> 4) * 4 * NG * 2;
+  // the first half, 4 of the second), lanes 8 .. 15 the next 16 channels; HALF: in
+  // the order in which codes8 puts the halves one behind the other
+  const int of = HALF ? 2 * (lane & 1) + (lane >> 2 & 1) + 8 * (lane & 2) : (lane & 3) + 4 * (lane & 4);
+  p.value = R::kCodes + (4 * (lane >> 4) + of) * R::kRow + (lane & 8) + (((lane >> 4) & (NG - 1)) << 5);
+  p.scale = 2 * R::kCodes + (lane >> 4) * 4 * NG * 2 + (HALF ? (lane >> 3 & 1) * 16 * NG * 2 : 0);
   const uint32_t s_at = 2 * R::kCodes + (lane & 15) * NG * 2, b_at = s_at + R::kMeta;
   p.affine0 = lane >> 4 <= (NG == 4 ? 1 : 0) ? b_at : s_at;
   p.affine1 = NG == 4 && lane >> 4 == 0 ? b_at : s_at;
@@ -291,7 +291,12 @@ struct RowSums {
 
 // One 32-key tile. masked (wave-uniform): some row does not see some key (t0 ..
 // t1 - 1 is what this lane's row sees) or a page does not exist.
-template <int D>
+//
+// HALF: there are at most 8 query rows, and each is two columns: column c has its
+// weights of the tile's first half of the keys, column c + 8 of the second half, so
+// that no lane's work on scores and weights is for nothing. The columns are joined
+// at the end like two wavefronts' parts.
+template <int D, bool HALF>
 __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LaneParts<D> &lp,
                                             const bf16x8_t (&q)[D / kGroup][2],
                                             const bf16x8_t &qaff, float scale2,
@@ -301,29 +306,58 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
   constexpr int NG = R::NG;
   const uint8_t *meta = stage + lp.scale;
   const CodeRegs kr = code_regs();
-  float s[8];
+  constexpr int H = HALF ? 1 : 2;  // halves whose keys are this lane's
+  const bool second = (lane & 8) != 0;
+  float s[4 * H];
+  if constexpr (HALF) {
+    f32x4_t x, acc[NG];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    uint32_t ws[2 * NG];
-    read_meta<NG>(meta + 16 * u * NG * 2, ws);
-    f32x4_t x = {0.f, 0.f, 0.f, 0.f};
-    x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(affine_keys<NG>(stage, lp, u), qaff, x, 0, 0, 0);
+    for (int u = 0; u < 2; ++u) {
+      f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+      v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(affine_keys<NG>(stage, lp, u), qaff, v, 0, 0, 0);
+      x = u == 0 || second ? v : x;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const uint2 c = *(const uint2 *)(stage + (lp.key ^ (g << 5)) + 16 * u * R::kRow);
-      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.x, kr), q[g][0], acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.y, kr), q[g][1], acc, 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = fmaf(bf16_at(ws, r * NG + g), acc[r], x[r]);
+      for (int g = 0; g < NG; ++g) {
+        const uint2 c = *(const uint2 *)(stage + (lp.key ^ (g << 5)) + 16 * u * R::kRow);
+        f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.x, kr), q[g][0], y, 0, 0, 0);
+        y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.y, kr), q[g][1], y, 0, 0, 0);
+        acc[g] = u == 0 || second ? y : acc[g];
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    uint32_t ws[2 * NG];
+    read_meta<NG>(meta, ws);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[4 * u + r] = x[r];
-    __builtin_amdgcn_sched_barrier(0);  // one half's operands at a time: registers
+    for (int r = 0; r < 4; ++r) {
+      s[r] = x[r];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) s[r] = fmaf(bf16_at(ws, r * NG + g), acc[g][r], s[r]);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t ws[2 * NG];
+      read_meta<NG>(meta + 16 * u * NG * 2, ws);
+      f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+      x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(affine_keys<NG>(stage, lp, u), qaff, x, 0, 0, 0);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint2 c = *(const uint2 *)(stage + (lp.key ^ (g << 5)) + 16 * u * R::kRow);
+        f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.x, kr), q[g][0], acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8(c.y, kr), q[g][1], acc, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = fmaf(bf16_at(ws, r * NG + g), acc[r], x[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[4 * u + r] = x[r];
+      __builtin_amdgcn_sched_barrier(0);  // one half's operands at a time: registers
+    }
   }
-  uint32_t ws[2][2 * NG], wb[2][2 * NG];
+  uint32_t ws[H][2 * NG], wb[H][2 * NG];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < H; ++u) {
     read_meta<NG>(meta + 2 * R::kMeta + 16 * u * NG * 2, ws[u]);
     read_meta<NG>(meta + 3 * R::kMeta + 16 * u * NG * 2, wb[u]);
   }
@@ -331,9 +365,9 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
     // An unseen slot may hold anything, NaN included: its score becomes -inf
     // and its value's scale and bias 0, by selection and never by a product.
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = i >> 2, r = i & 3, t = key0 + u * 16 + (lane >> 4) * 4 + r;
-      const bool seen = pages.page[u] >= 0 && t >= t0 && t < t1;
+    for (int i = 0; i < 4 * H; ++i) {
+      const int u = i >> 2, r = i & 3, t = key0 + (HALF ? 2 * (lane & 8) : u * 16) + (lane >> 4) * 4 + r;
+      const bool seen = (HALF && second ? pages.page[1] : pages.page[u]) >= 0 && t >= t0 && t < t1;
       s[i] = seen ? s[i] : kNegInf;
       if constexpr (NG == 1) {
         const uint32_t keep = seen ? 0xFFFFFFFFu : (r & 1 ? 0x0000FFFFu : 0xFFFF0000u);
@@ -350,7 +384,7 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
   }
   float mx = s[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
+  for (int i = 1; i < 4 * H; ++i) mx = fmaxf(mx, s[i]);
   if (__builtin_amdgcn_ballot_w64((mx - a.m) * scale2 > kSlack) != 0) {
     const float m = fmaxf(a.m, groups_max(mx));
     const float alpha = a.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((a.m - m) * scale2);
@@ -367,9 +401,9 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
     a.m = m;
   }
   const float ref = a.m == kNegInf ? 0.f : a.m;  // nothing seen yet: every weight is exp2(-inf) = 0
-  float p[8];
+  float p[4 * H];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4 * H; ++i) {
     p[i] = __builtin_amdgcn_exp2f((s[i] - ref) * scale2);  // see kSlack for this order
     a.l += p[i];
   }
@@ -380,18 +414,25 @@ __device__ __forceinline__ void attend_tile(const uint8_t *stage, const LanePart
     for (int i = 0; i < 2; ++i)
       vc[i] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
           (kv_lds_i32x2 *)(stage + (lp.value ^ (g << 5)) + 16 * i));
-    float ps[8];
+    float ps[4 * H];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4 * H; ++i) {
       const float sc = bf16_at(ws[i >> 2], (i & 3) * NG + g), bi = bf16_at(wb[i >> 2], (i & 3) * NG + g);
       ps[i] = p[i] * sc;
       a.c[g] = fmaf(p[i], fmaf(8.0f, sc, bi), a.c[g]);
     }
     // the keys in the order codes8 takes nibbles
-    const uint4 pw = make_uint4(pack_bf16x2(ps[0], ps[4]), pack_bf16x2(ps[1], ps[5]),
-                                pack_bf16x2(ps[2], ps[6]), pack_bf16x2(ps[3], ps[7]));
+    uint4 pw;
+    if constexpr (HALF) {
+      const uint32_t w0 = pack_bf16x2(ps[0], ps[1]), w1 = pack_bf16x2(ps[2], ps[3]);
+      a.w[g] = sum_bf16x2(w0, sum_bf16x2(w1, a.w[g]));
+      pw = make_uint4(second ? 0u : w0, second ? 0u : w1, second ? w0 : 0u, second ? w1 : 0u);
+    } else {
+      pw = make_uint4(pack_bf16x2(ps[0], ps[4]), pack_bf16x2(ps[1], ps[5]), pack_bf16x2(ps[2], ps[6]),
+                      pack_bf16x2(ps[3], ps[7]));
+      a.w[g] = sum_bf16x2(pw.x, sum_bf16x2(pw.y, sum_bf16x2(pw.z, sum_bf16x2(pw.w, a.w[g]))));
+    }
     const bf16x8_t pb = __builtin_bit_cast(bf16x8_t, pw);
-    a.w[g] = sum_bf16x2(pw.x, sum_bf16x2(pw.y, sum_bf16x2(pw.z, sum_bf16x2(pw.w, a.w[g]))));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       a.o[g][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes8((uint32_t)vc[j >> 1][j & 1], kr), pb,
@@ -515,7 +556,7 @@ __device__ __forceinline__ bool work_item(const Kv4Dims &dm, const Kv4Batch &bt,
 }
 
 // One row tile of a sequence and head (tile_i of `tiles`), and one split of its keys.
-template <int D, int W>
+template <int D, int W, bool HALF>
 __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc,
                                             const Kv4Batch &bt, const Kv4Attn &at, int seq, int head,
                                             int tile_i, int split, int splits, int per,
@@ -529,12 +570,13 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 
   // the tile's first and last token, and this lane's query row
-  const int tok0 = rt.row0 == 0 ? 0 : rt.row0 / G;
+  const int tok0 = HALF || rt.row0 == 0 ? 0 : rt.row0 / G;
   const int in0 = rt.row0 - tok0 * G;  // head of the first row in its group
-  const int row = min(rt.row0 + (lane & 15), rt.rows - 1) - rt.row0 + in0;
-  const bool real = rt.row0 + (lane & 15) < rt.rows;
-  const int tok = tok0 + row / G, hd = rt.head * G + row % G;
-  const int tok1 = __builtin_amdgcn_readlane(tok, 15);
+  const int col = HALF ? lane & 7 : lane & 15;
+  const int row = min(rt.row0 + col, rt.rows - 1) - rt.row0 + in0;
+  const bool real = rt.row0 + col < rt.rows;
+  const int tok = HALF ? 0 : tok0 + row / G, hd = rt.head * G + (HALF ? row : row % G);
+  const int tok1 = HALF ? 0 : __builtin_amdgcn_readlane(tok, 15);
   // its channels, in the order codes8 takes a word's nibbles
   bf16x8_t q[NG][2];
   float qsum[NG];
@@ -565,7 +607,7 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
       bt.table + (bt.rows ? (long long)rt.seq * dm.Hkv + rt.head : (long long)rt.seq) * dm.max_pages;
   uint8_t *ring = smem + wave * kStages * Ring<D>::kStage;
   const uint32_t ring_at = lds_address(ring);
-  LaneParts<D> lp = lane_parts<D>(kc, vc, lane);
+  LaneParts<D> lp = lane_parts<D, HALF>(kc, vc, lane);
   int tile = share.begin + wave;
   const int end = share.end;
   // pages of the tile in use, of the next one and (not loaded yet) of the one after
@@ -613,7 +655,7 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
     asm volatile("" ::: "memory");
     const int key0 = tile * kKvTile;
     const bool masked = key0 < all0 || key0 + (long long)kKvTile > all1 || here.page[0] < 0 || here.page[1] < 0;
-    attend_tile<D>(ring + stage * Ring<D>::kStage, lp, q, qaff, scale2, masked, lane, key0, t0, t1, here, a);
+    attend_tile<D, HALF>(ring + stage * Ring<D>::kStage, lp, q, qaff, scale2, masked, lane, key0, t0, t1, here, a);
     // every LDS read of this stage is done before the DMA refills it
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     here = next;
@@ -635,7 +677,8 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
   __syncthreads();
   float m = kNegInf;
 #pragma unroll
-  for (int w = 0; w < W; ++w) m = fmaxf(m, sm[w][lane & 15]);
+  for (int w = 0; w < W; ++w)
+    m = HALF ? fmaxf(m, fmaxf(sm[w][lane & 7], sm[w][(lane & 7) + 8])) : fmaxf(m, sm[w][lane & 15]);
   const float f = part_weight(a.m, a.l, m, scale2);
   float *so = (float *)ring + (lane & 15) * (D + 4) + 4 * (lane >> 4);
 #pragma unroll
@@ -648,25 +691,26 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
                       f * (a.o[g][j][3] + off));
   }
   __syncthreads();
-  constexpr int kThreadsRow = D / 4;
+  constexpr int kThreadsRow = D / 4, kParts = HALF ? 2 * W : W;
   for (int r = threadIdx.x / kThreadsRow; r < kAtRows && rt.row0 + r < rt.rows; r += W * kWave / kThreadsRow) {
     const int c = (threadIdx.x % kThreadsRow) * 4;
     float mr = kNegInf, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) mr = fmaxf(mr, sm[w][r]);
+    for (int i = 0; i < kParts; ++i) mr = fmaxf(mr, sm[i % W][r + i / W * 8]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float4 x = *(const float4 *)((float *)(smem + w * kStages * Ring<D>::kStage) + r * (D + 4) + c);
+    for (int i = 0; i < kParts; ++i) {
+      const int w = i % W, x_row = r + i / W * 8;
+      const float4 x = *(const float4 *)((float *)(smem + w * kStages * Ring<D>::kStage) + x_row * (D + 4) + c);
       o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-      l = fmaf(part_weight(sm[w][r], sl[w][r], mr, scale2), sl[w][r], l);
+      l = fmaf(part_weight(sm[w][x_row], sl[w][x_row], mr, scale2), sl[w][x_row], l);
     }
     if (share.used > 1) {
       const long long pr = part_index(dm, at, rt, r, splits, split);
       *(float4 *)(part + pr * D + c) = o;
       if (c == 0) *(float2 *)(part_stats(dm, bt, at, splits, part) + pr * 2) = make_float2(mr, l);
     } else {
-      const int x = r + in0, i = tok0 + x / G, h = rt.head * G + x % G;
+      const int x = r + in0, i = HALF ? 0 : tok0 + x / G, h = rt.head * G + (HALF ? x : x % G);
       store_row(dm, at, rt.sp.begin + i, h, c, l, o);
     }
   }
@@ -674,7 +718,7 @@ __device__ __forceinline__ void attend_rows(const Kv4Dims &dm, const Kv4Plane &k
 
 // Grid: x = row tile * splits + split, y = cache head, z = sequence; or, where
 // keys are split and a sequence has one row tile (flat), x = work items.
-template <int D, int W>
+template <int D, int W, bool HALF>
 __global__ __launch_bounds__(W *kWave, at_blocks<D>()) void kv4_attention_kernel(Kv4Dims dm, Kv4Plane kc, Kv4Plane vc,
                                                                     Kv4Batch bt, Kv4Attn at, int splits,
                                                                     bool flat, float *__restrict__ part) {
@@ -694,7 +738,7 @@ __global__ __launch_bounds__(W *kWave, at_blocks<D>()) void kv4_attention_kernel
     tile_i = blockIdx.x / splits;
     split = blockIdx.x - tile_i * splits;
   }
-  attend_rows<D, W>(dm, kc, vc, bt, at, seq, head, tile_i, split, splits, per, smem, sm, sl, part);
+  attend_rows<D, W, HALF>(dm, kc, vc, bt, at, seq, head, tile_i, split, splits, per, smem, sm, sl, part);
 }
 
 // Joins the splits' partial results of a row tile of ROWS. Few splits (C = D): D /
@@ -840,19 +884,19 @@ size_t kv4_attention_ws(const Kv4Dims &dm, int T, int max_new, int window, bool 
   return pre > few ? pre : few;
 }
 
-template <int D, int W>
+template <int D, int W, bool HALF>
 static hipError_t launch_rows(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
                               const Kv4Attn &at, int tokens, int splits, float *part, hipStream_t s) {
   if constexpr (at_lds_bytes<D, W>() > 64 * 1024) {
     static std::atomic<uint64_t> asked;
-    const hipError_t st = allow_lds((const void *)kv4_attention_kernel<D, W>, at_lds_bytes<D, W>(), asked);
+    const hipError_t st = allow_lds((const void *)kv4_attention_kernel<D, W, HALF>, at_lds_bytes<D, W>(), asked);
     if (st != hipSuccess) return st;
   }
   const long long tiles = kv4_row_tiles(dm, tokens);
   const bool flat = splits > 1 && tiles == 1 && dm.B <= kEvenMaxB;
   const dim3 grid = flat ? dim3((unsigned)(kv4_tasks(dm, tokens) * splits))
                          : dim3((unsigned)(tiles * splits), dm.Hkv, dm.B);
-  kv4_attention_kernel<D, W><<<grid, W * kWave, at_lds_bytes<D, W>(), s>>>(dm, kc, vc, bt, at, splits, flat, part);
+  kv4_attention_kernel<D, W, HALF><<<grid, W * kWave, at_lds_bytes<D, W>(), s>>>(dm, kc, vc, bt, at, splits, flat, part);
   return hipGetLastError();
 }
 
@@ -888,8 +932,18 @@ static hipError_t launch_all(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pla
   // Eight wavefronts where every workgroup has a CU to itself (a short sequence
   // ends sooner), four where there are more of them or keys are split.
   const bool alone = p.row_splits == 1 && kv4_tasks(dm, p.few) <= 256;
-  e = alone ? launch_rows<D, 8>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s)
-            : launch_rows<D, 4>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s);
+  // Rows that are sequences, of 8 heads or fewer: two columns a query row; and from three
+  // lists for every wavefront the card holds, a wavefront each, which joins nothing. us of
+  // the whole call with four / one, D = 128: 8 heads a list, 32 pages of 32 keys: 112 / 126
+  // for 3000 lists, 304 / 286 for 10,000, 543 / 505 for 18,000; 4 heads, 16 pages of 16:
+  // 228 / 202 for 12,000; 8 heads, 124 pages of 32: 256 / 337 for 3000, 710 / 701 for 9000.
+  const bool half = bt.rows && dm.Hq / dm.Hkv <= kAtRows / 2;
+  const bool single = half && p.row_splits == 1 && kv4_tasks(dm, p.few) >= 12ll * at_slots<D>();
+  e = single ? launch_rows<D, 1, true>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s)
+      : alone ? half ? launch_rows<D, 8, true>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s)
+                   : launch_rows<D, 8, false>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s)
+      : half ? launch_rows<D, 4, true>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s)
+             : launch_rows<D, 4, false>(dm, kc, vc, bt, at, p.few, p.row_splits, part, s);
   if (e == hipSuccess && p.row_splits > 1) e = launch_join<D, kAtRows>(dm, bt, at, p.few, p.row_splits, part, s);
   return e;
 }

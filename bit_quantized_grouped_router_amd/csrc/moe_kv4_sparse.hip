@@ -307,7 +307,7 @@ __device__ __forceinline__ bool score_tile(const Kv4Dims &dm, const Kv4Batch &bt
 
 // Few tokens a sequence. Grid: x = sequence, y = cache head, z = token tile + tiles *
 // chunk of pages (chunks that shorter sequences do not have come last: 64 sequences of
-// up to 32,000 tokens, D = 256, 24 us with them in between, ... without). 16 pages by
+// up to 32,000 tokens, D = 256, 24 us with them in between, 12.6 without). 16 pages by
 // 16 tokens a wavefront at a time; as a chunk of four loads goes to LDS to change
 // lanes, the next tile's takes its registers. Bound by the chain offsets - table -
 // bounds.
@@ -753,12 +753,12 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
     search(8);
     most = wave_max_u32(most);
     const float off = 2.0f * (score_error(G) * __uint_as_float(most) + kScoreFlushed);
-    // the keys of border + off and border - off, rounded away; all scored pages where sums are not finite
+    // the keys of border + off and border - off, rounded away; all scored pages where sums may not be finite
     const float top = key_logit(prefix << bits | ((1u << bits) - 1)), bottom = key_logit(prefix << bits);
     const float x = top + off, y = bottom - off;
     uint32_t above = logit_key(x * (1.0f + (x > 0.f ? 0x1p-22f : -0x1p-22f)));
     uint32_t below = logit_key(y * (1.0f - (y > 0.f ? 0x1p-22f : -0x1p-22f)));
-    if (most >= 0x7F800000u) above = kTaken - 1, below = 1;
+    if (most >= 0x7E800000u) above = kTaken - 1, below = 1;  // 2^126: sums may overflow
     int sure = 0, near = 0;
     each([&](int, int, uint32_t k) {
       sure += count_of(k > above);
@@ -909,7 +909,7 @@ static SparseWs sparse_ws(const Kv4Dims &dm, int T, const Kv4Select &sel) {
   const int size = sel.top + sel.first + sel.recent;
   w.pitch = (dm.max_pages + kScoreTile - 1) / kScoreTile * kScoreTile;
   // The prompt's kernels need 64 tokens a sequence and rows for its token tiles (us for
-  // the scores of 1500 tokens behind 60,000, D = 128: ... with, 39 without).
+  // the scores of 1500 tokens behind 60,000, D = 128: 5.3 + 22.9 us with, 39 without).
   const size_t slot = (size_t)dm.Hkv * 3 * 2 * dm.D * 16 * 2;
   w.prompt = sel.top > 0 && sel.max_new >= 64 && sel.max_new <= 1 << 20 && (long long)dm.B * 16 <= T &&
              dm.B * slot <= kPartBytes / 2;

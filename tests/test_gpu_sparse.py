@@ -356,6 +356,11 @@ MORE = [  # prompts and rows of several kinds: new, earlier, Hq, Hkv, D, page, t
     ([80] + [1] * 69, [900] + list(range(10, 1390, 20)), 4, 2, 64, 16, 3, 1, 1),   # many sequences, one of them a prompt
     ([150, 0, 65, 1], [0, 40, 2000, 700], 64, 1, 64, 16, 4, 2, 1),
     ([300], [0], 4, 4, 128, 16, 5, 1, 1),
+    ([400], [300], 16, 16, 256, 16, 3, 1, 1),     # three lists and more for each wavefront of the card
+    ([480], [200], 32, 32, 64, 16, 2, 0, 2),
+    ([290, 0, 1], [300, 60, 700], 64, 32, 128, 16, 3, 1, 1),
+    ([100], [700], 18, 2, 128, 16, 3, 1, 1),      # 9 heads a list
+    ([5, 1], [700, 90], 14, 2, 64, 16, 3, 1, 1),  # 7
 ]
 
 
@@ -450,3 +455,27 @@ def test_bounds_follow_a_rejected_draft():
     keys = whole(c)
     want = B.bounds(keys[b.table[0, :3], 0], 33)
     assert (host_bits(got)[b.table[0, :3], 0] == round_to_bf16_bits(want)).all()
+
+
+@pytest.mark.parametrize("new", [[2], [66]])
+def test_scores_next_to_the_largest_number(new):
+    """Scores on both sides of fp32's largest number: infinite ones tie, finite ones next to them do not."""
+    rng = np.random.default_rng(37)
+    b = Batch(rng, new, [16 * 200], 16)
+    c = filled(rng, b, 1, 64)
+    n = c.num_pages
+    top = 3.3e38 * (1 - 2.0 ** -rng.integers(3, 12, size=(n, 1, 1, 64)))
+    bounds = torch.from_numpy(np.concatenate([-top, top], axis=2).astype(np.float32)).cuda().to(BF16)
+    # 128 terms of 0.0083 times 3.3e38 (1 - 0.0277 on average) are 3.409e38, the largest number 3.403e38
+    q = torch.full((b.T, 2, 64), 0.0083, device="cuda").to(BF16)
+    q[:, 1] *= -1
+    blocks = torch.empty((b.T, 1, 42), dtype=torch.int32, device="cuda")
+    M.moe_kv4_sparse_attention(c, bounds, q, *b.dev, b.T, 40, blocks=blocks)
+    bb = bf16_to_f64(host_bits(bounds))[b.table[0], 0]
+    with np.errstate(over="ignore"):
+        score = np.abs(q[0].double().cpu().numpy()) @ bb[:, 1].T
+        finite = np.isfinite(score.sum(0).astype(np.float32))
+        assert 20 < finite[:200].sum() < 180
+        for t in range(b.T):
+            p = B.select(q[t].double().cpu().numpy(), bb[:, 0], bb[:, 1], np.ones(len(bb), bool), 3200 + t, 16, 40, 1, 1)
+            assert blocks[t, 0].tolist() == p.tolist()
