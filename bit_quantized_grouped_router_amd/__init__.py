@@ -559,9 +559,12 @@ def _rows(t: torch.Tensor, shape, name: str, dtypes) -> int:
         raise MoeError(f"{name} has dtype {t.dtype}; expected one of "
                        f"{', '.join(str(d) for d in dtypes)}")
     st = t.stride()
-    if shape[0] > 1 and st[-1] == 1:  # the usual cases first: host time counts for a single token
-        row = shape[-1] if len(shape) == 2 else shape[1] * shape[2]
-        if st[0] >= row and (len(shape) == 2 or st[1] == shape[2]):
+    # the usual cases first: host time counts for a single token
+    if st[-1] == 1 and (len(shape) == 2 or st[1] == shape[2]):
+        row = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+        if shape[0] <= 1:
+            return (row + 7) // 8 * 8
+        if st[0] >= row:
             return st[0]
     row = 1
     for i in range(t.dim() - 1, 0, -1):
@@ -964,8 +967,8 @@ def moe_kv4_rope_append(cache: KV4Cache, q: torch.Tensor, k: torch.Tensor, v: to
 
 # ------------------------------------------------------------------ attention over selected pages
 
-def _bounds(cache: KV4Cache, bounds: torch.Tensor) -> int:
-    n, heads, _, D = cache.sizes()
+def _bounds(dm: MoeKv4Dims, bounds: torch.Tensor) -> int:
+    n, heads, D = dm.num_pages, dm.Hkv, dm.D
     if bounds.shape != (n, heads, 2, D) or bounds.dtype not in BF16 or not bounds.is_contiguous():
         raise MoeError(f"bounds are {bounds.dtype} {tuple(bounds.shape)}; expected a contiguous bf16 tensor "
                        f"{(n, heads, 2, D)}")
@@ -976,7 +979,7 @@ def moe_kv4_bounds(cache: KV4Cache, bounds: torch.Tensor, page_table, cu, kv_len
     """Bring bounds (bf16 [num_pages, Hkv, 2, D]: smallest and largest key of each channel) up to
     date for the pages that the batch's T new tokens lie in. Call it after every write."""
     dm, c, b, s, _, _ = _kv4(cache, page_table, cu, kv_len, (bounds,), stream)
-    _check(lib().moe_kv4_bounds(dm, c, T, _bounds(cache, bounds), b, s), "moe_kv4_bounds")
+    _check(lib().moe_kv4_bounds(dm, c, T, _bounds(dm, bounds), b, s), "moe_kv4_bounds")
 
 
 def moe_kv4_sparse_attention_workspace_bytes(cache: KV4Cache, T: int, Hq: int, B: int, max_pages: int, max_new: int,
@@ -1019,7 +1022,7 @@ def moe_kv4_sparse_attention(cache: KV4Cache, bounds: torch.Tensor, q: torch.Ten
             ws = _empty((need,), torch.uint8, q.device, stream)
     else:
         need = ws.numel() * ws.element_size()
-    _check(L.moe_kv4_sparse_attention(dm, c, _bounds(cache, bounds), T, max_new, q.data_ptr(), qs, out.data_ptr(), os_, b,
+    _check(L.moe_kv4_sparse_attention(dm, c, _bounds(dm, bounds), T, max_new, q.data_ptr(), qs, out.data_ptr(), os_, b,
                                       pages, D ** -0.5 if scale is None else scale, _ptr(blocks), _ptr(ws), need, s),
            "moe_kv4_sparse_attention")
     return out
