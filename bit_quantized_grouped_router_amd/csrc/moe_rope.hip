@@ -44,11 +44,14 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// Sine and cosine of 2 pi t: the nearest quarter turn is taken off and the rest, at most
-// pi / 4, goes into the Taylor series, whose next terms are below 2^-45.
-__device__ __forceinline__ void sincos_turns(double t, double &sn, double &cs) {
+// Sine and cosine of a: the nearest quarter turn is taken off and the rest, at most pi /
+// 4, goes into the Taylor series, whose next terms are below 2^-45. Turns are a times 1 /
+// (2 pi) in two parts, so that no more is lost for large angles than for small ones.
+__device__ __forceinline__ void sincos64(double a, double &sn, double &cs) {
+  constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnRest = -0x1.6b01ec5417056p-57;
+  const double t = a * kTurn, rest = fma(a, kTurnRest, fma(a, kTurn, -t));
   const double quarter = rint(4.0 * t);
-  const double x = fma(-0.25, quarter, t) * 6.28318530717958647693, y = x * x;
+  const double x = (fma(-0.25, quarter, t) + rest) * 6.28318530717958647693, y = x * x;
   double s = 1.0 / 6227020800.0, c = -1.0 / 87178291200.0;
   s = fma(s, y, -1.0 / 39916800.0), c = fma(c, y, 1.0 / 479001600.0);
   s = fma(s, y, 1.0 / 362880.0), c = fma(c, y, -1.0 / 3628800.0);
@@ -73,7 +76,7 @@ __device__ __forceinline__ void lane_turn(const Rope &rope, int position, int at
   const int lane = threadIdx.x & (kWave - 1), half = rope.rot / 2;
   for (int i = lane; i < half; i += kWave) {
     double sn, cs;
-    sincos_turns((double)position * (double)rope.freqs[i] * 0.15915494309189533577, sn, cs);
+    sincos64((double)position * (double)rope.freqs[i], sn, cs);
     lds.turn[i] = make_float2((float)(cs * rope.magnitude), (float)(sn * rope.magnitude));
   }
   wave_lds_sync();
@@ -86,6 +89,13 @@ __device__ __forceinline__ void lane_turn(const Rope &rope, int position, int at
     t.c[i] = u.x;
     t.s[i] = second ? u.y : -u.y;
   }
+}
+
+// a c + b s, the products rounded (hipcc fuses them, __fmul_rn's too, unless told not to).
+__device__ __forceinline__ float products_sum(float a, float c, float b, float s) {
+#pragma clang fp contract(off)
+  const float p = a * c, q = b * s;
+  return p + q;
 }
 
 // Turns 8 channels of a head whose channel 0 is lane `first`'s.
@@ -119,7 +129,7 @@ __device__ __forceinline__ void rotate8(const Rope &rope, const LaneTurn &t, int
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(y[i], t.s[i]));
+    const float v = products_sum(x[i], t.c[i], y[i], t.s[i]);
     x[i] = at + i < rope.rot ? v : x[i];
   }
 }

@@ -359,3 +359,26 @@ def test_stream_argument():
         b = M.moe_rope(heads, r, pos, stream=s)
         s.synchronize()
         assert torch.equal(a[0], want[0]) and torch.equal(a[1], want[1]) and torch.equal(b, turned)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("first", [0, 100000, 2 ** 28])
+def test_products_are_rounded_apart(inter, first):
+    """fp32 results are the sum of two rounded products, bit for bit, with the cosines and sines that
+    (1, 0) is turned to; those are the ones in 64 bits, rounded, but where that is next to a tie."""
+    T, D = 300, 128
+    r, pos = M.Rope.make(D, interleaved=inter), i32(np.arange(first, first + T))
+    unit = torch.zeros((T, 1, D), device="cuda")
+    lo, hi = (slice(0, None, 2), slice(1, None, 2)) if inter else (slice(0, D // 2), slice(D // 2, None))
+    unit[..., lo] = 1
+    u = M.moe_rope(unit, r, pos)
+    c, s = u[..., lo], u[..., hi]
+    angle = pos.double()[:, None] * r.freqs.double()
+    for got, want in ((c[:, 0], torch.cos(angle)), (s[:, 0], torch.sin(angle))):
+        # off by half a step at the most, and what 2^-44 is of it (of the smallest sine, 2^-24 or so, more)
+        step = torch.nextafter(got.abs(), torch.full_like(got, 2.0)).double() - got.abs().double()
+        assert ((got.double() - want).abs() <= step / 2 + 2.0 ** -44).all()
+    _, x = values(np.random.default_rng(5), (T, 6, D), F32)
+    y = M.moe_rope(x, r, pos)
+    a, b = x[..., lo], x[..., hi]
+    assert torch.equal(y[..., lo], a * c - b * s) and torch.equal(y[..., hi], a * s + b * c)
