@@ -19,6 +19,11 @@
 //
 // The selected pages become page tables of their own, one for each token and
 // cache head, and the attention kernel for few query rows runs over those.
+//
+// us of scores + selection + attention (+ join of split keys), 16 heads on 2: one token
+// behind 131,149, D = 128, 32 of 2050 pages 5.3 + 8.0 + 8.7 + 4.0; 64 tokens behind up to
+// 32,000, D = 256, 24 pages each 12.4 + 10.9 + 21.5 + 4.7; 1500 tokens behind 60,000, D =
+// 128, 32 of 1922 pages each 28.1 + 26.3 + 75.5.
 #include "moe_kv4_sparse.h"
 
 #include "moe_kv4_device.h"
@@ -34,7 +39,8 @@ constexpr int kBoundWaves = 4;
 // wavefront all of them), and for each that is the first of the call in its page it
 // goes over the page's keys, up to the sequence's last. D / 8 lanes take a key, 8
 // channels each, and 64 keys are loaded at once. Bound by a chain of four loads
-// (offsets, page, codes, and the sums' way through LDS).
+// (offsets, page, codes, and the sums' way through LDS): us 5.6 for 64 single tokens, 2
+// heads of 256, pages of 64; 9.0 for all pages of 60,000 tokens, D = 128 (9.6 MB).
 template <int D>
 __global__ __launch_bounds__(kBoundWaves *kWave) void kv4_bounds_kernel(Kv4Dims dm, Kv4Plane kc, Kv4Batch bt,
                                                                         uint16_t *__restrict__ bounds, int run) {

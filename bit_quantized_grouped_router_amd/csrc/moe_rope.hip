@@ -16,8 +16,8 @@
 // LDS; each lane keeps those of its 8 channels for all of the token's heads. A
 // wavefront has one step's loads in flight and few registers, so that more of them
 // share a SIMD: with four steps' at a time 8192 tokens of 16 x 128 in bf16 take 15.6
-// us instead of 13.5 (5.0 TB/s). Prompts of 7480 tokens, 32 + 2 x 8 heads of 128 from
-// fp32, rotated and written in 60 us (4.0 TB/s); 8 tokens of 16 + 2 x 2 heads of 256 in
+// us instead of 13.9 (4.8 TB/s). Prompts of 7480 tokens, 32 + 2 x 8 heads of 128 from
+// fp32, rotated and written in 60 us (4.2 TB/s); 8 tokens of 16 + 2 x 2 heads of 256 in
 // 5.2.
 #include "moe_rope.h"
 
