@@ -483,7 +483,6 @@ constexpr int kMinTiles = 16;
 // the join for 2048 keys of one token, 16 heads on 2, D = 128: 10.9 + 3.9 with four,
 // 8.7 + 4.1 with two, 7.6 + 5.2 with one).
 constexpr int kMinTilesRows = 8;
-__host__ __device__ constexpr int min_tiles(bool rows) { return rows ? kMinTilesRows : kMinTiles; }
 // Workgroups of 4 wavefronts a CU holds: wavefronts a SIMD by their registers
 // (214, 130 and 90; a 4-wavefront limit at D = 128 spills a pointer of the loop,
 // and its reload waits for the DMA in flight).
@@ -501,13 +500,12 @@ constexpr int kEvenMaxB = 256;
 // tasks. (kv4_share raises it where `splits` are too few.)
 template <int D>
 __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch &bt, const Kv4Attn &at) {
-  if (dm.B > kEvenMaxB) return min_tiles(bt.rows);
+  if (dm.B > kEvenMaxB) return kMinTiles;
   const int lane = threadIdx.x & (kWave - 1), G = dm.Hq / dm.Hkv;
   const int cap = (int)kv4_capacity(dm);
   float total = 0.f, tasks = 0.f;  // rough figures will do
   for (int b = lane; b < dm.B; b += kWave) {
-    int n = bt.rows ? (bt.len[b] < 0 ? 0 : 1)
-                    : min(min(max(bt.cu[b + 1], 0), bt.T) - min(max(bt.cu[b], 0), bt.T), at.max_new);
+    int n = min(min(max(bt.cu[b + 1], 0), bt.T) - min(max(bt.cu[b], 0), bt.T), at.max_new);
     if (n * G > at.most) n = 0;
     float keys = (float)min(max(bt.len[b], 0), cap);
     if (at.window > 0) keys = fminf(keys, (float)at.window + (float)n);
@@ -518,7 +516,7 @@ __device__ __forceinline__ int tiles_per_split(const Kv4Dims &dm, const Kv4Batch
   total = wave_sum_dpp(total) * dm.Hkv;
   tasks = wave_sum_dpp(tasks) * dm.Hkv;
   const float room = fmaxf(at_slots<D>() - tasks, at_slots<D>() / 4);
-  return max(min_tiles(bt.rows), (int)fminf(ceilf(total / room), 67108864.0f));
+  return max(kMinTiles, (int)fminf(ceilf(total / room), 67108864.0f));
 }
 
 // Work item `item` of a call whose sequences have one row tile each: the
@@ -724,7 +722,7 @@ __global__ __launch_bounds__(W *kWave, at_blocks<D>()) void kv4_attention_kernel
                                                                     bool flat, float *__restrict__ part) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ float sm[W][kAtRows], sl[W][kAtRows];
-  const int per = splits > 1 ? tiles_per_split<D>(dm, bt, at) : 0;
+  const int per = splits > 1 && at.per == 0 ? tiles_per_split<D>(dm, bt, at) : at.per;
   int seq = blockIdx.z, head = blockIdx.y, tile_i = blockIdx.x, split = 0;
   if (flat) {
     // there are never more items than workgroups: a task has at most `splits`
@@ -758,7 +756,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Dims dm, Kv4Batch bt, 
   const RowTile rt = row_tile(dm, bt, at.max_new, tile_i, blockIdx.y, blockIdx.z, ROWS);
   if (rt.row0 + first - tile_i * ROWS >= rt.rows || rt.rows <= at.above || rt.rows > at.most) return;
   const Kv4Range range = tile_range(dm, rt, ROWS, at.causal, at.window);
-  const int per = ROWS == kAtRows ? tiles_per_split<D>(dm, bt, at) : kPfMinTiles;
+  const int per = ROWS != kAtRows ? kPfMinTiles : at.per > 0 ? at.per : tiles_per_split<D>(dm, bt, at);
   const int used = kv4_share(range, per, splits, 0).used;
   if (used <= 1 || rt.row0 + r >= rt.rows) return;
   const float *ml = part_stats(dm, bt, at, splits, part);
@@ -821,10 +819,19 @@ static long long kv4_keys(const Kv4Dims &dm, int tokens, int window) {
 // The most workgroups a row tile's keys are split over: as many as have
 // kMinTiles each, and no more than the card's slots over all tasks, or twice
 // that where sequences have one row tile each (work_item() evens those out).
+//
+// Rows that are sequences all have about as many keys as their tables hold, so each
+// takes the same number of workgroups, and none has to look at the lengths of all.
+static int row_tiles_all(const Kv4Dims &dm) { return (int)((kv4_capacity(dm) + kKvTile - 1) / kKvTile); }
 static int few_splits(const Kv4Dims &dm, int tokens, int window, bool rows) {
   const long long tasks = kv4_tasks(dm, tokens);
   const int slots = dm.D == 256 ? at_slots<256>() : dm.D == 128 ? at_slots<128>() : at_slots<64>();
-  const long long most = kv4_keys(dm, tokens, window) / (kKvTile * min_tiles(rows));
+  if (rows) {
+    const int all = row_tiles_all(dm);
+    const long long n = slots / tasks < all / kMinTilesRows ? slots / tasks : all / kMinTilesRows;
+    return n < 1 ? 1 : (int)n;
+  }
+  const long long most = kv4_keys(dm, tokens, window) / (kKvTile * kMinTiles);
   long long n = (kv4_row_tiles(dm, tokens) == 1 ? 2 : 1) * slots / tasks;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
@@ -893,7 +900,7 @@ static hipError_t launch_rows(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pl
     if (st != hipSuccess) return st;
   }
   const long long tiles = kv4_row_tiles(dm, tokens);
-  const bool flat = splits > 1 && tiles == 1 && dm.B <= kEvenMaxB;
+  const bool flat = splits > 1 && tiles == 1 && dm.B <= kEvenMaxB && at.per == 0;
   const dim3 grid = flat ? dim3((unsigned)(kv4_tasks(dm, tokens) * splits))
                          : dim3((unsigned)(tiles * splits), dm.Hkv, dm.B);
   kv4_attention_kernel<D, W, HALF><<<grid, W * kWave, at_lds_bytes<D, W>(), s>>>(dm, kc, vc, bt, at, splits, flat, part);
@@ -929,6 +936,7 @@ static hipError_t launch_all(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pla
   at.above = 0;
   at.most = p.many ? kManyRows : 0x7FFFFFFF;
   at.room = p.room;
+  at.per = bt.rows && p.row_splits > 1 ? (row_tiles_all(dm) + p.row_splits - 1) / p.row_splits : 0;
   // Eight wavefronts where every workgroup has a CU to itself (a short sequence
   // ends sooner), four where there are more of them or keys are split.
   const bool alone = p.row_splits == 1 && kv4_tasks(dm, p.few) <= 256;

@@ -1007,7 +1007,7 @@ hipError_t launch_kv4_sparse(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pla
     if (e != hipSuccess) return e;
     const Kv4Batch rows{so.table, nullptr, so.len, part.rows, true};
     const Kv4Attn at{sel.q + (long long)row0 * sel.q_stride, out + (long long)row0 * out_stride, sel.q_stride,
-                     out_stride, 1, scale, false, 0, 0, 0, 0};
+                     out_stride, 1, scale, false, 0, 0, 0, 0, 0};
     e = launch_kv4_attention(selected_dims(dm, part.rows, size), kc, vc, rows, at, (char *)ws + w.attention, s);
     if (e != hipSuccess) return e;
   }
