@@ -33,7 +33,7 @@
 // (offsets, pages, codes) for few short ones. us, one new token a sequence, 16
 // heads on 2: 64 sequences of up to 8101, D = 256 (113 MB) 33.2 and 5.4 for the
 // join, 3.4 TB/s; one of 131,150, D = 128 (38 MB) 16.9 and 6.8; one of 500, D =
-// 256 11.7. 3000 lists of 1024 keys of their own, 8 heads, D = 128: 75.6 (90.1 with
+// 256 11.7. 3000 lists of 1024 keys of their own, 8 heads, D = 128: 74.2 (90.1 with
 // half the columns empty), 90% of it vector instructions: the codes' conversion is 128
 // of 214 a tile, and a workgroup's start and end cost as much as three tiles.
 #include "moe_kv4_device.h"
@@ -480,8 +480,8 @@ constexpr int at_lds_bytes() {
 // instead of 512 took a batch of 64 mixed sequences from 33 to 57 us.
 constexpr int kMinTiles = 16;
 // Of rows that are sequences, which have few keys: two a wavefront (us of this kernel and
-// the join for 2048 keys of one token, 16 heads on 2, D = 128: 10.9 + 3.9 with four,
-// 8.7 + 4.1 with two, 7.6 + 5.2 with one).
+// the join for 2048 keys of one token, 16 heads on 2, D = 128: 9.5 + 2.9 with four,
+// 7.4 + 3.4 with two, 6.2 + 4.8 with one).
 constexpr int kMinTilesRows = 8;
 // Workgroups of 4 wavefronts a CU holds: wavefronts a SIMD by their registers
 // (214, 130 and 90; a 4-wavefront limit at D = 128 spills a pointer of the loop,
@@ -821,7 +821,9 @@ static long long kv4_keys(const Kv4Dims &dm, int tokens, int window) {
 // that where sequences have one row tile each (work_item() evens those out).
 //
 // Rows that are sequences all have about as many keys as their tables hold, so each
-// takes the same number of workgroups, and none has to look at the lengths of all.
+// takes the same number of workgroups, and none has to look at the lengths of all (64
+// tokens of 24 pages of 64 keys, 16 heads on 2, D = 256: 19.4 + 4.1 us so, 21.5 + 4.7
+// by the lengths).
 static int row_tiles_all(const Kv4Dims &dm) { return (int)((kv4_capacity(dm) + kKvTile - 1) / kKvTile); }
 static int few_splits(const Kv4Dims &dm, int tokens, int window, bool rows) {
   const long long tasks = kv4_tasks(dm, tokens);

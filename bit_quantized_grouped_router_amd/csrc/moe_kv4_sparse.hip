@@ -21,9 +21,9 @@
 // cache head, and the attention kernel for few query rows runs over those.
 //
 // us of scores + selection + attention (+ join of split keys), 16 heads on 2: one token
-// behind 131,149, D = 128, 32 of 2050 pages 5.3 + 8.0 + 8.7 + 4.0; 64 tokens behind up to
-// 32,000, D = 256, 24 pages each 12.4 + 10.9 + 21.5 + 4.7; 1500 tokens behind 60,000, D =
-// 128, 32 of 1922 pages each 28.1 + 26.3 + 75.5.
+// behind 131,149, D = 128, 32 of 2050 pages 5.3 + 7.9 + 7.3 + 3.5; 64 tokens behind up to
+// 32,000, D = 256, 24 pages each 12.5 + 10.9 + 19.6 + 4.1; 1500 tokens behind 60,000, D =
+// 128, 32 of 1922 pages each 27.9 + 26.3 + 74.2.
 #include "moe_kv4_sparse.h"
 
 #include "moe_kv4_device.h"
