@@ -18,32 +18,70 @@ namespace moe {
 
 constexpr int kNormThreads = 256;
 
-// Channels at .. at + 7 of a row, those from n on as 0.
-template <bool F32, bool VEC>
-__device__ __forceinline__ void norm_load8(const void *row, int at, int n, float (&x)[8]) {
-  if constexpr (VEC) {
-    if (F32) {
-      const float4 a = *(const float4 *)((const float *)row + at);
-      const float4 b = *(const float4 *)((const float *)row + at + 4);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-      const uint4 a = *(const uint4 *)((const uint16_t *)row + at);
-      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      }
-    }
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// Channels at .. at + 7 of a row as they lie in memory (F32: 8 words, else 4). Lanes past the
+// row's n channels load its first ones, so that all of a thread's loads are under way
+// together: under a condition each would be waited for (777 x 5120: 10.4 us).
+template <bool F32>
+struct Raw8 {
+  u32x4_t v[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ void norm_load8(const void *row, int at, int n, Raw8<F32> &x) {
+  const int c = at < n ? at : 0;
+  if constexpr (F32) {
+    x.v[0] = *(const u32x4_t *)((const float *)row + c);
+    x.v[1] = *(const u32x4_t *)((const float *)row + c + 4);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = 0.f;
-      if (at + i < n) x[i] = F32 ? ((const float *)row)[at + i] : bf16_to_f32(((const uint16_t *)row)[at + i]);
-    }
+    x.v[0] = *(const u32x4_t *)((const uint16_t *)row + c);
   }
 }
+
+template <bool F32>
+__device__ __forceinline__ void norm_unpack8(const Raw8<F32> &r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (F32)
+      x[i] = __uint_as_float(r.v[i / 4][i % 4]);
+    else
+      x[i] = __uint_as_float((i & 1) ? r.v[0][i / 2] & 0xFFFF0000u : r.v[0][i / 2] << 16);
+  }
+}
+
+// Channels at .. at + 7 of a row of any alignment, those from n on as 0.
+template <bool F32>
+__device__ __forceinline__ void norm_gather8(const void *row, int at, int n, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = 0.f;
+    if (at + i < n) x[i] = F32 ? ((const float *)row)[at + i] : bf16_to_f32(((const uint16_t *)row)[at + i]);
+  }
+}
+
+// A thread's C times 8 channels of a row, L * 8 apart. VEC: loaded in whole 16 bytes, all at
+// once; otherwise where they are asked for.
+template <int L, int C, bool F32, bool VEC>
+struct RowPart {
+  const void *row;
+  int lane, n;
+  Raw8<F32> raw[VEC ? C : 1];
+
+  __device__ __forceinline__ RowPart(const void *row, int lane, int n) : row(row), lane(lane), n(n) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) norm_load8<F32>(row, (lane + j * L) * 8, n, raw[j]);
+    }
+  }
+
+  __device__ __forceinline__ void get(int j, float (&v)[8]) const {
+    if constexpr (VEC)
+      norm_unpack8<F32>(raw[j], v);
+    else
+      norm_gather8<F32>(row, (lane + j * L) * 8, n, v);
+  }
+};
 
 template <bool VEC>
 __device__ __forceinline__ void norm_store8(void *row, bool f32, int at, int n, const float (&x)[8]) {
@@ -125,7 +163,7 @@ __device__ __forceinline__ uint2 to_8bit(const float (&y)[8], float scale, bool 
     for (int i = 0; i < 8; ++i) t[i] = scale > 0.f ? y[i] / scale : 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = fminf(fmaxf(t[i], -largest), largest);
+  for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_fmed3f(t[i], -largest, largest);  // no NaN is left
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -153,39 +191,25 @@ __global__ __launch_bounds__(L > kNormThreads ? L : kNormThreads) void rmsnorm_k
   for (long long row = (long long)blockIdx.x * kRows + threadIdx.x / L; row < a.T; row += (long long)gridDim.x * kRows) {
     const char *x = (const char *)a.x + row * a.x_stride * (X32 ? 4 : 2);
     const char *r = (const char *)a.r + row * a.r_stride * (RK == 2 ? 4 : 2);
-    float s[C][8], w[C][8];
+    const RowPart<L, C, X32, VEC> px(x, lane, a.d);
+    const RowPart<L, C, RK == 2, VEC && RK != 0> pr(r, lane, a.d);
+    const RowPart<L, C, false, VEC> pw(a.weight, lane, a.d);
+    float s[C][8], sum = 0.f;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      const int at = (lane + j * L) * 8;
-      if (at < a.d) norm_load8<X32, VEC>(x, at, a.d, s[j]);
-    }
-    if constexpr (RK != 0) {
-      float v[C][8];
+      px.get(j, s[j]);
+      if constexpr (RK != 0) {
+        float v[8];
+        pr.get(j, v);
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const int at = (lane + j * L) * 8;
-        if (at < a.d) norm_load8<RK == 2, VEC>(r, at, a.d, v[j]);
+        for (int i = 0; i < 8; ++i) s[j][i] += v[i];
       }
+      const bool in = (lane + j * L) * 8 < a.d;
 #pragma unroll
-      for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[j][i] += v[j][i];
-    }
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int at = (lane + j * L) * 8;
-      if (at < a.d) norm_load8<false, VEC>(a.weight, at, a.d, w[j]);
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int at = (lane + j * L) * 8;
-      if (at >= a.d) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[j][i] = w[j][i] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        s[j][i] = in ? s[j][i] : 0.f;
+        sum = fmaf(s[j][i], s[j][i], sum);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(s[j][i], s[j][i], sum);
     }
     sum = row_sum<L>(sum, (float *)sm);
     if (RK != 0 && a.h != nullptr) {
@@ -200,10 +224,13 @@ __global__ __launch_bounds__(L > kNormThreads ? L : kNormThreads) void rmsnorm_k
     uint32_t top[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) {
+      float w[8];
+      pw.get(j, w);
+      const bool in = (lane + j * L) * 8 < a.d;  // the others' weights are not theirs
       top[j] = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s[j][i] = s[j][i] * inv * (w[j][i] + one);
+        s[j][i] = s[j][i] * inv * ((in ? w[i] : 0.f) + one);
         top[j] = max(top[j], __float_as_uint(s[j][i]) & 0x7FFFFFFFu);
       }
     }
@@ -217,6 +244,7 @@ __global__ __launch_bounds__(L > kNormThreads ? L : kNormThreads) void rmsnorm_k
       continue;
     }
     uint8_t *y = (uint8_t *)a.y + row * a.y_stride;
+    const int shift = a.group == a.d ? 30 : a.group == 128 ? 7 : 6, mask = (1 << shift) - 1;  // d < 2^30
     uint32_t all = 0;
     if (a.group == a.d) {
 #pragma unroll
@@ -234,7 +262,7 @@ __global__ __launch_bounds__(L > kNormThreads ? L : kNormThreads) void rmsnorm_k
       }
       if (at >= a.d) continue;
       const float scale = group_scale(m, largest);
-      if (at % a.group == 0) scales[at / a.group] = scale;
+      if ((at & mask) == 0) scales[at >> shift] = scale;
       const uint2 q = to_8bit(s[j], scale, a.out == kOutE4m3);
       if constexpr (VEC) {
         *(uint2 *)(y + at) = q;
