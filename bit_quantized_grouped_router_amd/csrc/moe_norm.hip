@@ -10,8 +10,9 @@
 // squares and its output. L threads take a row, 8 channels (one 16-byte or two)
 // at a time and C times, so that a group of 64 or 128 channels is 8 or 16
 // neighbouring lanes and its maximum three or four DPP steps. us: 8192 x 2048 in fp32
-// with an fp32 residual 42.8 (235 MB, 5.5 TB/s); 777 x 5120 in bf16 to e4m3 10.5 (28 MB,
-// 2.7 TB/s: three rows a CU, half of the time vector instructions); one row 2.3.
+// with an fp32 residual 42.8 (235 MB, 5.5 TB/s); 777 x 5120 in bf16 to e4m3 10.0 (28 MB,
+// 2.8 TB/s: three or four rows a CU, so that little overlaps); one row 2.3. Rows whose
+// strides are no multiples of 8 are read element by element: 4096 x 12001 640.
 #include "moe_norm.h"
 
 namespace moe {
@@ -22,7 +23,8 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 // Channels at .. at + 7 of a row as they lie in memory (F32: 8 words, else 4). Lanes past the
 // row's n channels load its first ones, so that all of a thread's loads are under way
-// together: under a condition each would be waited for (777 x 5120: 10.4 us).
+// together: under a condition each would be waited for (4096 rows in bf16 with an fp32
+// residual, 5120 channels 43 us, so 38; 16384 channels 216 and 151).
 template <bool F32>
 struct Raw8 {
   u32x4_t v[F32 ? 2 : 1];
