@@ -5,6 +5,7 @@
 //            heads and the channels of max(q lo, q hi), the most that any key of
 //            the page could score, summed over the heads. With q+ = sum over the
 //            heads of max(q, 0) and q- = sum of min(q, 0) it is q- . lo + q+ . hi
+//            where all are finite; otherwise it is worked out head by head
 //   pages    the first `first`, the last `recent` (the token's own among them)
 //            and of the others the `top` with the best scores, ties to the lowest
 //   output   softmax attention over the keys of those pages
@@ -543,12 +544,29 @@ __device__ __forceinline__ double dpp_add64(double v) {
   return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// A lane's 64-bit terms of a page's score, summed, as the score's key; wave-uniform.
+__device__ __forceinline__ uint32_t score_key(double s) {
+  s = dpp_add64<0xb1, 0xf>(s);
+  s = dpp_add64<0x4e, 0xf>(s);
+  s = dpp_add64<0x141, 0xf>(s);
+  s = dpp_add64<0x140, 0xf>(s);
+  s = dpp_add64<0x142, 0xa>(s);
+  s = dpp_add64<0x143, 0xc>(s);
+  return __builtin_amdgcn_readlane(logit_key((float)s), kWave - 1);
+}
+
+// True where one of the two bf16 of a word is an infinity or a NaN.
+__device__ __forceinline__ bool any_not_finite(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
 // A wavefront's terms of a page's score in 64 bits: lane l has D / 32 channels, of
 // the smallest keys in the lower half, of the largest in the upper.
 template <int D>
 struct ExactScore {
   static constexpr int N = D / 32;
   double q[N];
+  bool odd;  // one of this lane's queries is an infinity or a NaN
 
   // N bf16 from p on, as 32-bit words.
   __device__ __forceinline__ static void words(const uint16_t *p, uint32_t (&w)[N / 2]) {
@@ -567,9 +585,12 @@ struct ExactScore {
   __device__ __forceinline__ void load(const uint16_t *queries, int G, int lane) {
 #pragma unroll
     for (int e = 0; e < N; ++e) q[e] = 0.0;
+    odd = false;
     for (int g = 0; g < G; ++g) {
       uint32_t w[N / 2];
       words(queries + g * D + (lane & 31) * N, w);
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) odd |= any_not_finite(w[e]);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const float x = (e & 1) ? __uint_as_float(w[e / 2] & 0xFFFF0000u) : __uint_as_float(w[e / 2] << 16);
@@ -579,18 +600,31 @@ struct ExactScore {
   }
 
   // The score's key, of a page's words; wave-uniform.
-  __device__ __forceinline__ uint32_t key(const uint32_t (&w)[N / 2]) const {
+  __device__ __forceinline__ uint32_t key(const uint32_t (&w)[N / 2], const uint16_t *page, const uint16_t *queries,
+                                          int G, int lane) const {
+    bool wild = odd;
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) wild |= any_not_finite(w[e]);
+    if (__builtin_amdgcn_ballot_w64(wild) != 0) return by_heads(page, queries, G, lane);
     double s = 0.0;
 #pragma unroll
     for (int e = 0; e < N; ++e)
       s = fma((double)((e & 1) ? __uint_as_float(w[e / 2] & 0xFFFF0000u) : __uint_as_float(w[e / 2] << 16)), q[e], s);
-    s = dpp_add64<0xb1, 0xf>(s);
-    s = dpp_add64<0x4e, 0xf>(s);
-    s = dpp_add64<0x141, 0xf>(s);
-    s = dpp_add64<0x140, 0xf>(s);
-    s = dpp_add64<0x142, 0xa>(s);
-    s = dpp_add64<0x143, 0xc>(s);
-    return __builtin_amdgcn_readlane(logit_key((float)s), kWave - 1);
+    return score_key(s);
+  }
+
+  // The same by the formula itself: an infinite bound counts where it is the larger product
+  // only, and 0 times it is NaN, neither of which q- . lo + q+ . hi knows.
+  __device__ __forceinline__ static uint32_t by_heads(const uint16_t *page, const uint16_t *queries, int G, int lane) {
+    double s = 0.0;
+    for (int c = lane; c < D; c += kWave) {
+      const double lo = bf16_to_f32(page[c]), hi = bf16_to_f32(page[D + c]);
+      for (int g = 0; g < G; ++g) {
+        const double x = bf16_to_f32(queries[g * D + c]), a = x * lo, b = x * hi;
+        s += a != a || a > b ? a : b;  // NaN where either is
+      }
+    }
+    return score_key(s);
   }
 };
 
@@ -793,10 +827,11 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
         });
         __syncthreads();
         for (int i = wave; i < near; i += waves) {
-          const long long page = (long long)__builtin_amdgcn_readfirstlane(list_place[i]) * dm.Hkv + head;
-          score.words(sel.bounds + page * 2 * D + lane * (D / 32), words);
+          const uint16_t *page =
+              sel.bounds + ((long long)__builtin_amdgcn_readfirstlane(list_place[i]) * dm.Hkv + head) * 2 * D;
+          score.words(page + lane * (D / 32), words);
           if (i == wave) score.load((const uint16_t *)queries, G, lane);
-          const uint32_t k = score.key(words);
+          const uint32_t k = score.key(words, page, (const uint16_t *)queries, G, lane);
           if (lane == 0) list_key[i] = k;
         }
         __syncthreads();
@@ -827,9 +862,10 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
           while (todo != 0) {
             const int w = __builtin_ctzll(todo);
             todo &= todo - 1;
-            const int pg = __builtin_amdgcn_readlane(entry, w);
-            score.words(sel.bounds + ((long long)pg * dm.Hkv + head) * 2 * D + lane * (D / 32), words);
-            const uint32_t e = score.key(words);
+            const uint16_t *page =
+                sel.bounds + ((long long)__builtin_amdgcn_readlane(entry, w) * dm.Hkv + head) * 2 * D;
+            score.words(page + lane * (D / 32), words);
+            const uint32_t e = score.key(words, page, (const uint16_t *)queries, G, lane);
             k = lane == w ? e : k;
           }
           if constexpr (R == 0) {

@@ -586,7 +586,9 @@ size_t moe_kv4_sparse_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t 
  * key inside its bounds could score, summed over the query heads of the cache head:
  *   sum_h sum_c max(q[t][h][c] * lo[c], q[t][h][c] * hi[c])
  * summed in 64 bits and rounded to fp32; ties go to the lower page of the sequence, a
- * NaN ranks below every number. Pages that do not exist are not taken.
+ * NaN ranks below every number. 0 times an infinity is NaN, and so is a maximum of which
+ * one side is; an infinite bound on the side that is not the larger does not count. Pages
+ * that do not exist are not taken.
  *   out[t][h] = moe_kv4_attention's, over the keys of those pages at positions up to the
  *   token's own. Where nothing is left out it is causal attention without a window.
  *   bounds  as moe_kv4_bounds leaves them

@@ -479,3 +479,43 @@ def test_scores_next_to_the_largest_number(new):
         for t in range(b.T):
             p = B.select(q[t].double().cpu().numpy(), bb[:, 0], bb[:, 1], np.ones(len(bb), bool), 3200 + t, 16, 40, 1, 1)
             assert blocks[t, 0].tolist() == p.tolist()
+
+
+@pytest.mark.parametrize("new,past,width", [([2], 900, 0), ([70], 900, 0), ([2], 3000, 0), ([70], 3000, 0),
+                                            ([300], 3000, 2100), ([2], 3000, 9000)])
+@pytest.mark.parametrize("D", [64, 256])
+def test_infinite_bounds_under_any_sign(new, past, width, D):
+    """Infinite bounds on either side, under channels whose queries are all positive, all negative, of
+    both signs or zero, and infinite queries: a page's score is the formula's, term by term."""
+    rng = np.random.default_rng(41)
+    b = Batch(rng, new, [past], 16)
+    if width:
+        b.table = np.concatenate([b.table, np.zeros((1, width - b.table.shape[1]), dtype=b.table.dtype)], axis=1)
+        b.dev = (i32(b.table), *b.dev[1:])
+    c = filled(rng, b, 2, D)
+    v = np.sort(rng.standard_normal((c.num_pages, 2, 2, D)), axis=2)
+    for kind, (side, value) in enumerate(((0, -np.inf), (1, np.inf), (0, np.inf), (1, -np.inf), (0, -np.inf))):
+        at = rng.random(c.num_pages) < 0.12
+        h, ch = rng.integers(0, 2, c.num_pages), rng.integers(0, D, c.num_pages)
+        v[at, h[at], side, ch[at]] = value
+        if kind >= 2:  # both sides, alike or not
+            v[at, h[at], 1 - side, ch[at]] = np.inf if kind == 4 else value
+    bounds = dev_bits(round_to_bf16_bits(v)).view(BF16)
+    q64, q = queries(rng, b.T, 6, D)
+    for ch in range(D):  # a sign for each channel, or none
+        sign = ch % 4
+        if sign < 2:
+            q64[:, :, ch] = np.abs(q64[:, :, ch]) * (1 - 2 * sign)
+        elif ch % 16 == 3:
+            q64[:, ch % 6, ch] = 0.0
+    q64[1, 1, 4], q64[1, 4, 5] = np.inf, -np.inf
+    q = torch.from_numpy(q64).cuda().to(BF16)
+    bb = bf16_to_f64(host_bits(bounds))
+    ok = np.ones(b.table.shape[1], bool)
+    for top in (4, 25, 45):
+        blocks = torch.empty((b.T, 2, top + 2), dtype=torch.int32, device="cuda")
+        M.moe_kv4_sparse_attention(c, bounds, q, *b.dev, b.T, top, blocks=blocks)
+        for t in range(b.T):
+            for h in range(2):
+                p = B.select(q64[t, 3 * h:3 * h + 3], bb[b.table[0], h, 0], bb[b.table[0], h, 1], ok, past + t, 16, top, 1, 1)
+                assert blocks[t, h].tolist() == p.tolist() + [-1] * (top + 2 - len(p)), (top, t, h)
