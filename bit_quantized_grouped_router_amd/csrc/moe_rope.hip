@@ -44,12 +44,15 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// Sine and cosine of a: the nearest quarter turn is taken off and the rest, at most pi /
-// 4, goes into the Taylor series, whose next terms are below 2^-45. Turns are a times 1 /
-// (2 pi) in two parts, so that no more is lost for large angles than for small ones.
-__device__ __forceinline__ void sincos64(double a, double &sn, double &cs) {
+// Sine and cosine of p f: the nearest quarter turn is taken off and the rest, at most pi /
+// 4, goes into the Taylor series, whose next terms are below 2^-45. The product of a 32-bit
+// position and fp32's 24 bits can have 55, so what fp64 rounds off it (2^-23 at position
+// 2^31) goes along. Turns are it times 1 / (2 pi) in two parts, so that no more is lost
+// for large angles than for small ones.
+__device__ __forceinline__ void sincos64(double p, double f, double &sn, double &cs) {
   constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnRest = -0x1.6b01ec5417056p-57;
-  const double t = a * kTurn, rest = fma(a, kTurnRest, fma(a, kTurn, -t));
+  const double a = p * f, off = fma(p, f, -a);
+  const double t = a * kTurn, rest = fma(off, kTurn, fma(a, kTurnRest, fma(a, kTurn, -t)));
   const double quarter = rint(4.0 * t);
   const double x = (fma(-0.25, quarter, t) + rest) * 6.28318530717958647693, y = x * x;
   double s = 1.0 / 6227020800.0, c = -1.0 / 87178291200.0;
@@ -76,7 +79,7 @@ __device__ __forceinline__ void lane_turn(const Rope &rope, int position, int at
   const int lane = threadIdx.x & (kWave - 1), half = rope.rot / 2;
   for (int i = lane; i < half; i += kWave) {
     double sn, cs;
-    sincos64((double)position * (double)rope.freqs[i], sn, cs);
+    sincos64(position, rope.freqs[i], sn, cs);
     lds.turn[i] = make_float2((float)(cs * rope.magnitude), (float)(sn * rope.magnitude));
   }
   wave_lds_sync();

@@ -382,3 +382,29 @@ def test_products_are_rounded_apart(inter, first):
     y = M.moe_rope(x, r, pos)
     a, b = x[..., lo], x[..., hi]
     assert torch.equal(y[..., lo], a * c - b * s) and torch.equal(y[..., hi], a * s + b * c)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("first", [2 ** 29 - 150, 2 ** 30 + 12345, 2 ** 31 - 300, -2 ** 31])
+def test_angles_of_the_farthest_positions(inter, first):
+    """Position times frequency has up to 55 bits; cosine and sine are those of the whole product,
+    rounded to fp32 but where that is next to a tie."""
+    T, D = 300, 128
+    r, pos = M.Rope.make(D, interleaved=inter), np.arange(first, first + T)
+    unit = torch.zeros((T, 1, D), device="cuda")
+    lo, hi = (slice(0, None, 2), slice(1, None, 2)) if inter else (slice(0, D // 2), slice(D // 2, None))
+    unit[..., lo] = 1
+    u = M.moe_rope(unit, r, i32(pos))
+    f = r.freqs.double().cpu().numpy()
+    angle = pos.astype(np.float64)[:, None] * f
+    # what fp64 rounds off the product, in whole numbers of 2^-60 (a frequency is at most 1 and at least 10000^-1)
+    whole = lambda v: int(v * 2.0 ** 60) if abs(v) < 2 else int(v) * 2 ** 60 + int((v - int(v)) * 2.0 ** 60)
+    off = np.array([[(int(p) * whole(float(g)) - whole(float(a))) * 2.0 ** -60 for g, a in zip(f, row)]
+                    for p, row in zip(pos, angle)])
+    assert (np.abs(off) <= 2.0 ** -23).all() and ((off != 0).any() or abs(first) < 2 ** 30)
+    cos, sin = np.cos(angle), np.sin(angle)
+    cos, sin = cos - off * sin - off ** 2 / 2 * cos, sin + off * cos - off ** 2 / 2 * sin  # off^3 is below 2^-69
+    for got, want in ((u[:, 0, lo], cos), (u[:, 0, hi], sin)):
+        got = got.cpu().numpy()
+        # half a step, and 2^-44 as in test_products_are_rounded_apart
+        assert (np.abs(got.astype(np.float64) - want) <= np.spacing(np.abs(got)).astype(np.float64) / 2 + 2.0 ** -44).all()
