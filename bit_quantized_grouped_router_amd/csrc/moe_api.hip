@@ -183,6 +183,13 @@ moe_status check_kv4_cache(const moe_kv4_cache *c, const moe_kv4_batch *b) {
   return check_ptr(b->kv_len);
 }
 
+// An output at the address of one of the cache's planes or of the batch's arrays.
+bool at_kv4_cache(const void *p, const moe_kv4_cache *c, const moe_kv4_batch *b) {
+  for (const moe_kv4_plane *pl : {&c->k, &c->v})
+    if (p == pl->codes || p == pl->scales || p == pl->biases) return true;
+  return p == b->page_table || p == b->cu || p == b->kv_len;
+}
+
 Kv4Plane to_kv4_plane(const moe_kv4_plane &p) { return Kv4Plane{p.codes, p.scales, p.biases}; }
 
 Kv4Batch to_kv4_batch(const moe_kv4_batch *b, int32_t T) {
@@ -655,7 +662,10 @@ moe_status moe_kv4_rope_append(const moe_kv4_dims *dm, const moe_kv4_cache *cach
   MOE_TRY(check_ptr(v));
   MOE_TRY(check_ptr(q_out));
   if (q == q_out && (dtype != MOE_BF16 || (q_stride != q_out_stride && T > 1))) return MOE_E_INVALID;
-  if (q_out == k || q_out == v) return MOE_E_INVALID;  // other wavefronts still read them
+  // other wavefronts still read or write them
+  if (q_out == k || q_out == v || (const void *)q_out == rope->freqs || (q_norm != nullptr && q_out == q_norm->weight) ||
+      (k_norm != nullptr && q_out == k_norm->weight) || at_kv4_cache(q_out, cache, batch))
+    return MOE_E_INVALID;
   const RopeAppend a{q, k, v, q_stride, k_stride, v_stride, q_out, q_out_stride, to_head_norm(q_norm),
                      to_head_norm(k_norm)};
   return hip_status(launch_kv4_rope_append(to_kv4_dims(dm), to_kv4_plane(cache->k), to_kv4_plane(cache->v),
@@ -668,6 +678,7 @@ moe_status moe_kv4_bounds(const moe_kv4_dims *dm, const moe_kv4_cache *cache, in
   if (T == 0) return MOE_OK;
   MOE_TRY(check_kv4_cache(cache, batch));
   MOE_TRY(check_ptr(bounds));
+  if (at_kv4_cache(bounds, cache, batch)) return MOE_E_INVALID;
   return hip_status(launch_kv4_bounds(to_kv4_dims(dm), to_kv4_plane(cache->k), to_kv4_batch(batch, T), bounds,
                                       as_stream(stream)));
 }
@@ -699,6 +710,13 @@ moe_status moe_kv4_sparse_attention(const moe_kv4_dims *dm, const moe_kv4_cache 
   const Kv4Dims d = to_kv4_dims(dm);
   if (ws_bytes < kv4_sparse_ws(d, T, sel)) return MOE_E_WORKSPACE;
   MOE_TRY(check_ptr(ws));
+  // one is written while others are still read
+  if (out == bounds || out == ws || at_kv4_cache(out, cache, batch) || ws == q || ws == bounds ||
+      at_kv4_cache(ws, cache, batch))
+    return MOE_E_INVALID;
+  if (blocks != nullptr && ((const void *)blocks == q || (const void *)blocks == out || (const void *)blocks == bounds ||
+                            blocks == ws || at_kv4_cache(blocks, cache, batch)))
+    return MOE_E_INVALID;
   return hip_status(launch_kv4_sparse(d, to_kv4_plane(cache->k), to_kv4_plane(cache->v), to_kv4_batch(batch, T), sel,
                                       out, out_stride, scale, ws, as_stream(stream)));
 }

@@ -547,6 +547,7 @@ moe_status moe_rope(int32_t T, int32_t H, int32_t D, const void *x, int64_t x_st
  *   q_norm, k_norm  may be NULL
  *   q_out     bf16 [T][Hq][D], out; may be q itself if that is bf16, with the same
  *             stride (MOE_E_INVALID with another), and overlaps nothing else
+ *             (MOE_E_INVALID at one address)
  * A token without a place in the cache has its queries turned and nothing written;
  * rows of no sequence are left as they are. Precondition as for moe_kv4_append.
  */
@@ -563,7 +564,8 @@ moe_status moe_kv4_rope_append(const moe_kv4_dims *dm, const moe_kv4_cache *cach
  * last token; other pages' bounds are left as they are. Call it after every write (the
  * attention below relies on the bounds of full pages).
  *   bounds  bf16 [num_pages][Hkv][2][D]: smallest, then largest, of the keys as
- *           moe_kv4_read gives them in bf16 (a zero is +0); NaN where a key is
+ *           moe_kv4_read gives them in bf16 (a zero is +0); NaN where a key is. Overlaps
+ *           neither cache nor batch (MOE_E_INVALID at one address)
  */
 moe_status moe_kv4_bounds(const moe_kv4_dims *dm, const moe_kv4_cache *cache, int32_t T,
                           uint16_t *bounds, const moe_kv4_batch *batch, void *stream);
@@ -595,7 +597,8 @@ size_t moe_kv4_sparse_attention_workspace_bytes(const moe_kv4_dims *dm, int32_t 
  *   blocks  int32 [T][Hkv][first + recent + top], out, or NULL: the pages taken, as their
  *           numbers 0, 1, .. in the sequence, ascending, -1 behind them
  *   other arguments as for moe_kv4_attention; a token past max_new of its sequence, or of
- *   no sequence, is left out (its rows of out and blocks stay as they are)
+ *   no sequence, is left out (its rows of out and blocks stay as they are). out (unless it
+ *   is q), blocks and ws overlap nothing (MOE_E_INVALID at one address)
  * Limits, besides moe_kv4_attention's: max_pages <= 2^20, Hq / Hkv <= 64
  * (MOE_E_UNSUPPORTED).
  */

@@ -151,6 +151,28 @@ def test_sparse_refusals(L):
     assert L.moe_kv4_sparse_attention_workspace_bytes(dims(), 0, 0, M.MoeKv4Pages(5, 1, 2)) == 0
 
 
+PLANES = M.MoeKv4Cache(*(0x2000000 + 0x100000 * i for i in range(6)))
+ARRAYS = M.MoeKv4Batch(*(0x3000000 + 0x100000 * i for i in range(3)))
+FREQS, QW, KW, WS = (0x4000000 + 0x100000 * i for i in range(4))
+HELD = [getattr(c, f) for c in (PLANES, ARRAYS) for f, _ in c._fields_]
+
+
+def test_outputs_at_inputs_addresses(L):
+    """What a call writes lies nowhere that its other workgroups read or write."""
+    for at in HELD + [FREQS, QW, KW, H, W]:
+        assert write(L, c=PLANES, b=ARRAYS, r=spec(freqs=FREQS), qn=M.MoeHeadNorm(QW, 1e-6, 0),
+                     kn=M.MoeHeadNorm(KW, 1e-6, 0), out=at) == INVALID, hex(at)
+    for at in HELD:
+        assert L.moe_kv4_bounds(dims(), PLANES, 3, at, ARRAYS, None) == INVALID, hex(at)
+    own = dict(c=PLANES, b=ARRAYS, ws=WS, blocks=H)
+    for at in HELD + [S, WS]:
+        assert sparse(L, **{**own, "out": at}) == INVALID, hex(at)
+    for at in HELD + [S, WS, X, Y]:
+        assert sparse(L, **{**own, "blocks": at}) == INVALID, hex(at)
+    for at in HELD + [S, X, Y, H]:
+        assert sparse(L, **{**own, "ws": at}) == INVALID, hex(at)
+
+
 def test_sparse_workspace_is_bounded(L):
     """Score keys are held for a part of a long call's rows: 256 MB and what the rows' lists take."""
     dm = dims(B=1, Hq=64, Hkv=8, page=16, max_pages=8192, num_pages=8192)
