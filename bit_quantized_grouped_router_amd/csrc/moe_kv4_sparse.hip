@@ -530,9 +530,9 @@ __device__ __forceinline__ int first16_sum(int v) {
 
 // What the selection leaves for the attention.
 struct SelectOut {
-  int32_t *table;  // [rows][Hkv][size]
+  int32_t *table;  // [rows][Hkv][width]
   int32_t *len;    // [rows]
-  int size;
+  int width;       // no list is longer
 };
 
 // v plus the value a DPP lane pattern brings in (see wave_sum_dpp).
@@ -897,8 +897,9 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
   int seen = wave > 0 ? __builtin_amdgcn_readlane(seen_upto, wave > 0 ? wave - 1 : 0) : 0;  // ties before this one's
   int at = wave > 0 ? __builtin_amdgcn_readlane(at_upto, wave > 0 ? wave - 1 : 0) : 0;      // its first place
   const int total = __builtin_amdgcn_readlane(at_upto, kWave - 1);
-  const long long row = item * out.size;
-  int32_t *blocks = sel.blocks == nullptr ? nullptr : sel.blocks + ((long long)tok * dm.Hkv + head) * out.size;
+  const long long row = item * out.width;
+  const int size = sel.top + sel.first + sel.recent;
+  int32_t *blocks = sel.blocks == nullptr ? nullptr : sel.blocks + ((long long)tok * dm.Hkv + head) * size;
   const uint64_t lower = (1ull << lane) - 1;
   each([&](int c, int entry, uint32_t k) {
     const bool tie = k != 0 && k == least;
@@ -906,7 +907,7 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
     const bool take = k > least || (tie && seen + __builtin_popcountll(tied & lower) < ties);
     const uint64_t taken = __builtin_amdgcn_ballot_w64(take);
     const int to = at + __builtin_popcountll(taken & lower);
-    if (take && to < out.size) {
+    if (take && to < out.width) {
       out.table[row + to] = entry;
       if (blocks != nullptr) blocks[to] = c;
     }
@@ -914,7 +915,7 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
     seen += __builtin_popcountll(tied);
   });
   if (blocks != nullptr)
-    for (int i = total + threadIdx.x; i < out.size; i += blockDim.x) blocks[i] = -1;
+    for (int i = total + threadIdx.x; i < size; i += blockDim.x) blocks[i] = -1;
   if (head == 0 && threadIdx.x == 0) {
     // whole pages, but for the token's own, which ends with it (and is the last)
     const long long cap = kv4_capacity(dm);
@@ -934,21 +935,28 @@ struct SparseWs {
   size_t keys, most, queries, table, len, attention, bytes;
 };
 
-// Score keys of a part, while it has more than one row; prompts' query operands have up to the same again.
+// Score keys of a part, while it has more than one row (its lists are no wider); prompts'
+// query operands have up to the same again.
 constexpr size_t kPartBytes = 256u << 20;
 
 static size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-static Kv4Dims selected_dims(const Kv4Dims &dm, int rows, int size) {
+// Pages that a list has room for: no more are taken than the sequence's table holds.
+static int list_width(const Kv4Dims &dm, const Kv4Select &sel) {
+  const int size = sel.top + sel.first + sel.recent;
+  return size < dm.max_pages ? size : dm.max_pages;
+}
+
+static Kv4Dims selected_dims(const Kv4Dims &dm, int rows, int width) {
   Kv4Dims d = dm;
   d.B = rows;
-  d.max_pages = size;
+  d.max_pages = width;
   return d;
 }
 
 static SparseWs sparse_ws(const Kv4Dims &dm, int T, const Kv4Select &sel) {
   SparseWs w;
-  const int size = sel.top + sel.first + sel.recent;
+  const int width = list_width(dm, sel);
   w.pitch = (dm.max_pages + kScoreTile - 1) / kScoreTile * kScoreTile;
   // The prompt's kernels need 64 tokens a sequence and rows for its token tiles (us for
   // the scores of 1500 tokens behind 60,000, D = 128: 5.3 + 22.9 us with, 39 without).
@@ -973,14 +981,14 @@ static SparseWs sparse_ws(const Kv4Dims &dm, int T, const Kv4Select &sel) {
   if (w.prompt && rows > kPartBytes / 2 / (slot / 16)) rows = kPartBytes / 2 / (slot / 16);
   if (rows < 1) rows = 1;
   w.rows = rows < (size_t)T ? (int)rows : T;
-  const size_t full = kv4_attention_ws(selected_dims(dm, w.rows, size), w.rows, 1, 0, true);
+  const size_t full = kv4_attention_ws(selected_dims(dm, w.rows, width), w.rows, 1, 0, true);
   const int rest = T % w.rows;
-  const size_t last = rest ? kv4_attention_ws(selected_dims(dm, rest, size), rest, 1, 0, true) : 0;
+  const size_t last = rest ? kv4_attention_ws(selected_dims(dm, rest, width), rest, 1, 0, true) : 0;
   w.keys = 0;
   w.most = align256(w.keys + w.rows * row);
   w.queries = align256(w.most + (size_t)w.rows * dm.Hkv * w.chunks * kScoreWaves * 4);
   w.table = align256(w.queries + (w.prompt ? slot * (w.rows / 16 + 4 + dm.B) : 0));
-  w.len = align256(w.table + (size_t)w.rows * dm.Hkv * size * 4);
+  w.len = align256(w.table + (size_t)w.rows * dm.Hkv * width * 4);
   w.attention = align256(w.len + (size_t)w.rows * 4);
   w.bytes = w.attention + (full > last ? full : last);
   return w;
@@ -1030,9 +1038,9 @@ static hipError_t launch_selection(const Kv4Dims &dm, const Kv4Batch &bt, const 
 hipError_t launch_kv4_sparse(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Plane &vc, const Kv4Batch &bt,
                              const Kv4Select &sel, uint16_t *out, long long out_stride, float scale, void *ws,
                              hipStream_t s) {
-  const int size = sel.top + sel.first + sel.recent;
+  const int width = list_width(dm, sel);
   const SparseWs w = sparse_ws(dm, bt.T, sel);
-  const SelectOut so{(int32_t *)((char *)ws + w.table), (int32_t *)((char *)ws + w.len), size};
+  const SelectOut so{(int32_t *)((char *)ws + w.table), (int32_t *)((char *)ws + w.len), width};
   for (int row0 = 0; row0 < bt.T; row0 += w.rows) {
     const ScorePart part{(uint32_t *)((char *)ws + w.keys), (uint32_t *)((char *)ws + w.most), row0,
                          bt.T - row0 < w.rows ? bt.T - row0 : w.rows, w.pitch, w.chunks, w.steps, w.tiles,
@@ -1044,7 +1052,7 @@ hipError_t launch_kv4_sparse(const Kv4Dims &dm, const Kv4Plane &kc, const Kv4Pla
     const Kv4Batch rows{so.table, nullptr, so.len, part.rows, true};
     const Kv4Attn at{sel.q + (long long)row0 * sel.q_stride, out + (long long)row0 * out_stride, sel.q_stride,
                      out_stride, 1, scale, false, 0, 0, 0, 0, 0};
-    e = launch_kv4_attention(selected_dims(dm, part.rows, size), kc, vc, rows, at, (char *)ws + w.attention, s);
+    e = launch_kv4_attention(selected_dims(dm, part.rows, width), kc, vc, rows, at, (char *)ws + w.attention, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -182,6 +182,17 @@ def test_sparse_workspace_is_bounded(L):
     assert 256 << 20 <= most <= 300 << 20
 
 
+def test_sparse_workspace_of_a_budget_past_the_table(L):
+    """Lists are as wide as the page table at the most, whatever a token may take."""
+    for T, new, Hq, Hkv, width in ((32768, 32768, 64, 8, 64), (1, 1, 16, 2, 40), (64, 1, 16, 2, 512)):
+        dm = dims(B=1 if new == T else T, Hq=Hq, Hkv=Hkv, max_pages=width, num_pages=4096)
+        need = lambda top: L.moe_kv4_sparse_attention_workspace_bytes(dm, T, new, M.MoeKv4Pages(top, 1, 1))
+        assert need(width - 2) == need(width - 1) == need(4094) > need(1), (T, width)
+    most = L.moe_kv4_sparse_attention_workspace_bytes(dims(B=1, Hq=64, Hkv=8, max_pages=4096, num_pages=4096), 2 ** 20,
+                                                      2 ** 20, M.MoeKv4Pages(4094, 1, 1))
+    assert 512 << 20 <= most <= 700 << 20  # keys and lists
+
+
 def test_binding_refusals():
     """Shapes, types and devices that the binding itself refuses (nothing reaches the library)."""
     x = torch.zeros(2, 8)

@@ -519,3 +519,19 @@ def test_infinite_bounds_under_any_sign(new, past, width, D):
             for h in range(2):
                 p = B.select(q64[t, 3 * h:3 * h + 3], bb[b.table[0], h, 0], bb[b.table[0], h, 1], ok, past + t, 16, top, 1, 1)
                 assert blocks[t, h].tolist() == p.tolist() + [-1] * (top + 2 - len(p)), (top, t, h)
+
+
+@pytest.mark.parametrize("new,past", [([1] * 5, [0, 70, 300, 16, 155]), ([90], [200])])
+def test_a_budget_past_the_table(new, past):
+    """More pages allowed than the table holds: as many as it holds, and the list ends there."""
+    rng = np.random.default_rng(43)
+    b = Batch(rng, new, past, 16)
+    W = b.table.shape[1]
+    c = filled(rng, b, 2, 128)
+    bounds = all_bounds(c, b)
+    q64, q = queries(rng, b.T, 8, 128)
+    lists = [torch.full((b.T, 2, top + 2), -7, dtype=torch.int32, device="cuda") for top in (W - 2, 4000)]
+    outs = [M.moe_kv4_sparse_attention(c, bounds, q, *b.dev, b.max_new(), x.shape[2] - 2, blocks=x) for x in lists]
+    assert torch.equal(*outs) and torch.equal(lists[1][:, :, :W], lists[0]) and (lists[1][:, :, W:] == -1).all()
+    want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, 128 ** -0.5)
+    check(outs[0], want, tol, "everything taken")
