@@ -898,7 +898,7 @@ class Rope:
             # index of the pair that turns so many times in the trained positions
             at = lambda turns: rot * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
             lo, hi = max(math.floor(at(fast)), 0), math.ceil(at(slow))
-            keep = [1.0 - min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(n)]
+            keep = [0.0 if i >= hi else 1.0 if i <= lo else 1.0 - (i - lo) / (hi - lo) for i in range(n)]
             f = [v * k + v / factor * (1.0 - k) for v, k in zip(f, keep)]
             magnitude = 0.1 * math.log(factor) + 1.0
         elif scaling not in ("none", "base"):

@@ -233,6 +233,21 @@ def test_frequencies():
             f(**bad)
 
 
+@pytest.mark.parametrize("trained", [1, 6, 7, 40, 128, 300, 4096, 10 ** 6])
+@pytest.mark.parametrize("fast,slow", [(32.0, 1.0), (64.0, 32.0), (2.0, 1.5), (1e-3, 1e-4)])
+def test_ramp_keeps_and_divides_what_it_says(trained, fast, slow):
+    """Pairs of at least `fast` turns stay and those of at most `slow` are divided, also where every
+    pair is one or the other; what lies between falls from one to the other."""
+    base = M.Rope.make(64, base=1e4, device="cpu").freqs.double()
+    ramp = M.Rope.make(64, base=1e4, scaling="ramp", factor=8.0, trained=trained, fast=fast, slow=slow, device="cpu").freqs
+    turns = trained * base / (2 * math.pi)
+    # the turns of fp32 frequencies, at a border, decide to 2^-20 of it
+    few, many = turns <= slow * (1 - 2.0 ** -20), turns >= fast * (1 + 2.0 ** -20)
+    assert torch.equal(ramp[few], (base[few] / 8).float()) and torch.equal(ramp[many], base[many].float())
+    assert (ramp <= base * (1 + 2.0 ** -24)).all() and (ramp >= base / 8 * (1 - 2.0 ** -24)).all()
+    assert ((ramp / base)[1:] <= (ramp / base)[:-1] * (1 + 2.0 ** -22)).all()
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_oracle_rope_keeps_products():
