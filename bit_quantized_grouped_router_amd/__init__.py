@@ -815,6 +815,8 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     if x.dim() != 2 or x.shape[1] == 0:
         raise MoeError("x must be [T, d], d at least 1")
     T, d = x.shape
+    if T > INT32_MAX or d > INT32_MAX:
+        raise MoeError(f"x is {T} x {d}; the library's integers are 32 bits wide")
     shape = (T, d)
     cur = torch.cuda.current_device()
     _here(cur, _NORM_TENSORS, (x, weight, residual, h, y, scales))
@@ -921,6 +923,8 @@ def moe_rope(x: torch.Tensor, rope: Rope, positions: torch.Tensor, weight=None, 
     if x.dim() != 3:
         raise MoeError("x must be [T, H, D]")
     T, H, D = x.shape
+    if T > INT32_MAX or H > INT32_MAX or D > INT32_MAX:
+        raise MoeError(f"x is {T} x {H} x {D}; the library's integers are 32 bits wide")
     cur = torch.cuda.current_device()
     _here(cur, _ROPE_TENSORS, (x, rope.freqs, positions, weight, out))
     if positions.shape != (T,) or positions.dtype != torch.int32:
@@ -978,6 +982,8 @@ def _bounds(dm: MoeKv4Dims, bounds: torch.Tensor) -> int:
 def moe_kv4_bounds(cache: KV4Cache, bounds: torch.Tensor, page_table, cu, kv_len, T: int, stream=None) -> None:
     """Bring bounds (bf16 [num_pages, Hkv, 2, D]: smallest and largest key of each channel) up to
     date for the pages that the batch's T new tokens lie in. Call it after every write."""
+    if not 0 <= T <= INT32_MAX:
+        raise MoeError(f"T {T} must be 0 .. {INT32_MAX}")
     dm, c, b, s, _, _ = _kv4(cache, page_table, cu, kv_len, (bounds,), stream)
     _check(lib().moe_kv4_bounds(dm, c, T, _bounds(dm, bounds), b, s), "moe_kv4_bounds")
 
@@ -985,6 +991,8 @@ def moe_kv4_bounds(cache: KV4Cache, bounds: torch.Tensor, page_table, cu, kv_len
 def moe_kv4_sparse_attention_workspace_bytes(cache: KV4Cache, T: int, Hq: int, B: int, max_pages: int, max_new: int,
                                              top: int, first: int = 1, recent: int = 1) -> int:
     num_pages, Hkv, page, D = cache.sizes()
+    if max(T, Hq, B, max_pages, top, first, recent) > INT32_MAX:
+        return 0
     dm = MoeKv4Dims(B, Hq, Hkv, D, page, num_pages, max_pages)
     return lib().moe_kv4_sparse_attention_workspace_bytes(dm, T, min(max_new, T), MoeKv4Pages(top, first, recent))
 

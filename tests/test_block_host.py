@@ -207,6 +207,29 @@ def test_binding_refusals():
             M.Rope(bad)
 
 
+def test_sizes_past_32_bits():
+    """Sizes that the C interface's integers would cut to others are refused."""
+    x = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="meta")
+    w, many = x(8), 2 ** 32 + 3
+    for bad in (x(many, 8), x(1, many)):
+        with pytest.raises(M.MoeError, match="32 bits"):
+            M.moe_rmsnorm(bad, w)
+    r = M.Rope(torch.ones(4))
+    for bad in (x(many, 1, 8), x(1, many, 8), x(1, 1, many)):
+        with pytest.raises(M.MoeError, match="32 bits"):
+            M.moe_rope(bad, r, w)
+    g = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t)
+    plane = lambda: M.W4Matrix(g(9, 2, 16, 32, t=torch.uint8), g(9, 2, 16, 1), g(9, 2, 16, 1))
+    c, i = M.KV4Cache(plane(), plane()), lambda *s: torch.zeros(s, dtype=torch.int32)
+    for T in (many, -1):
+        with pytest.raises(M.MoeError, match="T "):
+            M.moe_kv4_bounds(c, g(9, 2, 2, 64), i(1, 4), i(2), i(1), T)
+    ok = dict(cache=c, T=4, Hq=4, B=1, max_pages=4, max_new=4, top=2)
+    assert M.moe_kv4_sparse_attention_workspace_bytes(**ok) > 0
+    for k in ("T", "Hq", "B", "max_pages", "top", "first", "recent"):
+        assert M.moe_kv4_sparse_attention_workspace_bytes(**{**ok, k: 2 ** 32 + 4}) == 0, k
+
+
 def test_frequencies():
     """Each scaling at both ends: the fastest pair, the slowest, and no scaling at factor 1."""
     f = lambda **k: M.Rope.make(device="cpu", **k)
