@@ -535,3 +535,30 @@ def test_a_budget_past_the_table(new, past):
     assert torch.equal(*outs) and torch.equal(lists[1][:, :, :W], lists[0]) and (lists[1][:, :, W:] == -1).all()
     want, tol = K.attention(q64, K.Paged(*host_planes(c), b.table), b.cu, b.len, 128 ** -0.5)
     check(outs[0], want, tol, "everything taken")
+
+
+@pytest.mark.parametrize("new,past", [
+    ([20] * 30, [7 * i % 90 for i in range(30)]),  # tiles of few tokens
+    ([175, 334, 200], [40, 7, 100]),               # prompts; a workgroup's tiles before the part, across its border and in it
+])
+def test_parts_that_end_inside_a_tile(new, past):
+    """Parts of 341 rows, a multiple of no tile, out of place and in place (a tile's earlier rows then
+    hold results already): the oracle's pages and outputs for every row."""
+    rng = np.random.default_rng(44)
+    page, D, Hkv, W = 16, 64, 3, 2 ** 16
+    b = Batch(rng, new, past, page)
+    c = filled(rng, b, Hkv, D)
+    bounds = all_bounds(c, b)
+    q64, q = queries(rng, b.T, 2 * Hkv, D)
+    table = np.concatenate([b.table, np.zeros((b.B, W - b.table.shape[1]), dtype=b.table.dtype)], axis=1)
+    dev = (i32(table), *b.dev[1:])
+    one, two = (M.moe_kv4_sparse_attention_workspace_bytes(c, T, 2 * Hkv, b.B, W, b.max_new(), 3) for T in (341, 342))
+    assert b.T > 341 and one == two  # the 342nd row is another part's
+    blocks = torch.empty((b.T, Hkv, 5), dtype=torch.int32, device="cuda")
+    out = M.moe_kv4_sparse_attention(c, bounds, q, *dev, b.max_new(), 3, blocks=blocks)
+    want, tol, pages, _ = expected(q64, c, bounds, b.table, b.cu, b.len, b.T, 3, 1, 1)
+    assert (blocks.cpu().numpy() == pages).all()
+    check(out, want, tol, "parts")
+    again = torch.empty_like(blocks)
+    M.moe_kv4_sparse_attention(c, bounds, q, *dev, b.max_new(), 3, blocks=again, out=q)
+    assert torch.equal(again, blocks) and torch.equal(q, out)
