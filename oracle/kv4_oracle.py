@@ -104,12 +104,13 @@ class Paged:
 
 
 def attention(q, cache, cu, kv_len, scale, causal=True, window=0, taken=None):
-    """taken, if given (bool [T, heads, pages of the table]): the pages a token attends to. out fp64 [T, Hq, D], and what an implementation may be off by, element by element:
+    """out fp64 [T, Hq, D], and what an implementation may be off by, element by element:
       2^-8 |out|                     the result's rounding to bf16,
       2^-8 sum p s |code - 8|        each weight p s rounded to bf16,
       (n + 64) 2^-24 sum p (55 s + |b|)   fp32 sums of n keys with codes kept as 16 + code,
       2 d sum p |v|                  scores off by d: fp32 sums of 64 products with codes as
                                      16 + code, and an exponential good to 2^-22 of its range.
+    taken, if given (bool [T, heads, pages of the table]): the pages a token attends to.
     """
     T, Hq, D = q.shape
     out, tol = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
