@@ -555,9 +555,12 @@ __device__ __forceinline__ uint32_t score_key(double s) {
   return __builtin_amdgcn_readlane(logit_key((float)s), kWave - 1);
 }
 
-// True where one of the two bf16 of a word is an infinity or a NaN.
-__device__ __forceinline__ bool any_not_finite(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+// True (wave-uniform) where one of n words of two bf16 holds an infinity or a NaN.
+__device__ __forceinline__ bool any_not_finite(const uint32_t *words, int n, int lane) {
+  bool any = false;
+  for (int i = lane; i < n; i += kWave)
+    any |= (words[i] & 0x7F80u) == 0x7F80u || (words[i] & 0x7F800000u) == 0x7F800000u;
+  return __builtin_amdgcn_ballot_w64(any) != 0;
 }
 
 // A wavefront's terms of a page's score in 64 bits: lane l has D / 32 channels, of
@@ -566,7 +569,6 @@ template <int D>
 struct ExactScore {
   static constexpr int N = D / 32;
   double q[N];
-  bool odd;  // one of this lane's queries is an infinity or a NaN
 
   // N bf16 from p on, as 32-bit words.
   __device__ __forceinline__ static void words(const uint16_t *p, uint32_t (&w)[N / 2]) {
@@ -585,12 +587,9 @@ struct ExactScore {
   __device__ __forceinline__ void load(const uint16_t *queries, int G, int lane) {
 #pragma unroll
     for (int e = 0; e < N; ++e) q[e] = 0.0;
-    odd = false;
     for (int g = 0; g < G; ++g) {
       uint32_t w[N / 2];
       words(queries + g * D + (lane & 31) * N, w);
-#pragma unroll
-      for (int e = 0; e < N / 2; ++e) odd |= any_not_finite(w[e]);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const float x = (e & 1) ? __uint_as_float(w[e / 2] & 0xFFFF0000u) : __uint_as_float(w[e / 2] << 16);
@@ -600,12 +599,7 @@ struct ExactScore {
   }
 
   // The score's key, of a page's words; wave-uniform.
-  __device__ __forceinline__ uint32_t key(const uint32_t (&w)[N / 2], const uint16_t *page, const uint16_t *queries,
-                                          int G, int lane) const {
-    bool wild = odd;
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) wild |= any_not_finite(w[e]);
-    if (__builtin_amdgcn_ballot_w64(wild) != 0) return by_heads(page, queries, G, lane);
+  __device__ __forceinline__ uint32_t key(const uint32_t (&w)[N / 2]) const {
     double s = 0.0;
 #pragma unroll
     for (int e = 0; e < N; ++e)
@@ -817,6 +811,14 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
     } else {
       ExactScore<D> score;
       uint32_t words[D / 64];
+      // an infinity or a NaN among the bounds or queries shows in the sums of magnitudes
+      const bool wild = most >= 0x7F800000u;
+      const bool odd = wild && any_not_finite((const uint32_t *)queries, G * D / 2, lane);
+      const auto exact = [&](const uint16_t *page) {
+        if (wild && (odd || any_not_finite((const uint32_t *)page, D, lane)))
+          return score.by_heads(page, (const uint16_t *)queries, G, lane);
+        return score.key(words);
+      };
       if (near <= kWave) {
         each([&](int c, int entry, uint32_t k) {
           if (k >= below && k <= above) {
@@ -831,7 +833,7 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
               sel.bounds + ((long long)__builtin_amdgcn_readfirstlane(list_place[i]) * dm.Hkv + head) * 2 * D;
           score.words(page + lane * (D / 32), words);
           if (i == wave) score.load((const uint16_t *)queries, G, lane);
-          const uint32_t k = score.key(words, page, (const uint16_t *)queries, G, lane);
+          const uint32_t k = exact(page);
           if (lane == 0) list_key[i] = k;
         }
         __syncthreads();
@@ -865,7 +867,7 @@ __global__ __launch_bounds__(kSelectMostWaves *kWave) void kv4_select_kernel(Kv4
             const uint16_t *page =
                 sel.bounds + ((long long)__builtin_amdgcn_readlane(entry, w) * dm.Hkv + head) * 2 * D;
             score.words(page + lane * (D / 32), words);
-            const uint32_t e = score.key(words, page, (const uint16_t *)queries, G, lane);
+            const uint32_t e = exact(page);
             k = lane == w ? e : k;
           }
           if constexpr (R == 0) {
