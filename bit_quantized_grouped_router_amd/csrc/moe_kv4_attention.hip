@@ -33,7 +33,7 @@
 // (offsets, pages, codes) for few short ones. us, one new token a sequence, 16
 // heads on 2: 64 sequences of up to 8101, D = 256 (113 MB) 33.2 and 5.4 for the
 // join, 3.4 TB/s; one of 131,150, D = 128 (38 MB) 16.9 and 6.8; one of 500, D =
-// 256 11.7. 3000 lists of 1024 keys of their own, 8 heads, D = 128: 74.2 (90.1 with
+// 256 11.7. 3000 lists of 1024 keys of their own, 8 heads, D = 128: 74.3 (90.1 with
 // half the columns empty), 90% of it vector instructions: the codes' conversion is 128
 // of 214 a tile, and a workgroup's start and end cost as much as three tiles.
 #include "moe_kv4_device.h"
@@ -820,10 +820,11 @@ static long long kv4_keys(const Kv4Dims &dm, int tokens, int window) {
 // kMinTiles each, and no more than the card's slots over all tasks, or twice
 // that where sequences have one row tile each (work_item() evens those out).
 //
-// Rows that are sequences all have about as many keys as their tables hold, so each
-// takes the same number of workgroups, and none has to look at the lengths of all (64
-// tokens of 24 pages of 64 keys, 16 heads on 2, D = 256: 19.4 + 4.1 us so, 21.5 + 4.7
-// by the lengths).
+// Rows that are sequences each take the same number of workgroups, by the room of their
+// tables, and none has to look at the lengths of all (64 tokens of 24 pages of 64 keys,
+// 16 heads on 2, D = 256: 19.6 + 4.0 us so, 21.5 + 4.7 by the lengths). That is for tables
+// about as wide as the lists: 64 of 2048 keys in tables of 512 pages leave all to one
+// workgroup of four (60 us for the whole call, 36 in tables of 32 pages).
 static int row_tiles_all(const Kv4Dims &dm) { return (int)((kv4_capacity(dm) + kKvTile - 1) / kKvTile); }
 static int few_splits(const Kv4Dims &dm, int tokens, int window, bool rows) {
   const long long tasks = kv4_tasks(dm, tokens);

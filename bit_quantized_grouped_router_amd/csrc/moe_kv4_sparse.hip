@@ -22,9 +22,9 @@
 // cache head, and the attention kernel for few query rows runs over those.
 //
 // us of scores + selection + attention (+ join of split keys), 16 heads on 2: one token
-// behind 131,149, D = 128, 32 of 2050 pages 5.3 + 7.9 + 7.3 + 3.5; 64 tokens behind up to
-// 32,000, D = 256, 24 pages each 12.5 + 10.9 + 19.6 + 4.1; 1500 tokens behind 60,000, D =
-// 128, 32 of 1922 pages each 27.9 + 26.3 + 74.2.
+// behind 131,149, D = 128, 32 of 2050 pages 5.3 + 8.1 + 7.3 + 3.5; 64 tokens behind up to
+// 32,000, D = 256, 24 pages each 12.1 + 10.8 + 19.6 + 4.0; 1500 tokens behind 60,000, D =
+// 128, 32 of 1922 pages each 27.9 + 26.8 + 74.3.
 #include "moe_kv4_sparse.h"
 
 #include "moe_kv4_device.h"
@@ -1024,7 +1024,12 @@ static hipError_t launch_selection(const Kv4Dims &dm, const Kv4Batch &bt, const 
     if (e != hipSuccess) return e;
   }
   // Few lists: two pages a lane of as many wavefronts as that takes, for the shortest
-  // chain. Many: eight a lane of a quarter as many wavefronts, for fewer barriers.
+  // chain. Many: eight a lane of a quarter as many wavefronts, for fewer barriers. us with
+  // two / eight, D = 128: tables of 2000 pages 6.8 / 7.7 for 2 lists, 10.9 / 12.7 for 256,
+  // 16.8 / 12.6 for 400, 22.7 / 14.0 for 640, 82 / 30 for 3000. (Of 512 pages, four
+  // wavefronts either way, two stays ahead: 9.4 / 12.5 for 400, 18.2 / 26.6 for 3000.) With
+  // eight / any number: 4000 pages 9.0 / 12.2 for 2 lists, 25 / 60 for 1024; 8000 pages
+  // 12.3 / 19.8 and 51 / 95.
   const long long lists = (long long)part.rows * dm.Hkv;
   const int per = dm.max_pages <= 2 * kSelectMostWaves * kWave && lists < 512 ? 2
                   : dm.max_pages <= 8 * kSelectMostWaves * kWave              ? 8

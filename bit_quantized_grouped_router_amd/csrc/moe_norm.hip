@@ -10,9 +10,11 @@
 // squares and its output. L threads take a row, 8 channels (one 16-byte or two)
 // at a time and C times, so that a group of 64 or 128 channels is 8 or 16
 // neighbouring lanes and its maximum three or four DPP steps. us: 8192 x 2048 in fp32
-// with an fp32 residual 42.8 (235 MB, 5.5 TB/s); 777 x 5120 in bf16 to e4m3 10.0 (28 MB,
-// 2.8 TB/s: three or four rows a CU, so that little overlaps); one row 2.3. Rows whose
-// strides are no multiples of 8 are read element by element: 4096 x 12001 640.
+// with an fp32 residual 43.0 (235 MB, 5.5 TB/s); 777 x 5120 in bf16 to e4m3 10.1 (28 MB,
+// 2.8 TB/s: three or four rows a CU, so that little overlaps); one row 2.3. Where the width
+// or a stride is no multiple of 8, all is read and written element by element, and rows
+// above 8192 channels spill (124 to 324 bytes a lane): 4096 x 2047 52 (2048 channels: 17),
+// 4096 x 12001 641 (12000: 126).
 #include "moe_norm.h"
 
 namespace moe {

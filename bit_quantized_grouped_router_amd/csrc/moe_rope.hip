@@ -16,9 +16,10 @@
 // LDS; each lane keeps those of its 8 channels for all of the token's heads. A
 // wavefront has one step's loads in flight and few registers, so that more of them
 // share a SIMD: with four steps' at a time 8192 tokens of 16 x 128 in bf16 take 15.6
-// us instead of 13.9 (4.8 TB/s). Prompts of 7480 tokens, 32 + 2 x 8 heads of 128 from
-// fp32, rotated and written in 60 us (4.2 TB/s); 8 tokens of 16 + 2 x 2 heads of 256 in
-// 5.2.
+// us instead of 13.9 (13.8 to 14.2 from run to run, 4.7 TB/s). Prompts of 7480 tokens, 32 + 2 x 8 heads of 128 from
+// fp32, rotated and written in 61 us (4.1 TB/s); 8 tokens of 16 + 2 x 2 heads of 256 in
+// 5.1. Heads between the powers of two leave lanes idle: 8192 x 16 heads of 72, 80 or 96
+// channels take 12.6 us, those of 64 9.5; of 136 or 192 19.2 and 20.6, those of 128 13.8.
 #include "moe_rope.h"
 
 #include "moe_kv4_write.h"

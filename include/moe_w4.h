@@ -506,7 +506,8 @@ moe_status moe_rmsnorm(int32_t T, int32_t d, const void *x, int64_t x_stride, in
  * Rotary positions: the first rot channels of a head turn in pairs (a, b) =
  * channels (2i, 2i + 1) if interleaved, (i, i + rot / 2) otherwise, by t = position
  * * freqs[i]:  (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t).
- * The other channels pass. t is taken in 64 bits, the rest in fp32.
+ * The other channels pass. t (the whole product) and its cosine and sine are taken in 64
+ * bits, the rest in fp32.
  *   freqs  fp32 [rot / 2], radians a position, in device memory
  *   rot    even, 2 .. D
  */
@@ -518,7 +519,8 @@ typedef struct {
 } moe_rope_spec;
 
 /* A norm of every head before it turns: x / sqrt(mean x^2 + eps) * w over its D channels,
- * w = weight (bf16 [D]) or 1 + weight. eps > 0 and finite. */
+ * w = weight (bf16 [D]) or 1 + weight; squares are summed in fp32, as in moe_rmsnorm. eps > 0
+ * and finite. */
 typedef struct {
   const uint16_t *weight;
   float eps;
@@ -531,7 +533,7 @@ typedef struct {
  *   positions  int32 [T], any values
  *   out        bf16 or fp32 (out_dtype) [T][H][D], out; may be x itself with the same
  *              type and stride (MOE_E_INVALID with another), and overlaps nothing else
- * Limits: D % 8 == 0, 8 <= D <= 512, H >= 1, T * H * D < 2^40; strides multiples of 8
+ * Limits: D % 8 == 0, 8 <= D <= 512, H >= 1, H * D < 2^31, T * H * D < 2^40; strides multiples of 8
  * (MOE_E_UNSUPPORTED) and at least a token long (MOE_E_INVALID).
  */
 moe_status moe_rope(int32_t T, int32_t H, int32_t D, const void *x, int64_t x_stride, int32_t x_dtype,
